@@ -23,7 +23,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _abi
-from ._abi import (EP_BF16, EP_DEVERR_BAD_ID, EP_DEVERR_DEBUG_STRAY, EP_DEVERR_DEBUG_UNWRITTEN,
+from ._abi import (EP_ACT_GELU, EP_ACT_SILU, EP_BF16, EP_DEVERR_BAD_ID, EP_DEVERR_DEBUG_STRAY, EP_DEVERR_DEBUG_UNWRITTEN,
                    EP_DEVERR_ROW_OOB, EP_DEVERR_TIMEOUT, EP_F32, EP_NOALLOC_SCRATCH_BYTES,
                    EP_LAYOUT_PACKED, EP_LAYOUT_STRIDED, EP_PERMUTE_BULK, EP_PERMUTE_DEFAULT,
                    EP_PERMUTE_VEC, EpBufferInfo, EpConfig, EpDedupOut, EpDispatchOut, EpError,
@@ -34,18 +34,20 @@ __all__ = [
     "ep_buffer_required_bytes", "ep_buffer_init", "ep_buffer_destroy", "ep_dispatch_layout",
     "ep_dispatch", "ep_dispatch_permute", "ep_combine", "ep_combine_backward",
     "ep_dispatch_backward", "ep_dispatch_dedup", "ep_dedup_expand", "ep_expert_gemm",
+    "ep_expert_glu", "ep_expert_glu_backward", "ep_expert_gemm_backward",
     "ep_get_device_error", "DedupResult",
     "ep_buffer_query", "ep_dispatch_layout_noalloc", "ep_dispatch_layout_noalloc_scratch_bytes",
     "EP_NOALLOC_SCRATCH_BYTES", "ep_pattern_probe", "ep_pad_tokens", "group_num_tokens_per_rank",
     "ep_derive_max_tokens_pretrain",
     "ep_derive_max_tokens_inference", "ep_validate_max_tokens", "ep_status_string",
     "EP_BF16", "EP_F32", "EP_PERMUTE_DEFAULT", "EP_PERMUTE_VEC", "EP_PERMUTE_BULK",
-    "EP_LAYOUT_STRIDED", "EP_LAYOUT_PACKED",
+    "EP_LAYOUT_STRIDED", "EP_LAYOUT_PACKED", "EP_ACT_SILU", "EP_ACT_GELU",
     "EP_DEVERR_BAD_ID", "EP_DEVERR_ROW_OOB", "EP_DEVERR_TIMEOUT", "EP_DEVERR_DEBUG_UNWRITTEN",
     "EP_DEVERR_DEBUG_STRAY", "library_path",
 ]
 
 _TORCH_TO_EP = {torch.bfloat16: EP_BF16, torch.float32: EP_F32}
+_ACTS = {"silu": EP_ACT_SILU, "gelu": EP_ACT_GELU}
 _EP_TO_TORCH = {EP_BF16: torch.bfloat16, EP_F32: torch.float32}
 
 
@@ -191,6 +193,47 @@ def ep_expert_gemm(handle, x_recv: torch.Tensor, weights: torch.Tensor, din: int
         _check_dtype(t, torch.bfloat16, name)
     check(_abi.lib().ep_expert_gemm(handle, _ptr(x_recv), _ptr(weights), din, dout, _ptr(y_recv),
                                     _stream(stream)), "ep_expert_gemm")
+
+
+def ep_expert_glu(handle, x_recv: torch.Tensor, w_gate_up: torch.Tensor, din: int, dff: int,
+                  act: int, gate_up: torch.Tensor | None, h: torch.Tensor, stream=None) -> None:
+    for name, t in (("x_recv", x_recv), ("w_gate_up", w_gate_up), ("gate_up", gate_up), ("h", h)):
+        if t is not None:
+            _check_dtype(t, torch.bfloat16, name)
+    check(_abi.lib().ep_expert_glu(handle, _ptr(x_recv), _ptr(w_gate_up), din, dff, act,
+                                   _ptr(gate_up), _ptr(h), _stream(stream)), "ep_expert_glu")
+
+
+def ep_expert_glu_backward(handle, grad_y: torch.Tensor, w_down: torch.Tensor,
+                           gate_up: torch.Tensor, dff: int, dout: int, act: int,
+                           grad_gate_up: torch.Tensor, stream=None) -> None:
+    for name, t in (("grad_y", grad_y), ("w_down", w_down), ("gate_up", gate_up),
+                    ("grad_gate_up", grad_gate_up)):
+        _check_dtype(t, torch.bfloat16, name)
+    check(_abi.lib().ep_expert_glu_backward(handle, _ptr(grad_y), _ptr(w_down), _ptr(gate_up),
+                                            dff, dout, act, _ptr(grad_gate_up), _stream(stream)),
+          "ep_expert_glu_backward")
+
+
+def ep_expert_gemm_backward(handle, grad_y: torch.Tensor, x_recv: torch.Tensor | None,
+                            weights: torch.Tensor | None, din: int, dout: int,
+                            grad_x: torch.Tensor | None = None,
+                            grad_weights: torch.Tensor | None = None, accumulate: bool = False,
+                            stream=None) -> None:
+    """grad_weights may be bfloat16 or float32."""
+    for name, t in (("grad_y", grad_y), ("x_recv", x_recv), ("weights", weights),
+                    ("grad_x", grad_x)):
+        if t is not None:
+            _check_dtype(t, torch.bfloat16, name)
+    w_dtype = EP_BF16
+    if grad_weights is not None:
+        if grad_weights.dtype not in _TORCH_TO_EP:
+            raise TypeError(f"grad_weights must be bfloat16 or float32, got {grad_weights.dtype}")
+        w_dtype = _TORCH_TO_EP[grad_weights.dtype]
+    check(_abi.lib().ep_expert_gemm_backward(handle, _ptr(grad_y), _ptr(x_recv), _ptr(weights),
+                                             din, dout, _ptr(grad_x), _ptr(grad_weights), w_dtype,
+                                             int(accumulate), _stream(stream)),
+          "ep_expert_gemm_backward")
 
 
 def ep_get_device_error(handle, stream=None) -> int:
@@ -524,6 +567,139 @@ class Buffer:
             y_recv = torch.empty(lead + (dout,), dtype=torch.bfloat16, device=self.device)
         ep_expert_gemm(self.handle, x_recv, weights, din, dout, y_recv, stream)
         return y_recv
+
+    # -- the experts' gated feed-forward block ---------------------------------
+    def _rows(self, t: torch.Tensor, name: str, width: int) -> torch.Tensor:
+        """t, checked to be rows of the last call's receive layout, `width` columns wide."""
+        n = self.R * self._last_stride()
+        if t.dim() < 2 or t.shape[-1] != width or t.numel() != n * width:
+            raise ValueError(f"{name} must hold the receive layout's {n} rows of {width} "
+                             f"columns, got {tuple(t.shape)}")
+        return t
+
+    def _new_rows(self, width: int) -> torch.Tensor:
+        S = self._last_stride()
+        lead = (self.R * S,) if self.packed else (self.R, S)
+        return torch.empty(lead + (width,), dtype=torch.bfloat16, device=self.device)
+
+    def _scratch_rows(self, width: int, stream) -> torch.Tensor:
+        """Rows that only this call's kernels use: from the launching stream's own pool, so
+        that dropping them orders their reuse after those kernels."""
+        if stream is None:
+            return self._new_rows(width)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return self._new_rows(width)
+
+    def _out_rows(self, t: torch.Tensor | None, name: str, width: int) -> torch.Tensor:
+        return self._new_rows(width) if t is None else self._rows(t, name, width)
+
+    def _weights(self, w: torch.Tensor, name: str, *shape: int | None) -> torch.Size:
+        want = (self.E, *shape)
+        if w.dim() != len(want) or any(n is not None and n != m for n, m in zip(want, w.shape)):
+            raise ValueError(f"{name} must be {['any' if n is None else n for n in want]}, "
+                             f"got {list(w.shape)}")
+        return w.shape
+
+    @staticmethod
+    def _activation(act: str) -> int:
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+        return _ACTS[act]
+
+    def expert_glu(self, x_recv: torch.Tensor, w_gate_up: torch.Tensor, act: str = "silu",
+                   gate_up: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+        """h = act(x Wg^T) * (x Wu^T) over each expert's receive rows, one kernel.
+        w_gate_up is [E, 2 dff, din], gate rows first. gate_up, if given, receives the
+        pre-activations for the backward pass. Returns h in the receive layout."""
+        _, dff2, din = self._weights(w_gate_up, "w_gate_up", None, None)
+        if dff2 % 2:
+            raise ValueError(f"w_gate_up must hold gate and up rows, got {dff2} rows")
+        dff = dff2 // 2
+        self._rows(x_recv, "x_recv", din)
+        if gate_up is not None:
+            self._rows(gate_up, "gate_up", dff2)
+        h = self._out_rows(h, "h", dff)
+        ep_expert_glu(self.handle, x_recv, w_gate_up, din, dff, self._activation(act), gate_up, h,
+                      stream)
+        return h
+
+    def expert_ffn(self, x_recv: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                   act: str = "silu", save: bool = False, stream=None):
+        """The experts' gated feed-forward block, y = (act(x Wg^T) * (x Wu^T)) Wd^T, with
+        w_gate_up [E, 2 dff, din] (gate rows first) and w_down [E, dout, dff]: two kernels,
+        ready for combine. save=True returns (y, h, gate_up), what expert_ffn_backward needs."""
+        _, dff2, _ = self._weights(w_gate_up, "w_gate_up", None, None)
+        self._weights(w_down, "w_down", None, dff2 // 2)
+        gate_up = self._new_rows(dff2) if save else None
+        h = self._new_rows(dff2 // 2) if save else self._scratch_rows(dff2 // 2, stream)
+        self.expert_glu(x_recv, w_gate_up, act, gate_up, h, stream)
+        y = self.expert_gemm(h, w_down, stream=stream)
+        return (y, h, gate_up) if save else y
+
+    def expert_gemm_backward(self, grad_y: torch.Tensor, x_recv: torch.Tensor | None,
+                             weights: torch.Tensor | None, want_x: bool = True,
+                             want_weights: bool = True, grad_x: torch.Tensor | None = None,
+                             grad_weights: torch.Tensor | None = None, accumulate: bool = False,
+                             stream=None):
+        """(grad_x, grad_weights) of expert_gemm, None for one that is not wanted.
+        grad_weights may be a bfloat16 or float32 tensor [E, dout, din]; accumulate=True
+        adds to it (gradient accumulation over micro-batches)."""
+        dout = grad_y.shape[-1]
+        if want_x:
+            din = self._weights(weights, "weights", dout, None)[2]
+        else:
+            din = x_recv.shape[-1]
+        self._rows(grad_y, "grad_y", dout)
+        if want_weights:
+            self._rows(x_recv, "x_recv", din)
+            if grad_weights is None:
+                if accumulate:
+                    raise ValueError("accumulate=True needs grad_weights")
+                grad_weights = torch.empty((self.E, dout, din), dtype=torch.bfloat16,
+                                           device=self.device)
+            self._weights(grad_weights, "grad_weights", dout, din)
+        grad_x = self._out_rows(grad_x, "grad_x", din) if want_x else None
+        grad_weights = grad_weights if want_weights else None
+        ep_expert_gemm_backward(self.handle, grad_y, x_recv if want_weights else None,
+                                weights if want_x else None, din, dout, grad_x, grad_weights,
+                                accumulate, stream)
+        return grad_x, grad_weights
+
+    def expert_glu_backward(self, grad_y: torch.Tensor, w_down: torch.Tensor,
+                            gate_up: torch.Tensor, act: str = "silu",
+                            grad_gate_up: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+        """The gradient of the pre-activations [.., 2 dff] from the gradient of y, through
+        w_down [E, dout, dff] and the activation, one kernel."""
+        _, dout, dff = self._weights(w_down, "w_down", None, None)
+        self._rows(grad_y, "grad_y", dout)
+        self._rows(gate_up, "gate_up", 2 * dff)
+        grad_gate_up = self._out_rows(grad_gate_up, "grad_gate_up", 2 * dff)
+        ep_expert_glu_backward(self.handle, grad_y, w_down, gate_up, dff, dout,
+                               self._activation(act), grad_gate_up, stream)
+        return grad_gate_up
+
+    def expert_ffn_backward(self, grad_y: torch.Tensor, x_recv: torch.Tensor,
+                            w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                            gate_up: torch.Tensor, h: torch.Tensor, act: str = "silu",
+                            grad_w_gate_up: torch.Tensor | None = None,
+                            grad_w_down: torch.Tensor | None = None, accumulate: bool = False,
+                            stream=None):
+        """(grad_x, grad_w_gate_up, grad_w_down) of expert_ffn, from the gate_up and h that
+        expert_ffn(..., save=True) returned. The weight gradients may be given as bfloat16
+        or float32 tensors, with accumulate=True to add to them."""
+        grad_gate_up = self._scratch_rows(gate_up.shape[-1], stream)
+        self.expert_glu_backward(grad_y, w_down, gate_up, act, grad_gate_up, stream)
+        _, grad_w_down = self.expert_gemm_backward(grad_y, h, w_down, want_x=False,
+                                                   grad_weights=grad_w_down,
+                                                   accumulate=accumulate, stream=stream)
+        grad_x, grad_w_gate_up = self.expert_gemm_backward(grad_gate_up, x_recv, w_gate_up,
+                                                           grad_weights=grad_w_gate_up,
+                                                           accumulate=accumulate, stream=stream)
+        return grad_x, grad_w_gate_up, grad_w_down
 
     def _last_stride(self) -> int:
         return self._stride

@@ -31,6 +31,9 @@ EP_PERMUTE_BULK = 2
 EP_LAYOUT_STRIDED = 0
 EP_LAYOUT_PACKED = 1
 
+EP_ACT_SILU = 0
+EP_ACT_GELU = 1
+
 EP_DEVERR_BAD_ID = 0x1
 EP_DEVERR_ROW_OOB = 0x2
 EP_DEVERR_TIMEOUT = 0x4
@@ -135,6 +138,14 @@ SIGNATURES = {
     "ep_dedup_expand": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "ep_expert_gemm": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
                                  C.c_void_p, C.c_void_p]),
+    "ep_expert_glu": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
+                                C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "ep_expert_glu_backward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                         C.c_int64, C.c_int64, C.c_int32, C.c_void_p,
+                                         C.c_void_p]),
+    "ep_expert_gemm_backward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                          C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                          C.c_int32, C.c_int32, C.c_void_p]),
     "ep_get_device_error": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint32)]),
     "ep_buffer_query": (C.c_int, [C.c_void_p, C.POINTER(EpBufferInfo)]),
     "ep_dispatch_layout_noalloc": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32,

@@ -786,6 +786,135 @@ ep_status ep_expert_gemm(ep_buffer* buf, const void* x_recv, const void* weights
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
+// What the experts' products share: a bf16 buffer with a layout, sizes of the
+// documented multiples, and counts (rows, tiles, weight lines) that fit int32.
+// *rows: receive rows of the call (0: nothing routed, no row operand is needed).
+static ep_status check_expert(const ep_buffer* b, int64_t width_a, int64_t width_b, int64_t lines,
+                              int64_t* rows)
+{
+    if (!b) return EP_ERR_INVALID_ARG;
+    if (!b->has_layout) return EP_ERR_NO_LAYOUT;
+    if (b->cfg.dtype != EP_BF16) return EP_ERR_INVALID_ARG;
+    if (width_a < 64 || width_a % 64 != 0 || width_b < 128 || width_b % 128 != 0)
+        return EP_ERR_INVALID_ARG;
+    const int64_t E = b->cfg.num_experts;
+    *rows = (int64_t)b->cfg.num_ranks * b->last_S;
+    if (width_a > INT32_MAX || lines > INT32_MAX / E) return EP_ERR_CAPACITY;
+    const int64_t wider = width_a > lines ? width_a : lines;
+    if (*rows / 128 + E > INT32_MAX / (wider / 64 + 1)) return EP_ERR_CAPACITY;
+    return EP_OK;
+}
+
+static ep::GemmArgs expert_args(ep_buffer* b, int64_t contraction, int64_t columns, void* y)
+{
+    ep::GemmArgs a;
+    a.cnt = b->cnt;
+    a.expert_offset = b->expert_offset;
+    a.y = y;
+    a.din = contraction;
+    a.dout = columns;
+    a.E = b->cfg.num_experts;
+    a.kind = b->gemm_kind > 0
+                 ? b->gemm_kind
+                 : (b->last_T * b->cfg.topk >= (int64_t)512 * b->cfg.num_experts ? 2 : 1);
+    a.bk = 64;
+    a.light_rows = b->gemm_light_rows;
+    a.err = b->err;
+    return a;
+}
+
+static ep_status cuda_status(cudaError_t e)
+{
+    if (e == cudaErrorInvalidValue) return EP_ERR_INVALID_ARG;
+    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+
+ep_status ep_expert_glu(ep_buffer* buf, const void* x_recv, const void* w_gate_up, int64_t din,
+                        int64_t dff, int32_t act, void* gate_up, void* h, ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_glu");
+    int64_t rows = 0;
+    const ep_status st = check_expert(buf, din, dff, 2 * dff, &rows);
+    if (st != EP_OK) return st;
+    if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+    if (!x_recv || !w_gate_up || !h) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(x_recv, 16) || !is_aligned(w_gate_up, 16) || !is_aligned(gate_up, 16) ||
+        !is_aligned(h, 16))
+        return EP_ERR_ALIGNMENT;
+    if (rows <= 0) return EP_OK;
+    ep::GemmArgs a = expert_args(buf, din, dff, h);
+    a.aux = gate_up;
+    a.act = act;
+    return cuda_status(ep::launch_expert_glu(a, x_recv, rows, w_gate_up, buf->num_sms,
+                                             opts(buf, as_stream(stream))));
+}
+
+ep_status ep_expert_glu_backward(ep_buffer* buf, const void* grad_y, const void* w_down,
+                                 const void* gate_up, int64_t dff, int64_t dout, int32_t act,
+                                 void* grad_gate_up, ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_glu_backward");
+    int64_t rows = 0;
+    if (dff % 128 != 0) return EP_ERR_INVALID_ARG;
+    const ep_status st = check_expert(buf, dff, dout, dout, &rows);
+    if (st != EP_OK) return st;
+    if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+    if (!grad_y || !w_down || !gate_up || !grad_gate_up) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(grad_y, 16) || !is_aligned(w_down, 16) || !is_aligned(gate_up, 16) ||
+        !is_aligned(grad_gate_up, 16))
+        return EP_ERR_ALIGNMENT;
+    if (rows <= 0) return EP_OK;
+    ep::GemmArgs a = expert_args(buf, dout, dff, grad_gate_up);
+    a.aux = const_cast<void*>(gate_up);
+    a.act = act;
+    return cuda_status(ep::launch_expert_dgrad(a, true, grad_y, rows, w_down, buf->num_sms,
+                                               opts(buf, as_stream(stream))));
+}
+
+ep_status ep_expert_gemm_backward(ep_buffer* buf, const void* grad_y, const void* x_recv,
+                                  const void* weights, int64_t din, int64_t dout, void* grad_x,
+                                  void* grad_w, int32_t grad_w_dtype, int32_t accumulate,
+                                  ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_gemm_backward");
+    int64_t rows = 0;
+    const ep_status st = check_expert(buf, din, dout, dout, &rows);
+    if (st != EP_OK) return st;
+    if (grad_w_dtype != EP_BF16 && grad_w_dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (!grad_x && !grad_w) return EP_ERR_INVALID_ARG;
+    if (!grad_y || (grad_x && !weights) || (grad_w && !x_recv)) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(grad_y, 16) || !is_aligned(x_recv, 16) || !is_aligned(weights, 16) ||
+        !is_aligned(grad_x, 16) || !is_aligned(grad_w, 16))
+        return EP_ERR_ALIGNMENT;
+    const ep::LaunchOpts o = opts(buf, as_stream(stream));
+    if (rows <= 0) {   // no receive rows at all: grad_w is zero
+        if (!grad_w || accumulate) return EP_OK;
+        const size_t bytes = (size_t)buf->cfg.num_experts * (size_t)dout * (size_t)din *
+                             (size_t)elem_bytes(grad_w_dtype);
+        return cudaMemsetAsync(grad_w, 0, bytes, o.stream) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    }
+    if (grad_x) {
+        const ep::GemmArgs a = expert_args(buf, dout, din, grad_x);
+        const ep_status s = cuda_status(
+            ep::launch_expert_dgrad(a, false, grad_y, rows, weights, buf->num_sms, o));
+        if (s != EP_OK) return s;
+    }
+    if (grad_w) {
+        ep::WgradArgs a;
+        a.cnt = buf->cnt;
+        a.expert_offset = buf->expert_offset;
+        a.grad_w = grad_w;
+        a.din = din;
+        a.dout = dout;
+        a.E = buf->cfg.num_experts;
+        a.f32 = grad_w_dtype == EP_F32;
+        a.accumulate = accumulate != 0;
+        a.err = buf->err;
+        return cuda_status(ep::launch_expert_wgrad(a, grad_y, x_recv, rows, buf->num_sms, o));
+    }
+    return EP_OK;
+}
+
 ep_status ep_get_device_error(ep_buffer* buf, ep_stream_t stream, uint32_t* flags)
 {
     if (!buf || !flags) return EP_ERR_INVALID_ARG;

@@ -53,11 +53,41 @@ struct GemmArgs {
     int light_rows;                // experts with at most this many rows are scheduled as
                                    // light (interleaved with the rest); 0: none is
     uint32_t* err;
+    void* aux = nullptr;           // the gated block: [rows][2 dout] bf16 pre-activations, written
+                                   // (forward; null: not kept) or read (gradient)
+    int act = 0;                   // the gated block: 0 silu, 1 gelu (tanh form)
 };
 // x: [rows][din] bf16 receive rows; w: [E][dout][din] bf16.
 // kernel_used: the kind that ran (see GemmArgs::kind); grid_used: its CTAs.
 cudaError_t launch_expert_gemm(const GemmArgs& a, const void* x, int64_t rows, const void* w,
                                int grid, const LaunchOpts& o, int* kernel_used, int* grid_used);
+
+// The experts' gated feed-forward block (expert_ffn.cu). Fields of GemmArgs:
+// launch_expert_glu: y = h [rows][dout], h = act(x Wg^T) * (x Wu^T), w =
+// [E][2 dout][din] (gate rows first); aux = kept pre-activations or null.
+cudaError_t launch_expert_glu(const GemmArgs& a, const void* x, int64_t rows, const void* w,
+                              int grid, const LaunchOpts& o);
+// Data gradient of a product y = x W^T with W [E][din][dout]: out[p] = grad[p] W_e,
+// grad = [rows][din], out = [rows][dout] (din, dout: the forward's dout and din).
+// With glu, y = [rows][2 dout] receives the gradients of the pre-activations in
+// aux, through h = act(g) * u, instead of the gradient of h.
+cudaError_t launch_expert_dgrad(const GemmArgs& a, bool glu, const void* grad, int64_t rows,
+                                const void* w, int grid, const LaunchOpts& o);
+
+// Weight gradient (expert_wgrad.cu): grad_w[e] = grad_e^T x_e over each expert's
+// rows, grad = [rows][dout], x = [rows][din], both bf16.
+struct WgradArgs {
+    const int32_t* cnt;            // [E]
+    const int32_t* expert_offset;  // [E]
+    void* grad_w;                  // [E][dout][din], bf16 or fp32
+    int64_t din, dout;             // din % 64 == 0, dout % 128 == 0
+    int E;
+    bool f32;                      // grad_w's type
+    bool accumulate;               // add to what grad_w holds
+    uint32_t* err;
+};
+cudaError_t launch_expert_wgrad(const WgradArgs& a, const void* grad, const void* x, int64_t rows,
+                                int grid, const LaunchOpts& o);
 
 // Sentinel checks of the receive buffer (debug.cu, EP_DEBUG=1).
 constexpr uint32_t kErrDebugUnwritten = 0x8u;   // a row inside a rank's total kept the sentinel

@@ -348,6 +348,55 @@ EP_API ep_status ep_dedup_expand(ep_buffer* buf, const int32_t* topk_expert_ids_
 EP_API ep_status ep_expert_gemm(ep_buffer* buf, const void* x_recv, const void* weights,
                                 int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
 
+/* ---- The experts' gated feed-forward block -----------------------------------
+ * What a MoE layer's experts compute between dispatch and combine ([graph] "Tests":
+ * layout -> dispatch -> expert -> combine; "Internode" item 2: the counts stay on
+ * the device), for training and inference:
+ *     g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T
+ * over each expert's receive rows, as ep_expert_glu (g, u, h) and ep_expert_gemm
+ * (y). All of it takes bf16 buffers (EP_ERR_INVALID_ARG otherwise), the counts and
+ * offsets of the last layout on the buffer, and rows in the receive layout
+ * ([R*S][width], strided or packed; rows of no expert are neither read into any
+ * result nor written). Tensors are dense, bf16 unless said, 16-byte aligned, on the
+ * buffer's device; outputs must not overlap inputs. din, dff, dout are given as for
+ * the forward product: din % 64 == 0, dff % 128 == 0, dout % 128 == 0. */
+
+/* The gate's activation. */
+typedef enum {
+    EP_ACT_SILU = 0,              /* g / (1 + e^-g) */
+    EP_ACT_GELU = 1               /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} ep_act;
+
+/* Both projections, the activation and the product in one kernel: w_gate_up is
+ * [E][2 dff][din], each expert's dff gate rows before its dff up rows. h [R*S][dff]
+ * = bf16(act(g) * u) from the fp32 accumulators; gate_up [R*S][2 dff], if non-NULL,
+ * receives bf16(g) and bf16(u) for the backward pass. */
+EP_API ep_status ep_expert_glu(ep_buffer* buf, const void* x_recv, const void* w_gate_up,
+                               int64_t din, int64_t dff, int32_t act, void* gate_up, void* h,
+                               ep_stream_t stream);
+
+/* Gradient of the pre-activations from the gradient of y (grad_y [R*S][dout], w_down
+ * [E][dout][dff]): with grad h = grad_y W_down, kept in fp32,
+ *     grad_gate_up = bf16([grad h * u * act'(g), grad h * act(g)])   [R*S][2 dff]
+ * from gate_up as ep_expert_glu kept it. grad_x and grad W_gate_up then follow from
+ * ep_expert_gemm_backward with grad_y = grad_gate_up, dout = 2 dff. */
+EP_API ep_status ep_expert_glu_backward(ep_buffer* buf, const void* grad_y, const void* w_down,
+                                        const void* gate_up, int64_t dff, int64_t dout,
+                                        int32_t act, void* grad_gate_up, ep_stream_t stream);
+
+/* Gradients of ep_expert_gemm (y = x W_e^T), either or both:
+ *     grad_x[p] = grad_y[p] W_e                       [R*S][din] (NULL: not wanted)
+ *     grad_weights[e] = sum over e's rows of grad_y[p]^T x_recv[p]   [E][dout][din]
+ * in grad_w_dtype (EP_BF16 or EP_F32), summed in fp32. accumulate != 0 adds to what
+ * grad_weights holds (in fp32, rounded once) instead of replacing it; an expert
+ * without rows gets zeros, or keeps what it has when accumulating. weights is read
+ * only for grad_x and x_recv only for grad_weights. Deterministic: every element is
+ * summed by one CTA in row order. */
+EP_API ep_status ep_expert_gemm_backward(ep_buffer* buf, const void* grad_y, const void* x_recv,
+                                         const void* weights, int64_t din, int64_t dout,
+                                         void* grad_x, void* grad_weights, int32_t grad_w_dtype,
+                                         int32_t accumulate, ep_stream_t stream);
+
 /* Synchronously read and clear the device error word (EP_DEVERR_* bits).
  * Refused with EP_ERR_CAPTURE_HOST_SYNC while the stream is capturing. Status
  * stays on the device and is read only here ([graph] "Internode" item 1: no
