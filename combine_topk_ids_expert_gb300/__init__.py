@@ -27,7 +27,7 @@ from ._abi import (EP_ACT_GELU, EP_ACT_SILU, EP_BF16, EP_DEVERR_BAD_ID, EP_DEVER
                    EP_DEVERR_ROW_OOB, EP_DEVERR_TIMEOUT, EP_F32, EP_NOALLOC_SCRATCH_BYTES,
                    EP_LAYOUT_PACKED, EP_LAYOUT_STRIDED, EP_PERMUTE_BULK, EP_PERMUTE_DEFAULT,
                    EP_PERMUTE_VEC, EpBufferInfo, EpConfig, EpDedupOut, EpDispatchOut, EpError,
-                   EpLayout, check)
+                   EpLayout, EpW4, check)
 
 __all__ = [
     "Buffer", "Layout", "DispatchResult", "EpConfig", "EpError",
@@ -35,6 +35,7 @@ __all__ = [
     "ep_dispatch", "ep_dispatch_permute", "ep_combine", "ep_combine_backward",
     "ep_dispatch_backward", "ep_dispatch_dedup", "ep_dedup_expand", "ep_expert_gemm",
     "ep_expert_glu", "ep_expert_glu_backward", "ep_expert_gemm_backward",
+    "ep_expert_gemv_w4", "ep_expert_glu_w4", "W4", "EpW4",
     "ep_get_device_error", "DedupResult",
     "ep_buffer_query", "ep_dispatch_layout_noalloc", "ep_dispatch_layout_noalloc_scratch_bytes",
     "EP_NOALLOC_SCRATCH_BYTES", "ep_pattern_probe", "ep_pad_tokens", "group_num_tokens_per_rank",
@@ -234,6 +235,61 @@ def ep_expert_gemm_backward(handle, grad_y: torch.Tensor, x_recv: torch.Tensor |
                                              din, dout, _ptr(grad_x), _ptr(grad_weights), w_dtype,
                                              int(accumulate), _stream(stream)),
           "ep_expert_gemm_backward")
+
+
+@dataclass
+class W4:
+    """The experts' 4-bit weights [E, rows, din] with group scales: w = (code - zero) * scale.
+    A group is din / scales.shape[-1] consecutive elements: 32, 64 or 128."""
+    codes: torch.Tensor               # [E, rows, din / 2] uint8, element 2j in byte j's low nibble
+    scales: torch.Tensor              # [E, rows, din / group] bfloat16 or float32
+    zeros: torch.Tensor | None = None   # [E, rows, din / group] uint8 (0..15); None: 8 everywhere
+
+    def __post_init__(self):
+        c, s, z = self.codes, self.scales, self.zeros
+        _check_dtype(c, torch.uint8, "codes")
+        if s.dtype not in _TORCH_TO_EP:
+            raise TypeError(f"scales must be bfloat16 or float32, got {s.dtype}")
+        if c.dim() != 3 or s.dim() != 3 or c.shape[:2] != s.shape[:2] or not s.shape[2] \
+                or 2 * c.shape[2] % s.shape[2]:
+            raise ValueError(f"codes [E, rows, din / 2] and scales [E, rows, din / group] do not "
+                             f"fit: {tuple(c.shape)}, {tuple(s.shape)}")
+        if z is not None:
+            _check_dtype(z, torch.uint8, "zeros")
+            if z.shape != s.shape:
+                raise ValueError(f"zeros must be shaped as scales, got {tuple(z.shape)}")
+
+    @property
+    def din(self) -> int:
+        return 2 * self.codes.shape[2]
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def group(self) -> int:
+        return self.din // self.scales.shape[2]
+
+    def _struct(self) -> EpW4:
+        return EpW4(_ptr(self.codes), _ptr(self.scales), _ptr(self.zeros),
+                    _TORCH_TO_EP[self.scales.dtype], self.group)
+
+
+def ep_expert_gemv_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dout: int,
+                      y_recv: torch.Tensor, stream=None) -> None:
+    for name, t in (("x_recv", x_recv), ("y_recv", y_recv)):
+        _check_dtype(t, torch.bfloat16, name)
+    check(_abi.lib().ep_expert_gemv_w4(handle, _ptr(x_recv), C.byref(weights._struct()), din, dout,
+                                       _ptr(y_recv), _stream(stream)), "ep_expert_gemv_w4")
+
+
+def ep_expert_glu_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dff: int, act: int,
+                     h: torch.Tensor, stream=None) -> None:
+    for name, t in (("x_recv", x_recv), ("h", h)):
+        _check_dtype(t, torch.bfloat16, name)
+    check(_abi.lib().ep_expert_glu_w4(handle, _ptr(x_recv), C.byref(weights._struct()), din, dff,
+                                      act, _ptr(h), _stream(stream)), "ep_expert_glu_w4")
 
 
 def ep_get_device_error(handle, stream=None) -> int:
@@ -700,6 +756,40 @@ class Buffer:
                                                            grad_weights=grad_w_gate_up,
                                                            accumulate=accumulate, stream=stream)
         return grad_x, grad_w_gate_up, grad_w_down
+
+    # -- the same block on 4-bit weights ----------------------------------------
+    def expert_gemv_w4(self, x_recv: torch.Tensor, weights: W4,
+                       y_recv: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """y = x W_e^T over each expert's receive rows with 4-bit weights, for the few rows
+        per expert of a decode batch."""
+        self._weights(weights.codes, "weights.codes", None, None)
+        self._rows(x_recv, "x_recv", weights.din)
+        y_recv = self._out_rows(y_recv, "y_recv", weights.rows)
+        ep_expert_gemv_w4(self.handle, x_recv, weights, weights.din, weights.rows, y_recv, stream)
+        return y_recv
+
+    def expert_glu_w4(self, x_recv: torch.Tensor, w_gate_up: W4, act: str = "silu",
+                      h: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """expert_glu with 4-bit weights of 2 dff rows per expert, gate rows first."""
+        self._weights(w_gate_up.codes, "w_gate_up.codes", None, None)
+        if w_gate_up.rows % 2:
+            raise ValueError(f"w_gate_up must hold gate and up rows, got {w_gate_up.rows} rows")
+        dff = w_gate_up.rows // 2
+        self._rows(x_recv, "x_recv", w_gate_up.din)
+        h = self._out_rows(h, "h", dff)
+        ep_expert_glu_w4(self.handle, x_recv, w_gate_up, w_gate_up.din, dff,
+                         self._activation(act), h, stream)
+        return h
+
+    def expert_ffn_w4(self, x_recv: torch.Tensor, w_gate_up: W4, w_down: W4, act: str = "silu",
+                      y_recv: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """expert_ffn with 4-bit weights: two kernels, ready for combine."""
+        if w_down.din * 2 != w_gate_up.rows:
+            raise ValueError(f"w_down takes {w_down.din} columns, w_gate_up gives "
+                             f"{w_gate_up.rows // 2}")
+        h = self.expert_glu_w4(x_recv, w_gate_up, act,
+                               self._scratch_rows(w_down.din, stream), stream)
+        return self.expert_gemv_w4(h, w_down, y_recv, stream)
 
     def _last_stride(self) -> int:
         return self._stride

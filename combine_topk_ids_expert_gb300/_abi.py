@@ -115,6 +115,16 @@ class EpBufferInfo(C.Structure):
     ]
 
 
+class EpW4(C.Structure):
+    _fields_ = [
+        ("codes", C.c_void_p),
+        ("scales", C.c_void_p),
+        ("zeros", C.c_void_p),
+        ("scale_dtype", C.c_int32),
+        ("group", C.c_int32),
+    ]
+
+
 # name -> (restype, argtypes), in the order of include/ep.h
 SIGNATURES = {
     "ep_buffer_required_bytes": (C.c_size_t, [C.POINTER(EpConfig)]),
@@ -146,6 +156,10 @@ SIGNATURES = {
     "ep_expert_gemm_backward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                           C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
                                           C.c_int32, C.c_int32, C.c_void_p]),
+    "ep_expert_gemv_w4": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(EpW4), C.c_int64,
+                                    C.c_int64, C.c_void_p, C.c_void_p]),
+    "ep_expert_glu_w4": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(EpW4), C.c_int64,
+                                   C.c_int64, C.c_int32, C.c_void_p, C.c_void_p]),
     "ep_get_device_error": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint32)]),
     "ep_buffer_query": (C.c_int, [C.c_void_p, C.POINTER(EpBufferInfo)]),
     "ep_dispatch_layout_noalloc": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32,

@@ -915,6 +915,58 @@ ep_status ep_expert_gemm_backward(ep_buffer* buf, const void* grad_y, const void
     return EP_OK;
 }
 
+static ep_status enqueue_w4(ep_buffer* b, const void* x, const ep_w4* w, int64_t din, int64_t dout,
+                            bool glu, int32_t act, void* y, ep_stream_t stream)
+{
+    if (!b || !w) return EP_ERR_INVALID_ARG;
+    if (!b->has_layout) return EP_ERR_NO_LAYOUT;
+    if (b->cfg.dtype != EP_BF16) return EP_ERR_INVALID_ARG;
+    if (w->group != 32 && w->group != 64 && w->group != 128) return EP_ERR_INVALID_ARG;
+    if (w->scale_dtype != EP_BF16 && w->scale_dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (din < w->group || din % w->group != 0 || dout < 8 || dout % 8 != 0)
+        return EP_ERR_INVALID_ARG;
+    if (!x || !w->codes || !w->scales || !y) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(x, 16) || !is_aligned(w->codes, 16) || !is_aligned(y, 16) ||
+        !is_aligned(w->scales, (uintptr_t)elem_bytes(w->scale_dtype)))
+        return EP_ERR_ALIGNMENT;
+    const int64_t E = b->cfg.num_experts, rows = (int64_t)b->cfg.num_ranks * b->last_S;
+    if (din > INT32_MAX || dout > INT32_MAX / 2 / E) return EP_ERR_CAPACITY;
+    if (rows <= 0) return EP_OK;
+    // Units (row chunks times column blocks) and weight rows are counted in int32.
+    if (rows / 8 + E > INT32_MAX / (dout / 32 + 1)) return EP_ERR_CAPACITY;
+    ep::W4Args a;
+    a.cnt = b->cnt;
+    a.expert_offset = b->expert_offset;
+    a.scales = w->scales;
+    a.zeros = w->zeros;
+    a.scale_f32 = w->scale_dtype == EP_F32;
+    a.group = w->group;
+    a.y = y;
+    a.din = din;
+    a.dout = dout;
+    a.E = b->cfg.num_experts;
+    a.act = act;
+    a.err = b->err;
+    const bool wide = b->last_T * b->cfg.topk > 8 * E;
+    return cuda_status(ep::launch_expert_w4(a, glu, wide, x, rows, w->codes, b->num_sms,
+                                            opts(b, as_stream(stream))));
+}
+
+ep_status ep_expert_gemv_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights, int64_t din,
+                            int64_t dout, void* y_recv, ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_gemv_w4");
+    return enqueue_w4(buf, x_recv, weights, din, dout, false, 0, y_recv, stream);
+}
+
+ep_status ep_expert_glu_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights, int64_t din,
+                           int64_t dff, int32_t act, void* h, ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_glu_w4");
+    if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+    return enqueue_w4(buf, x_recv, weights, din, dff, true, act, h, stream);
+}
+
 ep_status ep_get_device_error(ep_buffer* buf, ep_stream_t stream, uint32_t* flags)
 {
     if (!buf || !flags) return EP_ERR_INVALID_ARG;

@@ -158,30 +158,6 @@ __device__ __forceinline__ uint64_t desc_b(uint32_t sb, int j)
                    : smem_desc<C>(sb + (uint32_t)j * (kUmmaK * 2));
 }
 
-// The gate's activation and its slope, in fp32. silu: g s, s + g s (1 - s) with
-// s = 1 / (1 + e^-g). gelu (tanh form): (1 + tanh w) / 2 = 1 / (1 + e^-2w), so it is
-// g p with p = 1 / (1 + e^-v), v = 2 sqrt(2 / pi) (g + 0.044715 g^3), and the slope
-// is p + g v' p (1 - p). __expf and __fdividef are off by a few ulp of fp32; the
-// results leave in bf16.
-constexpr float kGeluC = 1.5957691216057308f;   // 2 sqrt(2 / pi)
-__device__ __forceinline__ float sigmoid_of(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
-
-__device__ __forceinline__ float act_value(float g, int act)
-{
-    const float v = act == 0 ? g : kGeluC * (g + 0.044715f * g * g * g);
-    return g * sigmoid_of(v);
-}
-
-__device__ __forceinline__ void act_value_slope(float g, int act, float* value, float* slope)
-{
-    const float v = act == 0 ? g : kGeluC * (g + 0.044715f * g * g * g);
-    const float dv = act == 0 ? 1.0f : kGeluC * (1.0f + 3.0f * 0.044715f * g * g);
-    const float p = sigmoid_of(v);
-    *value = g * p;
-    const float t = p * (1.0f - p);
-    *slope = t > 0.0f ? p + g * dv * t : p;   // far out g v' overflows where t is zero
-}
-
 // tm_a: box of [128 rows][BK] over the receive rows; tm_a_half: [64 rows][BK]
 // (pairs' M = 128 tiles); tm_b: box of [kRowsB rows][BK] over the weights
 // (half a column block per CTA for pairs), or 64 x 64 boxes (load_b).

@@ -252,6 +252,30 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi)
     return r;
 }
 
+// The gate's activation and its slope, in fp32. silu: g s, s + g s (1 - s) with
+// s = 1 / (1 + e^-g). gelu (tanh form): (1 + tanh w) / 2 = 1 / (1 + e^-2w), so it is
+// g p with p = 1 / (1 + e^-v), v = 2 sqrt(2 / pi) (g + 0.044715 g^3), and the slope
+// is p + g v' p (1 - p). __expf and __fdividef are off by a few ulp of fp32; the
+// results leave in bf16.
+constexpr float kGeluC = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+__device__ __forceinline__ float sigmoid_of(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+__device__ __forceinline__ float act_value(float g, int act)
+{
+    const float v = act == 0 ? g : kGeluC * (g + 0.044715f * g * g * g);
+    return g * sigmoid_of(v);
+}
+
+__device__ __forceinline__ void act_value_slope(float g, int act, float* value, float* slope)
+{
+    const float v = act == 0 ? g : kGeluC * (g + 0.044715f * g * g * g);
+    const float dv = act == 0 ? 1.0f : kGeluC * (1.0f + 3.0f * 0.044715f * g * g);
+    const float p = sigmoid_of(v);
+    *value = g * p;
+    const float t = p * (1.0f - p);
+    *slope = t > 0.0f ? p + g * dv * t : p;   // far out g v' overflows where t is zero
+}
+
 // 32 bf16 columns of one row, packed from fp32 / unpacked into fp32.
 __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32])
 {

@@ -397,6 +397,36 @@ EP_API ep_status ep_expert_gemm_backward(ep_buffer* buf, const void* grad_y, con
                                          void* grad_x, void* grad_weights, int32_t grad_w_dtype,
                                          int32_t accumulate, ep_stream_t stream);
 
+/* ---- Products with 4-bit weights, for decoding ---------------------------------
+ * The same block served: weights of 4-bit codes with one scale (and zero point) per
+ * group of consecutive elements of a row,
+ *     w[o][i] = (code[o][i] - zero[o][i / group]) * scale[o][i / group],
+ * for the few rows that each expert gets from a batch of single tokens. Any number of
+ * rows is computed correctly; the kernels are made for up to about 32 per expert,
+ * where reading the weights is what the call costs. All pointers are device memory,
+ * codes 16-byte aligned, the rest aligned to their elements. */
+typedef struct {
+    const uint8_t* codes;         /* [E][rows][din / 2]: element 2j in the low nibble of byte j */
+    const void* scales;           /* [E][rows][din / group] of scale_dtype */
+    const uint8_t* zeros;         /* [E][rows][din / group], values 0..15; NULL: every zero is 8 */
+    int32_t scale_dtype;          /* ep_dtype */
+    int32_t group;                /* 32, 64 or 128 */
+} ep_w4;
+
+/* y_recv[p][o] = sum_i w[e][o][i] * x_recv[p][i] for each expert's rows p: x_recv
+ * [R*S][din], y_recv [R*S][dout], bf16, in the receive layout as for ep_expert_gemm
+ * (same buffers, errors and rows left alone); din % group == 0, dout % 8 == 0. code -
+ * zero and x are multiplied exactly and summed in fp32 within a group, the groups'
+ * sums scaled and summed in fp32 in a fixed order, and rounded once to bf16. */
+EP_API ep_status ep_expert_gemv_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights,
+                                   int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
+
+/* The gated projections on 4-bit weights: weights has 2 dff rows per expert, gate rows
+ * first; h [R*S][dff] = bf16(act(g) * u), both sums in fp32. dff % 8 == 0. */
+EP_API ep_status ep_expert_glu_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights,
+                                  int64_t din, int64_t dff, int32_t act, void* h,
+                                  ep_stream_t stream);
+
 /* Synchronously read and clear the device error word (EP_DEVERR_* bits).
  * Refused with EP_ERR_CAPTURE_HOST_SYNC while the stream is capturing. Status
  * stays on the device and is read only here ([graph] "Internode" item 1: no
