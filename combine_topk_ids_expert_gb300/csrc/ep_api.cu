@@ -932,14 +932,17 @@ static ep_status enqueue_w4(ep_buffer* b, const void* x, const ep_w4* w, int64_t
     const int64_t E = b->cfg.num_experts, rows = (int64_t)b->cfg.num_ranks * b->last_S;
     if (din > INT32_MAX || dout > INT32_MAX / 2 / E) return EP_ERR_CAPACITY;
     if (rows <= 0) return EP_OK;
-    // Units (row chunks times column blocks) and weight rows are counted in int32.
-    if (rows / 8 + E > INT32_MAX / (dout / 32 + 1)) return EP_ERR_CAPACITY;
+    // Row chunks times column blocks, and weight rows, are counted in int32.
+    if (rows / 8 + E > INT32_MAX / (dout / 16 + 1)) return EP_ERR_CAPACITY;
     ep::W4Args a;
     a.cnt = b->cnt;
     a.expert_offset = b->expert_offset;
+    a.x = x;
+    a.codes = w->codes;
     a.scales = w->scales;
     a.zeros = w->zeros;
     a.scale_f32 = w->scale_dtype == EP_F32;
+    a.glu = glu;
     a.group = w->group;
     a.y = y;
     a.din = din;
@@ -947,8 +950,10 @@ static ep_status enqueue_w4(ep_buffer* b, const void* x, const ep_w4* w, int64_t
     a.E = b->cfg.num_experts;
     a.act = act;
     a.err = b->err;
-    const bool wide = b->last_T * b->cfg.topk > 8 * E;
-    return cuda_status(ep::launch_expert_w4(a, glu, wide, x, rows, w->codes, b->num_sms,
+    // Rows an expert is likely to have: twice the mean (routing is uneven), no more than
+    // the call's tokens.
+    const int64_t mean2 = (2 * b->last_T * b->cfg.topk + E - 1) / E;
+    return cuda_status(ep::launch_expert_w4(a, std::min(mean2, b->last_T), b->num_sms,
                                             opts(b, as_stream(stream))));
 }
 

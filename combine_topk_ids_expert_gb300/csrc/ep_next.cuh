@@ -89,14 +89,17 @@ struct WgradArgs {
 cudaError_t launch_expert_wgrad(const WgradArgs& a, const void* grad, const void* x, int64_t rows,
                                 int grid, const LaunchOpts& o);
 
-// Products with 4-bit weights (expert_w4.cuh): codes [E][rows of W][din / 2], where
-// W has dout rows per expert, or dout gate rows and dout up rows with glu.
+// Products with 4-bit weights (expert_w4.cuh): W has dout rows per expert, or dout gate
+// rows and dout up rows with glu (y is then act(g) * u).
 struct W4Args {
     const int32_t* cnt;            // [E]
     const int32_t* expert_offset;  // [E]
+    const void* x;                 // [rows][din] bf16
+    const uint8_t* codes;          // [E][rows of W][din / 2]
     const void* scales;            // [E][rows of W][din / group], bf16 or fp32
     const uint8_t* zeros;          // same shape, or null: 8
     bool scale_f32;
+    bool glu;
     int group;                     // 32, 64 or 128 elements of din
     void* y;                       // [rows][dout] bf16
     int64_t din, dout;             // din % group == 0, dout % 8 == 0
@@ -104,11 +107,11 @@ struct W4Args {
     int act;                       // glu: as GemmArgs::act
     uint32_t* err;
 };
-// wide: 16 rows of an expert at a time instead of 8.
-cudaError_t launch_expert_w4(const W4Args& a, bool glu, bool wide, const void* x, int64_t rows,
-                             const void* codes, int num_sms, const LaunchOpts& o);
-cudaError_t launch_expert_w4_wide(const W4Args& a, bool glu, const void* x, int64_t rows,
-                                  const void* codes, int num_sms, const LaunchOpts& o);
+// expected_rows: rows per expert that the call is likely to have.
+cudaError_t launch_expert_w4(const W4Args& a, int64_t expected_rows, int num_sms,
+                             const LaunchOpts& o);
+cudaError_t launch_expert_w4_16(const W4Args& a, int num_sms, const LaunchOpts& o);
+cudaError_t launch_expert_w4_32(const W4Args& a, int num_sms, const LaunchOpts& o);
 
 // Sentinel checks of the receive buffer (debug.cu, EP_DEBUG=1).
 constexpr uint32_t kErrDebugUnwritten = 0x8u;   // a row inside a rank's total kept the sentinel

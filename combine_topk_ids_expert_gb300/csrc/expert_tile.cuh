@@ -74,18 +74,6 @@ struct Cfg {
     static_assert(kSmem <= (size_t)kSmemLimit, "ring does not fit in shared memory");
 };
 
-// Index e with pre[e] <= i < pre[e+1] of a non-decreasing prefix (i < pre[E]).
-__device__ __forceinline__ int expert_of(const int* pre, int E, int i)
-{
-    int lo = 0, hi = E;   // invariant: pre[lo] <= i < pre[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= i) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 struct TileRef {
     int e;       // expert
     int mt;      // row tile (of kTileRows rows) within the expert

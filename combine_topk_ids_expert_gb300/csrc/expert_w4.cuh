@@ -1,32 +1,37 @@
 // expert_w4.cuh - the products of each expert's few rows with 4-bit weights and
-// group scales, for decoding (expert_w4.cu, expert_w4_wide.cu instantiate it):
+// group scales, for decoding (expert_w4_8.cu, _16.cu and _32.cu instantiate it):
 //     y[p][o] = sum over groups G of s[e][o][G] * sum over i in G of (q[e][o][i] - z) x[p][i]
 // and the gated form h = act(g) * u over gate and up rows of the same matrix.
 //
 // What bounds it: the weights are read once for a handful of rows, half a byte
-// each, so the floor is HBM. On the way a code has to become a bf16 operand in
-// fewer than about three instructions per lane and code, or the SMs fall behind
-// HBM: two codes at a time are masked onto the bits of 128.0 in bf16 (128 + q is
-// exact there) and 128 + z is subtracted in one packed instruction, also exact.
-// q - z and x are exact in bf16, so a group's sum is a plain fp32 accumulation on
-// mma.sync (16 output columns x 8 rows x 16; too small and too memory-bound for
-// tcgen05 to matter), and the group's scale enters once, as one fp32 fma.
+// each, so the floor is HBM: at its rate an SM has about 350 cycles for 16 KB of
+// codes (32768 of them), under 1.4 instruction slots for 32 codes. Unpacking codes
+// into 16-bit operands (a shift, a mask and a subtraction for every two) costs
+// several times that; the kernel avoids it:
+//   - a nibble q, zero-extended to a byte, IS an fp8 number: read as e4m3 it is
+//     q * 2^-9 exactly (the subnormals and the first binade share one step). So
+//     8 codes become two 32-bit operands with one shift and two masks;
+//   - 128 elements of a row of x are scaled by a power of two that puts the largest
+//     into [128, 256) and split into two e4m3 terms, x = hi + lo / 32. A bf16 has 8
+//     significant bits, an e4m3 number 4: the two are exact for every element down
+//     to 2^-14 of the block's largest, and off by at most 2^-22 of it below;
+//   - the tensor cores multiply and sum in fp32: tcgen05.mma.kind::f8f6f4 with the
+//     codes as A (128 output columns on TMEM's lanes, written there by tcgen05.st
+//     without passing shared memory again) and the two terms of at most NR rows as
+//     B (N = 2 NR). Each scale group has its own accumulator;
+//   - draining a group, a lane holds one output column: its scale enters as one fp32
+//     fma per row (with what undoes x's scale), its zero point as one more with the
+//     group's sum of x.
 //
-// Layout: codes stay as a user has them, [E][dout][din / 2] bytes, the even
-// element in the low nibble. The order of the contraction inside one MMA is free as
-// long as both operands agree: a lane takes a 32-bit word (8 consecutive codes) of
-// its row, whose masks yield the pairs (0, 4), (1, 5), (2, 6), (3, 7), and picks the
-// same pairs out of 16 bytes of x.
+// Work: 16-column blocks of all (expert, chunk of NR rows), laid end to end and cut
+// into equal contiguous shares, one per CTA (one CTA per SM); a share is walked in
+// tiles of at most 128 columns (gated: 64 gate and 64 up). x is converted when the
+// expert or chunk changes and stays in shared memory for the tiles that follow; the
+// copies of the codes run ahead over tile boundaries all the while.
 //
-// Work: a unit is 64 output columns (gated: 32 gate and 32 up) of one expert for at
-// most NR of its rows over the whole contraction; an expert's row chunks follow
-// each other for the same columns, so that the second finds the weights in L2.
-// The contraction is cut into slices of 128 and dealt to the CTA's 8 warps in turn,
-// across unit boundaries. Each warp fills its own ring of slices by TMA (codes with
-// the 64-byte swizzle, which makes the word loads free of bank conflicts; x as
-// [32-element chunk][row]) two slices ahead, also into the next unit, and needs no
-// other warp until the unit's sums are added up through shared memory, in warp
-// order. Every wait is bounded.
+// Roles (14 warps): 0 copies codes (TMA, 256-code slices of 16 columns per box, 128-
+// byte swizzle), 1 issues the MMAs, 2-9 move codes to TMEM (two sets, alternate
+// slices), 10-13 drain; 2-13 convert x together. Every wait is bounded.
 #pragma once
 
 #include "umma.cuh"
@@ -34,57 +39,86 @@
 namespace ep {
 namespace {
 
-constexpr int kW4Warps = 8;
-constexpr int kW4Threads = 32 * kW4Warps;
-constexpr int kW4Cols = 64;         // weight rows (output columns) of a unit
-constexpr int kW4Slice = 128;       // contraction elements of a slice
-constexpr int kW4Chunks = kW4Slice / 32;
-constexpr uint32_t kW4CodeBytes = kW4Cols * kW4Slice / 2;
+constexpr int kW4Slice = 256;             // contraction elements of a slice
+constexpr int kW4Block = 16;              // output columns of a block
+constexpr uint32_t kW4BoxBytes = kW4Block * kW4Slice / 2;
+constexpr uint32_t kW4StageBytes = 8 * kW4BoxBytes;
+constexpr int kW4MaxStages = 8, kW4MinStages = 4;
+constexpr int kW4ASlots = 4;              // slices of A in TMEM, 64 columns each
+constexpr int kW4DCols = 256;             // TMEM columns of accumulators, then A
+constexpr uint32_t kW4ABase = kW4DCols;
+constexpr int kW4MaxDSlots = 8;
+constexpr uint32_t kW4StateBytes = 1024;  // barriers and small state
+constexpr int kW4Bars = 2 * kW4MaxStages + 2 * kW4ASlots + 2 * kW4MaxDSlots + 4;
 
-template <int NR_, int CPG_, bool GLU_>
+template <int NR_, int GROUP_>
 struct W4Cfg {
-    static constexpr int NR = NR_;          // rows of x a unit takes: 8 or 16
-    static constexpr int NT = NR / 8;       // MMA row tiles (its N)
-    static constexpr int CPG = CPG_;        // 32-element chunks of a scale group: 1, 2, 4
-    static constexpr int GROUPS = kW4Chunks / CPG;
-    static constexpr bool GLU = GLU_;
-    static constexpr int kOut = GLU ? kW4Cols / 2 : kW4Cols;
-    static constexpr int kPerSm = NR == 8 ? 2 : 1;
-    static constexpr int SLOTS = NR == 8 ? 2 : 3;
-    static constexpr uint32_t kXBytes = NR * kW4Slice * 2;
-    static constexpr uint32_t kSlotBytes = kW4CodeBytes + kXBytes;
-    static constexpr int kRedStride = NR + 1;
-    static constexpr size_t kRing = (size_t)kW4Warps * SLOTS * kSlotBytes;
-    static constexpr size_t kRed = (size_t)(kW4Warps / 2) * kW4Cols * kRedStride * 4;
-    static constexpr size_t kSmemFixed = 512 + kRing + kRed + 8 * kW4Warps * SLOTS + 64;
+    static constexpr int NR = NR_, GROUP = GROUP_;
+    static constexpr int N = 2 * NR;                         // hi rows, then lo rows
+    // Sets of four warps that move codes to TMEM, alternate slices. Two need 14 warps,
+    // which leaves 128 registers to a thread: enough while a lane drains few rows.
+    static constexpr int kSets = 1;
+    static constexpr int kConvThreads = 128 * (kSets + 1);
+    static constexpr int kThreads = 64 + kConvThreads;
+    static constexpr int GPS = kW4Slice / GROUP;             // scale groups of a slice
+    static constexpr int GB = GPS < 128 / N ? GPS : 128 / N;             // groups per accumulator slot
+    static constexpr int DSLOTS = kW4DCols / (GB * N);
+    static constexpr int SPB = 8 / GPS;                      // slices whose scales a lane loads at once
+    static constexpr int STEPS = GROUP / 32;                 // MMAs (K = 32) of a group
+    // kind::f8f6f4: fp32 accumulate, A and B e4m3 (0), both K-major, N, M = 128.
+    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    static constexpr uint32_t kPanelBytes = N * 128;         // B of 128 contraction elements
+    static constexpr int kSwap = 64 * (NR + 1) * 4;          // gated: up sums on their way to gate lanes
+    static_assert(GPS % GB == 0 && N % 16 == 0 && N <= 64 && DSLOTS <= kW4MaxDSlots, "slots");
 };
 
-// mma.sync m16n8k16: a = 16 output columns x 16, b = 16 x 8 rows.
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1)
+// Shared memory: the ring, x, its group sums, the swap area, barriers, row state, tables.
+struct W4Plan {
+    int stages;      // ring slices
+    int panel;       // contraction elements of x held at once (a multiple of 256)
+    size_t smem;
+};
+
+// Accumulators D, operand A in TMEM at d + a few columns, B in shared memory.
+__device__ __forceinline__ void umma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-// Two codes of w as bf16 q - z: bits 0-3 and 16-19 of w onto 128.0, minus zc =
-// {128 + z, 128 + z}.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t zc)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
 {
-    const uint32_t q = (w & 0x000F000Fu) | 0x43004300u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(q), "r"(zc));
-    return r;
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+          "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+          "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+          "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+        : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+__device__ __forceinline__ void tmem_wait_st()
 {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
 }
 
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
@@ -94,406 +128,864 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
                  : "r"(addr));
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
-                                            int c2, uint32_t bar)
+// {lo, hi} as two e4m3 bytes (round to nearest even, saturating), and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
-// A warp's place in the slices of its CTA's units, dealt to the warps in turn.
-struct W4Cursor {
-    int unit = 0, slice;
-    __device__ __forceinline__ W4Cursor(int warp, int slices) : slice(warp) { wrap(slices); }
-    __device__ __forceinline__ void advance(int slices)
-    {
-        slice += kW4Warps;
-        wrap(slices);
-    }
-    __device__ __forceinline__ void wrap(int slices)
-    {
-        while (slice >= slices) {
-            slice -= slices;
-            ++unit;
-        }
-    }
-};
-
-struct W4Unit {
-    int e, row0, rows, col0;   // expert, first receive row, rows (1..NR), first output column
-};
-
-// pre[e]: units of the experts before e.
-template <class C>
-__device__ __forceinline__ W4Unit w4_unit(const W4Args& a, const int* pre, int E, int u)
+__device__ __forceinline__ void from_e4m3x2(uint32_t v, float* lo, float* hi)
 {
-    W4Unit w;
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= u) lo = mid;
-        else hi = mid;
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(*lo), "=f"(*hi)
+        : "r"(h));
+}
+
+// A barrier among some warps of the CTA that gives up on an abort: each warp arrives
+// once, then waits. (A hardware barrier could not be left.)
+struct W4Sync {
+    uint32_t bar;
+    volatile int* abort;
+    uint32_t phase = 0u;
+    __device__ __forceinline__ bool operator()(int lane)
+    {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+        const bool ok = warp_all(wait_or_abort(bar, phase, abort));
+        phase ^= 1u;
+        return ok;
     }
-    w.e = lo;
-    const int cnt = __ldcg(a.cnt + lo);
-    const int chunks = (cnt + C::NR - 1) / C::NR;
-    const int v = u - pre[lo];
-    const int chunk = v % chunks;
-    w.col0 = (v / chunks) * C::kOut;
-    w.row0 = __ldcg(a.expert_offset + lo) + chunk * C::NR;
-    w.rows = min(C::NR, cnt - chunk * C::NR);
+};
+
+// A tile: up to 8 blocks (gated: 4) of one expert's columns for one chunk of its rows.
+struct W4Tile {
+    int e, chunk, row0, rows, col0, blocks;
+};
+
+struct W4Tables {
+    const int* pre;   // [E + 1] blocks of the experts before each
+    const int* cnt;   // [E]
+    const int* off;   // [E]
+};
+
+template <class C>
+__device__ __forceinline__ W4Tile w4_tile(const W4Tables& t, int E, int nb, int most, int b, int end)
+{
+    W4Tile w;
+    w.e = expert_of(t.pre, E, b);
+    const int local = b - t.pre[w.e];
+    w.chunk = local / nb;
+    const int blk = local - w.chunk * nb;
+    w.col0 = blk * kW4Block;
+    w.row0 = t.off[w.e] + w.chunk * C::NR;
+    w.rows = min(C::NR, t.cnt[w.e] - w.chunk * C::NR);
+    w.blocks = min(min(most, nb - blk), end - b);
     return w;
 }
 
-// Scale groups of one slice for the two weight rows that a lane looks after (row
-// `lane` of each half of the unit).
-template <class C>
-struct W4Scales {
-    float s[2][C::GROUPS];
-    uint32_t z[2];             // zero points, one byte per group
+// A ring position: slot and the parity of its current phase.
+struct W4Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n)
+    {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
-template <class C>
-__device__ __forceinline__ void w4_load_scales(const W4Args& a, const W4Unit& w, int slice,
-                                               int lane, W4Scales<C>& v)
+__device__ __forceinline__ float w4_scale_at(const W4Args& a, int64_t i)
 {
-    const int groups = (int)(a.din / (32 * C::CPG));
+    // Through L1 (a lane's next groups share its sectors); complete once griddep_wait
+    // has returned.
+    if (a.scale_f32) {
+        float v;
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(static_cast<const float*>(a.scales) + i));
+        return v;
+    }
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(static_cast<const uint16_t*>(a.scales) + i));
+    return __uint_as_float((uint32_t)v << 16);
+}
+
+__device__ __forceinline__ float w4_zero_at(const W4Args& a, int64_t i)
+{
+    if (!a.zeros) return 8.0f;
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(a.zeros + i));
+    return (float)v;
+}
+
+// The power of two that takes a block whose largest magnitude has these bits to [128,
+// 256) (as far as fp32 reaches), and what undoes it.
+__device__ __forceinline__ uint32_t w4_scale_exponent(uint32_t max_bits)
+{
+    return min(261u - (max_bits >> 23), 253u);
+}
+
+__device__ __forceinline__ float w4_unscale(uint32_t max_bits)
+{
+    return __uint_as_float((254u - w4_scale_exponent(max_bits)) << 23);
+}
+
+__device__ __forceinline__ bool w4_odd(uint32_t bits) { return (bits & 0x7F800000u) == 0x7F800000u; }
+
+// Element j (0..7) of 8 bf16 as fp32 bits.
+__device__ __forceinline__ uint32_t w4_element(const int4& v, int j)
+{
+    const uint32_t w = (uint32_t)((j >> 1) == 0 ? v.x : (j >> 1) == 1 ? v.y : (j >> 1) == 2 ? v.z : v.w);
+    return (j & 1) ? w & 0xFFFF0000u : w << 16;
+}
+
+// The largest magnitude of 8 bf16 as bf16 bits, and the 8 with infinities and NaNs
+// as zeros.
+__device__ __forceinline__ uint32_t w4_largest(const int4& v)
+{
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2((uint32_t)v.x & kAbs, (uint32_t)v.y & kAbs),
+                                __vmaxu2((uint32_t)v.z & kAbs, (uint32_t)v.w & kAbs));
+    return max(m & 0xFFFFu, m >> 16);
+}
+
+__device__ __forceinline__ int4 w4_finite(const int4& v)
+{
+    int w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int o = w.col0 + (C::GLU ? 0 : 32 * half) + lane;
-        const bool in = o < a.dout;
-        const int64_t row = C::GLU ? ((int64_t)w.e * 2 + half) * a.dout + o
-                                   : (int64_t)w.e * a.dout + o;
-        v.z[half] = 0x08080808u;
-        if (a.zeros) v.z[half] = 0u;
-#pragma unroll
-        for (int j = 0; j < C::GROUPS; ++j) {
-            const int g = slice * C::GROUPS + j;
-            v.s[half][j] = 0.0f;
-            if (in && g < groups) {
-                const int64_t at = row * groups + g;
-                // Through L1: neighbouring slices read the same sectors. The scales
-                // are complete once griddep_wait has returned.
-                if (a.scale_f32) {
-                    asm volatile("ld.global.f32 %0, [%1];"
-                                 : "=f"(v.s[half][j])
-                                 : "l"(static_cast<const float*>(a.scales) + at));
-                } else {
-                    uint16_t b;
-                    asm volatile("ld.global.u16 %0, [%1];"
-                                 : "=h"(b)
-                                 : "l"(static_cast<const uint16_t*>(a.scales) + at));
-                    v.s[half][j] = __uint_as_float((uint32_t)b << 16);
-                }
-                if (a.zeros) {
-                    uint32_t b;
-                    asm volatile("ld.global.u8 %0, [%1];" : "=r"(b) : "l"(a.zeros + at));
-                    v.z[half] |= b << (8 * j);
-                }
-            }
+    for (int i = 0; i < 4; ++i) {
+        if (w4_odd((uint32_t)w[i])) w[i] &= 0x0000FFFF;
+        if (w4_odd((uint32_t)w[i] << 16)) w[i] &= (int)0xFFFF0000;
+    }
+    return make_int4(w[0], w[1], w[2], w[3]);
+}
+
+// Converts the tile's rows of x, contraction elements [k0, k0 + panel): two e4m3 terms
+// of each block of 128 elements, scaled, as B of the MMAs; what undoes the scale; and
+// the group sums. An infinity or a NaN counts as zero here and
+// marks its row (its terms are added to the row's results one by one). Warps 2 and
+// up; ct: thread among them.
+constexpr int kW4Batch = 4;   // 16-byte loads of a thread in flight
+//
+// A call, not inlined: two roles come here, seldom, and neither should hold its
+// registers or repeat its code.
+template <class C>
+__device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, int ct, int k0,
+                                        int panel, uint8_t* s_x, float* s_xsum, int* s_odd,
+                                        int* s_odd_next, W4Sync sync)
+{
+    const int lane = ct & 31;
+    const int per_row = panel / 8;   // octets; a warp's are of one row
+    float* s_undo = s_xsum + panel / C::GROUP * C::NR;
+    x += k0;
+    int4 v[kW4Batch];
+    int row = 0, octet = ct;             // the next one to process
+    int load_row = 0, load_octet = ct;   // the next one to load
+    auto step = [&](int& r, int& o) {
+        o += C::kConvThreads;
+        while (o >= per_row) {
+            o -= per_row;
+            ++r;
         }
+    };
+    auto load = [&] {
+#pragma unroll
+        for (int i = 0; i < kW4Batch; ++i) {
+            v[i] = make_int4(0, 0, 0, 0);
+            if (load_row < rows && k0 + 8 * load_octet < din)
+                v[i] = ld_cg_v4(x + (int64_t)load_row * din + 8 * load_octet);
+            step(load_row, load_octet);
+        }
+    };
+    while (octet >= per_row) {
+        octet -= per_row;
+        ++row;
+    }
+    load_row = row;
+    load_octet = octet;
+    load();                               // on their way while the previous tile is drained
+    if (!sync(lane)) return false;        // it is: x and its sums are free
+    if (ct < C::NR) s_odd_next[ct] = 0;   // nobody uses the other half of the row state now
+    // One octet's code, not unrolled: a warp runs it a few times, and what it would
+    // save in instructions it would lose fetching them.
+    for (int u = 0; row < rows; step(row, octet)) {
+        int4 w = u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3];
+        if (++u == kW4Batch) {
+            u = 0;
+            load();
+        }
+        uint32_t m = w4_largest(w);
+        if (m >= 0x7F80u) {   // rare: an infinity or a NaN
+            s_odd[row] = 1;
+            w = w4_finite(w);
+            m = w4_largest(w);
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m <<= 16;
+        const float scale = __uint_as_float(w4_scale_exponent(m) << 23);
+        float f[8], h[8], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float e = __uint_as_float(w4_element(w, j));
+            f[j] = e * scale;
+            sum += e;
+        }
+        // Bytes in the order of the unpacked codes: even elements, then odd ones.
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t p = to_e4m3x2(f[i], f[i + 2]), q = to_e4m3x2(f[i + 4], f[i + 6]);
+            from_e4m3x2(p, &h[0], &h[1]);
+            from_e4m3x2(q, &h[2], &h[3]);
+            hi[i] = p | (q << 16);
+            lo[i] = to_e4m3x2((f[i] - h[0]) * 32.0f, (f[i + 2] - h[1]) * 32.0f) |
+                    (to_e4m3x2((f[i + 4] - h[2]) * 32.0f, (f[i + 6] - h[3]) * 32.0f) << 16);
+        }
+        const int pos = (8 * octet) & 127;
+        uint8_t* dst = s_x + (uint32_t)((8 * octet) >> 7) * C::kPanelBytes + row * 128 +
+                       (((pos >> 4) ^ (row & 7)) << 4) + (pos & 8);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + C::NR * 128) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+        for (int d = 1; d < C::GROUP / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if ((lane & (C::GROUP / 8 - 1)) == 0) s_xsum[8 * octet / C::GROUP * C::NR + row] = sum;
+        if ((lane & 15) == 0) s_undo[(octet >> 4) * C::NR + row] = w4_unscale(m);
+    }
+    fence_proxy_async();   // the MMAs read B through the async proxy
+    __syncwarp();
+    return true;
+}
+
+// The terms of a row's infinities and NaNs in one output column.
+__device__ __forceinline__ float w4_odd_terms(const W4Args& a, int row, int64_t wrow, int groups)
+{
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)row * a.din;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < a.din; k += 8) {
+        const int4 v = ld_cg_v4(x + k);
+        if (w4_largest(v) < 0x7F80u) continue;
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = w4_element(v, j);
+            if (!w4_odd(b)) continue;
+            const int i = k + j;
+            const int code = (a.codes[(wrow * a.din + i) >> 1] >> (4 * (i & 1))) & 15;
+            const int64_t at = wrow * groups + i / a.group;
+            sum += ((float)code - w4_zero_at(a, at)) * w4_scale_at(a, at) * __uint_as_float(b);
+        }
+    }
+    return sum;
+}
+
+// Starts the scales (and zero points) of `rows` weight rows on their way to L2: the
+// drain reads them a few groups at a time, too little to wait for HBM each time.
+__device__ __forceinline__ void w4_prefetch_bytes(const void* p, int64_t bytes)
+{
+    const uintptr_t lo = (reinterpret_cast<uintptr_t>(p) + 15u) & ~(uintptr_t)15u;
+    const int64_t n = (bytes - (int64_t)(lo - reinterpret_cast<uintptr_t>(p))) & ~(int64_t)15;
+    if (n > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"((uint32_t)n)
+                     : "memory");
+}
+
+__device__ __forceinline__ void w4_prefetch_scales(const W4Args& a, int64_t row, int rows)
+{
+    const int64_t groups = a.din / a.group, at = row * groups, n = rows * groups;
+    w4_prefetch_bytes(static_cast<const uint8_t*>(a.scales) + at * (a.scale_f32 ? 4 : 2),
+                      n * (a.scale_f32 ? 4 : 2));
+    if (a.zeros) w4_prefetch_bytes(a.zeros + at, n);
+}
+
+// A drain lane's column of a tile and the scales of 8 groups of it.
+struct W4Lane {
+    int o;             // output column
+    int64_t wrow;      // weight row
+    bool live;         // a column of the tile
+    bool warp_live;    // its warp has one
+};
+
+__device__ __forceinline__ W4Lane w4_lane(const W4Args& a, const W4Tile& t, int64_t wrows, int r)
+{
+    W4Lane l;
+    const int rr = a.glu ? r & 63 : r;
+    l.o = t.col0 + rr;
+    l.live = rr < kW4Block * t.blocks && l.o < a.dout;
+    l.warp_live = (rr & ~31) < kW4Block * t.blocks;
+    l.wrow = (int64_t)t.e * wrows + (a.glu && r >= 64 ? a.dout : 0) + l.o;
+    return l;
+}
+
+// The scales and zero points of 8 groups as loaded: nothing is done with them until
+// they are used, so that the loads' latency lies in between.
+// wide: the rows' groups are a multiple of 8 and the arrays aligned to 16 (zeros 8)
+// bytes, so that 8 groups are one or two loads. One at a time they kept the loads of a
+// lane's own line (32 lines for a warp) busy longer than HBM needed for the codes: 49
+// against 30 us without them (13 rows, 8 x 2048 x 4096 codes, groups of 32, fp32).
+struct W4Scales {
+    uint32_t s[8];   // fp32 bits; bf16 in pairs (wide), or one in each
+    uint32_t z[2];   // bytes
+};
+
+__device__ __forceinline__ void w4_load_scales(const W4Args& a, const W4Lane& l, int groups,
+                                               bool wide, int first, W4Scales& v)
+{
+    const int64_t at = l.wrow * groups + first;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v.s[j] = 0u;   // a column that is not there: scale 0
+    v.z[0] = v.z[1] = 0x08080808u;
+    if (!l.live || first >= groups) return;
+    if (wide) {
+        if (a.scale_f32) {
+            const float* p = static_cast<const float*>(a.scales) + at;
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.s[0]), "=r"(v.s[1]), "=r"(v.s[2]), "=r"(v.s[3]) : "l"(p));
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.s[4]), "=r"(v.s[5]), "=r"(v.s[6]), "=r"(v.s[7]) : "l"(p + 4));
+        } else {
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.s[0]), "=r"(v.s[1]), "=r"(v.s[2]), "=r"(v.s[3])
+                         : "l"(static_cast<const uint16_t*>(a.scales) + at));
+        }
+        if (a.zeros)
+            asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.z[0]), "=r"(v.z[1])
+                         : "l"(a.zeros + at));
+        return;
+    }
+    uint32_t z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const bool in = first + j < groups;
+        z[j] = 0u;
+        if (in && a.scale_f32)
+            asm volatile("ld.global.u32 %0, [%1];" : "=r"(v.s[j])
+                         : "l"(static_cast<const float*>(a.scales) + at + j));
+        if (in && !a.scale_f32) {
+            uint16_t b;
+            asm volatile("ld.global.u16 %0, [%1];" : "=h"(b)
+                         : "l"(static_cast<const uint16_t*>(a.scales) + at + j));
+            v.s[j] = b;
+        }
+        if (in && a.zeros) asm volatile("ld.global.u8 %0, [%1];" : "=r"(z[j]) : "l"(a.zeros + at + j));
+    }
+    if (a.zeros) {
+        v.z[0] = z[0] | (z[1] << 8) | (z[2] << 16) | (z[3] << 24);
+        v.z[1] = z[4] | (z[5] << 8) | (z[6] << 16) | (z[7] << 24);
+    }
+}
+
+// Into the lane's places [8][128]: the scale times the codes' 2^9, and minus the scale
+// times the zero point. Only the lane itself reads them (by a group index that is not
+// a constant, so not from registers).
+__device__ __forceinline__ void w4_keep_scales(const W4Scales& v, bool f32, bool wide, float2* mine)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t pair = v.s[j >> 1];
+        const uint32_t bits = f32 ? v.s[j] : !wide ? v.s[j] << 16 : (j & 1) ? pair & 0xFFFF0000u : pair << 16;
+        const float scale = __uint_as_float(bits);
+        mine[j * 128] = make_float2(scale * 512.0f,
+                                    -scale * (float)((v.z[j >> 2] >> (8 * (j & 3))) & 0xFFu));
     }
 }
 
 template <class C>
-__global__ void __launch_bounds__(kW4Threads, C::kPerSm)
+__global__ void __launch_bounds__(C::kThreads, 1)
 expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
-                 const __grid_constant__ CUtensorMap tm_x,
-                 const __grid_constant__ CUtensorMap tm_x1, W4Args a)
+                 const __grid_constant__ CUtensorMap tm_half, const __grid_constant__ W4Args a,
+                 const __grid_constant__ W4Plan plan)
 {
-    constexpr int NT = C::NT, SLOTS = C::SLOTS;
+    constexpr int NR = C::NR, N = C::N;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
-    uint8_t* smem = smem_raw + ((512u - (raw & 511u)) & 511u);
-    float* s_red = reinterpret_cast<float*>(smem + C::kRing);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kRed);
-    int* s_sum = reinterpret_cast<int*>(bars + kW4Warps * SLOTS);   // [8] warp totals
-    volatile int* s_abort = s_sum + kW4Warps;
-    int* s_pre = s_sum + kW4Warps + 2;                                // [E + 1]
+    // Barriers and small state first (their addresses are then one register and
+    // constants), the ring, x with its sums, the tables.
+    uint8_t* state = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t code_full0 = smem_u32(state);
+    const uint32_t code_empty0 = code_full0 + 8u * kW4MaxStages;
+    const uint32_t a_full0 = code_empty0 + 8u * kW4MaxStages;
+    const uint32_t a_empty0 = a_full0 + 8u * kW4ASlots;
+    const uint32_t d_full0 = a_empty0 + 8u * kW4ASlots;
+    const uint32_t d_empty0 = d_full0 + 8u * kW4MaxDSlots;
+    const uint32_t x_full = d_empty0 + 8u * kW4MaxDSlots;
+    const uint32_t drain = x_full + 8u;
+    const uint32_t conv = drain + 8u;      // warps 2 and up
+    const uint32_t swapped = conv + 8u;    // the drain's
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(state + 8 * kW4Bars);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    int* s_warp = reinterpret_cast<int*>(s_tmem + 2);   // [16] scan
+    // [2][NR], this tile's rows and the next ones: the row has an infinity or a NaN.
+    int* s_odd0 = s_warp + 16;
+    static_assert(8 * kW4Bars + 8 + 4 * 16 + 8 * NR <= (int)kW4StateBytes, "state");
+    uint8_t* smem = state + kW4StateBytes;
+    const int stages = plan.stages, panel = plan.panel;
+    uint8_t* s_x = smem + (size_t)stages * kW4StageBytes;                 // B, panel / 128 parts
+    float* s_xsum = reinterpret_cast<float*>(s_x + (size_t)panel * N);    // [panel / GROUP][NR]
+    float* s_undo = s_xsum + panel / C::GROUP * NR;                       // [panel / 128][NR]
+    float* s_swap = s_undo + panel / 128 * NR;
+    float2* s_scale = reinterpret_cast<float2*>(s_swap + C::kSwap / 4);   // [8][128]
+    int* s_pre = reinterpret_cast<int*>(s_scale + 8 * 128);
+    const int E = a.E;
+    int* s_cnt = s_pre + E + 1;
+    int* s_off = s_cnt + E;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, q = lane & 3;
-    const int E = a.E;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * SLOTS) * C::kSlotBytes;
-    const uint32_t bar0 = smem_u32(bars) + 8u * (uint32_t)(warp * SLOTS);
-    const int nblk = (int)((a.dout + C::kOut - 1) / C::kOut);
+    const int nb = (int)((a.dout + kW4Block - 1) / kW4Block);
+    const int most = a.glu ? 4 : 8;
     const int slices = (int)((a.din + kW4Slice - 1) / kW4Slice);
+    const int per_panel = panel / kW4Slice;
+    const int64_t wrows = a.glu ? 2 * a.dout : a.dout;   // weight rows of an expert
 
-    if (lane == 0)
-        for (int s = 0; s < SLOTS; ++s) mbar_init(bar0 + 8u * s, 1u);
-    if (threadIdx.x == 0) *s_abort = 0;
-    fence_mbar_init();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kW4MaxStages; ++s) {
+            mbar_init(code_full0 + 8u * s, 1u);
+            mbar_init(code_empty0 + 8u * s, 4u);
+        }
+        for (int s = 0; s < kW4ASlots; ++s) {
+            mbar_init(a_full0 + 8u * s, 4u);
+            mbar_init(a_empty0 + 8u * s, 1u);
+        }
+        for (int s = 0; s < kW4MaxDSlots; ++s) {
+            mbar_init(d_full0 + 8u * s, 1u);
+            mbar_init(d_empty0 + 8u * s, 4u);
+        }
+        mbar_init(x_full, C::kConvThreads / 32);
+        mbar_init(drain, 1u);
+        mbar_init(conv, C::kConvThreads / 32);
+        mbar_init(swapped, 4u);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    if ((int)threadIdx.x < 2 * NR) s_odd0[threadIdx.x] = 0;
+    if (warp == 1) {
+        tmem_alloc<false>(smem_u32(s_tmem), 512u);
+        tmem_relinquish<false>();
+    }
     griddep_wait();   // counts, offsets and the rows come from earlier kernels
 
-    // Units before each expert: thread t takes experts [t c, t c + c).
+    // Blocks before each expert: thread t takes experts [t c, t c + c).
     {
-        const int c = (E + kW4Threads - 1) / kW4Threads, e0 = (int)threadIdx.x * c;
+        const int c = (E + C::kThreads - 1) / C::kThreads, e0 = (int)threadIdx.x * c;
         int own = 0;
-        for (int e = e0; e < min(E, e0 + c); ++e)
-            own += (__ldcg(a.cnt + e) + C::NR - 1) / C::NR * nblk;
+        for (int e = e0; e < min(E, e0 + c); ++e) {
+            s_cnt[e] = __ldcg(a.cnt + e);
+            s_off[e] = __ldcg(a.expert_offset + e);
+            own += (s_cnt[e] + NR - 1) / NR * nb;
+        }
         int incl = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += n;
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
         }
-        if (lane == 31) s_sum[warp] = incl;
+        if (lane == 31) s_warp[warp] = incl;
         __syncthreads();
         int at = incl - own;
-        for (int w = 0; w < warp; ++w) at += s_sum[w];
+        for (int w = 0; w < warp; ++w) at += s_warp[w];
         for (int e = e0; e < min(E, e0 + c); ++e) {
             s_pre[e] = at;
-            at += (__ldcg(a.cnt + e) + C::NR - 1) / C::NR * nblk;
+            at += (s_cnt[e] + NR - 1) / NR * nb;
         }
-        if (threadIdx.x == kW4Threads - 1) s_pre[E] = at;
-        __syncthreads();
+        if (threadIdx.x == C::kThreads - 1) s_pre[E] = at;
     }
-    const int total = s_pre[E];
-    const int mine = total > (int)blockIdx.x
-                         ? (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const W4Tables tab = {s_pre, s_cnt, s_off};
+    const int64_t total = s_pre[E];
+    const int first = (int)(total * blockIdx.x / gridDim.x);
+    const int last = (int)(total * (blockIdx.x + 1) / gridDim.x);
 
-    // The next slice to copy and its unit.
-    W4Cursor fill(warp, slices);
-    int fill_unit = -1, issued = 0;
-    W4Unit fu = {};
-    auto issue = [&](int slot) {
-        if (fill.unit >= mine) return;
-        if (fill.unit != fill_unit) {
-            fu = w4_unit<C>(a, s_pre, E, (int)blockIdx.x + fill.unit * (int)gridDim.x);
-            fill_unit = fill.unit;
-        }
-        if (lane == 0) {
-            const uint32_t dst = ring + (uint32_t)slot * C::kSlotBytes;
-            const uint32_t bar = bar0 + 8u * (uint32_t)slot;
-            const bool one = fu.rows == 1;
-            mbar_expect_tx(bar, kW4CodeBytes + (one ? kW4Slice * 2u : C::kXBytes));
-            const int row = (C::GLU ? 2 : 1) * fu.e * (int)a.dout + fu.col0;
-            tma_load_2d(dst, &tm_w, fill.slice * (kW4Slice / 2), row, bar);
-            tma_load_2d(dst + kW4CodeBytes / 2, &tm_w, fill.slice * (kW4Slice / 2),
-                        row + (C::GLU ? (int)a.dout : 32), bar);
-            tma_load_3d(dst + kW4CodeBytes, one ? &tm_x1 : &tm_x, 0, fu.row0,
-                        fill.slice * kW4Chunks, bar);
-        }
-        ++issued;
-        fill.advance(slices);
-    };
-    for (int s = 0; s < SLOTS; ++s) issue(s);
-
-    W4Cursor at(warp, slices);   // this warp's next slice
-    int n_done = 0;              // slices it has taken
-    W4Cursor ahead = at;         // the slice whose scales come next
-    W4Scales<C> next;
-    int next_unit = -1;
-    W4Unit nu = {};
-    auto prefetch = [&] {
-        if (ahead.unit >= mine) return;
-        if (ahead.unit != next_unit) {
-            nu = w4_unit<C>(a, s_pre, E, (int)blockIdx.x + ahead.unit * (int)gridDim.x);
-            next_unit = ahead.unit;
-        }
-        w4_load_scales<C>(a, nu, ahead.slice, lane, next);
-        ahead.advance(slices);
-    };
-    prefetch();
-
-    for (int iu = 0; iu < mine; ++iu) {
-        const W4Unit w = w4_unit<C>(a, s_pre, E, (int)blockIdx.x + iu * (int)gridDim.x);
-        const uint32_t x_rows = w.rows == 1 ? 1u : (uint32_t)C::NR;   // rows of the copied box
-        float total_acc[4][NT][4] = {};
+    if (warp == 0) {
+        // ---- codes: TMA into the ring (the warp waits together, one lane issues) ----
+        W4Ring c;
+        int issued = 0;
         bool ok = true;
-        for (; at.unit == iu; at.advance(slices), ++n_done) {
-            const int slot = n_done % SLOTS;
-            const W4Scales<C> cur = next;
-            prefetch();
-            ok = warp_all(wait_or_abort(bar0 + 8u * slot, (uint32_t)((n_done / SLOTS) & 1), s_abort));
-            if (!ok) break;
-            const uint32_t codes = ring + (uint32_t)slot * C::kSlotBytes;
-            const uint32_t xs = codes + kW4CodeBytes;
-#pragma unroll
-            for (int j = 0; j < C::GROUPS; ++j) {
-                float acc[4][NT][4] = {};
-                uint32_t zc[4][2];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t z = __shfl_sync(0xffffffffu, cur.z[t >> 1],
-                                                       16 * (t & 1) + 8 * i + g);
-                        zc[t][i] = (((z >> (8 * j)) & 0xFFu) * 0x00010001u) | 0x43004300u;
-                    }
-#pragma unroll
-                for (int cc = 0; cc < C::CPG; ++cc) {
-                    const int c = j * C::CPG + cc;
-                    uint32_t b[NT][4];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t v[4];
-                        const uint32_t r = min((uint32_t)(8 * n + g), x_rows - 1u);
-                        lds128(xs + ((uint32_t)c * x_rows + r) * 64u + (uint32_t)q * 16u, v);
-                        b[n][0] = __byte_perm(v[0], v[2], 0x5410);   // elements 0, 4
-                        b[n][1] = __byte_perm(v[0], v[2], 0x7632);   // 1, 5
-                        b[n][2] = __byte_perm(v[1], v[3], 0x5410);   // 2, 6
-                        b[n][3] = __byte_perm(v[1], v[3], 0x7632);   // 3, 7
-                    }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        // 64-byte swizzle: 16-byte unit c of line row lands at c ^ (row / 2 % 4).
-                        const uint32_t r0 = (uint32_t)(16 * t + g);
-                        const uint32_t sw = ((uint32_t)c ^ ((r0 >> 1) & 3u)) * 16u + (uint32_t)q * 4u;
-                        const uint32_t w0 = lds32(codes + r0 * 64u + sw);
-                        const uint32_t w1 = lds32(codes + (r0 + 8u) * 64u + sw);
-                        uint32_t a0[4] = {w4_pair(w0, zc[t][0]), w4_pair(w1, zc[t][1]),
-                                          w4_pair(w0 >> 4, zc[t][0]), w4_pair(w1 >> 4, zc[t][1])};
-                        uint32_t a1[4] = {w4_pair(w0 >> 8, zc[t][0]), w4_pair(w1 >> 8, zc[t][1]),
-                                          w4_pair(w0 >> 12, zc[t][0]), w4_pair(w1 >> 12, zc[t][1])};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_16816(acc[t][n], a0, b[n][0], b[n][1]);
-                            mma_16816(acc[t][n], a1, b[n][2], b[n][3]);
+        for (int b = first; b < last && ok;) {
+            const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
+            b += t.blocks;
+            const int row = (int)(t.e * wrows) + t.col0;
+            const int row2 = a.glu ? row + (int)a.dout : row + 64;   // of the tile's second half
+            const bool whole = t.blocks == most;
+            if (elect_one())
+                for (int half = 0; half < (a.glu ? 2 : 1); ++half)
+                    w4_prefetch_scales(a, (int64_t)row + half * a.dout,
+                                       min(t.blocks * kW4Block, (int)a.dout - t.col0));
+            for (int k = 0; k < slices; ++k) {
+                ok = warp_all(wait_or_abort(code_empty0 + 8u * c.slot, c.phase ^ 1u, s_abort));
+                if (!ok) break;
+                const uint32_t bar = code_full0 + 8u * c.slot;
+                const uint32_t dst = smem_u32(smem) + (uint32_t)c.slot * kW4StageBytes;
+                const int kb = k * (kW4Slice / 2);
+                if (elect_one()) {
+                    if (whole) {
+                        mbar_expect_tx(bar, kW4StageBytes);
+                        tma_load_2d(dst, &tm_half, kb, row, bar);
+                        tma_load_2d(dst + 4 * kW4BoxBytes, &tm_half, kb, row2, bar);
+                    } else {
+                        mbar_expect_tx(bar, (uint32_t)(a.glu ? 2 * t.blocks : t.blocks) * kW4BoxBytes);
+                        for (int j = 0; j < t.blocks; ++j) {
+                            tma_load_2d(dst + j * kW4BoxBytes, &tm_w, kb, row + 16 * j, bar);
+                            if (a.glu)
+                                tma_load_2d(dst + (4 + j) * kW4BoxBytes, &tm_w, kb, row2 + 16 * j, bar);
                         }
                     }
                 }
+                __syncwarp();
+                ++issued;
+                c.next(stages);
+            }
+        }
+        // The copies land before shared memory goes away (also after an abort).
+        const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
+        for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+            mbar_wait_until(code_full0 + 8u * (uint32_t)(i % stages), (uint32_t)(i / stages) & 1u,
+                            deadline);
+    } else if (warp == 1) {
+        // ---- MMA issuer (the warp waits together, one lane issues) --------------
+        W4Ring as, ds;
+        uint32_t x_phase = 0u;
+        int e_have = -1, chunk_have = -1;
+        bool issued = false, ok = true;
+        const uint64_t x_desc = smem_desc_k128(smem_u32(s_x));
+        for (int b = first; b < last && ok;) {
+            const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
+            b += t.blocks;
+            const bool new_rows = t.e != e_have || t.chunk != chunk_have;
+            e_have = t.e;
+            chunk_have = t.chunk;
+            int in_panel = 0;
+            for (int k = 0; k < slices; ++k, ++in_panel) {
+                if (in_panel == per_panel) in_panel = 0;
+                if (in_panel == 0 && (new_rows || per_panel < slices)) {
+                    ok = warp_all(wait_or_abort(x_full, x_phase, s_abort));
+                    x_phase ^= 1u;
+                    if (!ok) break;
+                }
+                ok = warp_all(wait_or_abort(a_full0 + 8u * as.slot, as.phase, s_abort));
+                if (!ok) break;
+                const uint64_t bx = x_desc + (uint64_t)((uint32_t)in_panel * (2u * C::kPanelBytes >> 4));
+                const uint32_t at = tmem + kW4ABase + (uint32_t)as.slot * 64u;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const float s0 = __shfl_sync(0xffffffffu, cur.s[t >> 1][j], 16 * (t & 1) + g);
-                    const float s1 = __shfl_sync(0xffffffffu, cur.s[t >> 1][j], 16 * (t & 1) + 8 + g);
+                for (int g0 = 0; g0 < C::GPS; g0 += C::GB) {
+                    if (ok) ok = warp_all(wait_or_abort(d_empty0 + 8u * ds.slot, ds.phase ^ 1u, s_abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(ds.slot * C::GB * N);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        total_acc[t][n][0] = fmaf(s0, acc[t][n][0], total_acc[t][n][0]);
-                        total_acc[t][n][1] = fmaf(s0, acc[t][n][1], total_acc[t][n][1]);
-                        total_acc[t][n][2] = fmaf(s1, acc[t][n][2], total_acc[t][n][2]);
-                        total_acc[t][n][3] = fmaf(s1, acc[t][n][3], total_acc[t][n][3]);
+                        for (int i = 0; i < C::GB * C::STEPS; ++i) {
+                            const int step = g0 * C::STEPS + i;   // of 32 elements in the slice
+                            umma_e4m3_ts(d + (uint32_t)(i / C::STEPS * N), at + (uint32_t)step * 8u,
+                                         bx + (uint64_t)(((step >> 2) * C::kPanelBytes + (step & 3) * 32) >> 4),
+                                         C::kIdesc, i % C::STEPS != 0 ? 1u : 0u);
+                        }
+                        umma_commit<false>(d_full0 + 8u * ds.slot);
+                        if (g0 + C::GB == C::GPS) umma_commit<false>(a_empty0 + 8u * as.slot);
+                    }
+                    __syncwarp();
+                    issued = true;
+                    ds.next(C::DSLOTS);
+                }
+                if (!ok) break;
+                as.next(kW4ASlots);
+            }
+        }
+        if (issued) {   // every MMA has finished before TMEM is freed
+            if (elect_one()) umma_commit_local<false>(drain);
+            __syncwarp();
+            mbar_wait(drain, 0u);
+        }
+    } else if (warp >= 2) {
+        const int ct = (int)threadIdx.x - 64;
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;                // output column of the tile / TMEM lane
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const bool drains = warp >= 2 + 4 * C::kSets;
+        const int groups = (int)(a.din / C::GROUP);
+        const bool wide = groups % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0u &&
+                          (reinterpret_cast<uintptr_t>(a.zeros) & 7u) == 0u;
+        float2* mine = s_scale + r;
+        W4Sync conv_sync = {conv, s_abort};
+        int e_have = -1, chunk_have = -1, half = 1;   // half: of the row state
+        bool ok = true, new_rows = false;
+        auto begin = [&](const W4Tile& t) {
+            new_rows = t.e != e_have || t.chunk != chunk_have;
+            if (new_rows) half ^= 1;
+            e_have = t.e;
+            chunk_have = t.chunk;
+        };
+        // Before slice k0 of tile t: converts the panel of its rows that begins there,
+        // unless it is there. Every warp gets here for the same panels.
+        auto need_x = [&](const W4Tile& t, int k0) {
+            if (!new_rows && per_panel >= slices) return true;
+            const bool done =
+                w4_convert<C>(static_cast<const uint16_t*>(a.x) + (int64_t)t.row0 * a.din, t.rows,
+                              (int)a.din, ct, k0 * kW4Slice, panel, s_x, s_xsum, s_odd0 + half * NR,
+                              s_odd0 + (half ^ 1) * NR, conv_sync);
+            conv_sync.phase ^= 1u;
+            if (done && lane == 0) mbar_arrive(x_full);
+            return done;
+        };
+        if (!drains) {
+            // ---- codes to TMEM ----------------------------------------------------
+            const int set = (warp - 2) >> 2;
+            W4Ring c, as;
+            int g = 0;   // slices seen
+#pragma unroll 1
+            for (int b = first; b < last && ok;) {
+                const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
+                b += t.blocks;
+                const bool warp_live = w4_lane(a, t, wrows, r).warp_live;
+                begin(t);
+#pragma unroll 1
+                for (int k0 = 0; k0 < slices && ok; k0 += per_panel) {
+                    ok = need_x(t, k0);
+                    if (!ok) break;
+                    const int k1 = min(slices, k0 + per_panel);
+#pragma unroll 1
+                    for (int k = k0; k < k1; ++k, ++g, c.next(stages), as.next(kW4ASlots)) {
+                        if (C::kSets > 1 && (g & 1) != set) continue;
+                        ok = warp_all(wait_or_abort(code_full0 + 8u * c.slot, c.phase, s_abort));
+                        if (!ok) break;
+                        uint32_t w[8][4];
+                        if (warp_live) {
+                            const uint32_t base = smem_u32(smem) + (uint32_t)c.slot * kW4StageBytes +
+                                                  (uint32_t)r * 128u;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                lds128(base + (uint32_t)((i ^ (r & 7)) << 4), w[i]);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(code_empty0 + 8u * c.slot);
+                        ok = warp_all(wait_or_abort(a_empty0 + 8u * as.slot, as.phase ^ 1u, s_abort));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (warp_live) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t v[32];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const uint32_t q = w[4 * h + (i >> 2)][i & 3];
+                                    v[2 * i] = q & 0x0F0F0F0Fu;
+                                    v[2 * i + 1] = (q >> 4) & 0x0F0F0F0Fu;
+                                }
+                                tmem_st32(t_lane + kW4ABase + (uint32_t)(as.slot * 64 + h * 32), v);
+                            }
+                            tmem_wait_st();
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(a_full0 + 8u * as.slot);
                     }
                 }
             }
-            __syncwarp();   // every lane has read the slot
-            issue(slot);
-        }
-        // The unit's sums: warps 4-7 leave theirs in shared memory, warps 0-3 add
-        // their own to them, and the four parts are added in order.
-        float* red = s_red + (warp % (kW4Warps / 2)) * (kW4Cols * C::kRedStride);
-        auto leave = [&](bool add) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float* v = red + (16 * t + g + 8 * (i >> 1)) * C::kRedStride + 8 * n +
-                                   2 * q + (i & 1);
-                        *v = add ? *v + total_acc[t][n][i] : total_acc[t][n][i];
-                    }
-        };
-        if (warp >= kW4Warps / 2) leave(false);
-        __syncthreads();
-        if (warp < kW4Warps / 2) leave(true);
-        __syncthreads();
-        if (*s_abort) break;   // the same for every warp: a wait gave up before the barrier
-        uint16_t* y = static_cast<uint16_t*>(a.y);
-        for (int i = threadIdx.x; i < C::kOut * w.rows; i += kW4Threads) {
-            const int o = i % C::kOut, n = i / C::kOut;
-            auto sum = [&](int r) {
-                float v = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kW4Warps / 2; ++k)
-                    v += s_red[(k * kW4Cols + r) * C::kRedStride + n];
-                return v;
+        } else {
+            // ---- drain ---------------------------------------------------------------
+            W4Sync swap_sync = {swapped, s_abort};
+            W4Ring ds;
+            W4Scales next;
+            auto load_scales = [&](const W4Tile& t, int k) {
+                w4_load_scales(a, w4_lane(a, t, wrows, r), groups, wide, k * C::GPS, next);
             };
-            float v = sum(o);
-            if (C::GLU) v = act_value(v, a.act) * sum(o + 32);
-            if (w.col0 + o < a.dout)
-                y[(int64_t)(w.row0 + n) * a.dout + w.col0 + o] =
-                    (uint16_t)(pack_bf16x2_rn(v, 0.0f) & 0xFFFFu);
+            if (first < last) load_scales(w4_tile<C>(tab, E, nb, most, first, last), 0);
+#pragma unroll 1
+            for (int b = first; b < last && ok;) {
+                const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
+                b += t.blocks;
+                const bool warp_live = w4_lane(a, t, wrows, r).warp_live;
+                begin(t);
+                float acc[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) acc[n] = 0.0f;
+#pragma unroll 1
+                for (int k0 = 0; k0 < slices && ok; k0 += per_panel) {
+                    ok = need_x(t, k0);
+                    if (!ok) break;
+                    const int k1 = min(slices, k0 + per_panel);
+#pragma unroll 1
+                    for (int k = k0; k < k1 && ok; ++k) {
+                        if ((k & (C::SPB - 1)) == 0) {
+                            // The next 8 groups' scales, loaded while the 8 before were used;
+                            // over the tile's end too.
+                            w4_keep_scales(next, a.scale_f32, wide, mine);
+                            if (k + C::SPB < slices) load_scales(t, k + C::SPB);
+                            else if (b < last) load_scales(w4_tile<C>(tab, E, nb, most, b, last), 0);
+                        }
+                        const float2* sc = mine + (k & (C::SPB - 1)) * C::GPS * 128;
+                        const float* sums = s_xsum + (k - k0) * (C::GPS * NR);
+                        const float* undo = s_undo + (k - k0) * (2 * NR);
+#pragma unroll 1
+                        for (int g0 = 0; g0 < C::GPS; g0 += C::GB) {
+                            ok = warp_all(wait_or_abort(d_full0 + 8u * ds.slot, ds.phase, s_abort));
+                            if (!ok) break;
+                            tc_fence_after();
+                            // 32 accumulator columns at a time: 16 pairs of terms, of one
+                            // group (NR >= 16; half of one for NR = 32) or of two.
+                            constexpr int kParts = C::GB * N / 32;
+                            constexpr int kRun = NR < 16 ? NR : 16;   // rows of a part's group
+                            const uint32_t d = t_lane + (uint32_t)(ds.slot * C::GB * N);
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part) {
+                                uint32_t q[32];
+                                if (warp_live) {
+                                    if (N <= 32) {
+                                        tmem_ld32(d + 32u * part, q);
+                                    } else {
+                                        tmem_ld16(d + 64u * (part >> 1) + 16u * (part & 1), q);
+                                        tmem_ld16(d + 64u * (part >> 1) + NR + 16u * (part & 1), q + 16);
+                                    }
+                                    tmem_wait_ld();
+                                }
+                                if (part == kParts - 1) {   // the slot is free as soon as it is read
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive(d_empty0 + 8u * ds.slot);
+                                }
+                                if (!warp_live) continue;
+#pragma unroll
+                                for (int u = 0; u < 16 / kRun; ++u) {
+                                    const int gi = g0 + (N <= 32 ? part * (32 / N) + u : part >> 1);
+                                    const int n0 = N <= 32 ? 0 : 16 * (part & 1);
+                                    const float2 s = sc[gi * 128];
+                                    const float4* xs = reinterpret_cast<const float4*>(sums + gi * NR + n0);
+                                    const float4* un =
+                                        reinterpret_cast<const float4*>(undo + gi * C::GROUP / 128 * NR + n0);
+#pragma unroll
+                                    for (int n4 = 0; n4 < kRun / 4; ++n4) {
+                                        const float4 x4 = xs[n4], u4 = un[n4];
+                                        const float xv[4] = {x4.x, x4.y, x4.z, x4.w};
+                                        const float uv[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const int hi = (N <= 32 ? u * N : 0) + 4 * n4 + i;
+                                            const float v = fmaf(__uint_as_float(q[hi + kRun]), 0.03125f,
+                                                                 __uint_as_float(q[hi]));
+                                            float& sum = acc[n0 + 4 * n4 + i];
+                                            sum = fmaf(s.x * uv[i], v, fmaf(s.y, xv[i], sum));
+                                        }
+                                    }
+                                }
+                            }
+                            ds.next(C::DSLOTS);
+                        }
+                    }
+                }
+                if (!ok) break;
+                const W4Lane l = w4_lane(a, t, wrows, r);
+                for (int n = 0; n < t.rows; ++n)
+                    if (s_odd0[half * NR + n] && l.live) {
+                        const float terms = w4_odd_terms(a, t.row0 + n, l.wrow, groups);
+#pragma unroll
+                        for (int m = 0; m < NR; ++m)
+                            if (m == n) acc[m] += terms;
+                    }
+                if (a.glu) {
+                    float* swap = s_swap + (r & 63) * (NR + 1);
+                    if (r >= 64)
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) swap[n] = acc[n];
+                    ok = swap_sync(lane);
+                    if (!ok) break;
+                    if (r < 64)
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            if (n < t.rows) acc[n] = act_value(acc[n], a.act) * swap[n];
+                    ok = swap_sync(lane);   // the swap area is free again
+                    if (!ok) break;
+                }
+                if (l.live && (!a.glu || r < 64)) {
+                    uint16_t* y = static_cast<uint16_t*>(a.y) + (int64_t)t.row0 * a.dout + l.o;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        if (n < t.rows) y[n * a.dout] = (uint16_t)(pack_bf16x2_rn(acc[n], 0.0f) & 0xFFFFu);
+                }
+            }
         }
-        __syncthreads();
     }
 
-    // After an abort, the copies in flight land before shared memory goes away.
-    if (*s_abort) {
-        const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
-        for (int s = 0; s < SLOTS; ++s) {
-            const int k = issued - 1 - ((issued - 1 - s) % SLOTS + SLOTS) % SLOTS;   // last into s
-            if (k >= 0) mbar_wait_until(bar0 + 8u * s, (uint32_t)((k / SLOTS) & 1), deadline);
-        }
-        if (threadIdx.x == 0) atomicOr(a.err, kErrTimeout);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *s_abort) atomicOr(a.err, kErrTimeout);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<false>(tmem, 512u);
     }
     griddep_launch_dependents();
 }
 
-// 2-D map of the codes: [rows][din / 2] bytes, boxes of 32 rows x 64 bytes.
-inline bool make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows)
+// 2-D map of the codes: [rows][din / 2] bytes, boxes of box_rows rows x 128 bytes.
+inline bool make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+                          int box_rows)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {row_bytes, rows};
     const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {kW4Slice / 2, 32};
+    const cuuint32_t box[2] = {kW4Slice / 2, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map of the rows: 32 elements, rows, 32-element chunks; boxes of 4 chunks of box_rows rows.
-inline bool make_chunk_map(CUtensorMap* m, const void* base, uint64_t din, uint64_t rows,
-                           uint32_t box_rows)
+// Ring slices and x panel that fit: x whole if it leaves kW4MinStages, else in parts.
+template <class C>
+W4Plan w4_plan(int64_t din, int E)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {32, rows, din / 32};
-    const cuuint64_t strides[2] = {din * 2, 64};
-    const cuuint32_t box[3] = {32, box_rows, kW4Chunks};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const size_t fixed = 1024 + kW4StateBytes + C::kSwap + 8 * 128 * 8 + 4 * (3 * (size_t)E + 1);
+    const size_t per_slice = (size_t)kW4Slice * C::N + (size_t)(C::GPS + 2) * C::NR * 4;   // of x
+    const int64_t slices = (din + kW4Slice - 1) / kW4Slice;
+    const int64_t fit =
+        (int64_t)((kSmemLimit - fixed - (size_t)kW4MinStages * kW4StageBytes) / per_slice);
+    const int64_t held = slices < fit ? slices : fit;
+    W4Plan p;
+    p.panel = (int)(held * kW4Slice);
+    const size_t left = kSmemLimit - fixed - (size_t)held * per_slice;
+    p.stages = (int)(left / kW4StageBytes);
+    if (p.stages > kW4MaxStages) p.stages = kW4MaxStages;
+    p.smem = fixed + (size_t)held * per_slice + (size_t)p.stages * kW4StageBytes;
+    return p;
 }
 
 template <class C>
-cudaError_t launch_w4_cfg(const W4Args& a, const void* x, int64_t rows, const void* codes,
-                          int num_sms, const LaunchOpts& o)
+cudaError_t launch_w4_cfg(const W4Args& a, const void* codes, int num_sms, const LaunchOpts& o)
 {
-    const size_t smem = C::kSmemFixed + 4 * (size_t)(a.E + 2);
+    const W4Plan plan = w4_plan<C>(a.din, a.E);
     cudaError_t e = cudaFuncSetAttribute(expert_w4_kernel<C>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
-    CUtensorMap tw, tx, tx1;
-    const uint64_t wrows = (uint64_t)a.E * (uint64_t)a.dout * (C::GLU ? 2 : 1);
-    if (!make_code_map(&tw, codes, (uint64_t)a.din / 2, wrows) ||
-        !make_chunk_map(&tx, x, (uint64_t)a.din, (uint64_t)rows, C::NR) ||
-        !make_chunk_map(&tx1, x, (uint64_t)a.din, (uint64_t)rows, 1))
+    CUtensorMap tw, th;
+    const uint64_t wrows = (uint64_t)a.E * (uint64_t)a.dout * (a.glu ? 2 : 1);
+    if (!make_code_map(&tw, codes, (uint64_t)a.din / 2, wrows, kW4Block) ||
+        !make_code_map(&th, codes, (uint64_t)a.din / 2, wrows, 64))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3((unsigned)(num_sms * C::kPerSm));
-    cfg.blockDim = dim3(kW4Threads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)num_sms);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = o.stream;
     set_attrs(&cfg, attr, false, o.pdl);
-    e = cudaLaunchKernelEx(&cfg, expert_w4_kernel<C>, tw, tx, tx1, a);
+    e = cudaLaunchKernelEx(&cfg, expert_w4_kernel<C>, tw, th, a, plan);
     if (e == cudaSuccess && o.launches) ++*o.launches;
     return e;
 }
 
 template <int NR>
-cudaError_t launch_w4_rows(const W4Args& a, bool glu, const void* x, int64_t rows,
-                           const void* codes, int num_sms, const LaunchOpts& o)
+cudaError_t launch_w4_rows(const W4Args& a, const void* codes, int num_sms, const LaunchOpts& o)
 {
-    switch (a.group) {
-        case 32:
-            return glu ? launch_w4_cfg<W4Cfg<NR, 1, true>>(a, x, rows, codes, num_sms, o)
-                       : launch_w4_cfg<W4Cfg<NR, 1, false>>(a, x, rows, codes, num_sms, o);
-        case 64:
-            return glu ? launch_w4_cfg<W4Cfg<NR, 2, true>>(a, x, rows, codes, num_sms, o)
-                       : launch_w4_cfg<W4Cfg<NR, 2, false>>(a, x, rows, codes, num_sms, o);
-        case 128:
-            return glu ? launch_w4_cfg<W4Cfg<NR, 4, true>>(a, x, rows, codes, num_sms, o)
-                       : launch_w4_cfg<W4Cfg<NR, 4, false>>(a, x, rows, codes, num_sms, o);
-    }
-    return cudaErrorInvalidValue;
+    if (a.group == 32) return launch_w4_cfg<W4Cfg<NR, 32>>(a, codes, num_sms, o);
+    if (a.group == 64) return launch_w4_cfg<W4Cfg<NR, 64>>(a, codes, num_sms, o);
+    return launch_w4_cfg<W4Cfg<NR, 128>>(a, codes, num_sms, o);
 }
 
 }  // namespace

@@ -77,11 +77,6 @@ __device__ __forceinline__ int ragged_rows(int rows)
     return (last & (kUmmaK - 1)) ? last : 0;
 }
 
-__device__ __forceinline__ void fence_proxy_async()
-{
-    asm volatile("fence.proxy.async;" ::: "memory");
-}
-
 template <class C>
 __global__ void __launch_bounds__(kWgradThreads, 1)
 expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,

@@ -31,6 +31,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr)
            ((uint64_t)(C::kSbo >> 4) << 32) | ((uint64_t)1 << 46) | (C::kSwizzleMode << 61);
 }
 
+// The same for lines of 128 bytes whatever the element type (128-byte swizzle).
+__device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 // Descriptor of an MN-major tile (the M or N axis contiguous in memory, K across
 // lines) written by TMA in boxes of 64 elements x BK lines with the 128-byte
 // swizzle: a line is 64 elements of one k; leading offset = bytes from one box to
@@ -321,6 +328,38 @@ __device__ __forceinline__ bool wait_or_abort_cluster(uint32_t bar, uint32_t par
     const bool done = wait_or_abort(bar, parity, abort);
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     return done;
+}
+
+// Index e with pre[e] <= i < pre[e+1] of a non-decreasing prefix (i < pre[E]).
+__device__ __forceinline__ int expert_of(const int* pre, int E, int i)
+{
+    int lo = 0, hi = E;   // invariant: pre[lo] <= i < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// One lane of a converged warp. The values that it then issues with are the same in
+// every lane, so the compiler keeps them in uniform registers, which the tcgen05
+// instructions take; a role of a single lane has to move them there each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0u;
+}
+
+// Shared-memory writes of this thread, before the async proxy (an MMA) reads them.
+__device__ __forceinline__ void fence_proxy_async()
+{
+    asm volatile("fence.proxy.async;" ::: "memory");
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
