@@ -12,13 +12,15 @@
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
 //   - 128 elements of a row of x are scaled by a power of two that puts the largest
-//     into [128, 256) and split into two e4m3 terms, x = hi + lo / 32. A bf16 has 8
+//     into [128, 256) and split into two e4m3 terms, x = hi + lo. A bf16 has 8
 //     significant bits, an e4m3 number 4: the two are exact for every element down
-//     to 2^-14 of the block's largest, and off by at most 2^-22 of it below;
+//     to 2^-9 of the block's largest, and off by at most 2^-17 of it below (e4m3 ends
+//     at 2^-9), less than what fp32 sums of the block lose to rounding in the worst case
+//     and far below the result's bf16;
 //   - the tensor cores multiply and sum in fp32: tcgen05.mma.kind::f8f6f4 with the
 //     codes as A (128 output columns on TMEM's lanes, written there by tcgen05.st
-//     without passing shared memory again) and the two terms of at most NR rows as
-//     B (N = 2 NR). Each scale group has its own accumulator;
+//     without passing shared memory again) and the terms of at most NR rows as B, one
+//     after the other into the same accumulator. Each scale group has its own;
 //   - draining a group, a lane holds one output column: its scale enters as one fp32
 //     fma per row (with what undoes x's scale), its zero point as one more with the
 //     group's sum of x.
@@ -54,7 +56,7 @@ constexpr int kW4Bars = 2 * kW4MaxStages + 2 * kW4ASlots + 2 * kW4MaxDSlots + 4;
 template <int NR_, int GROUP_>
 struct W4Cfg {
     static constexpr int NR = NR_, GROUP = GROUP_;
-    static constexpr int N = 2 * NR;                         // hi rows, then lo rows
+    static constexpr int N = NR < 16 ? 16 : NR;              // of the MMA (M = 128 wants 16)
     // Sets of four warps that move codes to TMEM, alternate slices. Two need 14 warps,
     // which leaves 128 registers to a thread: enough while a lane drains few rows.
     static constexpr int kSets = 1;
@@ -67,9 +69,11 @@ struct W4Cfg {
     static constexpr int STEPS = GROUP / 32;                 // MMAs (K = 32) of a group
     // kind::f8f6f4: fp32 accumulate, A and B e4m3 (0), both K-major, N, M = 128.
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
-    static constexpr uint32_t kPanelBytes = N * 128;         // B of 128 contraction elements
+    static constexpr uint32_t kTermBytes = NR * 128;         // a term of 128 contraction elements
+    static constexpr uint32_t kPanelBytes = 2 * kTermBytes;  // hi rows, then lo rows
+    static constexpr int PG = GB < 32 / NR ? GB : 32 / NR;   // groups that a lane drains at once
     static constexpr int kSwap = 64 * (NR + 1) * 4;          // gated: up sums on their way to gate lanes
-    static_assert(GPS % GB == 0 && N % 16 == 0 && N <= 64 && DSLOTS <= kW4MaxDSlots, "slots");
+    static_assert(GPS % GB == 0 && GB % PG == 0 && NR <= 32 && DSLOTS <= kW4MaxDSlots, "slots");
 };
 
 // Shared memory: the ring, x, its group sums, the swap area, barriers, row state, tables.
@@ -110,15 +114,28 @@ __device__ __forceinline__ void tmem_wait_st()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v)
+// COLS (8, 16 or 32) accumulator columns of this lane.
+template <int COLS>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v)
 {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
+    if (COLS == 8)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+              "=r"(v[7])
+            : "r"(taddr));
+    else
+#pragma unroll
+        for (int h = 0; h < COLS / 16; ++h)
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                : "=r"(v[16 * h + 0]), "=r"(v[16 * h + 1]), "=r"(v[16 * h + 2]), "=r"(v[16 * h + 3]),
+                  "=r"(v[16 * h + 4]), "=r"(v[16 * h + 5]), "=r"(v[16 * h + 6]), "=r"(v[16 * h + 7]),
+                  "=r"(v[16 * h + 8]), "=r"(v[16 * h + 9]), "=r"(v[16 * h + 10]),
+                  "=r"(v[16 * h + 11]), "=r"(v[16 * h + 12]), "=r"(v[16 * h + 13]),
+                  "=r"(v[16 * h + 14]), "=r"(v[16 * h + 15])
+                : "r"(taddr + 16u * h));
 }
 
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
@@ -269,7 +286,6 @@ __device__ __forceinline__ int4 w4_finite(const int4& v)
 // the group sums. An infinity or a NaN counts as zero here and
 // marks its row (its terms are added to the row's results one by one). Warps 2 and
 // up; ct: thread among them.
-constexpr int kW4Batch = 4;   // 16-byte loads of a thread in flight
 //
 // A call, not inlined: two roles come here, seldom, and neither should hold its
 // registers or repeat its code.
@@ -278,83 +294,77 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
                                         int panel, uint8_t* s_x, float* s_xsum, int* s_odd,
                                         int* s_odd_next, W4Sync sync)
 {
-    const int lane = ct & 31;
-    const int per_row = panel / 8;   // octets; a warp's are of one row
+    // A lane takes 32 elements at a time, four lanes a block of 128.
+    const int per_row = panel / 32, total = rows * per_row;
     float* s_undo = s_xsum + panel / C::GROUP * C::NR;
-    x += k0;
-    int4 v[kW4Batch];
-    int row = 0, octet = ct;             // the next one to process
-    int load_row = 0, load_octet = ct;   // the next one to load
-    auto step = [&](int& r, int& o) {
-        o += C::kConvThreads;
-        while (o >= per_row) {
-            o -= per_row;
-            ++r;
-        }
-    };
-    auto load = [&] {
+    int4 w[4];
+    auto load = [&](int at) {
+        const int row = at / per_row, k = k0 + 32 * (at - row * per_row);
+        const bool in = at < total && k < din;
 #pragma unroll
-        for (int i = 0; i < kW4Batch; ++i) {
-            v[i] = make_int4(0, 0, 0, 0);
-            if (load_row < rows && k0 + 8 * load_octet < din)
-                v[i] = ld_cg_v4(x + (int64_t)load_row * din + 8 * load_octet);
-            step(load_row, load_octet);
-        }
+        for (int i = 0; i < 4; ++i)
+            w[i] = in ? ld_cg_v4(x + (int64_t)row * din + k + 8 * i) : make_int4(0, 0, 0, 0);
     };
-    while (octet >= per_row) {
-        octet -= per_row;
-        ++row;
-    }
-    load_row = row;
-    load_octet = octet;
-    load();                               // on their way while the previous tile is drained
-    if (!sync(lane)) return false;        // it is: x and its sums are free
+    load(ct);                             // on their way while the previous tile is drained
+    if (!sync(ct & 31)) return false;     // it is: x and its sums are free
     if (ct < C::NR) s_odd_next[ct] = 0;   // nobody uses the other half of the row state now
-    // One octet's code, not unrolled: a warp runs it a few times, and what it would
-    // save in instructions it would lose fetching them.
-    for (int u = 0; row < rows; step(row, octet)) {
-        int4 w = u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3];
-        if (++u == kW4Batch) {
-            u = 0;
-            load();
-        }
-        uint32_t m = w4_largest(w);
+#pragma unroll 1
+    for (int base = ct & ~31; base < total; base += C::kConvThreads) {   // the same for a warp
+        const int at = base + (ct & 31), row = at / per_row, part = at - row * per_row;
+        if (base >= C::kConvThreads) load(at);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, w4_largest(w[i]));
         if (m >= 0x7F80u) {   // rare: an infinity or a NaN
             s_odd[row] = 1;
-            w = w4_finite(w);
-            m = w4_largest(w);
-        }
+            m = 0u;
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        m <<= 16;
+            for (int i = 0; i < 4; ++i) {
+                w[i] = w4_finite(w[i]);
+                m = max(m, w4_largest(w[i]));
+            }
+        }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2)) << 16;
         const float scale = __uint_as_float(w4_scale_exponent(m) << 23);
-        float f[8], h[8], sum = 0.0f;
+        float sum = 0.0f;
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float e = __uint_as_float(w4_element(w, j));
-            f[j] = e * scale;
-            sum += e;
+        for (int i = 0; i < 4; ++i) {
+            float f[8], h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = __uint_as_float(w4_element(w[i], j));
+                f[j] = e * scale;
+                sum += e;
+            }
+            // Bytes in the order of the unpacked codes: even elements, then odd ones.
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t p = to_e4m3x2(f[j], f[j + 2]), q = to_e4m3x2(f[j + 4], f[j + 6]);
+                from_e4m3x2(p, &h[0], &h[1]);
+                from_e4m3x2(q, &h[2], &h[3]);
+                hi[2 * i + j] = p | (q << 16);
+                lo[2 * i + j] = to_e4m3x2(f[j] - h[0], f[j + 2] - h[1]) |
+                                (to_e4m3x2(f[j + 4] - h[2], f[j + 6] - h[3]) << 16);
+            }
         }
-        // Bytes in the order of the unpacked codes: even elements, then odd ones.
-        uint32_t hi[2], lo[2];
+        if (C::GROUP >= 64) sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        if (C::GROUP >= 128) sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (at < total) {
+            uint8_t* dst = s_x + (uint32_t)(part >> 2) * C::kPanelBytes + row * 128;
+            const int c = 2 * (part & 3);   // the first of its two 16-byte units
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t p = to_e4m3x2(f[i], f[i + 2]), q = to_e4m3x2(f[i + 4], f[i + 6]);
-            from_e4m3x2(p, &h[0], &h[1]);
-            from_e4m3x2(q, &h[2], &h[3]);
-            hi[i] = p | (q << 16);
-            lo[i] = to_e4m3x2((f[i] - h[0]) * 32.0f, (f[i + 2] - h[1]) * 32.0f) |
-                    (to_e4m3x2((f[i + 4] - h[2]) * 32.0f, (f[i + 6] - h[3]) * 32.0f) << 16);
+            for (int i = 0; i < 2; ++i) {
+                const int at16 = ((c + i) ^ (row & 7)) << 4;
+                *reinterpret_cast<uint4*>(dst + at16) =
+                    make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                *reinterpret_cast<uint4*>(dst + C::kTermBytes + at16) =
+                    make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            }
+            if ((part & (C::GROUP / 32 - 1)) == 0) s_xsum[part / (C::GROUP / 32) * C::NR + row] = sum;
+            if ((part & 3) == 0) s_undo[(part >> 2) * C::NR + row] = w4_unscale(m);
         }
-        const int pos = (8 * octet) & 127;
-        uint8_t* dst = s_x + (uint32_t)((8 * octet) >> 7) * C::kPanelBytes + row * 128 +
-                       (((pos >> 4) ^ (row & 7)) << 4) + (pos & 8);
-        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + C::NR * 128) = make_uint2(lo[0], lo[1]);
-#pragma unroll
-        for (int d = 1; d < C::GROUP / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if ((lane & (C::GROUP / 8 - 1)) == 0) s_xsum[8 * octet / C::GROUP * C::NR + row] = sum;
-        if ((lane & 15) == 0) s_undo[(octet >> 4) * C::NR + row] = w4_unscale(m);
     }
     fence_proxy_async();   // the MMAs read B through the async proxy
     __syncwarp();
@@ -525,7 +535,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
     uint8_t* smem = state + kW4StateBytes;
     const int stages = plan.stages, panel = plan.panel;
     uint8_t* s_x = smem + (size_t)stages * kW4StageBytes;                 // B, panel / 128 parts
-    float* s_xsum = reinterpret_cast<float*>(s_x + (size_t)panel * N);    // [panel / GROUP][NR]
+    float* s_xsum = reinterpret_cast<float*>(s_x + (size_t)panel * 2 * NR);    // [panel / GROUP][NR]
     float* s_undo = s_xsum + panel / C::GROUP * NR;                       // [panel / 128][NR]
     float* s_swap = s_undo + panel / 128 * NR;
     float2* s_scale = reinterpret_cast<float2*>(s_swap + C::kSwap / 4);   // [8][128]
@@ -682,9 +692,15 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
 #pragma unroll
                         for (int i = 0; i < C::GB * C::STEPS; ++i) {
                             const int step = g0 * C::STEPS + i;   // of 32 elements in the slice
-                            umma_e4m3_ts(d + (uint32_t)(i / C::STEPS * N), at + (uint32_t)step * 8u,
-                                         bx + (uint64_t)(((step >> 2) * C::kPanelBytes + (step & 3) * 32) >> 4),
-                                         C::kIdesc, i % C::STEPS != 0 ? 1u : 0u);
+                            const uint64_t hi =
+                                bx + (uint64_t)(((step >> 2) * C::kPanelBytes + (step & 3) * 32) >> 4);
+                            const uint32_t to = d + (uint32_t)(i / C::STEPS * N);
+                            // Both terms into one accumulator. (For NR = 8 the MMA's columns
+                            // 8-15 see rows that follow the term's; nobody reads them.)
+                            umma_e4m3_ts(to, at + (uint32_t)step * 8u, hi, C::kIdesc,
+                                         i % C::STEPS != 0 ? 1u : 0u);
+                            umma_e4m3_ts(to, at + (uint32_t)step * 8u, hi + (C::kTermBytes >> 4),
+                                         C::kIdesc, 1u);
                         }
                         umma_commit<false>(d_full0 + 8u * ds.slot);
                         if (g0 + C::GB == C::GPS) umma_commit<false>(a_empty0 + 8u * as.slot);
@@ -827,49 +843,40 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                             ok = warp_all(wait_or_abort(d_full0 + 8u * ds.slot, ds.phase, s_abort));
                             if (!ok) break;
                             tc_fence_after();
-                            // 32 accumulator columns at a time: 16 pairs of terms, of one
-                            // group (NR >= 16; half of one for NR = 32) or of two.
-                            constexpr int kParts = C::GB * N / 32;
-                            constexpr int kRun = NR < 16 ? NR : 16;   // rows of a part's group
+                            // As many groups at a time as 32 accumulator columns hold.
                             const uint32_t d = t_lane + (uint32_t)(ds.slot * C::GB * N);
 #pragma unroll
-                            for (int part = 0; part < kParts; ++part) {
-                                uint32_t q[32];
+                            for (int p0 = 0; p0 < C::GB; p0 += C::PG) {
+                                uint32_t q[C::PG * NR];
                                 if (warp_live) {
-                                    if (N <= 32) {
-                                        tmem_ld32(d + 32u * part, q);
-                                    } else {
-                                        tmem_ld16(d + 64u * (part >> 1) + 16u * (part & 1), q);
-                                        tmem_ld16(d + 64u * (part >> 1) + NR + 16u * (part & 1), q + 16);
-                                    }
+#pragma unroll
+                                    for (int u = 0; u < C::PG; ++u)
+                                        tmem_ld_cols<NR>(d + (uint32_t)((p0 + u) * N), q + u * NR);
                                     tmem_wait_ld();
                                 }
-                                if (part == kParts - 1) {   // the slot is free as soon as it is read
+                                if (p0 + C::PG == C::GB) {   // the slot is free as soon as it is read
                                     tc_fence_before();
                                     __syncwarp();
                                     if (lane == 0) mbar_arrive(d_empty0 + 8u * ds.slot);
                                 }
                                 if (!warp_live) continue;
 #pragma unroll
-                                for (int u = 0; u < 16 / kRun; ++u) {
-                                    const int gi = g0 + (N <= 32 ? part * (32 / N) + u : part >> 1);
-                                    const int n0 = N <= 32 ? 0 : 16 * (part & 1);
+                                for (int u = 0; u < C::PG; ++u) {
+                                    const int gi = g0 + p0 + u;
                                     const float2 s = sc[gi * 128];
-                                    const float4* xs = reinterpret_cast<const float4*>(sums + gi * NR + n0);
+                                    const float4* xs = reinterpret_cast<const float4*>(sums + gi * NR);
                                     const float4* un =
-                                        reinterpret_cast<const float4*>(undo + gi * C::GROUP / 128 * NR + n0);
+                                        reinterpret_cast<const float4*>(undo + gi * C::GROUP / 128 * NR);
 #pragma unroll
-                                    for (int n4 = 0; n4 < kRun / 4; ++n4) {
+                                    for (int n4 = 0; n4 < NR / 4; ++n4) {
                                         const float4 x4 = xs[n4], u4 = un[n4];
                                         const float xv[4] = {x4.x, x4.y, x4.z, x4.w};
                                         const float uv[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
                                         for (int i = 0; i < 4; ++i) {
-                                            const int hi = (N <= 32 ? u * N : 0) + 4 * n4 + i;
-                                            const float v = fmaf(__uint_as_float(q[hi + kRun]), 0.03125f,
-                                                                 __uint_as_float(q[hi]));
-                                            float& sum = acc[n0 + 4 * n4 + i];
-                                            sum = fmaf(s.x * uv[i], v, fmaf(s.y, xv[i], sum));
+                                            float& sum = acc[4 * n4 + i];
+                                            sum = fmaf(s.x * uv[i], __uint_as_float(q[u * NR + 4 * n4 + i]),
+                                                       fmaf(s.y, xv[i], sum));
                                         }
                                     }
                                 }
@@ -942,7 +949,7 @@ template <class C>
 W4Plan w4_plan(int64_t din, int E)
 {
     const size_t fixed = 1024 + kW4StateBytes + C::kSwap + 8 * 128 * 8 + 4 * (3 * (size_t)E + 1);
-    const size_t per_slice = (size_t)kW4Slice * C::N + (size_t)(C::GPS + 2) * C::NR * 4;   // of x
+    const size_t per_slice = (size_t)kW4Slice * 2 * C::NR + (size_t)(C::GPS + 2) * C::NR * 4;   // of x
     const int64_t slices = (din + kW4Slice - 1) / kW4Slice;
     const int64_t fit =
         (int64_t)((kSmemLimit - fixed - (size_t)kW4MinStages * kW4StageBytes) / per_slice);
