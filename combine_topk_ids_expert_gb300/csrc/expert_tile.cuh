@@ -252,38 +252,45 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     q.total = q.uh + s_light[E] * nbk;
     const int total = q.total;
 
-    if (warp == 0 && lane == 0) {
+    // The copying and the issuing warp wait as a whole and elect a lane to issue: what
+    // a lane issues with is then uniform (see elect_one).
+    if (warp == 0) {
         // ---- TMA producer (each CTA fills its own ring) --------------------
         int g = 0;   // k-slices issued
-        for (int u = first; u < total && !*s_abort; u += step) {
+        bool ok = true;
+        for (int u = first; u < total && ok && !*s_abort; u += step) {
             const TileRef p = tile_of(q, E, nbk, u);
             const int row0 = __ldcg(a.expert_offset + p.e) + p.mt * C::kTileRows +
                              r * (p.half ? kBM / 2 : kBM);
             for (int k = 0; k < k_iters; ++k, ++g) {
                 const int s = g % STAGES;
                 const uint32_t ph = (uint32_t)((g / STAGES) & 1);
-                if (!wait_or_abort(empty0 + 8u * s, ph ^ 1u, s_abort)) break;
+                ok = warp_all(wait_or_abort(empty0 + 8u * s, ph ^ 1u, s_abort));
+                if (!ok) break;
                 const uint32_t sa = tiles_u32 + (uint32_t)s * C::kStageBytes;
                 const uint32_t sb = sa + C::kBytesA;
                 const int kc = k * BK;
-                if (!PAIR) {
-                    const uint32_t fb = full0 + 8u * s;
-                    mbar_expect_tx(fb, C::kStageBytes);
-                    tma_load_2d(sa, &tm_a, kc, row0, fb);
-                    load_b<C>(sb, &tm_b, a, p.e, p.nb, r, kc, fb);
-                } else {
-                    // Both CTAs' copies complete on the leader's barrier, which
-                    // expects the bytes of both (an M = 128 tile: 64 rows of x per CTA).
-                    if (leader)
-                        mbar_expect_tx(full0 + 8u * s,
-                                       2u * (p.half ? C::kBytesAHalf + C::kBytesB : C::kStageBytes));
-                    const uint32_t fb = lead_full0 + 8u * s;
-                    tma_load_2d_pair(sa, p.half ? &tm_a_half : &tm_a, kc, row0, fb);
-                    load_b<C>(sb, &tm_b, a, p.e, p.nb, r, kc, fb);
+                if (elect_one()) {
+                    if (!PAIR) {
+                        const uint32_t fb = full0 + 8u * s;
+                        mbar_expect_tx(fb, C::kStageBytes);
+                        tma_load_2d(sa, &tm_a, kc, row0, fb);
+                        load_b<C>(sb, &tm_b, a, p.e, p.nb, r, kc, fb);
+                    } else {
+                        // Both CTAs' copies complete on the leader's barrier, which
+                        // expects the bytes of both (an M = 128 tile: 64 rows of x per CTA).
+                        if (leader)
+                            mbar_expect_tx(full0 + 8u * s,
+                                           2u * (p.half ? C::kBytesAHalf + C::kBytesB : C::kStageBytes));
+                        const uint32_t fb = lead_full0 + 8u * s;
+                        tma_load_2d_pair(sa, p.half ? &tm_a_half : &tm_a, kc, row0, fb);
+                        load_b<C>(sb, &tm_b, a, p.e, p.nb, r, kc, fb);
+                    }
                 }
+                __syncwarp();
             }
         }
-        // The copies this thread issued land before shared memory goes away
+        // The copies this warp issued land before shared memory goes away
         // (a pair's copies are tracked by the leader's barrier: wait for the
         // MMAs to release the stages instead).
         const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
@@ -292,38 +299,40 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             if (PAIR) mbar_wait_until(empty0 + 8u * s, par, deadline);
             else mbar_wait_until(full0 + 8u * s, par, deadline);
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ---- MMA issuer (pairs: the leader's, for both SMs) ----------------
         int g = 0, tl = 0;
-        bool issued = false;
-        for (int u = first; u < total && !*s_abort; u += step, ++tl) {
+        bool issued = false, ok = true;
+        for (int u = first; u < total && ok && !*s_abort; u += step, ++tl) {
             const int acc = tl & 1, use = tl >> 1;      // accumulator and its use count
-            if (!wait_or_abort(accum_empty0 + 8u * acc, (uint32_t)((use & 1) ^ 1), s_abort)) break;
+            ok = warp_all(wait_or_abort(accum_empty0 + 8u * acc, (uint32_t)((use & 1) ^ 1), s_abort));
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
             const uint32_t idesc = tile_of(q, E, nbk, u).half ? C::kIdescHalf : C::kIdesc;
-            bool ok = true;
             for (int k = 0; k < k_iters; ++k, ++g) {
                 const int s = g % STAGES;
-                if (!wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort)) {
-                    ok = false;
-                    break;
-                }
+                ok = warp_all(wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort));
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = tiles_u32 + (uint32_t)s * C::kStageBytes;
+                if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < BK / kUmmaK; ++j)
-                    umma_bf16<PAIR>(d_tmem, smem_desc<C>(sa + j * kUmmaK * 2),
-                                    desc_b<C>(sa + C::kBytesA, j), idesc,
-                                    (k | j) != 0 ? 1u : 0u);
+                    for (int j = 0; j < BK / kUmmaK; ++j)
+                        umma_bf16<PAIR>(d_tmem, smem_desc<C>(sa + j * kUmmaK * 2),
+                                        desc_b<C>(sa + C::kBytesA, j), idesc,
+                                        (k | j) != 0 ? 1u : 0u);
+                    umma_commit<PAIR>(empty0 + 8u * s);   // frees the stage (in both CTAs of a pair)
+                    if (k == k_iters - 1)
+                        umma_commit<PAIR>(accum_full0 + 8u * acc);   // the accumulator is complete
+                }
+                __syncwarp();
                 issued = true;
-                umma_commit<PAIR>(empty0 + 8u * s);   // frees the stage (in both CTAs of a pair)
             }
-            if (!ok) break;
-            umma_commit<PAIR>(accum_full0 + 8u * acc);   // the tile's accumulator is complete
         }
-        if (issued) {   // every MMA this thread issued has finished before TMEM is freed
-            umma_commit_local<PAIR>(drain);
+        if (issued) {   // every MMA this warp issued has finished before TMEM is freed
+            if (elect_one()) umma_commit_local<PAIR>(drain);
+            __syncwarp();
             mbar_wait(drain, 0u);
         }
     } else if (warp >= 2) {
@@ -423,6 +432,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         }
     }
 
+    __syncwarp();
     if (threadIdx.x == 0 && *s_abort) atomicOr(a.err, kErrTimeout);
     tc_fence_before();
     __syncthreads();

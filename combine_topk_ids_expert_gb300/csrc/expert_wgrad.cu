@@ -137,10 +137,11 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---- TMA producer (each CTA fills its own ring) --------------------
         int g = 0;
-        for (int64_t u = first; u < total && !*s_abort; u += step) {
+        bool ok = true;
+        for (int64_t u = first; u < total && ok && !*s_abort; u += step) {
             const WUnit w = wgrad_unit(s_cnt, nmb, nnb, u);
             if (w.k_iters == 0) continue;
             const int row0 = s_off[w.e];
@@ -150,76 +151,83 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
             for (int k = 0; k < w.k_iters; ++k, ++g) {
                 const int s = g % STAGES;
                 const uint32_t ph = (uint32_t)((g / STAGES) & 1);
-                if (!wait_or_abort(empty0 + 8u * s, ph ^ 1u, s_abort)) break;
+                ok = warp_all(wait_or_abort(empty0 + 8u * s, ph ^ 1u, s_abort));
+                if (!ok) break;
                 const uint32_t sa = tiles_u32 + (uint32_t)s * C::kStageBytes;
                 const uint32_t sb = sa + C::kBytesA;
                 const int kr = row0 + k * kWgradBK;
                 // A ragged slice completes on this CTA's own barrier, for warp 6;
                 // every other one on the (leader's) full barrier.
                 const bool fix = ragged && k == w.k_iters - 1;
-                if (fix || !PAIR) {
-                    const uint32_t bar = (fix ? landed0 : full0) + 8u * s;
-                    mbar_expect_tx(bar, C::kStageBytes);
+                if (elect_one()) {
+                    if (fix || !PAIR) {
+                        const uint32_t bar = (fix ? landed0 : full0) + 8u * s;
+                        mbar_expect_tx(bar, C::kStageBytes);
 #pragma unroll
-                    for (int j = 0; j < C::kBoxesA; ++j)
-                        tma_load_2d(sa + j * kMnBoxBytes, &tm_a, m0 + 64 * j, kr, bar);
+                        for (int j = 0; j < C::kBoxesA; ++j)
+                            tma_load_2d(sa + j * kMnBoxBytes, &tm_a, m0 + 64 * j, kr, bar);
 #pragma unroll
-                    for (int j = 0; j < C::kBoxesB; ++j)
-                        tma_load_2d(sb + j * kMnBoxBytes, &tm_b, n0 + 64 * j, kr, bar);
-                } else {
-                    if (leader) mbar_expect_tx(full0 + 8u * s, 2u * C::kStageBytes);
-                    const uint32_t bar = lead_full0 + 8u * s;
+                        for (int j = 0; j < C::kBoxesB; ++j)
+                            tma_load_2d(sb + j * kMnBoxBytes, &tm_b, n0 + 64 * j, kr, bar);
+                    } else {
+                        if (leader) mbar_expect_tx(full0 + 8u * s, 2u * C::kStageBytes);
+                        const uint32_t bar = lead_full0 + 8u * s;
 #pragma unroll
-                    for (int j = 0; j < C::kBoxesA; ++j)
-                        tma_load_2d_pair(sa + j * kMnBoxBytes, &tm_a, m0 + 64 * j, kr, bar);
+                        for (int j = 0; j < C::kBoxesA; ++j)
+                            tma_load_2d_pair(sa + j * kMnBoxBytes, &tm_a, m0 + 64 * j, kr, bar);
 #pragma unroll
-                    for (int j = 0; j < C::kBoxesB; ++j)
-                        tma_load_2d_pair(sb + j * kMnBoxBytes, &tm_b, n0 + 64 * j, kr, bar);
+                        for (int j = 0; j < C::kBoxesB; ++j)
+                            tma_load_2d_pair(sb + j * kMnBoxBytes, &tm_b, n0 + 64 * j, kr, bar);
+                    }
                 }
+                __syncwarp();
             }
         }
-        // The copies this thread issued land before shared memory goes away: the
+        // The copies this warp issued land before shared memory goes away: the
         // MMAs (or, after an abort, the wait limit) release their stages.
         const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
         for (int i = (g > STAGES ? g - STAGES : 0); i < g; ++i)
             mbar_wait_until(empty0 + 8u * (uint32_t)(i % STAGES), (uint32_t)((i / STAGES) & 1),
                             deadline);
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ---- MMA issuer (pairs: the leader's, for both SMs) ----------------
         int g = 0, tl = 0;
-        bool issued = false;
-        for (int64_t u = first; u < total && !*s_abort; u += step) {
+        bool issued = false, ok = true;
+        for (int64_t u = first; u < total && ok && !*s_abort; u += step) {
             const WUnit w = wgrad_unit(s_cnt, nmb, nnb, u);
             if (w.k_iters == 0) continue;
             const int acc = tl & 1, use = tl >> 1;
             ++tl;
-            if (!wait_or_abort(accum_empty0 + 8u * acc, (uint32_t)((use & 1) ^ 1), s_abort)) break;
+            ok = warp_all(wait_or_abort(accum_empty0 + 8u * acc, (uint32_t)((use & 1) ^ 1), s_abort));
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
-            bool ok = true;
             for (int k = 0; k < w.k_iters; ++k, ++g) {
                 const int s = g % STAGES;
-                if (!wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort)) {
-                    ok = false;
-                    break;
-                }
+                ok = warp_all(wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort));
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = tiles_u32 + (uint32_t)s * C::kStageBytes;
                 const int left = w.rows - k * kWgradBK;
                 const int steps = left >= kWgradBK ? kWgradBK / kUmmaK
                                                    : (left + kUmmaK - 1) / kUmmaK;
-                for (int j = 0; j < steps; ++j)
-                    umma_bf16<PAIR>(d_tmem, smem_desc_mn(sa + j * (kUmmaK * kMnLineBytes)),
-                                    smem_desc_mn(sa + C::kBytesA + j * (kUmmaK * kMnLineBytes)),
-                                    C::kIdesc, (k | j) != 0 ? 1u : 0u);
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < kWgradBK / kUmmaK; ++j)
+                        if (j < steps)
+                            umma_bf16<PAIR>(d_tmem, smem_desc_mn(sa + j * (kUmmaK * kMnLineBytes)),
+                                            smem_desc_mn(sa + C::kBytesA + j * (kUmmaK * kMnLineBytes)),
+                                            C::kIdesc, (k | j) != 0 ? 1u : 0u);
+                    umma_commit<PAIR>(empty0 + 8u * s);
+                    if (k == w.k_iters - 1) umma_commit<PAIR>(accum_full0 + 8u * acc);
+                }
+                __syncwarp();
                 issued = true;
-                umma_commit<PAIR>(empty0 + 8u * s);
             }
-            if (!ok) break;
-            umma_commit<PAIR>(accum_full0 + 8u * acc);
         }
         if (issued) {
-            umma_commit_local<PAIR>(drain);
+            if (elect_one()) umma_commit_local<PAIR>(drain);
+            __syncwarp();
             mbar_wait(drain, 0u);
         }
     } else if (warp >= 2 && warp < 6) {
