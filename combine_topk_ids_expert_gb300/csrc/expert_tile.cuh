@@ -25,13 +25,13 @@ constexpr int kGemmThreads = 192;   // warp 0 TMA, warp 1 MMA + TMEM, warps 2-5 
 
 enum TileMode { kPlain = 0, kGlu = 1, kDgrad = 2, kDgradGlu = 3 };
 
-// Bytes after the ring: barriers, TMEM address, abort flag, the two
-// per-expert tile prefixes (heavy, light) and the per-expert row counts (all
-// sized for the largest expert count).
+// Bytes after the ring: the epilogue warps' staging, barriers, TMEM address, abort
+// flag, the two per-expert tile prefixes (heavy, light) and the per-expert row counts
+// (all sized for the largest expert count).
 template <int STAGES>
 constexpr int tail_bytes()
 {
-    return 8 * (2 * STAGES + 5) + 8 + 8 * (kMaxExperts + 1) + 4 * kMaxExperts;
+    return 4 * kStageWarpBytes + 8 * (2 * STAGES + 5) + 8 + 8 * (kMaxExperts + 1) + 4 * kMaxExperts;
 }
 
 template <int BN_, int BK_, int STAGES_, bool PAIR_, int MODE_ = kPlain>
@@ -164,7 +164,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
     const uint32_t tiles_u32 = smem_u32(smem);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageBytes + 4 * kStageWarpBytes);
     const uint32_t full0 = smem_u32(bars);                 // STAGES (pairs: the leader's count)
     const uint32_t empty0 = full0 + 8u * STAGES;           // STAGES
     const uint32_t accum_full0 = empty0 + 8u * STAGES;     // 2: one per accumulator
@@ -338,14 +338,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     } else if (warp >= 2) {
         // ---- epilogue: TMEM -> bf16 -> global ------------------------------
         const int quarter = warp & 3;                  // TMEM lanes this warp may read
-        const int r_in = quarter * 32 + lane;          // accumulator row = tile row (of this CTA)
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t stage = tiles_u32 + STAGES * C::kStageBytes + (uint32_t)(quarter * kStageWarpBytes);
         uint16_t* y = static_cast<uint16_t*>(a.y);
         int tl = 0;
         for (int u = first; u < total && !*s_abort; u += step, ++tl) {
             const int acc = tl & 1, use = tl >> 1;
-            if (!warp_all(wait_or_abort(accum_full0 + 8u * acc, (uint32_t)(use & 1), s_abort))) break;
-            tc_fence_after();
             const uint32_t t_acc = t_lane + (uint32_t)(acc * BN);
             const TileRef p = tile_of(q, E, nbk, u);
             // The rows this warp drains and the output columns they cover. A full
@@ -353,14 +351,24 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             // column. A pair's M = 128 tile: the CTA's 64 rows appear twice, lanes
             // 0-63 with output columns [0, BN/2) and lanes 64-127 with
             // [BN/2, BN), both in accumulator columns [0, BN/2).
-            const int sub = p.half ? 32 * (quarter & 1) + lane : r_in;
+            const int sub0 = 32 * (p.half ? quarter & 1 : quarter);
             const int col0 = p.half ? (BN / 2) * (quarter >> 1) : 0;
             const int ncols = p.half ? BN / 2 : BN;
             const int part = p.half ? kBM / 2 : kBM;       // rows of this CTA's part
             const int m_in = p.mt * C::kTileRows + r * part;
-            const int rows = min(part, q.cnt[p.e] - m_in);
-            const int64_t row = (int64_t)__ldcg(a.expert_offset + p.e) + m_in + sub;
+            const int rows = min(part, q.cnt[p.e] - m_in) - sub0;   // of this warp's 32
+            const int64_t row0 = (int64_t)__ldcg(a.expert_offset + p.e) + m_in + sub0;
+            int4 next_g[4], next_u[4];
+            if (C::MODE == kDgradGlu) {
+                const uint16_t* gate_up =
+                    static_cast<const uint16_t*>(a.aux) + row0 * 2 * a.dout + p.nb * BN + col0;
+                warp_fetch_bf16x32(next_g, lane, gate_up, 2 * a.dout, rows);
+                warp_fetch_bf16x32(next_u, lane, gate_up + a.dout, 2 * a.dout, rows);
+            }
+            if (!warp_all(wait_or_abort(accum_full0 + 8u * acc, (uint32_t)(use & 1), s_abort))) break;
+            tc_fence_after();
             if (C::MODE == kPlain || C::MODE == kDgrad) {
+                uint16_t* at = y + row0 * a.dout + p.nb * BN + col0;
 #pragma unroll 1
                 for (int c = 0; c < ncols; c += 32) {
                     uint32_t q32[32];
@@ -368,57 +376,58 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                     tmem_ld32(t_acc + (uint32_t)c, q32);
                     tmem_wait_ld();
                     as_floats(q32, v);
-                    if (sub < rows) store_bf16x32(y + row * a.dout + p.nb * BN + col0 + c, v);
+                    warp_store_bf16x32(stage, lane, v, at + c, a.dout, rows);
                 }
             } else if (C::MODE == kGlu) {
                 // Accumulator columns [128 b, 128 b + 64) are g and the next 64 u of
                 // the tile's output columns [64 b, 64 b + 64).
                 uint16_t* gate_up = static_cast<uint16_t*>(a.aux);
+                const int64_t col = p.nb * C::kOutBN + col0 / 2;
 #pragma unroll 1
                 for (int c = 0; c < ncols / 2; c += 32) {
                     uint32_t qg[32], qu[32];
+                    float g[32], u[32];
                     const uint32_t at = (uint32_t)((c >> 6) * 128 + (c & 63));
                     tmem_ld32(t_acc + at, qg);
                     tmem_ld32(t_acc + at + 64u, qu);
                     tmem_wait_ld();
-                    if (sub < rows) {
-                        float g[32], u[32], h[32];
-                        as_floats(qg, g);
-                        as_floats(qu, u);
-                        const int64_t col = p.nb * C::kOutBN + col0 / 2 + c;
-                        if (gate_up) {
-                            uint16_t* at_row = gate_up + row * 2 * a.dout + col;
-                            store_bf16x32(at_row, g);
-                            store_bf16x32(at_row + a.dout, u);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = act_value(g[i], a.act) * u[i];
-                        store_bf16x32(y + row * a.dout + col, h);
+                    as_floats(qg, g);
+                    as_floats(qu, u);
+                    if (gate_up) {
+                        uint16_t* to = gate_up + row0 * 2 * a.dout + col + c;
+                        warp_store_bf16x32(stage, lane, g, to, 2 * a.dout, rows);
+                        warp_store_bf16x32(stage, lane, u, to + a.dout, 2 * a.dout, rows);
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] *= act_value(g[i], a.act);
+                    warp_store_bf16x32(stage, lane, u, y + row0 * a.dout + col + c, a.dout, rows);
                 }
             } else {
-                const uint16_t* gate_up = static_cast<const uint16_t*>(a.aux);
+                // The pre-activations of the next 32 columns are on their way meanwhile.
+                const int64_t at = row0 * 2 * a.dout + p.nb * BN + col0;
+                const uint16_t* gate_up = static_cast<const uint16_t*>(a.aux) + at;
 #pragma unroll 1
                 for (int c = 0; c < ncols; c += 32) {
                     uint32_t q32[32];
+                    float gh[32], g[32], u[32];
                     tmem_ld32(t_acc + (uint32_t)c, q32);
-                    tmem_wait_ld();
-                    if (sub < rows) {
-                        float gh[32], g[32], u[32];
-                        as_floats(q32, gh);
-                        const int64_t at = row * 2 * a.dout + p.nb * BN + col0 + c;
-                        load_bf16x32(gate_up + at, g);
-                        load_bf16x32(gate_up + at + a.dout, u);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float value, slope;
-                            act_value_slope(g[i], a.act, &value, &slope);
-                            g[i] = gh[i] * u[i] * slope;
-                            u[i] = gh[i] * value;
-                        }
-                        store_bf16x32(y + at, g);
-                        store_bf16x32(y + at + a.dout, u);
+                    warp_spread_bf16x32(stage, lane, next_g, g);
+                    warp_spread_bf16x32(stage, lane, next_u, u);
+                    if (c + 32 < ncols) {
+                        warp_fetch_bf16x32(next_g, lane, gate_up + c + 32, 2 * a.dout, rows);
+                        warp_fetch_bf16x32(next_u, lane, gate_up + a.dout + c + 32, 2 * a.dout, rows);
                     }
+                    tmem_wait_ld();
+                    as_floats(q32, gh);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float value, slope;
+                        act_value_slope(g[i], a.act, &value, &slope);
+                        g[i] = gh[i] * u[i] * slope;
+                        u[i] = gh[i] * value;
+                    }
+                    warp_store_bf16x32(stage, lane, g, y + at + c, 2 * a.dout, rows);
+                    warp_store_bf16x32(stage, lane, u, y + at + a.dout + c, 2 * a.dout, rows);
                 }
             }
             // This warp's reads of the accumulator are done: one arrival per

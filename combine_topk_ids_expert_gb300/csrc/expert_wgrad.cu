@@ -35,9 +35,10 @@ struct WCfg {
     static constexpr int kBoxesA = kBM / 64, kBoxesB = kColsB / 64;
     static constexpr uint32_t kBytesA = kBoxesA * kMnBoxBytes;
     static constexpr uint32_t kStageBytes = (kBoxesA + kBoxesB) * kMnBoxBytes;
-    // Behind the ring: barriers and flags, then every expert's rows and first row.
+    // Behind the ring: barriers and flags, every expert's rows and first row, and the
+    // epilogue warps' staging.
     static constexpr int kBarBytes = 512;
-    static constexpr int kTail = kBarBytes + 2 * 4 * kMaxExperts;
+    static constexpr int kTail = kBarBytes + 2 * 4 * kMaxExperts + 4 * kStageWarpBytes;
     static constexpr int kFit = (kSmemLimit - 1024 - kTail) / (int)kStageBytes;
     static constexpr int STAGES = kFit > 8 ? 8 : kFit;
     static constexpr size_t kSmem = 1024 + (size_t)STAGES * kStageBytes + kTail;
@@ -233,7 +234,8 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
     } else if (warp >= 2 && warp < 6) {
         // ---- epilogue: TMEM -> grad_w ---------------------------------------
         const int quarter = warp & 3;
-        const int m_in = r * kBM + quarter * 32 + lane;
+        const int m0 = r * kBM + quarter * 32;   // this warp's rows of the tile
+        const uint32_t stage = smem_u32(s_off + kMaxExperts) + (uint32_t)(quarter * kStageWarpBytes);
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         int tl = 0;
         for (int64_t u = first; u < total && !*s_abort; u += step) {
@@ -247,7 +249,7 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
                 tc_fence_after();
                 ++tl;
             }
-            const int64_t at = ((int64_t)w.e * a.dout + w.mb * C::kTileM + m_in) * a.din + w.nb * BN;
+            const int64_t at = ((int64_t)w.e * a.dout + w.mb * C::kTileM + m0) * a.din + w.nb * BN;
 #pragma unroll 1
             for (int c = 0; c < BN; c += 32) {
                 float v[32];
@@ -261,7 +263,8 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
                     as_floats(q, v);
                 }
                 if (a.f32) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.grad_w) + at + c);
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.grad_w) + at +
+                                                            lane * a.din + c);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float4 o = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -274,12 +277,14 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
                 } else {
                     uint16_t* dst = static_cast<uint16_t*>(a.grad_w) + at + c;
                     if (a.accumulate) {
+                        int4 old[4];
                         float p[32];
-                        load_bf16x32(dst, p);
+                        warp_fetch_bf16x32(old, lane, dst, a.din, 32);
+                        warp_spread_bf16x32(stage, lane, old, p);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] += p[i];
                     }
-                    store_bf16x32(dst, v);
+                    warp_store_bf16x32(stage, lane, v, dst, a.din, 32);
                 }
             }
             if (!empty) {

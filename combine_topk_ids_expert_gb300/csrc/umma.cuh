@@ -283,26 +283,76 @@ __device__ __forceinline__ void act_value_slope(float g, int act, float* value, 
     *slope = t > 0.0f ? p + g * dv * t : p;   // far out g v' overflows where t is zero
 }
 
-// 32 bf16 columns of one row, packed from fp32 / unpacked into fp32.
-__device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32])
+// 32 rows x 32 bf16 columns of a warp, one row per lane, from and to memory by way of
+// the warp's 2 KB of shared memory: a lane's own row would be 16 bytes of 32 different
+// lines per instruction, this way an instruction covers 64 bytes of 8 rows. `base`: the
+// first row's first column; rows [0, rows) exist. The row's 16-byte units are XORed with
+// the row so that neither side has bank conflicts.
+constexpr int kStageWarpBytes = 2048;
+
+__device__ __forceinline__ uint32_t stage_at(uint32_t stage, int row, int unit)
 {
+    return stage + (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ int4 lds_int4(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void warp_store_bf16x32(uint32_t stage, int lane, const float (&v)[32],
+                                                   uint16_t* base, int64_t stride, int rows)
+{
+    __syncwarp();   // the warp is done with what the stage held
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        int4 w;
-        w.x = (int)pack_bf16x2_rn(v[8 * g + 0], v[8 * g + 1]);
-        w.y = (int)pack_bf16x2_rn(v[8 * g + 2], v[8 * g + 3]);
-        w.z = (int)pack_bf16x2_rn(v[8 * g + 4], v[8 * g + 5]);
-        w.w = (int)pack_bf16x2_rn(v[8 * g + 6], v[8 * g + 7]);
-        reinterpret_cast<int4*>(dst)[g] = w;
+    for (int g = 0; g < 4; ++g)
+        sts128(stage_at(stage, lane, g), pack_bf16x2_rn(v[8 * g + 0], v[8 * g + 1]),
+               pack_bf16x2_rn(v[8 * g + 2], v[8 * g + 3]), pack_bf16x2_rn(v[8 * g + 4], v[8 * g + 5]),
+               pack_bf16x2_rn(v[8 * g + 6], v[8 * g + 7]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2), unit = lane & 3;
+        const int4 w = lds_int4(stage_at(stage, row, unit));
+        if (row < rows) *reinterpret_cast<int4*>(base + row * stride + 8 * unit) = w;
     }
 }
 
-__device__ __forceinline__ void load_bf16x32(const uint16_t* src, float (&v)[32])
+// The loads of warp_load_bf16x32, which its second half takes to the lanes' rows.
+__device__ __forceinline__ void warp_fetch_bf16x32(int4 (&w)[4], int lane, const uint16_t* base,
+                                                   int64_t stride, int rows)
 {
 #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        w[i] = row < rows ? ld_cg_v4(base + row * stride + 8 * (lane & 3)) : make_int4(0, 0, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void warp_spread_bf16x32(uint32_t stage, int lane, const int4 (&w)[4],
+                                                    float (&v)[32])
+{
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sts128(stage_at(stage, 8 * i + (lane >> 2), lane & 3), (uint32_t)w[i].x, (uint32_t)w[i].y,
+               (uint32_t)w[i].z, (uint32_t)w[i].w);
+    __syncwarp();
+#pragma unroll
     for (int g = 0; g < 4; ++g) {
-        const int4 w = ld_cg_v4(src + 8 * g);
-        const uint32_t q[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
+        const int4 p = lds_int4(stage_at(stage, lane, g));
+        const uint32_t q[4] = {(uint32_t)p.x, (uint32_t)p.y, (uint32_t)p.z, (uint32_t)p.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[8 * g + 2 * i] = __uint_as_float(q[i] << 16);
