@@ -78,6 +78,16 @@ __device__ __forceinline__ int ragged_rows(int rows)
     return (last & (kUmmaK - 1)) ? last : 0;
 }
 
+// A ragged slice takes longer to get ready than the ring looks ahead, so it is copied
+// kEarly slices before its turn: it is at position ragged_at of the ring's order and
+// still the last to be multiplied (see the roles). 1385 and 1496 TFLOP/s without
+// (mixtral rows, down and gate/up weights), 1637 and 1714 with nothing to repair.
+constexpr int kEarly = 2;
+__device__ __forceinline__ int ragged_at(const WUnit& w)
+{
+    return ragged_rows(w.rows) ? w.k_iters - 1 - min(kEarly, w.k_iters - 1) : w.k_iters - 1;
+}
+
 template <class C>
 __global__ void __launch_bounds__(kWgradThreads, 1)
 expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -93,8 +103,8 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
     const uint32_t full0 = smem_u32(bars);               // STAGES (pairs: the leader's count)
     const uint32_t empty0 = full0 + 8u * STAGES;         // STAGES
     const uint32_t landed0 = empty0 + 8u * STAGES;       // STAGES: a ragged slice, this CTA's copies
-    const uint32_t peer0 = landed0 + 8u * STAGES;        // STAGES: a ragged slice, repaired by the peer
-    const uint32_t accum_full0 = peer0 + 8u * STAGES;    // 2
+    const uint32_t fixed0 = landed0 + 8u * STAGES;       // STAGES: a ragged slice, repaired in both CTAs
+    const uint32_t accum_full0 = fixed0 + 8u * STAGES;    // 2
     const uint32_t accum_empty0 = accum_full0 + 16u;     // 2
     const uint32_t drain = accum_empty0 + 16u;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 5);
@@ -110,11 +120,12 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
     const int nmb = (int)(a.dout / C::kTileM), nnb = (int)(a.din / BN);
     const int64_t total = (int64_t)a.E * nmb * nnb;
     const uint32_t lead_full0 = PAIR ? map_to_rank(full0, 0) : full0;
-    const uint32_t lead_peer0 = PAIR ? map_to_rank(peer0, 0) : peer0;
+    const uint32_t lead_fixed0 = PAIR ? map_to_rank(fixed0, 0) : fixed0;
     const uint32_t lead_accum_empty0 = PAIR ? map_to_rank(accum_empty0, 0) : accum_empty0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 4 * STAGES; ++s) mbar_init(full0 + 8u * s, 1u);
+        for (int s = 0; s < 3 * STAGES; ++s) mbar_init(full0 + 8u * s, 1u);
+        for (int s = 0; s < STAGES; ++s) mbar_init(fixed0 + 8u * s, PAIR ? 2u : 1u);
         for (int b = 0; b < 2; ++b) {
             mbar_init(accum_full0 + 8u * b, 1u);
             mbar_init(accum_empty0 + 8u * b, C::kReleaseCount);
@@ -149,7 +160,9 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
             const int m0 = w.mb * C::kTileM + r * kBM;
             const int n0 = w.nb * BN + r * C::kColsB;
             const bool ragged = ragged_rows(w.rows) != 0;
-            for (int k = 0; k < w.k_iters; ++k, ++g) {
+            const int last_at = ragged_at(w);
+            for (int i = 0; i < w.k_iters; ++i, ++g) {
+                const int k = i < last_at ? i : i == last_at ? w.k_iters - 1 : i - 1;   // slice
                 const int s = g % STAGES;
                 const uint32_t ph = (uint32_t)((g / STAGES) & 1);
                 ok = warp_all(wait_or_abort(empty0 + 8u * s, ph ^ 1u, s_abort));
@@ -194,6 +207,7 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
         // ---- MMA issuer (pairs: the leader's, for both SMs) ----------------
         int g = 0, tl = 0;
         bool issued = false, ok = true;
+        uint32_t fixed_parity = 0u;   // per stage: the phase its next ragged slice completes
         for (int64_t u = first; u < total && ok && !*s_abort; u += step) {
             const WUnit w = wgrad_unit(s_cnt, nmb, nnb, u);
             if (w.k_iters == 0) continue;
@@ -203,9 +217,16 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
             if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
-            for (int k = 0; k < w.k_iters; ++k, ++g) {
-                const int s = g % STAGES;
-                ok = warp_all(wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort));
+            const bool ragged = ragged_rows(w.rows) != 0;
+            const int last_at = ragged_at(w);
+            for (int k = 0; k < w.k_iters; ++k) {
+                const int at = g + (k < last_at ? k : k < w.k_iters - 1 ? k + 1 : last_at);
+                const int s = at % STAGES;
+                ok = warp_all(wait_or_abort(full0 + 8u * s, (uint32_t)((at / STAGES) & 1), s_abort));
+                if (ok && ragged && k == w.k_iters - 1) {
+                    ok = warp_all(wait_or_abort<PAIR>(fixed0 + 8u * s, (fixed_parity >> s) & 1u, s_abort));
+                    fixed_parity ^= 1u << s;
+                }
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = tiles_u32 + (uint32_t)s * C::kStageBytes;
@@ -225,6 +246,7 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
                 __syncwarp();
                 issued = true;
             }
+            g += w.k_iters;
         }
         if (issued) {
             if (elect_one()) umma_commit_local<PAIR>(drain);
@@ -302,10 +324,10 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
         uint32_t parity = 0u;   // per stage: the phase its next ragged slice completes
         for (int64_t u = first; u < total && !*s_abort; u += step) {
             const WUnit w = wgrad_unit(s_cnt, nmb, nnb, u);
-            g += w.k_iters;
             const int valid = ragged_rows(w.rows);
+            const int s = (g + ragged_at(w)) % STAGES;
+            g += w.k_iters;
             if (valid == 0) continue;
-            const int s = (g - 1) % STAGES;
             const uint32_t par = (parity >> s) & 1u;
             parity ^= 1u << s;
             if (!warp_all(wait_or_abort(landed0 + 8u * s, par, s_abort))) break;
@@ -320,11 +342,10 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
             }
             fence_proxy_async();   // the MMAs read shared memory through the async proxy
             __syncwarp();
-            if (PAIR && !leader) {
-                if (lane == 0) mbar_arrive_cluster(lead_peer0 + 8u * s);
-            } else {
-                if (PAIR && !warp_all(wait_or_abort_cluster(peer0 + 8u * s, par, s_abort))) break;
-                if (lane == 0) mbar_arrive(full0 + 8u * s);
+            if (lane == 0) {
+                if (leader) mbar_arrive(full0 + 8u * s);   // its phase passes without copies
+                if (PAIR) mbar_arrive_cluster(lead_fixed0 + 8u * s);
+                else mbar_arrive(fixed0 + 8u * s);
             }
         }
     }

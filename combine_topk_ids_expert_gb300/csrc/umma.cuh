@@ -236,14 +236,31 @@ __device__ __forceinline__ int cluster_count()
     return (int)r;
 }
 
+// CLUSTER: with what the other CTAs of the cluster wrote before they arrived.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_try_wait_scope(uint32_t bar, uint32_t parity)
+{
+    if (!CLUSTER) return mbar_try_wait(bar, parity);
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0u;
+}
+
 // Bounded wait that also gives up when another role has aborted.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort)
 {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_scope<CLUSTER>(bar, parity)) return true;
     const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
     while (true) {
         for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (mbar_try_wait_scope<CLUSTER>(bar, parity)) return true;
         if (*abort) return false;
         if (globaltimer_ns() > deadline) {
             *abort = 1;
@@ -371,15 +388,6 @@ __device__ __forceinline__ void as_floats(const uint32_t (&q)[32], float (&v)[32
 // follows its waits are warp-wide instructions).
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
 
-// As wait_or_abort, with what other CTAs of the cluster wrote before their arrivals.
-__device__ __forceinline__ bool wait_or_abort_cluster(uint32_t bar, uint32_t parity,
-                                                      volatile int* abort)
-{
-    const bool done = wait_or_abort(bar, parity, abort);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return done;
-}
-
 // Index e with pre[e] <= i < pre[e+1] of a non-decreasing prefix (i < pre[E]).
 __device__ __forceinline__ int expert_of(const int* pre, int E, int i)
 {
@@ -409,7 +417,7 @@ __device__ __forceinline__ bool elect_one()
 // Shared-memory writes of this thread, before the async proxy (an MMA) reads them.
 __device__ __forceinline__ void fence_proxy_async()
 {
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
