@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
+from functools import cached_property
 
 import torch
 
@@ -66,9 +67,16 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: 0.2 against 3 us, of
+# calls that take about 10.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -237,7 +245,7 @@ def ep_expert_gemm_backward(handle, grad_y: torch.Tensor, x_recv: torch.Tensor |
           "ep_expert_gemm_backward")
 
 
-@dataclass
+@dataclass(frozen=True)
 class W4:
     """The experts' 4-bit weights [E, rows, din] with group scales: w = (code - zero) * scale.
     A group is din / scales.shape[-1] consecutive elements: 32, 64 or 128."""
@@ -259,19 +267,21 @@ class W4:
             if z.shape != s.shape:
                 raise ValueError(f"zeros must be shaped as scales, got {tuple(z.shape)}")
 
-    @property
+    @cached_property
     def din(self) -> int:
         return 2 * self.codes.shape[2]
 
-    @property
+    @cached_property
     def rows(self) -> int:
         return self.codes.shape[1]
 
-    @property
+    @cached_property
     def group(self) -> int:
         return self.din // self.scales.shape[2]
 
+    @cached_property
     def _struct(self) -> EpW4:
+        """The C struct: this object's own fields, which cannot be set again."""
         return EpW4(_ptr(self.codes), _ptr(self.scales), _ptr(self.zeros),
                     _TORCH_TO_EP[self.scales.dtype], self.group)
 
@@ -280,7 +290,7 @@ def ep_expert_gemv_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dout:
                       y_recv: torch.Tensor, stream=None) -> None:
     for name, t in (("x_recv", x_recv), ("y_recv", y_recv)):
         _check_dtype(t, torch.bfloat16, name)
-    check(_abi.lib().ep_expert_gemv_w4(handle, _ptr(x_recv), C.byref(weights._struct()), din, dout,
+    check(_abi.lib().ep_expert_gemv_w4(handle, _ptr(x_recv), C.byref(weights._struct), din, dout,
                                        _ptr(y_recv), _stream(stream)), "ep_expert_gemv_w4")
 
 
@@ -288,7 +298,7 @@ def ep_expert_glu_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dff: i
                      h: torch.Tensor, stream=None) -> None:
     for name, t in (("x_recv", x_recv), ("h", h)):
         _check_dtype(t, torch.bfloat16, name)
-    check(_abi.lib().ep_expert_glu_w4(handle, _ptr(x_recv), C.byref(weights._struct()), din, dff,
+    check(_abi.lib().ep_expert_glu_w4(handle, _ptr(x_recv), C.byref(weights._struct), din, dff,
                                       act, _ptr(h), _stream(stream)), "ep_expert_glu_w4")
 
 
@@ -651,12 +661,15 @@ class Buffer:
     def _out_rows(self, t: torch.Tensor | None, name: str, width: int) -> torch.Tensor:
         return self._new_rows(width) if t is None else self._rows(t, name, width)
 
-    def _weights(self, w: torch.Tensor, name: str, *shape: int | None) -> torch.Size:
-        want = (self.E, *shape)
-        if w.dim() != len(want) or any(n is not None and n != m for n, m in zip(want, w.shape)):
-            raise ValueError(f"{name} must be {['any' if n is None else n for n in want]}, "
-                             f"got {list(w.shape)}")
-        return w.shape
+    def _weights(self, w: torch.Tensor, name: str, rows: int | None,
+                 cols: int | None) -> tuple[int, int]:
+        """(rows, columns) of w, checked to be [E, rows, cols] (None: any number)."""
+        shape = tuple(w.shape)
+        if len(shape) != 3 or shape[0] != self.E or (rows is not None and rows != shape[1]) \
+                or (cols is not None and cols != shape[2]):
+            want = [self.E, *("any" if n is None else n for n in (rows, cols))]
+            raise ValueError(f"{name} must be {want}, got {list(shape)}")
+        return shape[1], shape[2]
 
     @staticmethod
     def _activation(act: str) -> int:
@@ -670,7 +683,7 @@ class Buffer:
         """h = act(x Wg^T) * (x Wu^T) over each expert's receive rows, one kernel.
         w_gate_up is [E, 2 dff, din], gate rows first. gate_up, if given, receives the
         pre-activations for the backward pass. Returns h in the receive layout."""
-        _, dff2, din = self._weights(w_gate_up, "w_gate_up", None, None)
+        dff2, din = self._weights(w_gate_up, "w_gate_up", None, None)
         if dff2 % 2:
             raise ValueError(f"w_gate_up must hold gate and up rows, got {dff2} rows")
         dff = dff2 // 2
@@ -687,7 +700,7 @@ class Buffer:
         """The experts' gated feed-forward block, y = (act(x Wg^T) * (x Wu^T)) Wd^T, with
         w_gate_up [E, 2 dff, din] (gate rows first) and w_down [E, dout, dff]: two kernels,
         ready for combine. save=True returns (y, h, gate_up), what expert_ffn_backward needs."""
-        _, dff2, _ = self._weights(w_gate_up, "w_gate_up", None, None)
+        dff2, _ = self._weights(w_gate_up, "w_gate_up", None, None)
         self._weights(w_down, "w_down", None, dff2 // 2)
         gate_up = self._new_rows(dff2) if save else None
         h = self._new_rows(dff2 // 2) if save else self._scratch_rows(dff2 // 2, stream)
@@ -705,7 +718,7 @@ class Buffer:
         adds to it (gradient accumulation over micro-batches)."""
         dout = grad_y.shape[-1]
         if want_x:
-            din = self._weights(weights, "weights", dout, None)[2]
+            _, din = self._weights(weights, "weights", dout, None)
         else:
             din = x_recv.shape[-1]
         self._rows(grad_y, "grad_y", dout)
@@ -730,7 +743,7 @@ class Buffer:
                             stream=None) -> torch.Tensor:
         """The gradient of the pre-activations [.., 2 dff] from the gradient of y, through
         w_down [E, dout, dff] and the activation, one kernel."""
-        _, dout, dff = self._weights(w_down, "w_down", None, None)
+        dout, dff = self._weights(w_down, "w_down", None, None)
         self._rows(grad_y, "grad_y", dout)
         self._rows(gate_up, "gate_up", 2 * dff)
         grad_gate_up = self._out_rows(grad_gate_up, "grad_gate_up", 2 * dff)

@@ -814,9 +814,9 @@ static ep::GemmArgs expert_args(ep_buffer* b, int64_t contraction, int64_t colum
     a.din = contraction;
     a.dout = columns;
     a.E = b->cfg.num_experts;
-    a.kind = b->gemm_kind > 0
-                 ? b->gemm_kind
-                 : (b->last_T * b->cfg.topk >= (int64_t)512 * b->cfg.num_experts ? 2 : 1);
+    a.kind = b->gemm_kind;
+    a.row_tiles = std::max<int64_t>(std::min<int64_t>(a.E, b->last_T * b->cfg.topk),
+                                    b->last_T * b->cfg.topk / 128);
     a.bk = 64;
     a.light_rows = b->gemm_light_rows;
     a.err = b->err;

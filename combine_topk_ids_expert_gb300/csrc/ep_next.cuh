@@ -56,6 +56,7 @@ struct GemmArgs {
     void* aux = nullptr;           // the gated block: [rows][2 dout] bf16 pre-activations, written
                                    // (forward; null: not kept) or read (gradient)
     int act = 0;                   // the gated block: 0 silu, 1 gelu (tanh form)
+    int64_t row_tiles = 0;         // row tiles that the call is likely to have (kind 0)
 };
 // x: [rows][din] bf16 receive rows; w: [E][dout][din] bf16.
 // kernel_used: the kind that ran (see GemmArgs::kind); grid_used: its CTAs.

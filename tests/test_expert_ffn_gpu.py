@@ -109,9 +109,10 @@ CASES = {
 }
 
 
-@pytest.fixture(params=["1", "2"])
+@pytest.fixture(params=["0", "1", "2"])
 def kind(request, monkeypatch):
-    """Tiles of 128 rows on one SM, and of 256 on an SM pair where the sizes allow."""
+    """Tiles as the sizes choose them, of 128 rows on one SM, and of 256 on an SM pair where
+    the sizes allow."""
     monkeypatch.setenv("EP_GEMM_KERNEL", request.param)
     return request.param
 
