@@ -145,6 +145,32 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
                  : "r"(addr));
 }
 
+// Two fp32 values in one register pair, and their products and fmas, one instruction
+// for both.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi)
+{
+    return ((uint64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi)
+{
+    return pair_of(__float_as_uint(lo), __float_as_uint(hi));
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // {lo, hi} as two e4m3 bytes (round to nearest even, saturating), and back.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
 {
@@ -818,9 +844,9 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                 b += t.blocks;
                 const bool warp_live = w4_lane(a, t, wrows, r).warp_live;
                 begin(t);
-                float acc[NR];
+                uint64_t acc[NR / 2];   // rows 2n and 2n + 1
 #pragma unroll
-                for (int n = 0; n < NR; ++n) acc[n] = 0.0f;
+                for (int n = 0; n < NR / 2; ++n) acc[n] = 0ull;
 #pragma unroll 1
                 for (int k0 = 0; k0 < slices && ok; k0 += per_panel) {
                     ok = need_x(t, k0);
@@ -864,20 +890,20 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                 for (int u = 0; u < C::PG; ++u) {
                                     const int gi = g0 + p0 + u;
                                     const float2 s = sc[gi * 128];
-                                    const float4* xs = reinterpret_cast<const float4*>(sums + gi * NR);
-                                    const float4* un =
-                                        reinterpret_cast<const float4*>(undo + gi * C::GROUP / 128 * NR);
+                                    const ulonglong2* xs =
+                                        reinterpret_cast<const ulonglong2*>(sums + gi * NR);
+                                    const ulonglong2* un =
+                                        reinterpret_cast<const ulonglong2*>(undo + gi * C::GROUP / 128 * NR);
+                                    const uint64_t sx = pair_of(s.x, s.x), sy = pair_of(s.y, s.y);
 #pragma unroll
                                     for (int n4 = 0; n4 < NR / 4; ++n4) {
-                                        const float4 x4 = xs[n4], u4 = un[n4];
-                                        const float xv[4] = {x4.x, x4.y, x4.z, x4.w};
-                                        const float uv[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            float& sum = acc[4 * n4 + i];
-                                            sum = fmaf(s.x * uv[i], __uint_as_float(q[u * NR + 4 * n4 + i]),
-                                                       fmaf(s.y, xv[i], sum));
-                                        }
+                                        const ulonglong2 x4 = xs[n4], u4 = un[n4];
+                                        const uint32_t* v = q + u * NR + 4 * n4;
+                                        uint64_t* sum = acc + 2 * n4;
+                                        sum[0] = fma2(mul2(sx, u4.x), pair_of(v[0], v[1]),
+                                                      fma2(sy, x4.x, sum[0]));
+                                        sum[1] = fma2(mul2(sx, u4.y), pair_of(v[2], v[3]),
+                                                      fma2(sy, x4.y, sum[1]));
                                     }
                                 }
                             }
@@ -887,24 +913,28 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                 }
                 if (!ok) break;
                 const W4Lane l = w4_lane(a, t, wrows, r);
+                float out[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    out[n] = __uint_as_float((uint32_t)(acc[n / 2] >> (32 * (n & 1))));
                 for (int n = 0; n < t.rows; ++n)
                     if (s_odd0[half * NR + n] && l.live) {
                         const float terms = w4_odd_terms(a, t.row0 + n, l.wrow, groups);
 #pragma unroll
                         for (int m = 0; m < NR; ++m)
-                            if (m == n) acc[m] += terms;
+                            if (m == n) out[m] += terms;
                     }
                 if (a.glu) {
                     float* swap = s_swap + (r & 63) * (NR + 1);
                     if (r >= 64)
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) swap[n] = acc[n];
+                        for (int n = 0; n < NR; ++n) swap[n] = out[n];
                     ok = swap_sync(lane);
                     if (!ok) break;
                     if (r < 64)
 #pragma unroll
                         for (int n = 0; n < NR; ++n)
-                            if (n < t.rows) acc[n] = act_value(acc[n], a.act) * swap[n];
+                            if (n < t.rows) out[n] = act_value(out[n], a.act) * swap[n];
                     ok = swap_sync(lane);   // the swap area is free again
                     if (!ok) break;
                 }
@@ -912,7 +942,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                     uint16_t* y = static_cast<uint16_t*>(a.y) + (int64_t)t.row0 * a.dout + l.o;
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
-                        if (n < t.rows) y[n * a.dout] = (uint16_t)(pack_bf16x2_rn(acc[n], 0.0f) & 0xFFFFu);
+                        if (n < t.rows) y[n * a.dout] = (uint16_t)(pack_bf16x2_rn(out[n], 0.0f) & 0xFFFFu);
                 }
             }
         }
