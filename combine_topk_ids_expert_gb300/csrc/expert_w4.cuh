@@ -21,9 +21,9 @@
 //     codes as A (128 output columns on TMEM's lanes, written there by tcgen05.st
 //     without passing shared memory again) and the terms of at most NR rows as B, one
 //     after the other into the same accumulator. Each scale group has its own;
-//   - draining a group, a lane holds one output column: its scale enters as one fp32
-//     fma per row (with what undoes x's scale), its zero point as one more with the
-//     group's sum of x.
+//   - draining a group, a lane holds one output column: per row, its sum times the
+//     column's scale, the group's sum of x times minus scale and zero point, and an fma
+//     of the two by what undoes x's scale, two rows an instruction.
 //
 // Work: 16-column blocks of all (expert, chunk of NR rows), laid end to end and cut
 // into equal contiguous shares, one per CTA (one CTA per SM); a share is walked in
@@ -309,7 +309,7 @@ __device__ __forceinline__ int4 w4_finite(const int4& v)
 
 // Converts the tile's rows of x, contraction elements [k0, k0 + panel): two e4m3 terms
 // of each block of 128 elements, scaled, as B of the MMAs; what undoes the scale; and
-// the group sums. An infinity or a NaN counts as zero here and
+// the scaled groups' sums. An infinity or a NaN counts as zero here and
 // marks its row (its terms are added to the row's results one by one). Warps 2 and
 // up; ct: thread among them.
 //
@@ -360,9 +360,8 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
             float f[8], h[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float e = __uint_as_float(w4_element(w[i], j));
-                f[j] = e * scale;
-                sum += e;
+                f[j] = __uint_as_float(w4_element(w[i], j)) * scale;
+                sum += f[j];
             }
             // Bytes in the order of the unpacked codes: even elements, then odd ones.
 #pragma unroll
@@ -804,8 +803,6 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                             for (int i = 0; i < 8; ++i)
                                 lds128(base + (uint32_t)((i ^ (r & 7)) << 4), w[i]);
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(code_empty0 + 8u * c.slot);
                         ok = warp_all(wait_or_abort(a_empty0 + 8u * as.slot, as.phase ^ 1u, s_abort));
                         if (!ok) break;
                         tc_fence_after();
@@ -821,10 +818,14 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                 }
                                 tmem_st32(t_lane + kW4ABase + (uint32_t)(as.slot * 64 + h * 32), v);
                             }
-                            tmem_wait_st();
                         }
+                        if (warp_live) tmem_wait_st();
+                        // The slot is free once every lane has its codes: after the stores
+                        // that need them, not as soon as the loads are issued (the arrival
+                        // overtook them, and the next copy what they had yet to read).
                         tc_fence_before();
                         __syncwarp();
+                        if (lane == 0) mbar_arrive(code_empty0 + 8u * c.slot);
                         if (lane == 0) mbar_arrive(a_full0 + 8u * as.slot);
                     }
                 }
@@ -900,10 +901,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                         const ulonglong2 x4 = xs[n4], u4 = un[n4];
                                         const uint32_t* v = q + u * NR + 4 * n4;
                                         uint64_t* sum = acc + 2 * n4;
-                                        sum[0] = fma2(mul2(sx, u4.x), pair_of(v[0], v[1]),
-                                                      fma2(sy, x4.x, sum[0]));
-                                        sum[1] = fma2(mul2(sx, u4.y), pair_of(v[2], v[3]),
-                                                      fma2(sy, x4.y, sum[1]));
+                                        sum[0] = fma2(u4.x, fma2(sy, x4.x, mul2(sx, pair_of(v[0], v[1]))),
+                                                      sum[0]);
+                                        sum[1] = fma2(u4.y, fma2(sy, x4.y, mul2(sx, pair_of(v[2], v[3]))),
+                                                      sum[1]);
                                     }
                                 }
                             }

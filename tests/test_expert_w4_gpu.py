@@ -125,6 +125,61 @@ def test_ffn_is_its_parts_and_feeds_combine():
     c.done()
 
 
+def test_back_to_back_runs_agree():
+    # Long contractions over many experts, one call behind the other: the ring of codes
+    # turns over while conversions, copies and products of several tiles are in flight.
+    # Every run gives the bits of the first, and those are right.
+    c = Case(21, 32, 96, 8, 1, "uniform", "packed")
+    din, dout = 7168, 1024
+    w = [weights(c, dout, din, 128, False, "bf16") for _ in range(2)]
+    x = c.recv(din)
+    ref, m = products(c, x, dequantised(w[0]))
+    first = c.buf.expert_gemv_w4(x, w[0], c.out(dout))
+    c.check_rows(first, ref, 2.0 ** -8 * ref.abs() + sum_tol(din, m) + 1e-38)
+    del ref, m
+    runs = [c.buf.expert_gemv_w4(x, w[i % 2], c.out(dout)) for i in range(24)]
+    for i in range(0, 24, 2):
+        assert torch.equal(runs[i].view(torch.int16), first.view(torch.int16)), i
+        assert torch.equal(runs[i + 1].view(torch.int16), runs[1].view(torch.int16)), i
+    c.done()
+
+
+def test_long_contraction_in_parts():
+    # x of 8 rows does not fit in shared memory: it is converted part by part, for every
+    # tile again.
+    c = Case(22, 11, 3, 2, 1, "zipf")
+    for din, group in ((16384, 128), (11008, 32)):
+        x, w = c.recv(din), weights(c, 200, din, group, True, "bf16")
+        y = c.buf.expert_gemv_w4(x, w, c.out(200))
+        ref, m = products(c, x, dequantised(w))
+        c.check_rows(y, ref, 2.0 ** -8 * ref.abs() + sum_tol(din, m) + 1e-38)
+    c.done()
+
+
+def test_extreme_rows():
+    # Rows at both ends of bf16's range, and rows whose elements span it: an element far
+    # below its block's largest may be off by 2^-17 of that, or by 2^-136 (see the kernel),
+    # which the bound allows for each element.
+    c = Case(23, 6, 1, 1, 1)
+    din, dout = 512, 64
+    x, w = c.recv(din), weights(c, dout, din, 64, True, "f32")
+    x[0] = x[0].sign() * 2.0 ** 126
+    x[1] *= 2.0 ** -126
+    x[2] = 0.0
+    x[3] *= torch.exp2(torch.randint(-40, 40, (din,), generator=c.gen, device="cuda").float())
+    x[4, 7] = 3e4
+    y = c.buf.expert_gemv_w4(x, w, c.out(dout))
+    d = dequantised(w)
+    ref, m = products(c, x, d)
+    block = x.to(F64).abs().view(c.rows, -1, 128).amax(2).repeat_interleave(128, 1)
+    _, off = products(c, torch.nan_to_num(block).clamp(min=2.0 ** -119), d)
+    tol = 2.0 ** -8 * ref.abs() + sum_tol(din, m) + 2.0 ** -17 * off + 1e-38
+    got = y.to(F64)
+    assert bool((got[2] == 0.0).all())
+    c.check_rows(y, ref, tol)
+    c.done()
+
+
 def test_rows_do_not_depend_on_their_batch():
     # A row's result is the same whether it comes alone or among others.
     c = Case(30, 1, 1, 1, 1)
