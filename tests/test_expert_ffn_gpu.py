@@ -262,6 +262,26 @@ def test_gradients_against_differences(act):
     c.done()
 
 
+def test_back_to_back_runs_agree(kind):
+    # Forward and backward, call behind call: every run gives the bits of the first.
+    c = Case(71, 1500, 12, 4, 2, "zipf")
+    din, dff, dout = 1024, 768, 1024
+    x, wgu = c.recv(din), c.randn(c.E, 2 * dff, din, std=din ** -0.5)
+    wd, gy = c.randn(c.E, dout, dff, std=dff ** -0.5), c.recv(dout)
+
+    def run():
+        y, h, gu = c.buf.expert_ffn(x, wgu, wd, save=True)
+        gx, gwgu, gwd = c.buf.expert_ffn_backward(gy, x, wgu, wd, gu, h)
+        rows = [t.reshape(c.rows, -1)[c.used] for t in (y, h, gu, gx)]
+        return [t.view(torch.int16) for t in (*rows, gwgu, gwd)]
+
+    runs = [run() for _ in range(6)]
+    for r in runs[1:]:
+        for a, b in zip(runs[0], r):
+            assert torch.equal(a, b)
+    c.done()
+
+
 def test_no_rows_at_all():
     # num_tokens_per_rank 0: nothing is routed; the weights' gradient is zero.
     buf = ep.Buffer(8, 64, 4, 1, 2, dtype=torch.bfloat16)
