@@ -1,13 +1,14 @@
 // expert_w4.cuh - the products of each expert's few rows with 4-bit weights and
-// group scales, for decoding (expert_w4_8.cu, _16.cu and _32.cu instantiate it):
+// group scales, for decoding (expert_w4.cu, _16.cu and _32.cu instantiate it):
 //     y[p][o] = sum over groups G of s[e][o][G] * sum over i in G of (q[e][o][i] - z) x[p][i]
 // and the gated form h = act(g) * u over gate and up rows of the same matrix.
 //
 // What bounds it: the weights are read once for a handful of rows, half a byte
-// each, so the floor is HBM: at its rate an SM has about 350 cycles for 16 KB of
-// codes (32768 of them), under 1.4 instruction slots for 32 codes. Unpacking codes
-// into 16-bit operands (a shift, a mask and a subtraction for every two) costs
-// several times that; the kernel avoids it:
+// each, so the floor is HBM: at its rate an SM has about 725 cycles for 16 KB of
+// codes, 2900 issue slots for 32768 of them. Unpacking codes into 16-bit operands on
+// mma.sync (a shift, a mask and a subtraction for every two, then operands of x and
+// scales at 16 x 8 outputs a step) took 14300 instructions for as many: 502 us where
+// this kernel takes 200 (4 rows, 64 x 4096 x 7168 codes, groups of 128; 1500 now). So:
 //   - a nibble q, zero-extended to a byte, IS an fp8 number: read as e4m3 it is
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
@@ -25,15 +26,26 @@
 //     column's scale, the group's sum of x times minus scale and zero point, and an fma
 //     of the two by what undoes x's scale, two rows an instruction.
 //
-// Work: 16-column blocks of all (expert, chunk of NR rows), laid end to end and cut
-// into equal contiguous shares, one per CTA (one CTA per SM); a share is walked in
-// tiles of at most 128 columns (gated: 64 gate and 64 up). x is converted when the
-// expert or chunk changes and stays in shared memory for the tiles that follow; the
-// copies of the codes run ahead over tile boundaries all the while.
+// Work: tiles of 128 columns (gated: 64 gate and 64 up) of all (expert, chunk of NR
+// rows), laid end to end and cut into contiguous shares, one per CTA (one CTA per SM).
+// Equal shares of 16-column blocks instead left tiles cut at both ends, which take as long
+// as whole ones wherever draining a slice takes longer than copying it: 66 against 57 us
+// (16 rows, 8 x 4096 x 4096 codes, groups of 64), and 203 against 197 us (4 rows, 64 x
+// 4096 x 7168, groups of 128). x is converted when the expert or the chunk changes and
+// stays in shared memory for the tiles that follow; the copies of the codes run ahead
+// over tile boundaries all the while.
 //
-// Roles (14 warps): 0 copies codes (TMA, 256-code slices of 16 columns per box, 128-
-// byte swizzle), 1 issues the MMAs, 2-9 move codes to TMEM (two sets, alternate
-// slices), 10-13 drain; 2-13 convert x together. Every wait is bounded.
+// Measured (a graph of calls on three sets of weights, one GB300): 200 us, 4.8 TB/s or
+// 72% of a copy's rate (the same 64 x 4096 x 7168 codes); 31 us, 3.9 TB/s (8 experts of
+// these, one row each); 57 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
+// where draining the scale groups is what takes long. The copies and barriers alone
+// take 164 of the 200 us, so the rest is the roles' latencies: each scheduler has one
+// warp that unpacks and one that drains.
+//
+// Roles (10 warps): 0 copies codes (TMA, slices of 256 codes of 64 columns a box, 128-byte
+// swizzle), 1 issues the MMAs, 2-5 move codes to TMEM, 6-9 drain; 2-9 convert x
+// together. With 14 warps (a second set of either) a thread has 128 registers instead of
+// 168 and the drain spills: 82 against 67 us. Every wait is bounded.
 #pragma once
 
 #include "umma.cuh"
@@ -57,10 +69,7 @@ template <int NR_, int GROUP_>
 struct W4Cfg {
     static constexpr int NR = NR_, GROUP = GROUP_;
     static constexpr int N = NR < 16 ? 16 : NR;              // of the MMA (M = 128 wants 16)
-    // Sets of four warps that move codes to TMEM, alternate slices. Two need 14 warps,
-    // which leaves 128 registers to a thread: enough while a lane drains few rows.
-    static constexpr int kSets = 1;
-    static constexpr int kConvThreads = 128 * (kSets + 1);
+    static constexpr int kConvThreads = 256;   // warps 2 and up: four unpack, four drain
     static constexpr int kThreads = 64 + kConvThreads;
     static constexpr int GPS = kW4Slice / GROUP;             // scale groups of a slice
     static constexpr int GB = GPS < 128 / N ? GPS : 128 / N;             // groups per accumulator slot
@@ -209,24 +218,29 @@ struct W4Tile {
     int e, chunk, row0, rows, col0, blocks;
 };
 
+// How the columns of an expert are cut: nb blocks, `most` to a tile, `tiles` of these.
+struct W4Cut {
+    int nb, most, tiles;
+};
+
 struct W4Tables {
-    const int* pre;   // [E + 1] blocks of the experts before each
+    const int* pre;   // [E + 1] tiles of the experts before each
     const int* cnt;   // [E]
     const int* off;   // [E]
 };
 
 template <class C>
-__device__ __forceinline__ W4Tile w4_tile(const W4Tables& t, int E, int nb, int most, int b, int end)
+__device__ __forceinline__ W4Tile w4_tile(const W4Tables& t, int E, const W4Cut& cut, int b)
 {
     W4Tile w;
     w.e = expert_of(t.pre, E, b);
     const int local = b - t.pre[w.e];
-    w.chunk = local / nb;
-    const int blk = local - w.chunk * nb;
+    w.chunk = local / cut.tiles;
+    const int blk = (local - w.chunk * cut.tiles) * cut.most;
     w.col0 = blk * kW4Block;
     w.row0 = t.off[w.e] + w.chunk * C::NR;
     w.rows = min(C::NR, t.cnt[w.e] - w.chunk * C::NR);
-    w.blocks = min(min(most, nb - blk), end - b);
+    w.blocks = min(cut.most, cut.nb - blk);
     return w;
 }
 
@@ -570,8 +584,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
     int* s_off = s_cnt + E;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nb = (int)((a.dout + kW4Block - 1) / kW4Block);
-    const int most = a.glu ? 4 : 8;
+    W4Cut cut;
+    cut.nb = (int)((a.dout + kW4Block - 1) / kW4Block);
+    cut.most = a.glu ? 4 : 8;
+    cut.tiles = (cut.nb + cut.most - 1) / cut.most;
     const int slices = (int)((a.din + kW4Slice - 1) / kW4Slice);
     const int per_panel = panel / kW4Slice;
     const int64_t wrows = a.glu ? 2 * a.dout : a.dout;   // weight rows of an expert
@@ -603,14 +619,14 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
     }
     griddep_wait();   // counts, offsets and the rows come from earlier kernels
 
-    // Blocks before each expert: thread t takes experts [t c, t c + c).
+    // Tiles before each expert: thread t takes experts [t c, t c + c).
     {
         const int c = (E + C::kThreads - 1) / C::kThreads, e0 = (int)threadIdx.x * c;
         int own = 0;
         for (int e = e0; e < min(E, e0 + c); ++e) {
             s_cnt[e] = __ldcg(a.cnt + e);
             s_off[e] = __ldcg(a.expert_offset + e);
-            own += (s_cnt[e] + NR - 1) / NR * nb;
+            own += (s_cnt[e] + NR - 1) / NR * cut.tiles;
         }
         int incl = own;
 #pragma unroll
@@ -624,7 +640,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         for (int w = 0; w < warp; ++w) at += s_warp[w];
         for (int e = e0; e < min(E, e0 + c); ++e) {
             s_pre[e] = at;
-            at += (s_cnt[e] + NR - 1) / NR * nb;
+            at += (s_cnt[e] + NR - 1) / NR * cut.tiles;
         }
         if (threadIdx.x == C::kThreads - 1) s_pre[E] = at;
     }
@@ -643,11 +659,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         int issued = 0;
         bool ok = true;
         for (int b = first; b < last && ok;) {
-            const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
-            b += t.blocks;
+            const W4Tile t = w4_tile<C>(tab, E, cut, b);
+            ++b;
             const int row = (int)(t.e * wrows) + t.col0;
             const int row2 = a.glu ? row + (int)a.dout : row + 64;   // of the tile's second half
-            const bool whole = t.blocks == most;
+            const bool whole = t.blocks == cut.most;
             if (elect_one())
                 for (int half = 0; half < (a.glu ? 2 : 1); ++half)
                     w4_prefetch_scales(a, (int64_t)row + half * a.dout,
@@ -690,8 +706,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         bool issued = false, ok = true;
         const uint64_t x_desc = smem_desc_k128(smem_u32(s_x));
         for (int b = first; b < last && ok;) {
-            const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
-            b += t.blocks;
+            const W4Tile t = w4_tile<C>(tab, E, cut, b);
+            ++b;
             const bool new_rows = t.e != e_have || t.chunk != chunk_have;
             e_have = t.e;
             chunk_have = t.chunk;
@@ -748,7 +764,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;                // output column of the tile / TMEM lane
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-        const bool drains = warp >= 2 + 4 * C::kSets;
+        const bool drains = warp >= 6;
         const int groups = (int)(a.din / C::GROUP);
         const bool wide = groups % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0u &&
                           (reinterpret_cast<uintptr_t>(a.zeros) & 7u) == 0u;
@@ -776,13 +792,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         };
         if (!drains) {
             // ---- codes to TMEM ----------------------------------------------------
-            const int set = (warp - 2) >> 2;
             W4Ring c, as;
-            int g = 0;   // slices seen
 #pragma unroll 1
             for (int b = first; b < last && ok;) {
-                const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
-                b += t.blocks;
+                const W4Tile t = w4_tile<C>(tab, E, cut, b);
+                ++b;
                 const bool warp_live = w4_lane(a, t, wrows, r).warp_live;
                 begin(t);
 #pragma unroll 1
@@ -791,8 +805,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                     if (!ok) break;
                     const int k1 = min(slices, k0 + per_panel);
 #pragma unroll 1
-                    for (int k = k0; k < k1; ++k, ++g, c.next(stages), as.next(kW4ASlots)) {
-                        if (C::kSets > 1 && (g & 1) != set) continue;
+                    for (int k = k0; k < k1; ++k, c.next(stages), as.next(kW4ASlots)) {
                         ok = warp_all(wait_or_abort(code_full0 + 8u * c.slot, c.phase, s_abort));
                         if (!ok) break;
                         uint32_t w[8][4];
@@ -838,11 +851,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
             auto load_scales = [&](const W4Tile& t, int k) {
                 w4_load_scales(a, w4_lane(a, t, wrows, r), groups, wide, k * C::GPS, next);
             };
-            if (first < last) load_scales(w4_tile<C>(tab, E, nb, most, first, last), 0);
+            if (first < last) load_scales(w4_tile<C>(tab, E, cut, first), 0);
 #pragma unroll 1
             for (int b = first; b < last && ok;) {
-                const W4Tile t = w4_tile<C>(tab, E, nb, most, b, last);
-                b += t.blocks;
+                const W4Tile t = w4_tile<C>(tab, E, cut, b);
+                ++b;
                 const bool warp_live = w4_lane(a, t, wrows, r).warp_live;
                 begin(t);
                 uint64_t acc[NR / 2];   // rows 2n and 2n + 1
@@ -860,7 +873,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                             // over the tile's end too.
                             w4_keep_scales(next, a.scale_f32, wide, mine);
                             if (k + C::SPB < slices) load_scales(t, k + C::SPB);
-                            else if (b < last) load_scales(w4_tile<C>(tab, E, nb, most, b, last), 0);
+                            else if (b < last) load_scales(w4_tile<C>(tab, E, cut, b), 0);
                         }
                         const float2* sc = mine + (k & (C::SPB - 1)) * C::GPS * 128;
                         const float* sums = s_xsum + (k - k0) * (C::GPS * NR);
