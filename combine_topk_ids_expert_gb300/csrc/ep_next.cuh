@@ -112,7 +112,6 @@ struct W4Args {
 cudaError_t launch_expert_w4(const W4Args& a, int64_t expected_rows, int num_sms,
                              const LaunchOpts& o);
 cudaError_t launch_expert_w4_16(const W4Args& a, int num_sms, const LaunchOpts& o);
-cudaError_t launch_expert_w4_32(const W4Args& a, int num_sms, const LaunchOpts& o);
 
 // Sentinel checks of the receive buffer (debug.cu, EP_DEBUG=1).
 constexpr uint32_t kErrDebugUnwritten = 0x8u;   // a row inside a rank's total kept the sentinel

@@ -1,5 +1,5 @@
 // expert_w4.cuh - the products of each expert's few rows with 4-bit weights and
-// group scales, for decoding (expert_w4.cu, _16.cu and _32.cu instantiate it):
+// group scales, for decoding (expert_w4.cu and expert_w4_16.cu instantiate it):
 //     y[p][o] = sum over groups G of s[e][o][G] * sum over i in G of (q[e][o][i] - z) x[p][i]
 // and the gated form h = act(g) * u over gate and up rows of the same matrix.
 //
@@ -7,8 +7,8 @@
 // each, so the floor is HBM: at its rate an SM has about 725 cycles for 16 KB of
 // codes, 2900 issue slots for 32768 of them. Unpacking codes into 16-bit operands on
 // mma.sync (a shift, a mask and a subtraction for every two, then operands of x and
-// scales at 16 x 8 outputs a step) took 14300 instructions for as many: 502 us where
-// this kernel takes 200 (4 rows, 64 x 4096 x 7168 codes, groups of 128; 1500 now). So:
+// scales at 16 x 8 outputs a step) took 3600 instructions for as many, and 328 us where
+// this kernel takes 200 and 1500 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
 //   - a nibble q, zero-extended to a byte, IS an fp8 number: read as e4m3 it is
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
@@ -82,7 +82,7 @@ struct W4Cfg {
     static constexpr uint32_t kPanelBytes = 2 * kTermBytes;  // hi rows, then lo rows
     static constexpr int PG = GB < 32 / NR ? GB : 32 / NR;   // groups that a lane drains at once
     static constexpr int kSwap = 64 * (NR + 1) * 4;          // gated: up sums on their way to gate lanes
-    static_assert(GPS % GB == 0 && GB % PG == 0 && NR <= 32 && DSLOTS <= kW4MaxDSlots, "slots");
+    static_assert(GPS % GB == 0 && GB % PG == 0 && NR <= 16 && DSLOTS <= kW4MaxDSlots, "slots");
 };
 
 // Shared memory: the ring, x, its group sums, the swap area, barriers, row state, tables.
