@@ -25,10 +25,12 @@ cudaError_t launch_mode(const GemmArgs& a, const void* x, int64_t rows, const vo
 }
 
 // Widest accumulator whose tiles occupy half of the SMs: 256 columns on an SM pair (two
-// SMs to a tile), else 128, else 64 (`least`: the narrowest that the mode has). A pair's last rows of an expert are M = 128 tiles of 64 rows to an SM, so
-// pairs win even where experts are small: 3.80 against 4.21 ms (gated projections, 65536
-// rows over 256 experts, 7168 -> 2 x 2048), while narrow tiles
-// win where few tiles are: 10.1 against 12.7 us (75 rows to each of 16 experts, 1024 -> 512). kind 1 or 2 asks for single SMs or pairs.
+// SMs to a tile), else 128, else 64 (`least`: the narrowest that the mode has). A pair's
+// last rows of an expert are M = 128 tiles of 64 rows to an SM, so pairs win even where
+// experts are small: 3.80 against 4.21 ms (gated projections, 65536 rows over 256
+// experts, 7168 -> 2 x 2048), while narrow tiles win where few tiles are: 10.1 against
+// 12.7 us (75 rows to each of 16 experts, 1024 -> 512). kind 1 or 2 asks for single SMs
+// or pairs.
 int accumulator_columns(const GemmArgs& a, int per_column, int sms, int least)
 {
     const int64_t cols = a.dout * per_column;   // accumulator columns

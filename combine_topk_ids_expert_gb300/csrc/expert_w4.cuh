@@ -23,8 +23,9 @@
 //     without passing shared memory again) and the terms of at most NR rows as B, one
 //     after the other into the same accumulator. Each scale group has its own;
 //   - draining a group, a lane holds one output column: per row, its sum times the
-//     column's scale, the group's sum of x times minus scale and zero point, and an fma
-//     of the two by what undoes x's scale, two rows an instruction.
+//     column's scale, the group's sum of x times minus scale and zero point, for the
+//     groups of a block of x together, and an fma by what undoes the block's scale, two
+//     rows an instruction.
 //
 // Work: tiles of 128 columns (gated: 64 gate and 64 up) of all (expert, chunk of NR
 // rows), laid end to end and cut into contiguous shares, one per CTA (one CTA per SM).
@@ -35,17 +36,20 @@
 // stays in shared memory for the tiles that follow; the copies of the codes run ahead
 // over tile boundaries all the while.
 //
-// Measured (a graph of calls on three sets of weights, one GB300): 200 us, 4.8 TB/s or
-// 72% of a copy's rate (the same 64 x 4096 x 7168 codes); 31 us, 3.9 TB/s (8 experts of
-// these, one row each); 57 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
-// where draining the scale groups is what takes long. The copies and barriers alone
-// take 164 of the 200 us, so the rest is the roles' latencies: each scheduler has one
-// warp that unpacks and one that drains.
+// Measured (a graph of calls on three sets of weights, one GB300): 197 us, 4.9 TB/s or
+// 73% of a copy's rate (the same 64 x 4096 x 7168 codes); 31 us, 3.9 TB/s (8 experts of
+// these, one row each); 51 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
+// where converting x and draining the scale groups are what takes long. Copies, barriers
+// and MMAs alone took 181 us where all took 210; the rest is the roles' latencies: each
+// scheduler has one warp that unpacks and one that drains.
 //
 // Roles (10 warps): 0 copies codes (TMA, slices of 256 codes of 64 columns a box, 128-byte
 // swizzle), 1 issues the MMAs, 2-5 move codes to TMEM, 6-9 drain; 2-9 convert x
 // together. With 14 warps (a second set of either) a thread has 128 registers instead of
-// 168 and the drain spills: 82 against 67 us. Every wait is bounded.
+// 168 and the drain spills: 82 against 67 us. (With shared memory full, what spills goes
+// to L2: unpacking half a slice at a time, which takes fewer registers, 52 -> 51 us, and
+// reading the next accumulators ahead, which takes more, 52 -> 73 us.) Every wait is
+// bounded.
 #pragma once
 
 #include "umma.cuh"
@@ -81,6 +85,7 @@ struct W4Cfg {
     static constexpr uint32_t kTermBytes = NR * 128;         // a term of 128 contraction elements
     static constexpr uint32_t kPanelBytes = 2 * kTermBytes;  // hi rows, then lo rows
     static constexpr int PG = GB < 32 / NR ? GB : 32 / NR;   // groups that a lane drains at once
+    static constexpr int SB = PG < 128 / GROUP ? PG : 128 / GROUP;   // of these, in one block of x
     static constexpr int kSwap = 64 * (NR + 1) * 4;          // gated: up sums on their way to gate lanes
     static_assert(GPS % GB == 0 && GB % PG == 0 && NR <= 16 && DSLOTS <= kW4MaxDSlots, "slots");
 };
@@ -123,7 +128,7 @@ __device__ __forceinline__ void tmem_wait_st()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// COLS (8, 16 or 32) accumulator columns of this lane.
+// COLS (8 or 16) accumulator columns of this lane.
 template <int COLS>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v)
 {
@@ -134,17 +139,13 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v)
               "=r"(v[7])
             : "r"(taddr));
     else
-#pragma unroll
-        for (int h = 0; h < COLS / 16; ++h)
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                : "=r"(v[16 * h + 0]), "=r"(v[16 * h + 1]), "=r"(v[16 * h + 2]), "=r"(v[16 * h + 3]),
-                  "=r"(v[16 * h + 4]), "=r"(v[16 * h + 5]), "=r"(v[16 * h + 6]), "=r"(v[16 * h + 7]),
-                  "=r"(v[16 * h + 8]), "=r"(v[16 * h + 9]), "=r"(v[16 * h + 10]),
-                  "=r"(v[16 * h + 11]), "=r"(v[16 * h + 12]), "=r"(v[16 * h + 13]),
-                  "=r"(v[16 * h + 14]), "=r"(v[16 * h + 15])
-                : "r"(taddr + 16u * h));
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+              "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+              "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(taddr));
 }
 
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
@@ -180,21 +181,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
-// {lo, hi} as two e4m3 bytes (round to nearest even, saturating), and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
-__device__ __forceinline__ void from_e4m3x2(uint32_t v, float* lo, float* hi)
+// The two e4m3 terms (round to nearest even) of two fp32 values below 256 that are
+// bf16 numbers times a power of two: by way of f16, which holds 2^-17 and above exactly
+// (what is smaller has zeros as its terms either way) and the first term's difference too.
+__device__ __forceinline__ void w4_terms(uint64_t v, uint32_t* hi, uint32_t* lo)
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(*lo), "=f"(*hi)
-        : "r"(h));
+    uint32_t f, b, d;
+    uint16_t h, l;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f)
+        : "f"(__uint_as_float((uint32_t)(v >> 32))), "f"(__uint_as_float((uint32_t)v)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(f));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(f), "r"(b));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
+    *hi = h;
+    *lo = l;
 }
 
 // A barrier among some warps of the CTA that gives up on an abort: each warp arrives
@@ -337,13 +345,13 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
     // A lane takes 32 elements at a time, four lanes a block of 128.
     const int per_row = panel / 32, total = rows * per_row;
     float* s_undo = s_xsum + panel / C::GROUP * C::NR;
-    int4 w[4];
+    int4 w[4], ahead[4];
     auto load = [&](int at) {
         const int row = at / per_row, k = k0 + 32 * (at - row * per_row);
         const bool in = at < total && k < din;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = in ? ld_cg_v4(x + (int64_t)row * din + k + 8 * i) : make_int4(0, 0, 0, 0);
+            ahead[i] = in ? ld_cg_v4(x + (int64_t)row * din + k + 8 * i) : make_int4(0, 0, 0, 0);
     };
     load(ct);                             // on their way while the previous tile is drained
     if (!sync(ct & 31)) return false;     // it is: x and its sums are free
@@ -351,7 +359,9 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
 #pragma unroll 1
     for (int base = ct & ~31; base < total; base += C::kConvThreads) {   // the same for a warp
         const int at = base + (ct & 31), row = at / per_row, part = at - row * per_row;
-        if (base >= C::kConvThreads) load(at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ahead[i];
+        load(at + C::kConvThreads);       // on their way while these are converted
         uint32_t m = 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, w4_largest(w[i]));
@@ -367,27 +377,27 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2)) << 16;
         const float scale = __uint_as_float(w4_scale_exponent(m) << 23);
-        float sum = 0.0f;
+        const uint64_t scale2 = pair_of(scale, scale);
+        uint64_t sum2 = 0ull;
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float f[8], h[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[j] = __uint_as_float(w4_element(w[i], j)) * scale;
-                sum += f[j];
-            }
             // Bytes in the order of the unpacked codes: even elements, then odd ones.
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t p = to_e4m3x2(f[j], f[j + 2]), q = to_e4m3x2(f[j + 4], f[j + 6]);
-                from_e4m3x2(p, &h[0], &h[1]);
-                from_e4m3x2(q, &h[2], &h[3]);
-                hi[2 * i + j] = p | (q << 16);
-                lo[2 * i + j] = to_e4m3x2(f[j] - h[0], f[j + 2] - h[1]) |
-                                (to_e4m3x2(f[j + 4] - h[2], f[j + 6] - h[3]) << 16);
+                uint32_t h[2], l[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint64_t v = mul2(pair_of(w4_element(w[i], j + 4 * u),
+                                                    w4_element(w[i], j + 4 * u + 2)), scale2);
+                    sum2 = add2(sum2, v);
+                    w4_terms(v, &h[u], &l[u]);
+                }
+                hi[2 * i + j] = h[0] | (h[1] << 16);
+                lo[2 * i + j] = l[0] | (l[1] << 16);
             }
         }
+        float sum = __uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32));
         if (C::GROUP >= 64) sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         if (C::GROUP >= 128) sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (at < total) {
@@ -808,24 +818,21 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                     for (int k = k0; k < k1; ++k, c.next(stages), as.next(kW4ASlots)) {
                         ok = warp_all(wait_or_abort(code_full0 + 8u * c.slot, c.phase, s_abort));
                         if (!ok) break;
-                        uint32_t w[8][4];
-                        if (warp_live) {
-                            const uint32_t base = smem_u32(smem) + (uint32_t)c.slot * kW4StageBytes +
-                                                  (uint32_t)r * 128u;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                lds128(base + (uint32_t)((i ^ (r & 7)) << 4), w[i]);
-                        }
+                        const uint32_t base = smem_u32(smem) + (uint32_t)c.slot * kW4StageBytes +
+                                              (uint32_t)r * 128u;
                         ok = warp_all(wait_or_abort(a_empty0 + 8u * as.slot, as.phase ^ 1u, s_abort));
                         if (!ok) break;
                         tc_fence_after();
                         if (warp_live) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                uint32_t v[32];
+                                uint32_t w[4][4], v[32];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    lds128(base + (uint32_t)(((4 * h + i) ^ (r & 7)) << 4), w[i]);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
-                                    const uint32_t q = w[4 * h + (i >> 2)][i & 3];
+                                    const uint32_t q = w[i >> 2][i & 3];
                                     v[2 * i] = q & 0x0F0F0F0Fu;
                                     v[2 * i + 1] = (q >> 4) & 0x0F0F0F0Fu;
                                 }
@@ -901,23 +908,34 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                 }
                                 if (!warp_live) continue;
 #pragma unroll
-                                for (int u = 0; u < C::PG; ++u) {
-                                    const int gi = g0 + p0 + u;
-                                    const float2 s = sc[gi * 128];
-                                    const ulonglong2* xs =
-                                        reinterpret_cast<const ulonglong2*>(sums + gi * NR);
+                                for (int u0 = 0; u0 < C::PG; u0 += C::SB) {
+                                    const int gi = g0 + p0 + u0;
+                                    uint64_t sx[C::SB], sy[C::SB];
+#pragma unroll
+                                    for (int u = 0; u < C::SB; ++u) {
+                                        const float2 v = sc[(gi + u) * 128];
+                                        sx[u] = pair_of(v.x, v.x);
+                                        sy[u] = pair_of(v.y, v.y);
+                                    }
                                     const ulonglong2* un =
                                         reinterpret_cast<const ulonglong2*>(undo + gi * C::GROUP / 128 * NR);
-                                    const uint64_t sx = pair_of(s.x, s.x), sy = pair_of(s.y, s.y);
 #pragma unroll
                                     for (int n4 = 0; n4 < NR / 4; ++n4) {
-                                        const ulonglong2 x4 = xs[n4], u4 = un[n4];
-                                        const uint32_t* v = q + u * NR + 4 * n4;
-                                        uint64_t* sum = acc + 2 * n4;
-                                        sum[0] = fma2(u4.x, fma2(sy, x4.x, mul2(sx, pair_of(v[0], v[1]))),
-                                                      sum[0]);
-                                        sum[1] = fma2(u4.y, fma2(sy, x4.y, mul2(sx, pair_of(v[2], v[3]))),
-                                                      sum[1]);
+                                        const ulonglong2 u4 = un[n4];
+                                        uint64_t d0, d1;
+#pragma unroll
+                                        for (int u = 0; u < C::SB; ++u) {
+                                            const ulonglong2 x4 = reinterpret_cast<const ulonglong2*>(
+                                                sums + (gi + u) * NR)[n4];
+                                            const uint32_t* v = q + (u0 + u) * NR + 4 * n4;
+                                            const uint64_t v0 = pair_of(v[0], v[1]), v1 = pair_of(v[2], v[3]);
+                                            d0 = u == 0 ? mul2(sx[u], v0) : fma2(sx[u], v0, d0);
+                                            d1 = u == 0 ? mul2(sx[u], v1) : fma2(sx[u], v1, d1);
+                                            d0 = fma2(sy[u], x4.x, d0);
+                                            d1 = fma2(sy[u], x4.y, d1);
+                                        }
+                                        acc[2 * n4] = fma2(u4.x, d0, acc[2 * n4]);
+                                        acc[2 * n4 + 1] = fma2(u4.y, d1, acc[2 * n4 + 1]);
                                     }
                                 }
                             }
