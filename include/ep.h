@@ -402,9 +402,10 @@ EP_API ep_status ep_expert_gemm_backward(ep_buffer* buf, const void* grad_y, con
  * group of consecutive elements of a row,
  *     w[o][i] = (code[o][i] - zero[o][i / group]) * scale[o][i / group],
  * for the few rows that each expert gets from a batch of single tokens. Any number of
- * rows is computed correctly; the kernels are made for up to about 32 per expert,
- * where reading the weights is what the call costs. All pointers are device memory,
- * codes 16-byte aligned, the rest aligned to their elements. */
+ * rows is computed correctly; the kernels are made for up to about 16 per expert,
+ * where reading the weights is what the call costs, and the weights stay as they are
+ * (nothing is laid out in advance). All pointers are device memory, codes 16-byte
+ * aligned, the rest aligned to their elements. */
 typedef struct {
     const uint8_t* codes;         /* [E][rows][din / 2]: element 2j in the low nibble of byte j */
     const void* scales;           /* [E][rows][din / group] of scale_dtype */
@@ -415,9 +416,12 @@ typedef struct {
 
 /* y_recv[p][o] = sum_i w[e][o][i] * x_recv[p][i] for each expert's rows p: x_recv
  * [R*S][din], y_recv [R*S][dout], bf16, in the receive layout as for ep_expert_gemm
- * (same buffers, errors and rows left alone); din % group == 0, dout % 8 == 0. code -
- * zero and x are multiplied exactly and summed in fp32 within a group, the groups'
- * sums scaled and summed in fp32 in a fixed order, and rounded once to bf16. */
+ * (same buffers, errors and rows left alone); din % group == 0, dout % 8 == 0. Codes
+ * and x are multiplied on the tensor cores as fp8 (e4m3), x as the sum of two such
+ * terms of each 128 elements' scaled values: exact for an element down to 2^-9 of the
+ * largest of its 128, and within 2^-17 of that one below. Sums are fp32, a group's
+ * scaled in fp32, all in a fixed order, and rounded once to bf16. An infinity or a NaN
+ * in x reaches exactly its own row's results. */
 EP_API ep_status ep_expert_gemv_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights,
                                    int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
 

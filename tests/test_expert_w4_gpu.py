@@ -1,9 +1,12 @@
 """Products with 4-bit weights and group scales against plain 64-bit products.
 
-code - zero and x are exact in bf16 and their products in fp32, so a group's sum of G
-of them and the sum of the din / G scaled groups are fp32 sums: within 2 din 2^-24
-sum|w x| of the exact one. One rounding to bf16 adds 2^-8 of the result (half an ulp is
-2^-9; the other half covers the activation's few ulp of fp32, as for the bf16 block).
+Codes and the two terms of x are exact as fp8 and their products in fp32, so a group's
+sums and the sum of the din / G scaled groups are fp32 sums, held to the bound of the
+direct sum: within 2 din 2^-24 sum|w x| of the exact one. (x below 2^-9 of its block's
+largest may be off by 2^-17 of that: nothing of that size among normal rows counts; the
+test of extreme rows allows for it.) One rounding to bf16 adds 2^-8 of the result (half
+an ulp is 2^-9; the other half covers the activation's few ulp of fp32, as for the bf16
+block).
 Receive rows of no expert hold NaNs: none may reach a result, and outputs there keep
 their contents.
 """
