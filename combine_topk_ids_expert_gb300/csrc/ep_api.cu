@@ -933,7 +933,7 @@ static ep_status enqueue_w4(ep_buffer* b, const void* x, const ep_w4* w, int64_t
     if (din > INT32_MAX || dout > INT32_MAX / 2 / E) return EP_ERR_CAPACITY;
     if (rows <= 0) return EP_OK;
     // Row chunks times column blocks, and weight rows, are counted in int32.
-    if (rows / 8 + E > INT32_MAX / (dout / 16 + 1)) return EP_ERR_CAPACITY;
+    if (rows / 4 + E > INT32_MAX / (dout / 16 + 1)) return EP_ERR_CAPACITY;
     ep::W4Args a;
     a.cnt = b->cnt;
     a.expert_offset = b->expert_offset;

@@ -111,6 +111,7 @@ struct W4Args {
 // expected_rows: rows per expert that the call is likely to have.
 cudaError_t launch_expert_w4(const W4Args& a, int64_t expected_rows, int num_sms,
                              const LaunchOpts& o);
+cudaError_t launch_expert_w4_4(const W4Args& a, int num_sms, const LaunchOpts& o);
 cudaError_t launch_expert_w4_16(const W4Args& a, int num_sms, const LaunchOpts& o);
 
 // Sentinel checks of the receive buffer (debug.cu, EP_DEBUG=1).

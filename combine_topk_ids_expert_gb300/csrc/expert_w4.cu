@@ -18,6 +18,7 @@ cudaError_t launch_expert_w4(const W4Args& a, int64_t expected_rows, int num_sms
         return cudaErrorInvalidValue;
     if (expected_rows > 8 && w4_plan<W4Cfg<16, 32>>(a.din, a.E).panel >= a.din)
         return launch_expert_w4_16(a, num_sms, o);
+    if (expected_rows <= 4) return launch_expert_w4_4(a, num_sms, o);
     return launch_w4_rows<8>(a, a.codes, num_sms, o);
 }
 

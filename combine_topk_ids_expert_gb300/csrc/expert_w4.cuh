@@ -84,7 +84,11 @@ struct W4Cfg {
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
     static constexpr uint32_t kTermBytes = NR * 128;         // a term of 128 contraction elements
     static constexpr uint32_t kPanelBytes = 2 * kTermBytes;  // hi rows, then lo rows
-    static constexpr int PG = GB < 32 / NR ? GB : 32 / NR;   // groups that a lane drains at once
+    // With 4 rows both terms fit the MMA's columns and the drain adds them up; with more,
+    // a second MMA adds the second term to the first one's accumulator.
+    static constexpr bool kBothTerms = 2 * NR <= 8;
+    static constexpr int LD = kBothTerms ? 2 * NR : NR;      // accumulator columns of a group to drain
+    static constexpr int PG = GB < 32 / LD ? GB : 32 / LD;   // groups that a lane drains at once
     static constexpr int SB = PG < 128 / GROUP ? PG : 128 / GROUP;   // of these, in one block of x
     static constexpr int kSwap = 64 * (NR + 1) * 4;          // gated: up sums on their way to gate lanes
     static_assert(GPS % GB == 0 && GB % PG == 0 && NR <= 16 && DSLOTS <= kW4MaxDSlots, "slots");
@@ -405,10 +409,10 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
             const int c = 2 * (part & 3);   // the first of its two 16-byte units
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int at16 = ((c + i) ^ (row & 7)) << 4;
-                *reinterpret_cast<uint4*>(dst + at16) =
+                *reinterpret_cast<uint4*>(dst + (((c + i) ^ (row & 7)) << 4)) =
                     make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                *reinterpret_cast<uint4*>(dst + C::kTermBytes + at16) =
+                *reinterpret_cast<uint4*>(dst + C::kTermBytes +
+                                          (((c + i) ^ ((row + C::NR) & 7)) << 4)) =
                     make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
             }
             if ((part & (C::GROUP / 32 - 1)) == 0) s_xsum[part / (C::GROUP / 32) * C::NR + row] = sum;
@@ -746,12 +750,13 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                             const uint64_t hi =
                                 bx + (uint64_t)(((step >> 2) * C::kPanelBytes + (step & 3) * 32) >> 4);
                             const uint32_t to = d + (uint32_t)(i / C::STEPS * N);
-                            // Both terms into one accumulator. (For NR = 8 the MMA's columns
-                            // 8-15 see rows that follow the term's; nobody reads them.)
+                            // (Where the MMA's columns are more than the terms', the rest
+                            // see what follows in shared memory; nobody reads them.)
                             umma_e4m3_ts(to, at + (uint32_t)step * 8u, hi, C::kIdesc,
                                          i % C::STEPS != 0 ? 1u : 0u);
-                            umma_e4m3_ts(to, at + (uint32_t)step * 8u, hi + (C::kTermBytes >> 4),
-                                         C::kIdesc, 1u);
+                            if (!C::kBothTerms)
+                                umma_e4m3_ts(to, at + (uint32_t)step * 8u,
+                                             hi + (C::kTermBytes >> 4), C::kIdesc, 1u);
                         }
                         umma_commit<false>(d_full0 + 8u * ds.slot);
                         if (g0 + C::GB == C::GPS) umma_commit<false>(a_empty0 + 8u * as.slot);
@@ -894,11 +899,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                             const uint32_t d = t_lane + (uint32_t)(ds.slot * C::GB * N);
 #pragma unroll
                             for (int p0 = 0; p0 < C::GB; p0 += C::PG) {
-                                uint32_t q[C::PG * NR];
+                                uint32_t q[C::PG * C::LD];
                                 if (warp_live) {
 #pragma unroll
                                     for (int u = 0; u < C::PG; ++u)
-                                        tmem_ld_cols<NR>(d + (uint32_t)((p0 + u) * N), q + u * NR);
+                                        tmem_ld_cols<C::LD>(d + (uint32_t)((p0 + u) * N), q + u * C::LD);
                                     tmem_wait_ld();
                                 }
                                 if (p0 + C::PG == C::GB) {   // the slot is free as soon as it is read
@@ -927,8 +932,12 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                         for (int u = 0; u < C::SB; ++u) {
                                             const ulonglong2 x4 = reinterpret_cast<const ulonglong2*>(
                                                 sums + (gi + u) * NR)[n4];
-                                            const uint32_t* v = q + (u0 + u) * NR + 4 * n4;
-                                            const uint64_t v0 = pair_of(v[0], v[1]), v1 = pair_of(v[2], v[3]);
+                                            const uint32_t* v = q + (u0 + u) * C::LD + 4 * n4;
+                                            uint64_t v0 = pair_of(v[0], v[1]), v1 = pair_of(v[2], v[3]);
+                                            if constexpr (C::kBothTerms) {
+                                                v0 = add2(v0, pair_of(v[NR], v[NR + 1]));
+                                                v1 = add2(v1, pair_of(v[NR + 2], v[NR + 3]));
+                                            }
                                             d0 = u == 0 ? mul2(sx[u], v0) : fma2(sx[u], v0, d0);
                                             d1 = u == 0 ? mul2(sx[u], v1) : fma2(sx[u], v1, d1);
                                             d0 = fma2(sy[u], x4.x, d0);
