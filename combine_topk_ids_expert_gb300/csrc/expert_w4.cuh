@@ -8,7 +8,7 @@
 // codes, 2900 issue slots for 32768 of them. Unpacking codes into 16-bit operands on
 // mma.sync (a shift, a mask and a subtraction for every two, then operands of x and
 // scales at 16 x 8 outputs a step) took 3600 instructions for as many, and 328 us where
-// this kernel takes 200 and 1500 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
+// this kernel takes 180 and 1500 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
 //   - a nibble q, zero-extended to a byte, IS an fp8 number: read as e4m3 it is
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
@@ -36,20 +36,19 @@
 // stays in shared memory for the tiles that follow; the copies of the codes run ahead
 // over tile boundaries all the while.
 //
-// Measured (a graph of calls on three sets of weights, one GB300): 197 us, 4.9 TB/s or
-// 73% of a copy's rate (the same 64 x 4096 x 7168 codes); 31 us, 3.9 TB/s (8 experts of
-// these, one row each); 51 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
-// where converting x and draining the scale groups are what takes long. Copies, barriers
-// and MMAs alone took 181 us where all took 210; the rest is the roles' latencies: each
-// scheduler has one warp that unpacks and one that drains.
+// Measured (a graph of calls on three sets of weights, one GB300): 180 us, 5.3 TB/s or
+// 80% of a copy's rate (the same 64 x 4096 x 7168 codes); 29 us, 4.2 TB/s (8 experts of
+// these, one row each); 46 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
+// where converting x and draining the scale groups are what takes long.
 //
-// Roles (10 warps): 0 copies codes (TMA, slices of 256 codes of 64 columns a box, 128-byte
-// swizzle), 1 issues the MMAs, 2-5 move codes to TMEM, 6-9 drain; 2-9 convert x
-// together. With 14 warps (a second set of either) a thread has 128 registers instead of
-// 168 and the drain spills: 82 against 67 us. (With shared memory full, what spills goes
-// to L2: unpacking half a slice at a time, which takes fewer registers, 52 -> 51 us, and
-// reading the next accumulators ahead, which takes more, 52 -> 73 us.) Every wait is
-// bounded.
+// Roles (12 warps): 0 copies codes (TMA, slices of 256 codes of 64 columns a box, 128-byte
+// swizzle), 1 issues the MMAs, 2-5 move codes to TMEM, 6-9 drain, 10-11 load scales and
+// zero points and lay them out for the drain (which, doing that itself, took 85 us where
+// it takes 76, and 706 where it takes 648: 64 tokens over 8 and 32 over 256 experts,
+// gated block); 2-9 convert x together. With 16 warps (a second set that unpacks or
+// drains) a thread would have 128 registers instead of 168 and the drain spills, and with
+// shared memory full what spills goes to L2: 82 against 67 us; reading the next
+// accumulators ahead spills too, 53 against 46 us. Every wait is bounded.
 #pragma once
 
 #include "umma.cuh"
@@ -67,18 +66,25 @@ constexpr int kW4DCols = 256;             // TMEM columns of accumulators, then 
 constexpr uint32_t kW4ABase = kW4DCols;
 constexpr int kW4MaxDSlots = 8;
 constexpr uint32_t kW4StateBytes = 1024;  // barriers and small state
-constexpr int kW4Bars = 2 * kW4MaxStages + 2 * kW4ASlots + 2 * kW4MaxDSlots + 4;
+constexpr int kW4ScaleSets = 2;           // of 8 groups of a tile, as the drain takes them
+constexpr uint32_t kW4SetBytes = 8 * 128 * 8;
+constexpr int kW4Bars = 2 * kW4MaxStages + 2 * kW4ASlots + 2 * kW4MaxDSlots + 2 * kW4ScaleSets + 4;
 
 template <int NR_, int GROUP_>
 struct W4Cfg {
     static constexpr int NR = NR_, GROUP = GROUP_;
     static constexpr int N = NR < 16 ? 16 : NR;              // of the MMA (M = 128 wants 16)
     static constexpr int kConvThreads = 256;   // warps 2 and up: four unpack, four drain
-    static constexpr int kThreads = 64 + kConvThreads;
+    static constexpr int kThreads = 64 + kConvThreads + 64;
     static constexpr int GPS = kW4Slice / GROUP;             // scale groups of a slice
     static constexpr int GB = GPS < 128 / N ? GPS : 128 / N;             // groups per accumulator slot
     static constexpr int DSLOTS = kW4DCols / (GB * N);
     static constexpr int SPB = 8 / GPS;                      // slices whose scales a lane loads at once
+    // Ring slices at most. Scales are a third as many bytes as the codes with groups of 32
+    // and come through L1, which gets what the ring leaves: 20.4 against 22.0 us with 6
+    // and 8 (13 rows, 8 x 2048 x 4096 codes, fp32 scales); groups of 128 want the longer
+    // ring, 648 against 661 us (gated block, 32 tokens over 256 experts).
+    static constexpr int STAGES = GROUP == 32 ? 6 : kW4MaxStages;
     static constexpr int STEPS = GROUP / 32;                 // MMAs (K = 32) of a group
     // kind::f8f6f4: fp32 accumulate, A and B e4m3 (0), both K-major, N, M = 128.
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
@@ -465,7 +471,7 @@ __device__ __forceinline__ void w4_prefetch_scales(const W4Args& a, int64_t row,
     if (a.zeros) w4_prefetch_bytes(a.zeros + at, n);
 }
 
-// A drain lane's column of a tile and the scales of 8 groups of it.
+// A column of a tile.
 struct W4Lane {
     int o;             // output column
     int64_t wrow;      // weight row
@@ -542,9 +548,8 @@ __device__ __forceinline__ void w4_load_scales(const W4Args& a, const W4Lane& l,
     }
 }
 
-// Into the lane's places [8][128]: the scale times the codes' 2^9, and minus the scale
-// times the zero point. Only the lane itself reads them (by a group index that is not
-// a constant, so not from registers).
+// Into the column's places [8][128] of a set: the scale times the codes' 2^9, and minus
+// the scale times the zero point.
 __device__ __forceinline__ void w4_keep_scales(const W4Scales& v, bool f32, bool wide, float2* mine)
 {
 #pragma unroll
@@ -579,6 +584,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
     const uint32_t drain = x_full + 8u;
     const uint32_t conv = drain + 8u;      // warps 2 and up
     const uint32_t swapped = conv + 8u;    // the drain's
+    const uint32_t sc_full0 = swapped + 8u;
+    const uint32_t sc_empty0 = sc_full0 + 8u * kW4ScaleSets;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(state + 8 * kW4Bars);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     int* s_warp = reinterpret_cast<int*>(s_tmem + 2);   // [16] scan
@@ -591,8 +598,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
     float* s_xsum = reinterpret_cast<float*>(s_x + (size_t)panel * 2 * NR);    // [panel / GROUP][NR]
     float* s_undo = s_xsum + panel / C::GROUP * NR;                       // [panel / 128][NR]
     float* s_swap = s_undo + panel / 128 * NR;
-    float2* s_scale = reinterpret_cast<float2*>(s_swap + C::kSwap / 4);   // [8][128]
-    int* s_pre = reinterpret_cast<int*>(s_scale + 8 * 128);
+    float2* s_scale = reinterpret_cast<float2*>(s_swap + C::kSwap / 4);   // [sets][8][128]
+    int* s_pre = reinterpret_cast<int*>(s_scale + kW4ScaleSets * 8 * 128);
     const int E = a.E;
     int* s_cnt = s_pre + E + 1;
     int* s_off = s_cnt + E;
@@ -623,6 +630,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         mbar_init(drain, 1u);
         mbar_init(conv, C::kConvThreads / 32);
         mbar_init(swapped, 4u);
+        for (int s = 0; s < kW4ScaleSets; ++s) {
+            mbar_init(sc_full0 + 8u * s, 2u);
+            mbar_init(sc_empty0 + 8u * s, 4u);
+        }
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -774,16 +785,47 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
             __syncwarp();
             mbar_wait(drain, 0u);
         }
-    } else if (warp >= 2) {
+    } else if (warp >= 10) {
+        // ---- scales and zero points, 8 groups of the tile's columns at a time -----
+        const int groups = (int)(a.din / C::GROUP);
+        const bool wide = groups % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0u &&
+                          (reinterpret_cast<uintptr_t>(a.zeros) & 7u) == 0u;
+        const int r = (int)threadIdx.x - 320;   // columns r and r + 64 of the tile
+        W4Ring set;
+        W4Scales next[2];
+        auto load = [&](const W4Tile& t, int k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w4_load_scales(a, w4_lane(a, t, wrows, r + 64 * h), groups, wide, k * C::GPS, next[h]);
+        };
+        bool ok = true;
+        if (first < last) load(w4_tile<C>(tab, E, cut, first), 0);
+#pragma unroll 1
+        for (int b = first; b < last && ok;) {
+            const W4Tile t = w4_tile<C>(tab, E, cut, b);
+            ++b;
+#pragma unroll 1
+            for (int k = 0; k < slices; k += C::SPB) {
+                ok = warp_all(wait_or_abort(sc_empty0 + 8u * set.slot, set.phase ^ 1u, s_abort));
+                if (!ok) break;
+                float2* to = s_scale + set.slot * (8 * 128) + r;
+                w4_keep_scales(next[0], a.scale_f32, wide, to);
+                w4_keep_scales(next[1], a.scale_f32, wide, to + 64);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_full0 + 8u * set.slot);
+                set.next(kW4ScaleSets);
+                // The next 8 groups' are on their way until the drain wants them; over the
+                // tile's end too.
+                if (k + C::SPB < slices) load(t, k + C::SPB);
+                else if (b < last) load(w4_tile<C>(tab, E, cut, b), 0);
+            }
+        }
+    } else {
         const int ct = (int)threadIdx.x - 64;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;                // output column of the tile / TMEM lane
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool drains = warp >= 6;
-        const int groups = (int)(a.din / C::GROUP);
-        const bool wide = groups % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0u &&
-                          (reinterpret_cast<uintptr_t>(a.zeros) & 7u) == 0u;
-        float2* mine = s_scale + r;
         W4Sync conv_sync = {conv, s_abort};
         int e_have = -1, chunk_have = -1, half = 1;   // half: of the row state
         bool ok = true, new_rows = false;
@@ -858,12 +900,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
         } else {
             // ---- drain ---------------------------------------------------------------
             W4Sync swap_sync = {swapped, s_abort};
-            W4Ring ds;
-            W4Scales next;
-            auto load_scales = [&](const W4Tile& t, int k) {
-                w4_load_scales(a, w4_lane(a, t, wrows, r), groups, wide, k * C::GPS, next);
-            };
-            if (first < last) load_scales(w4_tile<C>(tab, E, cut, first), 0);
+            W4Ring ds, set;
+            bool held = false;   // a set of scales
 #pragma unroll 1
             for (int b = first; b < last && ok;) {
                 const W4Tile t = w4_tile<C>(tab, E, cut, b);
@@ -881,13 +919,19 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
 #pragma unroll 1
                     for (int k = k0; k < k1 && ok; ++k) {
                         if ((k & (C::SPB - 1)) == 0) {
-                            // The next 8 groups' scales, loaded while the 8 before were used;
-                            // over the tile's end too.
-                            w4_keep_scales(next, a.scale_f32, wide, mine);
-                            if (k + C::SPB < slices) load_scales(t, k + C::SPB);
-                            else if (b < last) load_scales(w4_tile<C>(tab, E, cut, b), 0);
+                            // The set before was last used a slice ago: nothing of it is
+                            // still on its way from shared memory.
+                            if (held) {
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(sc_empty0 + 8u * set.slot);
+                                set.next(kW4ScaleSets);
+                            }
+                            held = true;
+                            ok = warp_all(wait_or_abort(sc_full0 + 8u * set.slot, set.phase, s_abort));
+                            if (!ok) break;
                         }
-                        const float2* sc = mine + (k & (C::SPB - 1)) * C::GPS * 128;
+                        const float2* sc = s_scale + set.slot * (8 * 128) + r +
+                                           (k & (C::SPB - 1)) * C::GPS * 128;
                         const float* sums = s_xsum + (k - k0) * (C::GPS * NR);
                         const float* undo = s_undo + (k - k0) * (2 * NR);
 #pragma unroll 1
@@ -960,7 +1004,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                     out[n] = __uint_as_float((uint32_t)(acc[n / 2] >> (32 * (n & 1))));
                 for (int n = 0; n < t.rows; ++n)
                     if (s_odd0[half * NR + n] && l.live) {
-                        const float terms = w4_odd_terms(a, t.row0 + n, l.wrow, groups);
+                        const float terms = w4_odd_terms(a, t.row0 + n, l.wrow, (int)(a.din / C::GROUP));
 #pragma unroll
                         for (int m = 0; m < NR; ++m)
                             if (m == n) out[m] += terms;
@@ -1019,7 +1063,8 @@ inline bool make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, 
 template <class C>
 W4Plan w4_plan(int64_t din, int E)
 {
-    const size_t fixed = 1024 + kW4StateBytes + C::kSwap + 8 * 128 * 8 + 4 * (3 * (size_t)E + 1);
+    const size_t fixed =
+        1024 + kW4StateBytes + C::kSwap + kW4ScaleSets * kW4SetBytes + 4 * (3 * (size_t)E + 1);
     const size_t per_slice = (size_t)kW4Slice * 2 * C::NR + (size_t)(C::GPS + 2) * C::NR * 4;   // of x
     const int64_t slices = (din + kW4Slice - 1) / kW4Slice;
     const int64_t fit =
@@ -1029,7 +1074,7 @@ W4Plan w4_plan(int64_t din, int E)
     p.panel = (int)(held * kW4Slice);
     const size_t left = kSmemLimit - fixed - (size_t)held * per_slice;
     p.stages = (int)(left / kW4StageBytes);
-    if (p.stages > kW4MaxStages) p.stages = kW4MaxStages;
+    if (p.stages > C::STAGES) p.stages = C::STAGES;
     p.smem = fixed + (size_t)held * per_slice + (size_t)p.stages * kW4StageBytes;
     return p;
 }
