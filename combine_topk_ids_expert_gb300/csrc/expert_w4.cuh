@@ -165,6 +165,14 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
                  : "r"(addr));
 }
 
+__device__ __forceinline__ void ld_cg_32(const void* p, int4& a, int4& b)
+{
+    asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                   "=r"(b.w)
+                 : "l"(p));
+}
+
 // Two fp32 values in one register pair, and their products and fmas, one instruction
 // for both.
 __device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi)
@@ -355,13 +363,22 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
     // A lane takes 32 elements at a time, four lanes a block of 128.
     const int per_row = panel / 32, total = rows * per_row;
     float* s_undo = s_xsum + panel / C::GROUP * C::NR;
+    // 32 bytes a load where x allows: 16 of each lane's 64 fetch every sector twice.
+    const bool by32 = (reinterpret_cast<uintptr_t>(x) & 31u) == 0u;
     int4 w[4], ahead[4];
     auto load = [&](int at) {
         const int row = at / per_row, k = k0 + 32 * (at - row * per_row);
         const bool in = at < total && k < din;
+        const uint16_t* p = x + (int64_t)row * din + k;
+        if (by32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            ahead[i] = in ? ld_cg_v4(x + (int64_t)row * din + k + 8 * i) : make_int4(0, 0, 0, 0);
+            for (int i = 0; i < 4; i += 2)
+                if (in) ld_cg_32(p + 8 * i, ahead[i], ahead[i + 1]);
+                else ahead[i] = ahead[i + 1] = make_int4(0, 0, 0, 0);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ahead[i] = in ? ld_cg_v4(p + 8 * i) : make_int4(0, 0, 0, 0);
     };
     load(ct);                             // on their way while the previous tile is drained
     if (!sync(ct & 31)) return false;     // it is: x and its sums are free

@@ -56,6 +56,8 @@ CASES = {
     "long":        (11, 5, 3, 2, 1, "uniform", "strided", 0.0, 7168, 96, 128, False, "bf16"),
     "long_fine":   (12, 40, 3, 2, 1, "uniform", "strided", 0.0, 4128, 96, 32, True, "f32"),
     "all_dropped": (13, 6, 4, 2, 1, "uniform", "strided", 1.0, 128, 64, 64, False, "bf16"),
+    "few_zipf":    (15, 40, 64, 2, 2, "zipf", "strided", 0.1, 544, 200, 32, True, "f32"),
+    "few_long":    (16, 4, 8, 2, 1, "uniform", "packed", 0.0, 4224, 136, 128, True, "bf16"),
     "units_many":  (14, 24, 64, 4, 4, "uniform", "strided", 0.0, 128, 1024, 64, True, "bf16"),
 }
 
@@ -92,6 +94,24 @@ def test_glu(name, act):
     a, _, _ = act_ref(g, act)
     tol = (2.0 ** -8 + 2.0 ** -15) * (a * u).abs() + 1.13 * dg * (u.abs() + du) + a.abs() * du
     c.check_rows(h, a * u, tol + 1e-38)
+    c.done()
+
+
+@pytest.mark.parametrize("name", ["few_long", "odd_chunks", "rows_many"])
+def test_rows_and_scales_at_their_least_alignment(name):
+    # x 16 bytes and scales an element past what allocations give: the same bits.
+    c, din, dout, kind = case(name)
+    x, w = c.recv(din), weights(c, dout, din, *kind)
+
+    def past(t, n):
+        flat = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")[n:]
+        return flat.copy_(t.reshape(-1)).view(t.shape)
+
+    y = c.buf.expert_gemv_w4(x, w).reshape(c.rows, -1)
+    w2 = ep.W4(w.codes, past(w.scales, 1), None if w.zeros is None else past(w.zeros, 1))
+    for xs, ws in ((past(x, 8), w), (x, w2)):
+        got = c.buf.expert_gemv_w4(xs, ws).reshape(c.rows, -1)
+        assert torch.equal(got[c.used].view(torch.int16), y[c.used].view(torch.int16))
     c.done()
 
 
