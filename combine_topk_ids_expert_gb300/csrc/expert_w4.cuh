@@ -1,5 +1,5 @@
 // expert_w4.cuh - the products of each expert's few rows with 4-bit weights and
-// group scales, for decoding (expert_w4.cu and expert_w4_16.cu instantiate it):
+// group scales, for decoding (expert_w4.cu, expert_w4_4.cu and expert_w4_16.cu instantiate it):
 //     y[p][o] = sum over groups G of s[e][o][G] * sum over i in G of (q[e][o][i] - z) x[p][i]
 // and the gated form h = act(g) * u over gate and up rows of the same matrix.
 //
@@ -8,7 +8,7 @@
 // codes, 2900 issue slots for 32768 of them. Unpacking codes into 16-bit operands on
 // mma.sync (a shift, a mask and a subtraction for every two, then operands of x and
 // scales at 16 x 8 outputs a step) took 3600 instructions for as many, and 328 us where
-// this kernel takes 180 and 1500 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
+// this kernel takes 175 and 1500 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
 //   - a nibble q, zero-extended to a byte, IS an fp8 number: read as e4m3 it is
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
@@ -21,7 +21,8 @@
 //   - the tensor cores multiply and sum in fp32: tcgen05.mma.kind::f8f6f4 with the
 //     codes as A (128 output columns on TMEM's lanes, written there by tcgen05.st
 //     without passing shared memory again) and the terms of at most NR rows as B, one
-//     after the other into the same accumulator. Each scale group has its own;
+//     after the other into the same accumulator (4 rows: side by side in one MMA, and
+//     the drain adds them). Each scale group has its own;
 //   - draining a group, a lane holds one output column: per row, its sum times the
 //     column's scale, the group's sum of x times minus scale and zero point, for the
 //     groups of a block of x together, and an fma by what undoes the block's scale, two
@@ -36,10 +37,10 @@
 // stays in shared memory for the tiles that follow; the copies of the codes run ahead
 // over tile boundaries all the while.
 //
-// Measured (a graph of calls on three sets of weights, one GB300): 180 us, 5.3 TB/s or
-// 80% of a copy's rate (the same 64 x 4096 x 7168 codes); 29 us, 4.2 TB/s (8 experts of
-// these, one row each); 46 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
-// where converting x and draining the scale groups are what takes long.
+// Measured (a graph of calls on three sets of weights, one GB300): 175 us, 5.5 TB/s or
+// 82% of a copy's rate (the same 64 x 4096 x 7168 codes); 29 us, 4.2 TB/s (8 experts of
+// these, one row each); 45 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
+// where converting x (9 us of it) and draining the scale groups are what takes long.
 //
 // Roles (12 warps): 0 copies codes (TMA, slices of 256 codes of 64 columns a box, 128-byte
 // swizzle), 1 issues the MMAs, 2-5 move codes to TMEM, 6-9 drain, 10-11 load scales and
