@@ -1,5 +1,5 @@
 // expert_w4.cuh - the products of each expert's few rows with 4-bit weights and
-// group scales, for decoding (expert_w4.cu, expert_w4_4.cu and expert_w4_16.cu instantiate it):
+// group scales, for decoding (expert_w4.cu, expert_w4_4.cu, expert_w4_16.cu instantiate it):
 //     y[p][o] = sum over groups G of s[e][o][G] * sum over i in G of (q[e][o][i] - z) x[p][i]
 // and the gated form h = act(g) * u over gate and up rows of the same matrix.
 //

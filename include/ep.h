@@ -420,7 +420,8 @@ typedef struct {
  * and x are multiplied on the tensor cores as fp8 (e4m3), x as the sum of two such
  * terms of each 128 elements' scaled values: exact for an element down to 2^-9 of the
  * largest of its 128, and within 2^-17 of that one below. Sums are fp32, a group's
- * scaled in fp32, all in a fixed order, and rounded once to bf16. An infinity or a NaN
+ * scaled in fp32, in an order fixed by the sizes and by how many rows an expert has on
+ * average, and rounded once to bf16. An infinity or a NaN
  * in x reaches exactly its own row's results. */
 EP_API ep_status ep_expert_gemv_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights,
                                    int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
