@@ -950,10 +950,10 @@ static ep_status enqueue_w4(ep_buffer* b, const void* x, const ep_w4* w, int64_t
     a.E = b->cfg.num_experts;
     a.act = act;
     a.err = b->err;
-    // Rows an expert is likely to have: twice the mean (routing is uneven), no more than
+    // Rows that few experts exceed: 1.6 times the mean (routing is uneven), no more than
     // the call's tokens.
-    const int64_t mean2 = (2 * b->last_T * b->cfg.topk + E - 1) / E;
-    return cuda_status(ep::launch_expert_w4(a, std::min(mean2, b->last_T), b->num_sms,
+    const int64_t likely = (8 * b->last_T * b->cfg.topk + 5 * E - 1) / (5 * E);
+    return cuda_status(ep::launch_expert_w4(a, std::min(likely, b->last_T), b->num_sms,
                                             opts(b, as_stream(stream))));
 }
 

@@ -108,7 +108,7 @@ struct W4Args {
     int act;                       // glu: as GemmArgs::act
     uint32_t* err;
 };
-// expected_rows: rows per expert that the call is likely to have.
+// expected_rows: rows that few of the call's experts exceed.
 cudaError_t launch_expert_w4(const W4Args& a, int64_t expected_rows, int num_sms,
                              const LaunchOpts& o);
 cudaError_t launch_expert_w4_4(const W4Args& a, int num_sms, const LaunchOpts& o);
