@@ -266,6 +266,11 @@ class W4:
             _check_dtype(z, torch.uint8, "zeros")
             if z.shape != s.shape:
                 raise ValueError(f"zeros must be shaped as scales, got {tuple(z.shape)}")
+        object.__setattr__(self, "_checked", self._form())
+
+    def _form(self) -> tuple:
+        c, s, z = self.codes, self.scales, self.zeros
+        return c.shape, c.dtype, s.shape, s.dtype, None if z is None else (z.shape, z.dtype)
 
     @cached_property
     def din(self) -> int:
@@ -279,9 +284,13 @@ class W4:
     def group(self) -> int:
         return self.din // self.scales.shape[2]
 
-    @cached_property
     def _struct(self) -> EpW4:
-        """The C struct: this object's own fields, which cannot be set again."""
+        """The C struct of one call. The fields cannot be set again, but a tensor's storage can
+        be swapped under it (t.data = ..., set_, a module's move to another device and back):
+        addresses, device and layout are taken anew each time."""
+        if self._form() != self._checked:
+            raise ValueError("the tensors of this W4 changed their shapes or types since it was "
+                             "made: make another one of them")
         return EpW4(_ptr(self.codes), _ptr(self.scales), _ptr(self.zeros),
                     _TORCH_TO_EP[self.scales.dtype], self.group)
 
@@ -290,7 +299,7 @@ def ep_expert_gemv_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dout:
                       y_recv: torch.Tensor, stream=None) -> None:
     for name, t in (("x_recv", x_recv), ("y_recv", y_recv)):
         _check_dtype(t, torch.bfloat16, name)
-    check(_abi.lib().ep_expert_gemv_w4(handle, _ptr(x_recv), C.byref(weights._struct), din, dout,
+    check(_abi.lib().ep_expert_gemv_w4(handle, _ptr(x_recv), C.byref(weights._struct()), din, dout,
                                        _ptr(y_recv), _stream(stream)), "ep_expert_gemv_w4")
 
 
@@ -298,7 +307,7 @@ def ep_expert_glu_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dff: i
                      h: torch.Tensor, stream=None) -> None:
     for name, t in (("x_recv", x_recv), ("h", h)):
         _check_dtype(t, torch.bfloat16, name)
-    check(_abi.lib().ep_expert_glu_w4(handle, _ptr(x_recv), C.byref(weights._struct), din, dff,
+    check(_abi.lib().ep_expert_glu_w4(handle, _ptr(x_recv), C.byref(weights._struct()), din, dff,
                                       act, _ptr(h), _stream(stream)), "ep_expert_glu_w4")
 
 
