@@ -528,6 +528,32 @@ class Buffer:
             recv_src=self._view(d.recv_src, torch.int32, lead),
             layout=self._layout(d.layout))
 
+    # -- memory of results -----------------------------------------------------
+    def _empty(self, shape: tuple, dtype: torch.dtype, stream, kept: bool = True) -> torch.Tensor:
+        """Memory for what a call's kernels write on `stream`: from that stream's own pool, so
+        that what used it before is done by then in stream order, and dropping it hands it on
+        only behind those kernels. kept: the caller gets it, and may drop it while the current
+        stream still works on it; that work is waited for too."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        here = torch.cuda.current_stream(self.device)
+        if stream == here:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        if kept:
+            t.record_stream(here)
+        return t
+
+    def _new_rows(self, width: int, stream, dtype: torch.dtype = torch.bfloat16,
+                  kept: bool = True) -> torch.Tensor:
+        """Memory for rows of the last call's receive layout."""
+        S = self._last_stride()
+        lead = (self.R * S,) if self.packed else (self.R, S)
+        return self._empty(lead + (width,), dtype, stream, kept)
+
     # -- calls -------------------------------------------------------------
     def dispatch_layout(self, topk_expert_ids_TK: torch.Tensor, num_tokens_per_rank: int,
                         stream=None, host_counts: bool = False):
@@ -561,7 +587,7 @@ class Buffer:
         T = topk_scores_TK.shape[0]
         if out is None:
             od = self.dtype if out_dtype is None else out_dtype
-            out = torch.empty((T, self.D), dtype=od, device=self.device)
+            out = self._empty((T, self.D), od, stream)
         if out.dtype not in _TORCH_TO_EP:
             raise TypeError(f"out dtype must be bfloat16 or float32, got {out.dtype}")
         ep_combine(self.handle, y_recv, topk_scores_TK, T, out, _TORCH_TO_EP[out.dtype], stream)
@@ -575,11 +601,8 @@ class Buffer:
         _check_dtype(grad_out, self.dtype, "grad_out")
         T = topk_scores_TK.shape[0]
         if grad_y is None:
-            S = self._last_stride()
-            lead = (self.R * S,) if self.packed else (self.R, S)
-            grad_y = torch.empty(lead + (self.D,), dtype=self.dtype, device=self.device)
-        gs = torch.empty((T, self.K), dtype=torch.float32, device=self.device) \
-            if want_scores else None
+            grad_y = self._new_rows(self.D, stream, self.dtype)
+        gs = self._empty((T, self.K), torch.float32, stream) if want_scores else None
         ep_combine_backward(self.handle, grad_out, y_recv, topk_scores_TK, T, grad_y, gs, stream)
         return grad_y, gs
 
@@ -589,10 +612,10 @@ class Buffer:
         """(grad_x [T, D], grad_scores [T, K] or None) for the last dispatch."""
         _check_dtype(grad_recv_x, self.dtype, "grad_recv_x")
         od = self.dtype if out_dtype is None else out_dtype
-        gx = torch.empty((num_tokens, self.D), dtype=od, device=self.device)
+        gx = self._empty((num_tokens, self.D), od, stream)
         gs = None
         if grad_recv_scores is not None:
-            gs = torch.empty((num_tokens, self.K), dtype=torch.float32, device=self.device)
+            gs = self._empty((num_tokens, self.K), torch.float32, stream)
         ep_dispatch_backward(self.handle, grad_recv_x, grad_recv_scores, num_tokens, gx,
                              _TORCH_TO_EP[od], gs, stream)
         return gx, gs
@@ -619,10 +642,8 @@ class Buffer:
                      stream=None) -> torch.Tensor:
         """The receiver's expansion of the last dedupe dispatch into per-expert rows
         (a tensor shaped like a dispatch's recv_x), ready for combine."""
-        S = self._last_stride()
-        lead = (self.R * S,) if self.packed else (self.R, S)
         if y_recv is None:
-            y_recv = torch.empty(lead + (self.D,), dtype=self.dtype, device=self.device)
+            y_recv = self._new_rows(self.D, stream, self.dtype)
         ep_dedup_expand(self.handle, topk_expert_ids_TK, y_recv, stream)
         return y_recv
 
@@ -636,10 +657,8 @@ class Buffer:
             raise ValueError(f"weights must have {self.E} experts, got {E}")
         if x_recv.shape[-1] != din:
             raise ValueError(f"x_recv has {x_recv.shape[-1]} columns, weights expect {din}")
-        S = self._last_stride()
-        lead = (self.R * S,) if self.packed else (self.R, S)
         if y_recv is None:
-            y_recv = torch.empty(lead + (dout,), dtype=torch.bfloat16, device=self.device)
+            y_recv = self._new_rows(dout, stream)
         ep_expert_gemm(self.handle, x_recv, weights, din, dout, y_recv, stream)
         return y_recv
 
@@ -652,23 +671,8 @@ class Buffer:
                              f"columns, got {tuple(t.shape)}")
         return t
 
-    def _new_rows(self, width: int) -> torch.Tensor:
-        S = self._last_stride()
-        lead = (self.R * S,) if self.packed else (self.R, S)
-        return torch.empty(lead + (width,), dtype=torch.bfloat16, device=self.device)
-
-    def _scratch_rows(self, width: int, stream) -> torch.Tensor:
-        """Rows that only this call's kernels use: from the launching stream's own pool, so
-        that dropping them orders their reuse after those kernels."""
-        if stream is None:
-            return self._new_rows(width)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):
-            return self._new_rows(width)
-
-    def _out_rows(self, t: torch.Tensor | None, name: str, width: int) -> torch.Tensor:
-        return self._new_rows(width) if t is None else self._rows(t, name, width)
+    def _out_rows(self, t: torch.Tensor | None, name: str, width: int, stream) -> torch.Tensor:
+        return self._new_rows(width, stream) if t is None else self._rows(t, name, width)
 
     def _weights(self, w: torch.Tensor, name: str, rows: int | None,
                  cols: int | None) -> tuple[int, int]:
@@ -699,7 +703,7 @@ class Buffer:
         self._rows(x_recv, "x_recv", din)
         if gate_up is not None:
             self._rows(gate_up, "gate_up", dff2)
-        h = self._out_rows(h, "h", dff)
+        h = self._out_rows(h, "h", dff, stream)
         ep_expert_glu(self.handle, x_recv, w_gate_up, din, dff, self._activation(act), gate_up, h,
                       stream)
         return h
@@ -711,8 +715,8 @@ class Buffer:
         ready for combine. save=True returns (y, h, gate_up), what expert_ffn_backward needs."""
         dff2, _ = self._weights(w_gate_up, "w_gate_up", None, None)
         self._weights(w_down, "w_down", None, dff2 // 2)
-        gate_up = self._new_rows(dff2) if save else None
-        h = self._new_rows(dff2 // 2) if save else self._scratch_rows(dff2 // 2, stream)
+        gate_up = self._new_rows(dff2, stream) if save else None
+        h = self._new_rows(dff2 // 2, stream, kept=save)
         self.expert_glu(x_recv, w_gate_up, act, gate_up, h, stream)
         y = self.expert_gemm(h, w_down, stream=stream)
         return (y, h, gate_up) if save else y
@@ -736,10 +740,9 @@ class Buffer:
             if grad_weights is None:
                 if accumulate:
                     raise ValueError("accumulate=True needs grad_weights")
-                grad_weights = torch.empty((self.E, dout, din), dtype=torch.bfloat16,
-                                           device=self.device)
+                grad_weights = self._empty((self.E, dout, din), torch.bfloat16, stream)
             self._weights(grad_weights, "grad_weights", dout, din)
-        grad_x = self._out_rows(grad_x, "grad_x", din) if want_x else None
+        grad_x = self._out_rows(grad_x, "grad_x", din, stream) if want_x else None
         grad_weights = grad_weights if want_weights else None
         ep_expert_gemm_backward(self.handle, grad_y, x_recv if want_weights else None,
                                 weights if want_x else None, din, dout, grad_x, grad_weights,
@@ -755,7 +758,7 @@ class Buffer:
         dout, dff = self._weights(w_down, "w_down", None, None)
         self._rows(grad_y, "grad_y", dout)
         self._rows(gate_up, "gate_up", 2 * dff)
-        grad_gate_up = self._out_rows(grad_gate_up, "grad_gate_up", 2 * dff)
+        grad_gate_up = self._out_rows(grad_gate_up, "grad_gate_up", 2 * dff, stream)
         ep_expert_glu_backward(self.handle, grad_y, w_down, gate_up, dff, dout,
                                self._activation(act), grad_gate_up, stream)
         return grad_gate_up
@@ -769,7 +772,7 @@ class Buffer:
         """(grad_x, grad_w_gate_up, grad_w_down) of expert_ffn, from the gate_up and h that
         expert_ffn(..., save=True) returned. The weight gradients may be given as bfloat16
         or float32 tensors, with accumulate=True to add to them."""
-        grad_gate_up = self._scratch_rows(gate_up.shape[-1], stream)
+        grad_gate_up = self._new_rows(gate_up.shape[-1], stream, kept=False)
         self.expert_glu_backward(grad_y, w_down, gate_up, act, grad_gate_up, stream)
         _, grad_w_down = self.expert_gemm_backward(grad_y, h, w_down, want_x=False,
                                                    grad_weights=grad_w_down,
@@ -786,7 +789,7 @@ class Buffer:
         per expert of a decode batch."""
         self._weights(weights.codes, "weights.codes", None, None)
         self._rows(x_recv, "x_recv", weights.din)
-        y_recv = self._out_rows(y_recv, "y_recv", weights.rows)
+        y_recv = self._out_rows(y_recv, "y_recv", weights.rows, stream)
         ep_expert_gemv_w4(self.handle, x_recv, weights, weights.din, weights.rows, y_recv, stream)
         return y_recv
 
@@ -798,7 +801,7 @@ class Buffer:
             raise ValueError(f"w_gate_up must hold gate and up rows, got {w_gate_up.rows} rows")
         dff = w_gate_up.rows // 2
         self._rows(x_recv, "x_recv", w_gate_up.din)
-        h = self._out_rows(h, "h", dff)
+        h = self._out_rows(h, "h", dff, stream)
         ep_expert_glu_w4(self.handle, x_recv, w_gate_up, w_gate_up.din, dff,
                          self._activation(act), h, stream)
         return h
@@ -810,7 +813,7 @@ class Buffer:
             raise ValueError(f"w_down takes {w_down.din} columns, w_gate_up gives "
                              f"{w_gate_up.rows // 2}")
         h = self.expert_glu_w4(x_recv, w_gate_up, act,
-                               self._scratch_rows(w_down.din, stream), stream)
+                               self._new_rows(w_down.din, stream, kept=False), stream)
         return self.expert_gemv_w4(h, w_down, y_recv, stream)
 
     def _last_stride(self) -> int:
