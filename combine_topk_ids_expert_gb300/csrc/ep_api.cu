@@ -751,10 +751,10 @@ ep_status ep_expert_gemm(ep_buffer* buf, const void* x_recv, const void* weights
     if (!buf->has_layout) return EP_ERR_NO_LAYOUT;
     if (buf->cfg.dtype != EP_BF16) return EP_ERR_INVALID_ARG;
     if (din < 64 || din % 64 != 0 || dout < 128 || dout % 128 != 0) return EP_ERR_INVALID_ARG;
-    if (!x_recv || !weights || !y_recv) return EP_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)buf->cfg.num_ranks * buf->last_S;
+    if (!weights || (rows > 0 && (!x_recv || !y_recv))) return EP_ERR_INVALID_ARG;
     if (!is_aligned(x_recv, 16) || !is_aligned(weights, 16) || !is_aligned(y_recv, 16))
         return EP_ERR_ALIGNMENT;
-    const int64_t rows = (int64_t)buf->cfg.num_ranks * buf->last_S;
     if (rows <= 0) return EP_OK;
     if ((int64_t)buf->cfg.num_experts * dout > INT32_MAX) return EP_ERR_CAPACITY;
     // Row tiles times column blocks (and work units) are counted in int32.
@@ -788,7 +788,8 @@ ep_status ep_expert_gemm(ep_buffer* buf, const void* x_recv, const void* weights
 
 // What the experts' products share: a bf16 buffer with a layout, sizes of the
 // documented multiples, and counts (rows, tiles, weight lines) that fit int32.
-// *rows: receive rows of the call (0: nothing routed, no row operand is needed).
+// *rows: receive rows of the call. 0 (an empty step): there is nothing to read or write in
+// row operands, and they may be NULL, which is what an empty tensor's address is.
 static ep_status check_expert(const ep_buffer* b, int64_t width_a, int64_t width_b, int64_t lines,
                               int64_t* rows)
 {
@@ -837,7 +838,7 @@ ep_status ep_expert_glu(ep_buffer* buf, const void* x_recv, const void* w_gate_u
     const ep_status st = check_expert(buf, din, dff, 2 * dff, &rows);
     if (st != EP_OK) return st;
     if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
-    if (!x_recv || !w_gate_up || !h) return EP_ERR_INVALID_ARG;
+    if (!w_gate_up || (rows > 0 && (!x_recv || !h))) return EP_ERR_INVALID_ARG;
     if (!is_aligned(x_recv, 16) || !is_aligned(w_gate_up, 16) || !is_aligned(gate_up, 16) ||
         !is_aligned(h, 16))
         return EP_ERR_ALIGNMENT;
@@ -859,7 +860,7 @@ ep_status ep_expert_glu_backward(ep_buffer* buf, const void* grad_y, const void*
     const ep_status st = check_expert(buf, dff, dout, dout, &rows);
     if (st != EP_OK) return st;
     if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
-    if (!grad_y || !w_down || !gate_up || !grad_gate_up) return EP_ERR_INVALID_ARG;
+    if (!w_down || (rows > 0 && (!grad_y || !gate_up || !grad_gate_up))) return EP_ERR_INVALID_ARG;
     if (!is_aligned(grad_y, 16) || !is_aligned(w_down, 16) || !is_aligned(gate_up, 16) ||
         !is_aligned(grad_gate_up, 16))
         return EP_ERR_ALIGNMENT;
@@ -881,8 +882,11 @@ ep_status ep_expert_gemm_backward(ep_buffer* buf, const void* grad_y, const void
     const ep_status st = check_expert(buf, din, dout, dout, &rows);
     if (st != EP_OK) return st;
     if (grad_w_dtype != EP_BF16 && grad_w_dtype != EP_F32) return EP_ERR_INVALID_ARG;
-    if (!grad_x && !grad_w) return EP_ERR_INVALID_ARG;
-    if (!grad_y || (grad_x && !weights) || (grad_w && !x_recv)) return EP_ERR_INVALID_ARG;
+    if (rows > 0) {
+        if (!grad_x && !grad_w) return EP_ERR_INVALID_ARG;
+        if (!grad_y || (grad_w && !x_recv)) return EP_ERR_INVALID_ARG;
+    }
+    if (grad_x && !weights) return EP_ERR_INVALID_ARG;
     if (!is_aligned(grad_y, 16) || !is_aligned(x_recv, 16) || !is_aligned(weights, 16) ||
         !is_aligned(grad_x, 16) || !is_aligned(grad_w, 16))
         return EP_ERR_ALIGNMENT;
@@ -925,11 +929,11 @@ static ep_status enqueue_w4(ep_buffer* b, const void* x, const ep_w4* w, int64_t
     if (w->scale_dtype != EP_BF16 && w->scale_dtype != EP_F32) return EP_ERR_INVALID_ARG;
     if (din < w->group || din % w->group != 0 || dout < 8 || dout % 8 != 0)
         return EP_ERR_INVALID_ARG;
-    if (!x || !w->codes || !w->scales || !y) return EP_ERR_INVALID_ARG;
+    const int64_t E = b->cfg.num_experts, rows = (int64_t)b->cfg.num_ranks * b->last_S;
+    if (!w->codes || !w->scales || (rows > 0 && (!x || !y))) return EP_ERR_INVALID_ARG;
     if (!is_aligned(x, 16) || !is_aligned(w->codes, 16) || !is_aligned(y, 16) ||
         !is_aligned(w->scales, (uintptr_t)elem_bytes(w->scale_dtype)))
         return EP_ERR_ALIGNMENT;
-    const int64_t E = b->cfg.num_experts, rows = (int64_t)b->cfg.num_ranks * b->last_S;
     if (din > INT32_MAX || dout > INT32_MAX / 2 / E) return EP_ERR_CAPACITY;
     if (rows <= 0) return EP_OK;
     // Row chunks times column blocks, and weight rows, are counted in int32.

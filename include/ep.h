@@ -344,7 +344,9 @@ EP_API ep_status ep_dedup_expand(ep_buffer* buf, const int32_t* topk_expert_ids_
  * interleaved in proportion with the others' (tensor-bound: weights reused
  * from L2), so skewed routing keeps both HBM and the tensor cores busy;
  * EP_GEMM_LIGHT_ROWS=n sets the threshold (0: all tiles in expert order).
- * The schedule changes which SM computes a tile, never its K order. */
+ * The schedule changes which SM computes a tile, never its K order. After a
+ * layout with num_tokens_per_rank 0 there are no rows: x_recv and y_recv may be
+ * NULL and nothing is written. */
 EP_API ep_status ep_expert_gemm(ep_buffer* buf, const void* x_recv, const void* weights,
                                 int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
 
@@ -359,7 +361,9 @@ EP_API ep_status ep_expert_gemm(ep_buffer* buf, const void* x_recv, const void* 
  * ([R*S][width], strided or packed; rows of no expert are neither read into any
  * result nor written). Tensors are dense, bf16 unless said, 16-byte aligned, on the
  * buffer's device; outputs must not overlap inputs. din, dff, dout are given as for
- * the forward product: din % 64 == 0, dff % 128 == 0, dout % 128 == 0. */
+ * the forward product: din % 64 == 0, dff % 128 == 0, dout % 128 == 0. After a layout
+ * with num_tokens_per_rank 0 there are no rows: every [R*S][..] operand may be NULL (an
+ * empty tensor's address), and only the weights' gradients are written. */
 
 /* The gate's activation. */
 typedef enum {
