@@ -23,10 +23,12 @@
 //     without passing shared memory again) and the terms of at most NR rows as B, one
 //     after the other into the same accumulator (4 rows: side by side in one MMA, and
 //     the drain adds them). Each scale group has its own;
-//   - draining a group, a lane holds one output column: per row, its sum times the
-//     column's scale, the group's sum of x times minus scale and zero point, for the
-//     groups of a block of x together, and an fma by what undoes the block's scale, two
-//     rows an instruction.
+//   - draining a group, a lane holds one output column: per row, its sum less the zero
+//     point times the group's sum of x, times the column's scale, for the groups of a
+//     block of x together, and an fma by what undoes the block's scale, two rows an
+//     instruction. The group's sum is of hi + lo, what the tensor cores multiplied, so
+//     that codes that equal the zero point leave nothing behind, and it is taken off
+//     before the scale's rounding.
 //
 // Work: tiles of 128 columns (gated: 64 gate and 64 up) of all (expert, chunk of NR
 // rows), laid end to end and cut into contiguous shares, one per CTA (one CTA per SM).
@@ -210,9 +212,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 // The two e4m3 terms (round to nearest even) of two fp32 values below 256 that are
 // bf16 numbers times a power of two: by way of f16, which holds 2^-17 and above exactly
 // (what is smaller has zeros as its terms either way) and the first term's difference too.
-__device__ __forceinline__ void w4_terms(uint64_t v, uint32_t* hi, uint32_t* lo)
+// Returns the terms' sum, the two values that the products are of.
+__device__ __forceinline__ uint64_t w4_terms(uint64_t v, uint32_t* hi, uint32_t* lo)
 {
-    uint32_t f, b, d;
+    uint32_t f, b, d, c;
     uint16_t h, l;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f)
         : "f"(__uint_as_float((uint32_t)(v >> 32))), "f"(__uint_as_float((uint32_t)v)));
@@ -220,8 +223,14 @@ __device__ __forceinline__ void w4_terms(uint64_t v, uint32_t* hi, uint32_t* lo)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(f), "r"(b));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"(l));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(c));   // exact: at most f's bits
     *hi = h;
     *lo = l;
+    float x0, x1;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(x0), "=f"(x1) : "r"(b));
+    return pair_of(x0, x1);
 }
 
 // A barrier among some warps of the CTA that gives up on an abort: each warp arrives
@@ -350,7 +359,7 @@ __device__ __forceinline__ int4 w4_finite(const int4& v)
 
 // Converts the tile's rows of x, contraction elements [k0, k0 + panel): two e4m3 terms
 // of each block of 128 elements, scaled, as B of the MMAs; what undoes the scale; and
-// the scaled groups' sums. An infinity or a NaN counts as zero here and
+// the groups' sums of both terms. An infinity or a NaN counts as zero here and
 // marks its row (its terms are added to the row's results one by one). Warps 2 and
 // up; ct: thread among them.
 //
@@ -418,8 +427,7 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
                 for (int u = 0; u < 2; ++u) {
                     const uint64_t v = mul2(pair_of(w4_element(w[i], j + 4 * u),
                                                     w4_element(w[i], j + 4 * u + 2)), scale2);
-                    sum2 = add2(sum2, v);
-                    w4_terms(v, &h[u], &l[u]);
+                    sum2 = add2(sum2, w4_terms(v, &h[u], &l[u]));
                 }
                 hi[2 * i + j] = h[0] | (h[1] << 16);
                 lo[2 * i + j] = l[0] | (l[1] << 16);
@@ -567,7 +575,7 @@ __device__ __forceinline__ void w4_load_scales(const W4Args& a, const W4Lane& l,
 }
 
 // Into the column's places [8][128] of a set: the scale times the codes' 2^9, and minus
-// the scale times the zero point.
+// the zero point in the codes' units of 2^-9.
 __device__ __forceinline__ void w4_keep_scales(const W4Scales& v, bool f32, bool wide, float2* mine)
 {
 #pragma unroll
@@ -576,7 +584,7 @@ __device__ __forceinline__ void w4_keep_scales(const W4Scales& v, bool f32, bool
         const uint32_t bits = f32 ? v.s[j] : !wide ? v.s[j] << 16 : (j & 1) ? pair & 0xFFFF0000u : pair << 16;
         const float scale = __uint_as_float(bits);
         mine[j * 128] = make_float2(scale * 512.0f,
-                                    -scale * (float)((v.z[j >> 2] >> (8 * (j & 3))) & 0xFFu));
+                                    -0x1p-9f * (float)((v.z[j >> 2] >> (8 * (j & 3))) & 0xFFu));
     }
 }
 
@@ -977,12 +985,12 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
 #pragma unroll
                                 for (int u0 = 0; u0 < C::PG; u0 += C::SB) {
                                     const int gi = g0 + p0 + u0;
-                                    uint64_t sx[C::SB], sy[C::SB];
+                                    uint64_t sx[C::SB], nz[C::SB];
 #pragma unroll
                                     for (int u = 0; u < C::SB; ++u) {
                                         const float2 v = sc[(gi + u) * 128];
                                         sx[u] = pair_of(v.x, v.x);
-                                        sy[u] = pair_of(v.y, v.y);
+                                        nz[u] = pair_of(v.y, v.y);
                                     }
                                     const ulonglong2* un =
                                         reinterpret_cast<const ulonglong2*>(undo + gi * C::GROUP / 128 * NR);
@@ -1000,10 +1008,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                 v0 = add2(v0, pair_of(v[NR], v[NR + 1]));
                                                 v1 = add2(v1, pair_of(v[NR + 2], v[NR + 3]));
                                             }
+                                            v0 = fma2(nz[u], x4.x, v0);
+                                            v1 = fma2(nz[u], x4.y, v1);
                                             d0 = u == 0 ? mul2(sx[u], v0) : fma2(sx[u], v0, d0);
                                             d1 = u == 0 ? mul2(sx[u], v1) : fma2(sx[u], v1, d1);
-                                            d0 = fma2(sy[u], x4.x, d0);
-                                            d1 = fma2(sy[u], x4.y, d1);
                                         }
                                         acc[2 * n4] = fma2(u4.x, d0, acc[2 * n4]);
                                         acc[2 * n4 + 1] = fma2(u4.y, d1, acc[2 * n4 + 1]);
