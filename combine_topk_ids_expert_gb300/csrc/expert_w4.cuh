@@ -13,11 +13,14 @@
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
 //   - 128 elements of a row of x are scaled by a power of two that puts the largest
-//     into [128, 256) and split into two e4m3 terms, x = hi + lo. A bf16 has 8
-//     significant bits, an e4m3 number 4: the two are exact for every element down
-//     to 2^-9 of the block's largest, and off by at most 2^-17 of it below (e4m3 ends
-//     at 2^-9), less than what fp32 sums of the block lose to rounding in the worst case
-//     and far below the result's bf16;
+//     into [128, 256) and split into two 8-bit terms, x = hi + lo. A bf16 has 8
+//     significant bits. hi is e4m3 (4 bits, down to 2^-9); what it leaves of a number of
+//     the binade 2^e is 0 to 8 times 2^(e-7), which 3 bits hold: lo is e5m2, down to
+//     2^-16 (with 4 rows e4m3 of 2^5 times it, down to 2^-14). So x is exact down to
+//     2^-13 of the block's largest, and off by at most 2^-21 of it below, where hi has run
+//     out of bits. With one element 2^12 times the others' size these lose 0.06% to that,
+//     less than bf16 has lost already (with lo as plain e4m3 it was 1.8%); the fp32 sums
+//     lose as much of them beside a product of its size;
 //   - the tensor cores multiply and sum in fp32: tcgen05.mma.kind::f8f6f4 with the
 //     codes as A (128 output columns on TMEM's lanes, written there by tcgen05.st
 //     without passing shared memory again) and the terms of at most NR rows as B, one
@@ -89,12 +92,14 @@ struct W4Cfg {
     // ring, 648 against 661 us (gated block, 32 tokens over 256 experts).
     static constexpr int STAGES = GROUP == 32 ? 6 : kW4MaxStages;
     static constexpr int STEPS = GROUP / 32;                 // MMAs (K = 32) of a group
-    // kind::f8f6f4: fp32 accumulate, A and B e4m3 (0), both K-major, N, M = 128.
+    // kind::f8f6f4: fp32 accumulate, A and B e4m3 (0), both K-major, N, M = 128; and with
+    // the second term, B e5m2 (1 at bits 10-12).
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    static constexpr uint32_t kIdescLo = kIdesc | (1u << 10);
     static constexpr uint32_t kTermBytes = NR * 128;         // a term of 128 contraction elements
     static constexpr uint32_t kPanelBytes = 2 * kTermBytes;  // hi rows, then lo rows
-    // With 4 rows both terms fit the MMA's columns and the drain adds them up; with more,
-    // a second MMA adds the second term to the first one's accumulator.
+    // With 4 rows both terms fit the MMA's columns, so both are e4m3, and the drain adds
+    // 2^-5 of the second; with more, a second MMA adds it to the first one's accumulator.
     static constexpr bool kBothTerms = 2 * NR <= 8;
     static constexpr int LD = kBothTerms ? 2 * NR : NR;      // accumulator columns of a group to drain
     static constexpr int PG = GB < 32 / LD ? GB : 32 / LD;   // groups that a lane drains at once
@@ -202,18 +207,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// The two e4m3 terms (round to nearest even) of two fp32 values below 256 that are
-// bf16 numbers times a power of two: by way of f16, which holds 2^-17 and above exactly
-// (what is smaller has zeros as its terms either way) and the first term's difference too.
-// Returns the terms' sum, the two values that the products are of.
-__device__ __forceinline__ uint64_t w4_terms(uint64_t v, uint32_t* hi, uint32_t* lo)
+// The two terms (round to nearest even) of two fp32 values below 256 that are bf16 numbers
+// times a power of two: by way of f16, which holds 2^-17 and above exactly (what is smaller
+// has zeros as its terms, or lo's least number) and the first term's difference too.
+// SCALED: lo is 2^5 times the second term in e4m3, else the second term in e5m2, the upper
+// half of an f16. Adds hi + lo, the two values that the products are of, to *sum (a pair).
+template <bool SCALED>
+__device__ __forceinline__ void w4_terms(uint64_t v, uint32_t* hi, uint32_t* lo, uint64_t* sum)
 {
     uint32_t f, b, d, c;
     uint16_t h, l;
@@ -222,15 +222,24 @@ __device__ __forceinline__ uint64_t w4_terms(uint64_t v, uint32_t* hi, uint32_t*
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(f));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(f), "r"(b));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"(l));
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(c));   // exact: at most f's bits
+    // The sums hi + lo are exact: at most f's bits.
+    if (SCALED) {
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x50005000u));   // 2^5
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"(l));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(b) : "r"(c), "r"(0x28002800u), "r"(b));   // 2^-5
+    } else {
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
+        c = __byte_perm((uint32_t)l, 0u, 0x1404);
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(c));
+    }
     *hi = h;
     *lo = l;
-    float x0, x1;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(x0), "=f"(x1) : "r"(b));
-    return pair_of(x0, x1);
+    float s0 = __uint_as_float((uint32_t)*sum), s1 = __uint_as_float((uint32_t)(*sum >> 32));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "add.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
+        : "+f"(s0), "+f"(s1) : "r"(b));
+    *sum = pair_of(s0, s1);
 }
 
 // A barrier among some warps of the CTA that gives up on an abort: each warp arrives
@@ -357,7 +366,7 @@ __device__ __forceinline__ int4 w4_finite(const int4& v)
     return make_int4(w[0], w[1], w[2], w[3]);
 }
 
-// Converts the tile's rows of x, contraction elements [k0, k0 + panel): two e4m3 terms
+// Converts the tile's rows of x, contraction elements [k0, k0 + panel): two 8-bit terms
 // of each block of 128 elements, scaled, as B of the MMAs; what undoes the scale; and
 // the groups' sums of both terms. An infinity or a NaN counts as zero here and
 // marks its row (its terms are added to the row's results one by one). Warps 2 and
@@ -427,7 +436,7 @@ __device__ __noinline__ bool w4_convert(const uint16_t* x, int rows, int din, in
                 for (int u = 0; u < 2; ++u) {
                     const uint64_t v = mul2(pair_of(w4_element(w[i], j + 4 * u),
                                                     w4_element(w[i], j + 4 * u + 2)), scale2);
-                    sum2 = add2(sum2, w4_terms(v, &h[u], &l[u]));
+                    w4_terms<C::kBothTerms>(v, &h[u], &l[u], &sum2);
                 }
                 hi[2 * i + j] = h[0] | (h[1] << 16);
                 lo[2 * i + j] = l[0] | (l[1] << 16);
@@ -793,7 +802,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                          i % C::STEPS != 0 ? 1u : 0u);
                             if (!C::kBothTerms)
                                 umma_e4m3_ts(to, at + (uint32_t)step * 8u,
-                                             hi + (C::kTermBytes >> 4), C::kIdesc, 1u);
+                                             hi + (C::kTermBytes >> 4), C::kIdescLo, 1u);
                         }
                         umma_commit<false>(d_full0 + 8u * ds.slot);
                         if (g0 + C::GB == C::GPS) umma_commit<false>(a_empty0 + 8u * as.slot);
@@ -1005,8 +1014,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap tm_w,
                                             const uint32_t* v = q + (u0 + u) * C::LD + 4 * n4;
                                             uint64_t v0 = pair_of(v[0], v[1]), v1 = pair_of(v[2], v[3]);
                                             if constexpr (C::kBothTerms) {
-                                                v0 = add2(v0, pair_of(v[NR], v[NR + 1]));
-                                                v1 = add2(v1, pair_of(v[NR + 2], v[NR + 3]));
+                                                v0 = fma2(pair_of(0x1p-5f, 0x1p-5f),
+                                                          pair_of(v[NR], v[NR + 1]), v0);
+                                                v1 = fma2(pair_of(0x1p-5f, 0x1p-5f),
+                                                          pair_of(v[NR + 2], v[NR + 3]), v1);
                                             }
                                             v0 = fma2(nz[u], x4.x, v0);
                                             v1 = fma2(nz[u], x4.y, v1);

@@ -421,12 +421,15 @@ typedef struct {
 /* y_recv[p][o] = sum_i w[e][o][i] * x_recv[p][i] for each expert's rows p: x_recv
  * [R*S][din], y_recv [R*S][dout], bf16, in the receive layout as for ep_expert_gemm
  * (same buffers, errors and rows left alone); din % group == 0, dout % 8 == 0. Codes
- * and x are multiplied on the tensor cores as fp8 (e4m3), x as the sum of two such
- * terms of each 128 elements' scaled values: exact for an element down to 2^-9 of the
- * largest of its 128, and within 2^-17 of that one below. Sums are fp32, a group's
- * scaled in fp32, in an order fixed by the sizes and by how many rows an expert has on
- * average, and rounded once to bf16. An infinity or a NaN
- * in x reaches exactly its own row's results. */
+ * and x are multiplied on the tensor cores as fp8, x as the sum x' of two such terms of
+ * each 128 elements' scaled values: exact for an element down to 2^-13 of the largest of
+ * its 128, and within 2^-21 of that one below. A group's results are
+ *     scale * (sum of code * x' - zero * sum of x')
+ * in fp32, so an element enters with its weight, x' - x too; beside an element that is
+ * 2^16 or more times as large, the others lose bits to the fp32 sums as well, whatever
+ * its weight. Groups are added in fp32, all in an order fixed by the sizes and by how many
+ * rows an expert has on average, and rounded once to bf16. An infinity or a NaN in x
+ * reaches exactly its own row's results. */
 EP_API ep_status ep_expert_gemv_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weights,
                                    int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
 

@@ -19,7 +19,7 @@ from test_expert_w4_gpu import dequantised, weights
 pytestmark = pytest.mark.gpu
 
 F64 = torch.float64
-EXACT, BITS = 9, 17
+EXACT, BITS = 13, 21
 ROWS = [2, 7, 24]      # taken 4, 8 and 16 at a time
 
 
