@@ -482,12 +482,21 @@ void set_attrs(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, bool pair, bo
 template <typename Kernel>
 int cluster_grid(Kernel kernel, int threads, size_t smem, int num_sms)
 {
+    // Kernels of one type share this function: an entry says whose it is. (A caller with
+    // more kernels and devices than entries asks each time.)
+    struct Entry {
+        const void* kernel;
+        int dev, fit;
+    };
     static std::mutex mu;
-    static int cached[64] = {};
-    int dev = 0;
+    static Entry entries[64];
+    static int used = 0;
+    int dev = 0, fit = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const void* k = reinterpret_cast<const void*>(kernel);
     std::lock_guard<std::mutex> lock(mu);
-    int fit = (dev >= 0 && dev < 64) ? cached[dev] : 0;
+    for (int i = 0; i < used && fit == 0; ++i)
+        if (entries[i].kernel == k && entries[i].dev == dev) fit = entries[i].fit;
     if (fit == 0) {
         int sms = 0;
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -503,7 +512,7 @@ int cluster_grid(Kernel kernel, int threads, size_t smem, int num_sms)
             return 0;
         }
         fit = 2 * n;
-        if (dev >= 0 && dev < 64) cached[dev] = fit;
+        if (used < 64) entries[used++] = {k, dev, fit};
     }
     const int budget = num_sms & ~1;
     return fit < budget ? fit : budget;
