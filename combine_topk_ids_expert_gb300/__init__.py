@@ -729,6 +729,12 @@ class Buffer:
         """(grad_x, grad_weights) of expert_gemm, None for one that is not wanted.
         grad_weights may be a bfloat16 or float32 tensor [E, dout, din]; accumulate=True
         adds to it (gradient accumulation over micro-batches)."""
+        if not want_x and not want_weights:
+            raise ValueError("neither gradient is wanted: want_x or want_weights")
+        if want_x and weights is None:
+            raise ValueError("grad_x needs weights (or want_x=False)")
+        if want_weights and x_recv is None:
+            raise ValueError("grad_weights needs x_recv (or want_weights=False)")
         dout = grad_y.shape[-1]
         if want_x:
             _, din = self._weights(weights, "weights", dout, None)
