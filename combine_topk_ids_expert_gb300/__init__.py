@@ -470,7 +470,11 @@ class DedupResult:
 
 class Buffer:
     """A dispatcher buffer: one workspace sized from num_max_tokens_per_rank,
-    reused by every call (no allocation after construction)."""
+    reused by every call (no allocation after construction).
+
+    stream: where a call's kernels run, the current stream by default. On another one, the
+    caller sees to it that inputs are complete in its order and stay until it is done with
+    them; what the call returns is complete in its order and may be dropped at any time."""
 
     def __init__(self, num_max_tokens_per_rank: int, hidden: int, num_experts: int,
                  num_ranks: int, topk: int, dtype: torch.dtype = torch.bfloat16,

@@ -4,18 +4,21 @@
 
 namespace ep {
 
-// Rows taken at once. 16 read the weights fewer times (the second chunk finds them in
-// L2) and share a tile's barriers and unpacking: 283 against 413 us (64 rows to each of
-// 64 experts, 2048 x 4096, groups of 128), 73 against 81 us (8 rows to each), 25.4 against
-// 28.1 us (7.5 rows to each of 8, 4096 x 4096), and lose 23.8 to 22.4 us with 5. 8 leave room
-// for all of a longer row of x (a panel of it is converted again for every tile
-// otherwise) and win where experts have one row more than 16 holds: 43 against 45 us (64
-// tokens, 2 of 8 experts each, 4096 x 4096, groups of 64). 32 at once were no faster than
-// 16 anywhere: the drain's time goes with the rows.
-// 4, where 1.6 times the mean is at most 2, take half the MMAs and multiplications of 8: 113
-// against 116 us (8 tokens, 8 of 64 experts each, 7168 x 4096, groups of 128), 15.5
-// against 16.0 us (groups of 32); with a mean of 2 rows, some experts' second chunks cost
-// what that saves, 155 against 148 us.
+// Rows taken at once, by expected_rows (1.6 times the mean, which few experts exceed).
+// 16 read the weights fewer times (the second chunk finds them in L2) and share a tile's
+// barriers and unpacking: 288 against 418 us (64 rows to each of 64 experts, 4096 -> 2048,
+// groups of 128), 74.7 against 81.7 us (8 rows to each), 26.3 against 29.0 us (7.5 rows to
+// each of 8, 4096 -> 4096), and lose 24.4 to 23.1 us with 5. They also lose where the mean
+// is 16, so that about half of the experts have a second chunk all the same: 46.6 against
+// 43.1 us (64 tokens, 2 of 8 experts each, 4096 -> 4096, groups of 64). Where x of 16 rows
+// would not fit whole beside the ring (asked for groups of 32, the least that fits: above
+// 4096 elements, less with hundreds of experts) 8 are taken: a panel of it is converted
+// again for every tile, 98.2 against 60.5 us (64 tokens, 2 of 8, 7168 -> 4096, groups of
+// 128). 32 at once were no faster than 16 anywhere: the drain's time goes with the rows.
+// 4, where expected_rows is at most 2, take half the MMAs and multiplications of 8: 114.4
+// against 116.7 us (8 tokens, 8 of 64 experts each, 7168 -> 4096, groups of 128), 203.7
+// against 210.0 us (groups of 32); with a mean of 2 rows, some experts' second chunks cost
+// what that saves, 156.7 against 148.7 us.
 cudaError_t launch_expert_w4(const W4Args& a, int64_t expected_rows, int num_sms,
                              const LaunchOpts& o)
 {

@@ -8,7 +8,7 @@
 // codes, 2900 issue slots for 32768 of them. Unpacking codes into 16-bit operands on
 // mma.sync (a shift, a mask and a subtraction for every two, then operands of x and
 // scales at 16 x 8 outputs a step) took 3600 instructions for as many, and 328 us where
-// this kernel takes 175 and 1500 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
+// this kernel takes 177 and 1510 (4 rows, 64 x 4096 x 7168 codes, groups of 128). So:
 //   - a nibble q, zero-extended to a byte, IS an fp8 number: read as e4m3 it is
 //     q * 2^-9 exactly (the subnormals and the first binade share one step). So
 //     8 codes become two 32-bit operands with one shift and two masks;
@@ -19,8 +19,8 @@
 //     2^-16 (with 4 rows e4m3 of 2^5 times it, down to 2^-14). So x is exact down to
 //     2^-13 of the block's largest, and off by at most 2^-21 of it below, where hi has run
 //     out of bits. With one element 2^12 times the others' size these lose 0.06% to that,
-//     less than bf16 has lost already (with lo as plain e4m3 it was 1.8%); the fp32 sums
-//     lose as much of them beside a product of its size;
+//     less than bf16 has lost already (with lo as plain e4m3 it was 1.8%), and fp32 sums
+//     with a product of its size lose about as much;
 //   - the tensor cores multiply and sum in fp32: tcgen05.mma.kind::f8f6f4 with the
 //     codes as A (128 output columns on TMEM's lanes, written there by tcgen05.st
 //     without passing shared memory again) and the terms of at most NR rows as B, one
@@ -36,25 +36,25 @@
 // Work: tiles of 128 columns (gated: 64 gate and 64 up) of all (expert, chunk of NR
 // rows), laid end to end and cut into contiguous shares, one per CTA (one CTA per SM).
 // Equal shares of 16-column blocks instead left tiles cut at both ends, which take as long
-// as whole ones wherever draining a slice takes longer than copying it: 66 against 57 us
-// (16 rows, 8 x 4096 x 4096 codes, groups of 64), and 203 against 197 us (4 rows, 64 x
-// 4096 x 7168, groups of 128). x is converted when the expert or the chunk changes and
+// as whole ones wherever draining a slice takes longer than copying it: 66 where whole tiles
+// then took 57 us (16 rows, 8 x 4096 x 4096 codes, groups of 64), 203 and 197 us (4 rows, 64
+// x 4096 x 7168, groups of 128). x is converted when the expert or the chunk changes and
 // stays in shared memory for the tiles that follow; the copies of the codes run ahead
 // over tile boundaries all the while.
 //
-// Measured (a graph of calls on three sets of weights, one GB300): 175 us, 5.5 TB/s or
-// 82% of a copy's rate (the same 64 x 4096 x 7168 codes); 29 us, 4.2 TB/s (8 experts of
-// these, one row each); 45 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
-// where converting x (9 us of it) and draining the scale groups are what takes long.
+// Measured (a graph of calls on three sets of weights, one GB300): 177 us, 5.4 TB/s or
+// 81% of a copy's rate (the same 64 x 4096 x 7168 codes); 29.5 us, 4.1 TB/s (8 experts of
+// these, one row each); 46.7 us (16 rows, 8 x 4096 x 4096, groups of 64, zero points),
+// where converting x (about 10 us of it) and draining the scale groups are what takes long.
 //
 // Roles (12 warps): 0 copies codes (TMA, slices of 256 codes of 64 columns a box, 128-byte
 // swizzle), 1 issues the MMAs, 2-5 move codes to TMEM, 6-9 drain, 10-11 load scales and
-// zero points and lay them out for the drain (which, doing that itself, took 85 us where
-// it takes 76, and 706 where it takes 648: 64 tokens over 8 and 32 over 256 experts,
-// gated block); 2-9 convert x together. With 16 warps (a second set that unpacks or
-// drains) a thread would have 128 registers instead of 168 and the drain spills, and with
-// shared memory full what spills goes to L2: 82 against 67 us; reading the next
-// accumulators ahead spills too, 53 against 46 us. Every wait is bounded.
+// zero points and lay them out for the drain (which, doing that itself, took 85 and 706 us
+// where it then took 76 and 648 without: 64 tokens over 8 and 32 over 256 experts, gated
+// block); 2-9 convert x together. With 16 warps (a second set that unpacks or drains) a
+// thread would have 128 registers instead of 168 and the drain spills, and with shared
+// memory full what spills goes to L2: 82 where it then took 67 us; reading the next
+// accumulators ahead spills too, 53 where it then took 46 us. Every wait is bounded.
 #pragma once
 
 #include "umma.cuh"

@@ -80,8 +80,8 @@ __device__ __forceinline__ int ragged_rows(int rows)
 
 // A ragged slice takes longer to get ready than the ring looks ahead, so it is copied
 // kEarly slices before its turn: it is at position ragged_at of the ring's order and
-// still the last to be multiplied (see the roles). 1385 and 1496 TFLOP/s without
-// (mixtral rows, down and gate/up weights), 1637 and 1714 with nothing to repair.
+// still the last to be multiplied (see the roles). 1366 and 1402 TFLOP/s without, 1468 and
+// 1494 with (mixtral rows, down and gate/up weights); 1637 and 1714 with nothing to repair.
 constexpr int kEarly = 2;
 __device__ __forceinline__ int ragged_at(const WUnit& w)
 {
