@@ -27,14 +27,17 @@ def pool_of(t):
     raise AssertionError("not the allocator's memory")
 
 
-def block_state(p):
+def block_states(places):
+    """The allocator's words for the blocks at these addresses, from one look at its record."""
+    found = dict.fromkeys(places, "gone")
     for seg in torch.cuda.memory_snapshot():
         at = seg["address"]
         for b in seg["blocks"]:
-            if at <= p < at + b["size"]:
-                return b["state"]
+            for p in places:
+                if at <= p < at + b["size"]:
+                    found[p] = b["state"]
             at += b["size"]
-    return "gone"
+    return found
 
 
 def setup():
@@ -105,14 +108,14 @@ def test_dropped_results_wait_for_the_current_stream(name):
     got = results(name, c, s)
     torch.cuda.synchronize()
     places = [t.data_ptr() for t in got]
-    torch.cuda._sleep(200_000_000)   # about a tenth of a second of the current stream's time
+    torch.cuda._sleep(400_000_000)   # about a fifth of a second of the current stream's time
     del got
-    states = [block_state(p) for p in places]
+    states = block_states(places)
     busy = not torch.cuda.current_stream().query()
     torch.cuda.synchronize()
     assert busy, "the current stream was done too early to tell"
     # in use no more, and not free yet
-    assert all(t.startswith("active_") and t.endswith("_free") for t in states), states
+    assert all(t.startswith("active_") and t.endswith("_free") for t in states.values()), states
     c.done()
 
 
