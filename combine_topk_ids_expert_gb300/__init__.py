@@ -17,6 +17,7 @@ everyday use and returns torch views into the workspace::
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from dataclasses import dataclass
 from functools import cached_property
@@ -25,10 +26,11 @@ import torch
 
 from . import _abi
 from ._abi import (EP_ACT_GELU, EP_ACT_SILU, EP_BF16, EP_DEVERR_BAD_ID, EP_DEVERR_DEBUG_STRAY, EP_DEVERR_DEBUG_UNWRITTEN,
-                   EP_DEVERR_ROW_OOB, EP_DEVERR_TIMEOUT, EP_F32, EP_NOALLOC_SCRATCH_BYTES,
+                   EP_DEVERR_ROW_OOB, EP_DEVERR_TIMEOUT, EP_F32, EP_FP4_MX, EP_FP4_NV,
+                   EP_NOALLOC_SCRATCH_BYTES, EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX,
                    EP_LAYOUT_PACKED, EP_LAYOUT_STRIDED, EP_PERMUTE_BULK, EP_PERMUTE_DEFAULT,
                    EP_PERMUTE_VEC, EpBufferInfo, EpConfig, EpDedupOut, EpDispatchOut, EpError,
-                   EpLayout, EpW4, check)
+                   EpFp4, EpLayout, EpW4, check)
 
 __all__ = [
     "Buffer", "Layout", "DispatchResult", "EpConfig", "EpError",
@@ -37,6 +39,9 @@ __all__ = [
     "ep_dispatch_backward", "ep_dispatch_dedup", "ep_dedup_expand", "ep_expert_gemm",
     "ep_expert_glu", "ep_expert_glu_backward", "ep_expert_gemm_backward",
     "ep_expert_gemv_w4", "ep_expert_glu_w4", "W4", "EpW4",
+    "route", "route_backward", "quantize_fp4", "tile_fp4_scales", "untile_fp4_scales", "FP4",
+    "ep_route", "ep_route_backward", "ep_fp4_scale_bytes", "ep_quantize_fp4", "ep_dequantize_fp4",
+    "ep_dispatch_fp4", "EpFp4", "EP_SCORE_SOFTMAX", "EP_SCORE_SIGMOID", "EP_FP4_MX", "EP_FP4_NV",
     "ep_get_device_error", "DedupResult",
     "ep_buffer_query", "ep_dispatch_layout_noalloc", "ep_dispatch_layout_noalloc_scratch_bytes",
     "EP_NOALLOC_SCRATCH_BYTES", "ep_pattern_probe", "ep_pad_tokens", "group_num_tokens_per_rank",
@@ -50,6 +55,9 @@ __all__ = [
 
 _TORCH_TO_EP = {torch.bfloat16: EP_BF16, torch.float32: EP_F32}
 _ACTS = {"silu": EP_ACT_SILU, "gelu": EP_ACT_GELU}
+_SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+_FP4_FORMATS = {"mx": EP_FP4_MX, "nv": EP_FP4_NV}
+_FP4_BLOCK = {"mx": 32, "nv": 16}
 _EP_TO_TORCH = {EP_BF16: torch.bfloat16, EP_F32: torch.float32}
 
 
@@ -80,6 +88,38 @@ def _stream(stream) -> int | None:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _empty_on(device: torch.device, shape: tuple, dtype: torch.dtype, stream,
+              kept: bool = True) -> torch.Tensor:
+    """Memory for what a call's kernels write on `stream`: from that stream's own pool, so
+    that what used it before is done by then in stream order, and dropping it hands it on
+    only behind those kernels. kept: the caller gets it, and may drop it while the current
+    stream still works on it; that work is waited for too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept:
+        t.record_stream(here)
+    return t
+
+
+def _on_device_of(first: torch.Tensor, **others: torch.Tensor | None):
+    """A context in which `first`'s device is the current one, checked to be the others' too."""
+    if not first.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    if first.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(first.device)
 
 
 def _check_dtype(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
@@ -311,6 +351,234 @@ def ep_expert_glu_w4(handle, x_recv: torch.Tensor, weights: W4, din: int, dff: i
                                       act, _ptr(h), _stream(stream)), "ep_expert_glu_w4")
 
 
+# -- the router ------------------------------------------------------------------
+
+def ep_route(logits_TE: torch.Tensor, select_TE: torch.Tensor | None, topk: int, score: int,
+             normalize: bool, scale: float, topk_expert_ids_TK: torch.Tensor,
+             topk_scores_TK: torch.Tensor, stream=None) -> None:
+    _check_dtype(topk_expert_ids_TK, torch.int32, "topk_expert_ids_TK")
+    _check_dtype(topk_scores_TK, torch.float32, "topk_scores_TK")
+    T, E = logits_TE.shape
+    check(_abi.lib().ep_route(_ptr(logits_TE), _TORCH_TO_EP[logits_TE.dtype], _ptr(select_TE), T, E,
+                              topk, score, int(normalize), scale, _ptr(topk_expert_ids_TK),
+                              _ptr(topk_scores_TK), _stream(stream)), "ep_route")
+
+
+def ep_route_backward(grad_scores_TK: torch.Tensor, logits_TE: torch.Tensor,
+                      topk_expert_ids_TK: torch.Tensor, score: int, normalize: bool, scale: float,
+                      grad_logits_TE: torch.Tensor, stream=None) -> None:
+    T, E = logits_TE.shape
+    check(_abi.lib().ep_route_backward(_ptr(grad_scores_TK), _ptr(logits_TE),
+                                       _TORCH_TO_EP[logits_TE.dtype], _ptr(topk_expert_ids_TK), T, E,
+                                       topk_expert_ids_TK.shape[1], score, int(normalize), scale,
+                                       _ptr(grad_logits_TE), _stream(stream)), "ep_route_backward")
+
+
+def _check_logits(logits: torch.Tensor, score: str) -> int:
+    if logits.dtype not in _TORCH_TO_EP:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return _SCORES[score]
+
+
+def route(logits_TE: torch.Tensor, topk: int, score: str = "softmax", normalize: bool = True,
+          select: torch.Tensor | None = None, scale: float = 1.0, stream=None):
+    """(topk_expert_ids_TK int32, topk_scores_TK fp32), as dispatch takes them: of each token the
+    topk experts with the largest `select` (fp32 [T, E]; the logits unless given: biased, masked
+    with -inf where a token may not go or does not exist), ties to the lowest index. Scores are
+    scale times the softmax or the sigmoids of the logits, shared out over the chosen ones if
+    normalize. A slot without an expert has id -1 and score 0."""
+    kind = _check_logits(logits_TE, score)
+    T, E = logits_TE.shape
+    if not 1 <= topk <= E:
+        raise ValueError(f"topk must be in 1..{E}, got {topk}")
+    if select is not None:
+        _check_dtype(select, torch.float32, "select")
+        if select.shape != logits_TE.shape:
+            raise ValueError(f"select must be shaped as logits, got {tuple(select.shape)}")
+    with _on_device_of(logits_TE, select=select):
+        ids = _empty_on(logits_TE.device, (T, topk), torch.int32, stream)
+        scores = _empty_on(logits_TE.device, (T, topk), torch.float32, stream)
+        ep_route(logits_TE, select, topk, kind, normalize, scale, ids, scores, stream)
+    return ids, scores
+
+
+def route_backward(grad_scores_TK: torch.Tensor, logits_TE: torch.Tensor,
+                   topk_expert_ids_TK: torch.Tensor, score: str = "softmax",
+                   normalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """The gradient of the logits (their type) from that of route's scores, fp32, which
+    Buffer.combine_backward returns."""
+    kind = _check_logits(logits_TE, score)
+    ids = topk_expert_ids_TK
+    _check_dtype(ids, torch.int32, "topk_expert_ids_TK")
+    _check_dtype(grad_scores_TK, torch.float32, "grad_scores_TK")
+    if ids.dim() != 2 or ids.shape[0] != logits_TE.shape[0] or grad_scores_TK.shape != ids.shape:
+        raise ValueError(f"ids and grad_scores must be [{logits_TE.shape[0]}, topk], got "
+                         f"{tuple(ids.shape)} and {tuple(grad_scores_TK.shape)}")
+    with _on_device_of(logits_TE, topk_expert_ids_TK=ids, grad_scores_TK=grad_scores_TK):
+        grad = _empty_on(logits_TE.device, tuple(logits_TE.shape), logits_TE.dtype, stream)
+        ep_route_backward(grad_scores_TK, logits_TE, ids, kind, normalize, scale, grad, stream)
+    return grad
+
+
+# -- microscaled 4-bit floating point ----------------------------------------------
+
+def ep_fp4_scale_bytes(rows: int, cols: int, format: int) -> int:
+    return int(_abi.lib().ep_fp4_scale_bytes(rows, cols, format))
+
+
+def _fp4_tiles(rows: int, cols: int, format: str) -> tuple:
+    """Shape of the scales of [rows, cols]."""
+    return (rows + 127) // 128, cols // (4 * _FP4_BLOCK[format]), 32, 4, 4
+
+
+def tile_fp4_scales(scales: torch.Tensor) -> torch.Tensor:
+    """Block scales (uint8) of one row after the other, [..., rows, cols / block], in the tiles
+    that FP4 holds."""
+    _check_dtype(scales, torch.uint8, "scales")
+    blocks = scales.shape[-1]
+    if scales.dim() < 2 or not blocks or blocks % 4:
+        raise ValueError(f"scales must be [..., rows, blocks] with 4 blocks or a multiple, got "
+                         f"{tuple(scales.shape)}")
+    flat = scales.reshape(-1, blocks)
+    flat = torch.nn.functional.pad(flat, (0, 0, 0, -flat.shape[0] % 128))
+    return flat.view(-1, 4, 32, blocks // 4, 4).permute(0, 3, 2, 1, 4).contiguous()
+
+
+def untile_fp4_scales(scales: torch.Tensor, rows: int) -> torch.Tensor:
+    """The reverse: [rows, cols / block]."""
+    g, kt = scales.shape[:2]
+    return scales.permute(0, 3, 2, 1, 4).reshape(128 * g, 4 * kt)[:rows]
+
+
+@dataclass(frozen=True)
+class FP4:
+    """A matrix [..., rows, cols] in microscaled 4-bit floating point: weights [E, rows, cols]
+    with rows a multiple of 128, receive rows, or any other. quantize_fp4 makes one."""
+    codes: torch.Tensor                # [..., rows, cols / 2] uint8, element 2j in byte j's low nibble
+    scales: torch.Tensor               # [ceil(all rows / 128), cols / (4 block), 32, 4, 4] uint8
+    format: str                        # "mx" (blocks of 32, ue8m0) or "nv" (16, ue4m3)
+    tensor_scale: torch.Tensor | None = None   # nv: fp32, one number for each matrix
+
+    def __post_init__(self):
+        c, s, g = self.codes, self.scales, self.tensor_scale
+        if self.format not in _FP4_FORMATS:
+            raise ValueError(f"format must be one of {sorted(_FP4_FORMATS)}, got {self.format!r}")
+        _check_dtype(c, torch.uint8, "codes")
+        _check_dtype(s, torch.uint8, "scales")
+        if c.dim() < 2 or not c.shape[-1] or c.shape[-1] % 64:
+            raise ValueError(f"codes must be [..., rows, cols / 2] with cols a multiple of 128, "
+                             f"got {tuple(c.shape)}")
+        want = _fp4_tiles(self.rows, self.cols, self.format)
+        if tuple(s.shape) != want:
+            raise ValueError(f"scales must be {list(want)} (tile_fp4_scales), got {list(s.shape)}")
+        if g is not None:
+            _check_dtype(g, torch.float32, "tensor_scale")
+            if self.format != "nv":
+                raise ValueError("only nv has a tensor_scale")
+            if g.numel() != self.matrices:
+                raise ValueError(f"tensor_scale must hold {self.matrices} numbers, got "
+                                 f"{tuple(g.shape)}")
+        object.__setattr__(self, "_checked", self._form())
+
+    def _form(self) -> tuple:
+        c, s, g = self.codes, self.scales, self.tensor_scale
+        return c.shape, c.dtype, s.shape, s.dtype, None if g is None else (g.shape, g.dtype)
+
+    @cached_property
+    def cols(self) -> int:
+        return 2 * self.codes.shape[-1]
+
+    @cached_property
+    def rows(self) -> int:
+        """All rows, of every matrix."""
+        return self.codes.numel() // self.codes.shape[-1]
+
+    @cached_property
+    def matrices(self) -> int:
+        n = 1
+        for d in self.codes.shape[:-2]:
+            n *= d
+        return n
+
+    def _struct(self) -> EpFp4:
+        """The C struct of one call, addresses taken anew each time (as W4's)."""
+        if self._form() != self._checked:
+            raise ValueError("the tensors of this FP4 changed their shapes or types since it was "
+                             "made: make another one of them")
+        g = self.tensor_scale
+        if self.scales.device != self.codes.device or \
+                (g is not None and g.device != self.codes.device):
+            raise ValueError("the tensors of this FP4 are on several devices")
+        return EpFp4(_ptr(self.codes), _ptr(self.scales), _ptr(g), _FP4_FORMATS[self.format])
+
+    def dequantize(self, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+        """The values, [..., rows, cols] in bfloat16 (rounded) or float32."""
+        if dtype not in _TORCH_TO_EP:
+            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+        with _on_device_of(self.codes):
+            out = _empty_on(self.codes.device, (*self.codes.shape[:-1], self.cols), dtype, stream)
+            ep_dequantize_fp4(self, out, stream)
+        return out
+
+
+def ep_quantize_fp4(x: torch.Tensor, out: FP4, stream=None) -> None:
+    _check_dtype(x, torch.bfloat16, "x")
+    if x.shape != (*out.codes.shape[:-1], out.cols):
+        raise ValueError(f"x must be {[*out.codes.shape[:-1], out.cols]}, got {list(x.shape)}")
+    check(_abi.lib().ep_quantize_fp4(_ptr(x), out.rows, out.cols, max(1, out.codes.shape[-2]),
+                                     C.byref(out._struct()), _stream(stream)), "ep_quantize_fp4")
+
+
+def ep_dequantize_fp4(q: FP4, out: torch.Tensor, stream=None) -> None:
+    if out.dtype not in _TORCH_TO_EP:
+        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+    if out.shape != (*q.codes.shape[:-1], q.cols):
+        raise ValueError(f"out must be {[*q.codes.shape[:-1], q.cols]}, got {list(out.shape)}")
+    check(_abi.lib().ep_dequantize_fp4(C.byref(q._struct()), q.rows, q.cols,
+                                       max(1, q.codes.shape[-2]), _ptr(out),
+                                       _TORCH_TO_EP[out.dtype], _stream(stream)),
+          "ep_dequantize_fp4")
+
+
+def quantize_fp4(x: torch.Tensor, format: str = "nv", tensor_scale: torch.Tensor | None = None,
+                 stream=None) -> FP4:
+    """x [..., rows, cols] (bf16, cols a multiple of 128) in microscaled 4-bit floating point.
+    tensor_scale (nv only): fp32, one number for each matrix, by which the block scales are
+    measured; amax / (6 * 448) of the matrix uses their whole range."""
+    _check_dtype(x, torch.bfloat16, "x")
+    if format not in _FP4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(_FP4_FORMATS)}, got {format!r}")
+    if x.dim() < 2 or not x.shape[-1] or x.shape[-1] % 128:
+        raise ValueError(f"x must be [..., rows, cols] with cols a multiple of 128, got "
+                         f"{tuple(x.shape)}")
+    with _on_device_of(x, tensor_scale=tensor_scale):
+        cols = x.shape[-1]
+        codes = _empty_on(x.device, (*x.shape[:-1], cols // 2), torch.uint8, stream)
+        scales = _empty_on(x.device, _fp4_tiles(x.numel() // cols, cols, format), torch.uint8,
+                           stream)
+        q = FP4(codes, scales, format, tensor_scale)
+        ep_quantize_fp4(x, q, stream)
+    return q
+
+
+def ep_dispatch_fp4(handle, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
+                    topk_expert_ids_TK: torch.Tensor, num_tokens: int, num_tokens_per_rank: int,
+                    rows: FP4, stream=None) -> EpDispatchOut:
+    _check_dtype(x_TD, torch.bfloat16, "x_TD")
+    _check_dtype(topk_scores_TK, torch.float32, "topk_scores_TK")
+    _check_dtype(topk_expert_ids_TK, torch.int32, "topk_expert_ids_TK")
+    out = EpDispatchOut()
+    check(_abi.lib().ep_dispatch_fp4(handle, _ptr(x_TD), _ptr(topk_scores_TK),
+                                     _ptr(topk_expert_ids_TK), num_tokens, num_tokens_per_rank,
+                                     C.byref(rows._struct()), _stream(stream), C.byref(out)),
+          "ep_dispatch_fp4")
+    return out
+
+
 def ep_get_device_error(handle, stream=None) -> int:
     v = C.c_uint32(0)
     check(_abi.lib().ep_get_device_error(handle, _stream(stream), C.byref(v)),
@@ -534,22 +802,8 @@ class Buffer:
 
     # -- memory of results -----------------------------------------------------
     def _empty(self, shape: tuple, dtype: torch.dtype, stream, kept: bool = True) -> torch.Tensor:
-        """Memory for what a call's kernels write on `stream`: from that stream's own pool, so
-        that what used it before is done by then in stream order, and dropping it hands it on
-        only behind those kernels. kept: the caller gets it, and may drop it while the current
-        stream still works on it; that work is waited for too."""
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        here = torch.cuda.current_stream(self.device)
-        if stream == here:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(stream):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        if kept:
-            t.record_stream(here)
-        return t
+        """Memory on the buffer's device for what a call's kernels write on `stream` (_empty_on)."""
+        return _empty_on(self.device, shape, dtype, stream, kept)
 
     def _new_rows(self, width: int, stream, dtype: torch.dtype = torch.bfloat16,
                   kept: bool = True) -> torch.Tensor:
@@ -825,6 +1079,39 @@ class Buffer:
         h = self.expert_glu_w4(x_recv, w_gate_up, act,
                                self._new_rows(w_down.din, stream, kept=False), stream)
         return self.expert_gemv_w4(h, w_down, y_recv, stream)
+
+    # -- the same block in 4-bit floating point ----------------------------------
+    def dispatch_fp4(self, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
+                     topk_expert_ids_TK: torch.Tensor, num_tokens_per_rank: int | None = None,
+                     format: str = "nv", tensor_scale: torch.Tensor | None = None,
+                     stream=None) -> DispatchResult:
+        """dispatch whose receive rows are quantised on the way: recv_x is an FP4 of
+        [R * S, D] rows (rows past each rank's total undefined), in memory of its own."""
+        T = x_TD.shape[0]
+        if x_TD.shape != (T, self.D) or topk_expert_ids_TK.shape != (T, self.K) or \
+                topk_scores_TK.shape != (T, self.K):
+            raise ValueError(f"x, scores and ids must be [T, {self.D}], [T, {self.K}] and "
+                             f"[T, {self.K}], got {tuple(x_TD.shape)}, "
+                             f"{tuple(topk_scores_TK.shape)}, {tuple(topk_expert_ids_TK.shape)}")
+        if format not in _FP4_FORMATS:
+            raise ValueError(f"format must be one of {sorted(_FP4_FORMATS)}, got {format!r}")
+        if self.D % 128:
+            raise ValueError(f"4-bit rows need a hidden size that is a multiple of 128, got {self.D}")
+        N = T if num_tokens_per_rank is None else num_tokens_per_rank
+        rows = self.R * ep_pad_tokens(N) * self.K
+        q = self._fp4_rows(rows, self.D, format, tensor_scale, stream)
+        d = ep_dispatch_fp4(self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, N, q, stream)
+        S = d.layout.rank_stride
+        lead = (self.R * S,) if self.packed else (self.R, S)
+        return DispatchResult(recv_x=q, recv_scores=self._view(d.recv_scores, torch.float32, lead),
+                              recv_src=self._view(d.recv_src, torch.int32, lead),
+                              layout=self._layout(d.layout))
+
+    def _fp4_rows(self, rows: int, cols: int, format: str, tensor_scale, stream,
+                  kept: bool = True) -> FP4:
+        return FP4(self._empty((rows, cols // 2), torch.uint8, stream, kept),
+                   self._empty(_fp4_tiles(rows, cols, format), torch.uint8, stream, kept), format,
+                   tensor_scale)
 
     def _last_stride(self) -> int:
         return self._stride

@@ -34,6 +34,12 @@ EP_LAYOUT_PACKED = 1
 EP_ACT_SILU = 0
 EP_ACT_GELU = 1
 
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+
+EP_FP4_MX = 0
+EP_FP4_NV = 1
+
 EP_DEVERR_BAD_ID = 0x1
 EP_DEVERR_ROW_OOB = 0x2
 EP_DEVERR_TIMEOUT = 0x4
@@ -125,6 +131,15 @@ class EpW4(C.Structure):
     ]
 
 
+class EpFp4(C.Structure):
+    _fields_ = [
+        ("codes", C.c_void_p),
+        ("scales", C.c_void_p),
+        ("tensor_scale", C.c_void_p),
+        ("format", C.c_int32),
+    ]
+
+
 # name -> (restype, argtypes), in the order of include/ep.h
 SIGNATURES = {
     "ep_buffer_required_bytes": (C.c_size_t, [C.POINTER(EpConfig)]),
@@ -160,6 +175,20 @@ SIGNATURES = {
                                     C.c_int64, C.c_void_p, C.c_void_p]),
     "ep_expert_glu_w4": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(EpW4), C.c_int64,
                                    C.c_int64, C.c_int32, C.c_void_p, C.c_void_p]),
+    "ep_route": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int64, C.c_int32, C.c_int32,
+                           C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
+                           C.c_void_p]),
+    "ep_route_backward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_int64,
+                                    C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_float,
+                                    C.c_void_p, C.c_void_p]),
+    "ep_fp4_scale_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int32]),
+    "ep_quantize_fp4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.POINTER(EpFp4),
+                                  C.c_void_p]),
+    "ep_dequantize_fp4": (C.c_int, [C.POINTER(EpFp4), C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                    C.c_int32, C.c_void_p]),
+    "ep_dispatch_fp4": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                  C.c_int64, C.POINTER(EpFp4), C.c_void_p,
+                                  C.POINTER(EpDispatchOut)]),
     "ep_get_device_error": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint32)]),
     "ep_buffer_query": (C.c_int, [C.c_void_p, C.POINTER(EpBufferInfo)]),
     "ep_dispatch_layout_noalloc": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32,

@@ -19,6 +19,7 @@
 
 #include "ep.h"
 #include "ep_kernels.cuh"
+#include "ep_fp4.cuh"
 #include "ep_next.cuh"
 
 struct ep_buffer {
@@ -974,6 +975,170 @@ ep_status ep_expert_glu_w4(ep_buffer* buf, const void* x_recv, const ep_w4* weig
     const Range range(buf, "ep_expert_glu_w4");
     if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
     return enqueue_w4(buf, x_recv, weights, din, dff, true, act, h, stream);
+}
+
+// Options of the calls without a buffer: programmatic dependent launch unless EP_PDL=0.
+static ep::LaunchOpts bare_opts(ep_stream_t stream)
+{
+    static const bool pdl = !env_is("EP_PDL", "0");
+    return ep::LaunchOpts{as_stream(stream), pdl, nullptr};
+}
+
+static ep_status check_route(const void* logits, int32_t dtype, const void* ids, const void* scores,
+                             int64_t T, int32_t E, int32_t K, int32_t score)
+{
+    if (dtype != EP_BF16 && dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || E > ep::kMaxExperts || K < 1 || K > E || K > ep::kMaxTopk)
+        return EP_ERR_INVALID_ARG;
+    if (T > INT32_MAX) return EP_ERR_CAPACITY;   // a warp each, four to a CTA of one grid
+    if (T > 0 && (!logits || !ids || !scores)) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(logits, (uintptr_t)elem_bytes(dtype)) || !is_aligned(ids, 4) ||
+        !is_aligned(scores, 4))
+        return EP_ERR_ALIGNMENT;
+    return EP_OK;
+}
+
+ep_status ep_route(const void* logits, int32_t dtype, const float* select, int64_t T, int32_t E,
+                   int32_t K, int32_t score, int32_t normalize, float scale, int32_t* ids,
+                   float* scores, ep_stream_t stream)
+{
+    const ep_status st = check_route(logits, dtype, ids, scores, T, E, K, score);
+    if (st != EP_OK) return st;
+    if (!is_aligned(select, 4)) return EP_ERR_ALIGNMENT;
+    if (T == 0) return EP_OK;
+    ep::RouteArgs a = {};
+    a.logits = logits;
+    a.select = select;
+    a.T = T;
+    a.E = E;
+    a.K = K;
+    a.bf16 = dtype == EP_BF16;
+    a.sigmoid = score == EP_SCORE_SIGMOID;
+    a.normalize = normalize != 0;
+    a.scale = scale;
+    a.ids = ids;
+    a.scores = scores;
+    return cuda_status(ep::launch_route(a, bare_opts(stream)));
+}
+
+ep_status ep_route_backward(const float* grad_scores, const void* logits, int32_t dtype,
+                            const int32_t* ids, int64_t T, int32_t E, int32_t K, int32_t score,
+                            int32_t normalize, float scale, void* grad_logits, ep_stream_t stream)
+{
+    const ep_status st = check_route(logits, dtype, ids, grad_scores, T, E, K, score);
+    if (st != EP_OK) return st;
+    if (T > 0 && !grad_logits) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(grad_logits, (uintptr_t)elem_bytes(dtype))) return EP_ERR_ALIGNMENT;
+    if (T == 0) return EP_OK;
+    ep::RouteArgs a = {};
+    a.logits = logits;
+    a.T = T;
+    a.E = E;
+    a.K = K;
+    a.bf16 = dtype == EP_BF16;
+    a.sigmoid = score == EP_SCORE_SIGMOID;
+    a.normalize = normalize != 0;
+    a.scale = scale;
+    a.ids = const_cast<int32_t*>(ids);
+    a.grad_scores = grad_scores;
+    a.grad_logits = grad_logits;
+    return cuda_status(ep::launch_route_backward(a, bare_opts(stream)));
+}
+
+size_t ep_fp4_scale_bytes(int64_t rows, int64_t cols, int32_t format)
+{
+    if (rows < 0 || cols < 128 || cols % 128 != 0 || cols > INT32_MAX) return 0;
+    if (format != EP_FP4_MX && format != EP_FP4_NV) return 0;
+    return (size_t)((rows + 127) / 128) * (size_t)(cols / (format == EP_FP4_MX ? 128 : 64)) * 512;
+}
+
+// A matrix of codes and scales with its sizes; EP_OK for one that may be empty.
+static ep_status check_fp4(const ep_fp4* q, int64_t rows, int64_t cols, int64_t rows_per_scale)
+{
+    if (!q || (q->format != EP_FP4_MX && q->format != EP_FP4_NV)) return EP_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 128 || cols % 128 != 0 || rows_per_scale < 1) return EP_ERR_INVALID_ARG;
+    if (q->format == EP_FP4_MX && q->tensor_scale) return EP_ERR_INVALID_ARG;
+    if (rows > 0 && (!q->codes || !q->scales)) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(q->codes, 16) || !is_aligned(q->scales, 16) || !is_aligned(q->tensor_scale, 4))
+        return EP_ERR_ALIGNMENT;
+    if (cols > INT32_MAX || rows > INT64_MAX / 4 / cols) return EP_ERR_CAPACITY;
+    return EP_OK;
+}
+
+static ep::Fp4Args fp4_args(const ep_fp4* q, int64_t rows, int64_t cols, int64_t rows_per_scale)
+{
+    ep::Fp4Args a = {};
+    a.rows = rows;
+    a.cols = cols;
+    a.rows_per_scale = rows_per_scale;
+    a.format = q->format;
+    a.codes = q->codes;
+    a.scales = q->scales;
+    a.tensor_scale = q->tensor_scale;
+    return a;
+}
+
+ep_status ep_quantize_fp4(const void* x, int64_t rows, int64_t cols, int64_t rows_per_scale,
+                          const ep_fp4* out, ep_stream_t stream)
+{
+    const ep_status st = check_fp4(out, rows, cols, rows_per_scale);
+    if (st != EP_OK) return st;
+    if (rows > 0 && !x) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(x, 16)) return EP_ERR_ALIGNMENT;
+    if (rows == 0) return EP_OK;
+    ep::Fp4Args a = fp4_args(out, rows, cols, rows_per_scale);
+    a.x = x;
+    return cuda_status(ep::launch_quantize_fp4(a, bare_opts(stream)));
+}
+
+ep_status ep_dequantize_fp4(const ep_fp4* q, int64_t rows, int64_t cols, int64_t rows_per_scale,
+                            void* out, int32_t out_dtype, ep_stream_t stream)
+{
+    const ep_status st = check_fp4(q, rows, cols, rows_per_scale);
+    if (st != EP_OK) return st;
+    if (out_dtype != EP_BF16 && out_dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (rows > 0 && !out) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(out, 16)) return EP_ERR_ALIGNMENT;
+    if (rows == 0) return EP_OK;
+    ep::Fp4Args a = fp4_args(q, rows, cols, rows_per_scale);
+    a.out = out;
+    a.out_f32 = out_dtype == EP_F32;
+    return cuda_status(ep::launch_dequantize_fp4(a, bare_opts(stream)));
+}
+
+ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x, const float* scores, const int32_t* ids,
+                          int64_t T, int64_t N, const ep_fp4* rows, ep_stream_t stream,
+                          ep_dispatch_out* out)
+{
+    const Range range(buf, "ep_dispatch_fp4");
+    const ep_status st = check_call(buf, ids, T, N);
+    if (st != EP_OK) return st;
+    if (buf->cfg.dtype != EP_BF16) return EP_ERR_INVALID_ARG;
+    const int64_t D = buf->cfg.hidden;
+    const ep_status sq = check_fp4(rows, (int64_t)buf->cfg.num_ranks * pad4(N) * buf->cfg.topk, D, 1);
+    if (sq != EP_OK) return sq;
+    if (T > 0 && (!x || !scores)) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(x, 16) || !is_aligned(scores, 4)) return EP_ERR_ALIGNMENT;
+    cudaStream_t s = as_stream(stream);
+    const ep_status sl = enqueue_layout(buf, ids, T, N, s);
+    if (sl != EP_OK) return sl;
+    fill_dispatch(buf, out);
+    if (T == 0) return EP_OK;
+    ep::PermuteFp4Args a = {};
+    a.x = x;
+    a.scores = scores;
+    a.pos = buf->pos;
+    a.T = T;
+    a.D = D;
+    a.K = buf->cfg.topk;
+    a.format = rows->format;
+    a.tensor_scale = rows->tensor_scale;
+    a.codes = rows->codes;
+    a.scales = rows->scales;
+    a.recv_scores = buf->recv_scores;
+    a.recv_src = buf->recv_src;
+    return cuda_status(ep::launch_permute_fp4(a, buf->num_sms, opts(buf, s)));
 }
 
 ep_status ep_get_device_error(ep_buffer* buf, ep_stream_t stream, uint32_t* flags)

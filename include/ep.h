@@ -441,6 +441,80 @@ EP_API ep_status ep_expert_glu_w4(ep_buffer* buf, const void* x_recv, const ep_w
                                   int64_t din, int64_t dff, int32_t act, void* h,
                                   ep_stream_t stream);
 
+/* ---- The router ------------------------------------------------------------------
+ * What gives a dispatch its ids and scores. For each token t, p is the softmax of
+ * logits_TE [T][E] or their sigmoids; the topk experts are those with the largest
+ * select_TE [T][E] (fp32; NULL: the logits), ties to the lowest index; an expert whose
+ * value is -inf or NaN is never chosen, so that masked experts and padded tokens are given
+ * as -inf there, and a slot without an expert gets id -1 and score 0, which route nowhere.
+ *     topk_scores_TK = scale * p, or, normalised, scale * p / (sum of the chosen p).
+ * Normalised scores are computed from the chosen logits alone. Sums and probabilities are
+ * fp32; a NaN or +inf among the logits that a score depends on makes it a NaN (an infinite
+ * sigmoid is 1). 1 <= E <= 1024, 1 <= topk <= min(E, 64). No buffer is involved, nothing is
+ * allocated; device pointers aligned to their elements, dense. */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score;
+
+EP_API ep_status ep_route(const void* logits_TE, int32_t logits_dtype, const float* select_TE,
+                          int64_t num_tokens, int32_t num_experts, int32_t topk, int32_t score,
+                          int32_t normalize, float scale, int32_t* topk_expert_ids_TK,
+                          float* topk_scores_TK, ep_stream_t stream);
+
+/* Its gradient: grad_logits_TE [T][E] (of logits_dtype, every element written) from
+ * grad_scores_TK and the ids that ep_route chose (the choice itself has no gradient; select_TE
+ * gets none). An id outside [0, E) stands for an empty slot; ids that occur twice add up. */
+EP_API ep_status ep_route_backward(const float* grad_scores_TK, const void* logits_TE,
+                                   int32_t logits_dtype, const int32_t* topk_expert_ids_TK,
+                                   int64_t num_tokens, int32_t num_experts, int32_t topk,
+                                   int32_t score, int32_t normalize, float scale,
+                                   void* grad_logits_TE, ep_stream_t stream);
+
+/* ---- Microscaled 4-bit floating point ---------------------------------------------
+ * Elements of e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one scale for each
+ * block of consecutive elements of a row:
+ *   EP_FP4_MX  blocks of 32, scale 2^(c - 127), c = floor(log2 amax) - 2 + 127, at least 0
+ *   EP_FP4_NV  blocks of 16, scale s of ue4m3, amax / (6 g) rounded to the nearest and at
+ *              most 448; g: one fp32 number for the matrix (tensor_scale, 2^-60 to 2^60), or 1
+ * An element stands for e2m1 * scale * g; quantised it is x / (scale * g) rounded to the
+ * nearest (ties to the even code) and at most 6 in magnitude, decided on the exact quotient.
+ * A block whose scale is 0 gets zeros. A block with an infinity or a NaN gets the scale
+ * NaN (0xFF, 0x7F) and zeros: its row's products are NaN.
+ * Scales lie in tiles of 128 rows x 4 blocks (512 bytes; tiles of one 128-row group in the
+ * order of their blocks, ceil(rows / 128) groups): row r's four bytes at 16 (r % 32) +
+ * 4 (r / 32 % 4) of its tile. Bytes of rows behind the last are not written and not used. */
+typedef enum { EP_FP4_MX = 0, EP_FP4_NV = 1 } ep_fp4_format;
+
+typedef struct {
+    uint8_t* codes;               /* [rows][cols / 2]: element 2j in the low nibble of byte j */
+    uint8_t* scales;              /* ep_fp4_scale_bytes(rows, cols, format) bytes, in tiles */
+    const float* tensor_scale;    /* g for each matrix of a batch, or NULL (MX: NULL) */
+    int32_t format;               /* ep_fp4_format */
+} ep_fp4;
+
+/* Bytes of the scales of [rows][cols]; 0 for sizes or a format that are not supported (rows >= 0,
+ * cols a positive multiple of 128). Host-only. */
+EP_API size_t ep_fp4_scale_bytes(int64_t rows, int64_t cols, int32_t format);
+
+/* x [rows][cols] (bf16) quantised into out's codes and scales. rows_per_scale: rows that share
+ * an element of out's tensor_scale (rows r of matrix r / rows_per_scale). codes and scales
+ * 16-byte aligned, as is x. */
+EP_API ep_status ep_quantize_fp4(const void* x, int64_t rows, int64_t cols, int64_t rows_per_scale,
+                                 const ep_fp4* out, ep_stream_t stream);
+
+/* The values that q stands for, in fp32 or bf16 (rounded once more). */
+EP_API ep_status ep_dequantize_fp4(const ep_fp4* q, int64_t rows, int64_t cols,
+                                   int64_t rows_per_scale, void* out, int32_t out_dtype,
+                                   ep_stream_t stream);
+
+/* ep_dispatch whose receive rows are quantised on the way: each token's row is read and
+ * quantised once and written to rows [R*S][D] of `rows`, caller-owned (a tensor_scale is one
+ * number); receive scores and sources are written to the workspace as by ep_dispatch, recv_x is
+ * not. D % 128 == 0, bf16 buffers only. Rows of no pair keep what they hold. Fills *out (may be
+ * NULL). */
+EP_API ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x_TD, const float* topk_scores_TK,
+                                 const int32_t* topk_expert_ids_TK, int64_t num_tokens,
+                                 int64_t num_tokens_per_rank, const ep_fp4* rows,
+                                 ep_stream_t stream, ep_dispatch_out* out);
+
 /* Synchronously read and clear the device error word (EP_DEVERR_* bits).
  * Refused with EP_ERR_CAPTURE_HOST_SYNC while the stream is capturing. Status
  * stays on the device and is read only here ([graph] "Internode" item 1: no
