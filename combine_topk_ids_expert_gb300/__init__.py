@@ -41,7 +41,7 @@ __all__ = [
     "ep_expert_gemv_w4", "ep_expert_glu_w4", "W4", "EpW4",
     "route", "route_backward", "quantize_fp4", "tile_fp4_scales", "untile_fp4_scales", "FP4",
     "ep_route", "ep_route_backward", "ep_fp4_scale_bytes", "ep_quantize_fp4", "ep_dequantize_fp4",
-    "ep_dispatch_fp4", "EpFp4", "EP_SCORE_SOFTMAX", "EP_SCORE_SIGMOID", "EP_FP4_MX", "EP_FP4_NV",
+    "ep_dispatch_fp4", "ep_expert_gemm_fp4", "ep_expert_glu_fp4", "EpFp4", "EP_SCORE_SOFTMAX", "EP_SCORE_SIGMOID", "EP_FP4_MX", "EP_FP4_NV",
     "ep_get_device_error", "DedupResult",
     "ep_buffer_query", "ep_dispatch_layout_noalloc", "ep_dispatch_layout_noalloc_scratch_bytes",
     "EP_NOALLOC_SCRATCH_BYTES", "ep_pattern_probe", "ep_pad_tokens", "group_num_tokens_per_rank",
@@ -579,6 +579,26 @@ def ep_dispatch_fp4(handle, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
     return out
 
 
+def ep_expert_gemm_fp4(handle, x_recv: FP4, weights: FP4, din: int, dout: int,
+                       y_recv: torch.Tensor, stream=None) -> None:
+    _check_dtype(y_recv, torch.bfloat16, "y_recv")
+    check(_abi.lib().ep_expert_gemm_fp4(handle, C.byref(x_recv._struct()),
+                                        C.byref(weights._struct()), din, dout, _ptr(y_recv),
+                                        _stream(stream)), "ep_expert_gemm_fp4")
+
+
+def ep_expert_glu_fp4(handle, x_recv: FP4, w_gate_up: FP4, din: int, dff: int, act: int,
+                      h: torch.Tensor | FP4, stream=None) -> None:
+    """h: bfloat16 rows, or an FP4 that receives them quantised."""
+    if not isinstance(h, FP4):
+        _check_dtype(h, torch.bfloat16, "h")
+    check(_abi.lib().ep_expert_glu_fp4(handle, C.byref(x_recv._struct()),
+                                       C.byref(w_gate_up._struct()), din, dff, act,
+                                       None if isinstance(h, FP4) else _ptr(h),
+                                       C.byref(h._struct()) if isinstance(h, FP4) else None,
+                                       _stream(stream)), "ep_expert_glu_fp4")
+
+
 def ep_get_device_error(handle, stream=None) -> int:
     v = C.c_uint32(0)
     check(_abi.lib().ep_get_device_error(handle, _stream(stream), C.byref(v)),
@@ -1112,6 +1132,74 @@ class Buffer:
         return FP4(self._empty((rows, cols // 2), torch.uint8, stream, kept),
                    self._empty(_fp4_tiles(rows, cols, format), torch.uint8, stream, kept), format,
                    tensor_scale)
+
+    def _rows_fp4(self, x: FP4, name: str, width: int) -> FP4:
+        """x, checked to be rows of the last call's receive layout, `width` columns wide."""
+        n = self.R * self._last_stride()
+        if not isinstance(x, FP4):
+            raise TypeError(f"{name} must be an FP4, got {type(x).__name__}")
+        if x.cols != width or x.rows != n or (x.tensor_scale is not None
+                                              and x.tensor_scale.numel() != 1):
+            raise ValueError(f"{name} must hold the receive layout's {n} rows of {width} columns "
+                             f"(with one tensor_scale), got {x.rows} of {x.cols}")
+        return x
+
+    def _weights_fp4(self, w: FP4, name: str, rows: int | None, format: str) -> int:
+        """Rows of each expert's w, checked to be [E, rows, any] in `format`."""
+        if not isinstance(w, FP4):
+            raise TypeError(f"{name} must be an FP4, got {type(w).__name__}")
+        n, _ = self._weights(w.codes, name + ".codes", rows, None)
+        if w.format != format:
+            raise ValueError(f"{name} is {w.format}, the rows are {format}")
+        if n % 128:
+            raise ValueError(f"{name} must hold a multiple of 128 rows for each expert, got {n}")
+        return n
+
+    def expert_gemm_fp4(self, x_recv: FP4, weights: FP4, y_recv: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+        """y = x W_e^T over each expert's receive rows (dispatch_fp4's recv_x) with weights
+        [E, dout, din], both in 4 bits; y in bf16."""
+        dout = self._weights_fp4(weights, "weights", None, x_recv.format)
+        self._rows_fp4(x_recv, "x_recv", weights.cols)
+        y_recv = self._out_rows(y_recv, "y_recv", dout, stream)
+        ep_expert_gemm_fp4(self.handle, x_recv, weights, weights.cols, dout, y_recv, stream)
+        return y_recv
+
+    def expert_glu_fp4(self, x_recv: FP4, w_gate_up: FP4, act: str = "silu",
+                       h: torch.Tensor | FP4 | None = None, quantize: bool = False,
+                       h_scale: torch.Tensor | None = None, stream=None):
+        """h = act(x Wg^T) * (x Wu^T) over each expert's receive rows, both in 4 bits: in bf16,
+        or, with quantize, as an FP4 of the same format (h_scale: its tensor_scale)."""
+        rows = self._weights_fp4(w_gate_up, "w_gate_up", None, x_recv.format)
+        if rows % 256:
+            raise ValueError(f"w_gate_up must hold gate and up rows, 128 of each or a multiple, "
+                             f"got {rows} rows")
+        dff = rows // 2
+        self._rows_fp4(x_recv, "x_recv", w_gate_up.cols)
+        if h is None and quantize:
+            h = self._fp4_rows(self.R * self._last_stride(), dff, x_recv.format, h_scale, stream)
+        elif isinstance(h, FP4):
+            self._rows_fp4(h, "h", dff)
+            if h.format != x_recv.format:
+                raise ValueError(f"h is {h.format}, the rows are {x_recv.format}")
+        else:
+            h = self._out_rows(h, "h", dff, stream)
+        ep_expert_glu_fp4(self.handle, x_recv, w_gate_up, w_gate_up.cols, dff,
+                          self._activation(act), h, stream)
+        return h
+
+    def expert_ffn_fp4(self, x_recv: FP4, w_gate_up: FP4, w_down: FP4, act: str = "silu",
+                       h_scale: torch.Tensor | None = None, y_recv: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+        """expert_ffn with rows, weights and what is between them in 4 bits: two kernels, y in
+        bf16, ready for combine."""
+        dff = self._weights_fp4(w_gate_up, "w_gate_up", None, x_recv.format) // 2
+        if w_down.cols != dff:
+            raise ValueError(f"w_down takes {w_down.cols} columns, w_gate_up gives {dff}")
+        h = self._fp4_rows(self.R * self._last_stride(), dff, x_recv.format, h_scale, stream,
+                           kept=False)
+        self.expert_glu_fp4(x_recv, w_gate_up, act, h, stream=stream)
+        return self.expert_gemm_fp4(h, w_down, y_recv, stream)
 
     def _last_stride(self) -> int:
         return self._stride

@@ -1141,6 +1141,71 @@ ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x, const float* scores, co
     return cuda_status(ep::launch_permute_fp4(a, buf->num_sms, opts(buf, s)));
 }
 
+static ep_status enqueue_fp4(ep_buffer* b, const ep_fp4* x, const ep_fp4* w, int64_t din,
+                             int64_t dout, bool glu, int32_t act, void* y, const ep_fp4* y_fp4,
+                             ep_stream_t stream)
+{
+    int64_t rows = 0;
+    const int64_t lines = glu ? 2 * dout : dout;   // W's rows of an expert
+    const ep_status st = check_expert(b, din, dout, lines, &rows);
+    if (st != EP_OK) return st;
+    const int64_t E = b->cfg.num_experts;
+    if (!x || !w || x->format != w->format || (y_fp4 && y_fp4->format != w->format))
+        return EP_ERR_INVALID_ARG;
+    const ep_status sx = check_fp4(x, rows, din, 1), sw = check_fp4(w, E * lines, din, 1);
+    if (sx != EP_OK || sw != EP_OK) return sx != EP_OK ? sx : sw;
+    if (y && y_fp4) return EP_ERR_INVALID_ARG;
+    if (y_fp4) {
+        const ep_status sy = check_fp4(y_fp4, rows, dout, 1);
+        if (sy != EP_OK) return sy;
+    } else if (rows > 0 && !y) {
+        return EP_ERR_INVALID_ARG;
+    }
+    if (!is_aligned(y, 16)) return EP_ERR_ALIGNMENT;
+    if (rows <= 0) return EP_OK;
+    ep::ExpertFp4Args a = {};
+    a.cnt = b->cnt;
+    a.expert_offset = b->expert_offset;
+    a.x_codes = x->codes;
+    a.x_scales = x->scales;
+    a.x_scale = x->tensor_scale;
+    a.w_codes = w->codes;
+    a.w_scales = w->scales;
+    a.w_scale = w->tensor_scale;
+    a.y = y_fp4 ? y_fp4->codes : y;
+    a.y_scales = y_fp4 ? y_fp4->scales : nullptr;
+    a.h_scale = y_fp4 ? y_fp4->tensor_scale : nullptr;
+    a.rows = rows;
+    a.din = din;
+    a.dout = dout;
+    a.format = w->format;
+    a.E = b->cfg.num_experts;
+    a.act = act;
+    a.glu = glu;
+    a.kind = b->gemm_kind;
+    a.light_rows = b->gemm_light_rows;
+    a.row_tiles = std::max<int64_t>(std::min<int64_t>(E, b->last_T * b->cfg.topk),
+                                    b->last_T * b->cfg.topk / 256);
+    a.err = b->err;
+    return cuda_status(ep::launch_expert_fp4(a, b->num_sms, opts(b, as_stream(stream))));
+}
+
+ep_status ep_expert_gemm_fp4(ep_buffer* buf, const ep_fp4* x_recv, const ep_fp4* weights,
+                             int64_t din, int64_t dout, void* y_recv, ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_gemm_fp4");
+    return enqueue_fp4(buf, x_recv, weights, din, dout, false, 0, y_recv, nullptr, stream);
+}
+
+ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const ep_fp4* w_gate_up,
+                            int64_t din, int64_t dff, int32_t act, void* h, const ep_fp4* h_fp4,
+                            ep_stream_t stream)
+{
+    const Range range(buf, "ep_expert_glu_fp4");
+    if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+    return enqueue_fp4(buf, x_recv, w_gate_up, din, dff, true, act, h, h_fp4, stream);
+}
+
 ep_status ep_get_device_error(ep_buffer* buf, ep_stream_t stream, uint32_t* flags)
 {
     if (!buf || !flags) return EP_ERR_INVALID_ARG;

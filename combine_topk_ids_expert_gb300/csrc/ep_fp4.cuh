@@ -54,4 +54,27 @@ struct PermuteFp4Args {
 };
 cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const LaunchOpts& o);
 
+// The experts' products in 4 bits (expert_fp4.cu).
+struct ExpertFp4Args {
+    const int32_t* cnt;            // [E]
+    const int32_t* expert_offset;  // [E]
+    const uint8_t* x_codes;        // [rows][din / 2]
+    const uint8_t* x_scales;
+    const float* x_scale;          // one number or null
+    const uint8_t* w_codes;        // [E][dout or 2 dout][din / 2]
+    const uint8_t* w_scales;
+    const float* w_scale;          // [E] or null
+    void* y;                       // [rows][dout] bf16, or codes [rows][dout / 2] with y_scales
+    uint8_t* y_scales;             // glu only: quantise h (the format of x and W)
+    const float* h_scale;          // its matrix's scale: one number or null
+    int64_t rows, din, dout;       // din % 128 == 0, dout % 128 == 0
+    int format, E, act;
+    bool glu;                      // W has dout gate rows, then dout up rows; y = act(g) * u
+    int kind;                      // 1 single SMs, 2 pairs, 0: by the number of tiles
+    int light_rows;                // as GemmArgs
+    int64_t row_tiles;             // row tiles that the call is likely to have
+    uint32_t* err;
+};
+cudaError_t launch_expert_fp4(const ExpertFp4Args& a, int num_sms, const LaunchOpts& o);
+
 }  // namespace ep

@@ -93,6 +93,41 @@ struct Schedule {
     bool halves;        // pairs: last row tiles of at most tile_rows / 2 rows run as M = 128
 };
 
+// Prefixes over experts of their row tiles (of tile_rows rows each), one per class: experts
+// with at most light_rows rows are light. Called by one warp; also leaves the row counts in
+// s_cnt [E].
+__device__ __forceinline__ void row_tile_prefixes(const int32_t* cnt, int E, int light_rows,
+                                                  int tile_rows, int* s_heavy, int* s_light,
+                                                  int* s_cnt)
+{
+    const int lane = threadIdx.x & 31;
+    int carry_h = 0, carry_l = 0;
+    if (lane == 0) s_heavy[0] = s_light[0] = 0;
+    for (int base = 0; base < E; base += 32) {
+        const int e = base + lane;
+        const int c = (e < E) ? __ldcg(cnt + e) : 0;
+        if (e < E) s_cnt[e] = c;
+        const int m = (c + tile_rows - 1) / tile_rows;
+        const bool is_light = c <= light_rows;
+        int mh = is_light ? 0 : m, ml = is_light ? m : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int nh = __shfl_up_sync(0xffffffffu, mh, d);
+            const int nl = __shfl_up_sync(0xffffffffu, ml, d);
+            if (lane >= d) {
+                mh += nh;
+                ml += nl;
+            }
+        }
+        if (e < E) {
+            s_heavy[e + 1] = carry_h + mh;
+            s_light[e + 1] = carry_l + ml;
+        }
+        carry_h += __shfl_sync(0xffffffffu, mh, 31);
+        carry_l += __shfl_sync(0xffffffffu, ml, 31);
+    }
+}
+
 // Unit u is the h-th heavy unit when floor((u + 1) uh / total) steps past
 // h = floor(u uh / total), else the (u - h)-th light one: the heavy units
 // before u are exactly floor(u uh / total), so every unit of both classes
@@ -208,35 +243,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
 
     griddep_wait();   // counts, offsets and the receive rows come from earlier kernels
 
-    // Prefixes over experts of their row tiles (kTileRows rows each), one per
-    // class: experts with at most light_rows rows are light.
-    if (warp == 0) {
-        int carry_h = 0, carry_l = 0;
-        if (lane == 0) s_heavy[0] = s_light[0] = 0;
-        for (int base = 0; base < E; base += 32) {
-            const int e = base + lane;
-            const int c = (e < E) ? __ldcg(a.cnt + e) : 0;
-            if (e < E) s_cnt[e] = c;
-            const int m = (c + C::kTileRows - 1) / C::kTileRows;
-            const bool is_light = c <= a.light_rows;
-            int mh = is_light ? 0 : m, ml = is_light ? m : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int nh = __shfl_up_sync(0xffffffffu, mh, d);
-                const int nl = __shfl_up_sync(0xffffffffu, ml, d);
-                if (lane >= d) {
-                    mh += nh;
-                    ml += nl;
-                }
-            }
-            if (e < E) {
-                s_heavy[e + 1] = carry_h + mh;
-                s_light[e + 1] = carry_l + ml;
-            }
-            carry_h += __shfl_sync(0xffffffffu, mh, 31);
-            carry_l += __shfl_sync(0xffffffffu, ml, 31);
-        }
-    }
+    if (warp == 0)
+        row_tile_prefixes(a.cnt, E, a.light_rows, C::kTileRows, s_heavy, s_light, s_cnt);
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();   // the peer's barriers exist before any copy or arrival reaches them

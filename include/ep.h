@@ -515,6 +515,25 @@ EP_API ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x_TD, const float* 
                                  int64_t num_tokens_per_rank, const ep_fp4* rows,
                                  ep_stream_t stream, ep_dispatch_out* out);
 
+/* The experts' products with both operands in 4 bits, of one format, on the tensor cores'
+ * block-scaled instructions: for each expert's rows, as ep_expert_gemm and ep_expert_glu (same
+ * buffers, layouts, counts and rows left alone),
+ *     y_recv[p][o] = sum_i w[e][o][i] * x_recv[p][i]         [R*S][dout] bf16
+ *     h = act(g) * u                                          [R*S][dff]
+ * x_recv: [R*S][din], its tensor_scale one number or NULL; weights: [E][dout][din] (2 dff rows,
+ * gate rows first), tensor_scale [E] or NULL. Products are exact, sums fp32, rounded once. h
+ * goes to `h` as bf16, or, where `h_fp4` is given instead, quantised from fp32 into it (the
+ * same format, its tensor_scale one number or NULL), ready for the down projection.
+ * din % 128 == 0, dout % 128 == 0, dff % 128 == 0. Tiles of 256 rows x 256 columns on an SM
+ * pair where they fill at least a quarter of the SMs, else 128 x 128 on one; both add a row's
+ * products in the same order. */
+EP_API ep_status ep_expert_gemm_fp4(ep_buffer* buf, const ep_fp4* x_recv, const ep_fp4* weights,
+                                    int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
+
+EP_API ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const ep_fp4* w_gate_up,
+                                   int64_t din, int64_t dff, int32_t act, void* h,
+                                   const ep_fp4* h_fp4, ep_stream_t stream);
+
 /* Synchronously read and clear the device error word (EP_DEVERR_* bits).
  * Refused with EP_ERR_CAPTURE_HOST_SYNC while the stream is capturing. Status
  * stays on the device and is read only here ([graph] "Internode" item 1: no
