@@ -41,7 +41,8 @@ __all__ = [
     "ep_expert_gemv_w4", "ep_expert_glu_w4", "W4", "EpW4",
     "route", "route_backward", "quantize_fp4", "tile_fp4_scales", "untile_fp4_scales", "FP4",
     "ep_route", "ep_route_backward", "ep_fp4_scale_bytes", "ep_quantize_fp4", "ep_dequantize_fp4",
-    "ep_dispatch_fp4", "ep_expert_gemm_fp4", "ep_expert_glu_fp4", "EpFp4", "EP_SCORE_SOFTMAX", "EP_SCORE_SIGMOID", "EP_FP4_MX", "EP_FP4_NV",
+    "ep_dispatch_fp4", "ep_expert_gemm_fp4", "ep_expert_glu_fp4", "EpFp4",
+    "ep_moe_layer", "ep_moe_layer_fp4", "ep_moe_layer_workspace_bytes", "EP_SCORE_SOFTMAX", "EP_SCORE_SIGMOID", "EP_FP4_MX", "EP_FP4_NV",
     "ep_get_device_error", "DedupResult",
     "ep_buffer_query", "ep_dispatch_layout_noalloc", "ep_dispatch_layout_noalloc_scratch_bytes",
     "EP_NOALLOC_SCRATCH_BYTES", "ep_pattern_probe", "ep_pad_tokens", "group_num_tokens_per_rank",
@@ -597,6 +598,44 @@ def ep_expert_glu_fp4(handle, x_recv: FP4, w_gate_up: FP4, din: int, dff: int, a
                                        None if isinstance(h, FP4) else _ptr(h),
                                        C.byref(h._struct()) if isinstance(h, FP4) else None,
                                        _stream(stream)), "ep_expert_glu_fp4")
+
+
+# -- a whole layer for a few tokens ---------------------------------------------------
+
+def ep_moe_layer_workspace_bytes(handle, num_tokens: int, dff: int) -> int:
+    return int(_abi.lib().ep_moe_layer_workspace_bytes(handle, num_tokens, dff))
+
+
+def _moe_layer(call: str, handle, x_TD, topk_scores_TK, topk_expert_ids_TK, num_tokens, w_gate_up,
+               w_down, dff, act, out_TD, workspace, stream) -> None:
+    _check_dtype(x_TD, torch.bfloat16, "x_TD")
+    _check_dtype(topk_scores_TK, torch.float32, "topk_scores_TK")
+    _check_dtype(topk_expert_ids_TK, torch.int32, "topk_expert_ids_TK")
+    if out_TD.dtype not in _TORCH_TO_EP:
+        raise TypeError(f"out must be bfloat16 or float32, got {out_TD.dtype}")
+    check(getattr(_abi.lib(), call)(
+        handle, _ptr(x_TD), _ptr(topk_scores_TK), _ptr(topk_expert_ids_TK), num_tokens, w_gate_up,
+        w_down, dff, act, _ptr(out_TD), _TORCH_TO_EP[out_TD.dtype], _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)), call)
+
+
+def ep_moe_layer(handle, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
+                 topk_expert_ids_TK: torch.Tensor, num_tokens: int, w_gate_up: torch.Tensor,
+                 w_down: torch.Tensor, dff: int, act: int, out_TD: torch.Tensor,
+                 workspace: torch.Tensor, stream=None) -> None:
+    for name, t in (("w_gate_up", w_gate_up), ("w_down", w_down)):
+        _check_dtype(t, torch.bfloat16, name)
+    _moe_layer("ep_moe_layer", handle, x_TD, topk_scores_TK, topk_expert_ids_TK, num_tokens,
+               _ptr(w_gate_up), _ptr(w_down), dff, act, out_TD, workspace, stream)
+
+
+def ep_moe_layer_fp4(handle, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
+                     topk_expert_ids_TK: torch.Tensor, num_tokens: int, w_gate_up: FP4,
+                     w_down: FP4, dff: int, act: int, out_TD: torch.Tensor,
+                     workspace: torch.Tensor, stream=None) -> None:
+    _moe_layer("ep_moe_layer_fp4", handle, x_TD, topk_scores_TK, topk_expert_ids_TK, num_tokens,
+               C.byref(w_gate_up._struct()), C.byref(w_down._struct()), dff, act, out_TD, workspace,
+               stream)
 
 
 def ep_get_device_error(handle, stream=None) -> int:
@@ -1200,6 +1239,48 @@ class Buffer:
                            kept=False)
         self.expert_glu_fp4(x_recv, w_gate_up, act, h, stream=stream)
         return self.expert_gemm_fp4(h, w_down, y_recv, stream)
+
+    # -- the whole layer for a few tokens ------------------------------------------
+    def moe_layer(self, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
+                  topk_expert_ids_TK: torch.Tensor, w_gate_up, w_down, act: str = "silu",
+                  out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                  stream=None) -> torch.Tensor:
+        """dispatch, the experts' gated block and combine in two kernels, for at most 64 tokens
+        and 512 (token, k) pairs: weights w_gate_up [E, 2 dff, D] and w_down [E, D, dff], bf16
+        tensors or FP4 (activations keep bf16's precision). Leaves the last dispatch's layout and
+        receive rows alone."""
+        fp4 = isinstance(w_gate_up, FP4)
+        if fp4 != isinstance(w_down, FP4):
+            raise TypeError("w_gate_up and w_down must both be tensors or both FP4")
+        if fp4:
+            if w_gate_up.format != w_down.format:
+                raise ValueError(f"w_gate_up is {w_gate_up.format}, w_down {w_down.format}")
+            shapes = [(*w.codes.shape[:-1], w.cols) for w in (w_gate_up, w_down)]
+        else:
+            shapes = [tuple(w_gate_up.shape), tuple(w_down.shape)]
+        dff = shapes[1][-1]
+        if shapes != [(self.E, 2 * dff, self.D), (self.E, self.D, dff)]:
+            raise ValueError(f"weights must be [{self.E}, 2 dff, {self.D}] and [{self.E}, {self.D}, "
+                             f"dff], got {shapes}")
+        T = x_TD.shape[0]
+        if x_TD.shape != (T, self.D) or topk_expert_ids_TK.shape != (T, self.K) or \
+                topk_scores_TK.shape != (T, self.K):
+            raise ValueError(f"x, scores and ids must be [T, {self.D}], [T, {self.K}] and "
+                             f"[T, {self.K}], got {tuple(x_TD.shape)}, "
+                             f"{tuple(topk_scores_TK.shape)}, {tuple(topk_expert_ids_TK.shape)}")
+        if out is None:
+            out = self._empty((T, self.D), torch.bfloat16 if out_dtype is None else out_dtype, stream)
+        elif out.shape != (T, self.D):
+            raise ValueError(f"out must be {[T, self.D]}, got {list(out.shape)}")
+        nbytes = ep_moe_layer_workspace_bytes(self.handle, T, dff)
+        if nbytes == 0:
+            raise EpError(_abi.EP_ERR_CAPACITY if T > 64 or T * self.K > 512
+                          else _abi.EP_ERR_INVALID_ARG, "ep_moe_layer")
+        work = self._empty((nbytes,), torch.uint8, stream, kept=False)
+        (ep_moe_layer_fp4 if fp4 else ep_moe_layer)(
+            self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, w_gate_up, w_down, dff,
+            self._activation(act), out, work, stream)
+        return out
 
     def _last_stride(self) -> int:
         return self._stride

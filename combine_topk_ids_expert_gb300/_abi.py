@@ -194,6 +194,13 @@ SIGNATURES = {
     "ep_expert_glu_fp4": (C.c_int, [C.c_void_p, C.POINTER(EpFp4), C.POINTER(EpFp4), C.c_int64,
                                     C.c_int64, C.c_int32, C.c_void_p, C.POINTER(EpFp4),
                                     C.c_void_p]),
+    "ep_moe_layer_workspace_bytes": (C.c_size_t, [C.c_void_p, C.c_int64, C.c_int64]),
+    "ep_moe_layer": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                               C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
+                               C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "ep_moe_layer_fp4": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                   C.POINTER(EpFp4), C.POINTER(EpFp4), C.c_int64, C.c_int32,
+                                   C.c_void_p, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
     "ep_get_device_error": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint32)]),
     "ep_buffer_query": (C.c_int, [C.c_void_p, C.POINTER(EpBufferInfo)]),
     "ep_dispatch_layout_noalloc": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32,

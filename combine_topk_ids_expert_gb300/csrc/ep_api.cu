@@ -1206,6 +1206,123 @@ ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const ep_fp4* 
     return enqueue_fp4(buf, x_recv, w_gate_up, din, dff, true, act, h, h_fp4, stream);
 }
 
+namespace {
+
+// The layer's workspace: h, its tiles' maxima, the pairs' results, the counters.
+struct LayerWorkspace {
+    size_t h, h_most, y, done, total;
+};
+
+LayerWorkspace layer_workspace(int64_t pairs, int64_t D, int64_t dff)
+{
+    Carve cv;
+    LayerWorkspace w;
+    w.h = cv.take((size_t)(pairs * dff * 2));
+    w.h_most = cv.take((size_t)(pairs * (dff / 32) * 4));
+    w.y = cv.take((size_t)(pairs * D * 4));
+    w.done = cv.take((size_t)(D / 32 * 4));
+    w.total = cv.off;
+    return w;
+}
+
+ep_status check_layer(const ep_buffer* b, int64_t T, int64_t dff)
+{
+    if (!b) return EP_ERR_INVALID_ARG;
+    if (b->cfg.dtype != EP_BF16 || T < 0) return EP_ERR_INVALID_ARG;
+    if (b->cfg.hidden % 128 != 0 || dff < 128 || dff % 128 != 0) return EP_ERR_INVALID_ARG;
+    if (T > ep::kLayerMaxTokens || T * b->cfg.topk > ep::kLayerMaxPairs ||
+        T > b->cfg.num_max_tokens_per_rank)
+        return EP_ERR_CAPACITY;
+    const int64_t E = b->cfg.num_experts;
+    // The weights' rows and the units are counted in int32.
+    if (dff > INT32_MAX / 2 / E || b->cfg.hidden > INT32_MAX / E) return EP_ERR_CAPACITY;
+    if ((int64_t)ep::kLayerMaxPairs * (dff / 64 + b->cfg.hidden / 128) > INT32_MAX) return EP_ERR_CAPACITY;
+    return EP_OK;
+}
+
+ep_status enqueue_layer(ep_buffer* b, const void* x, const float* scores, const int32_t* ids, int64_t T,
+                        int64_t dff, int32_t act, void* out, int32_t out_dtype, void* workspace,
+                        size_t workspace_bytes, ep_stream_t stream, ep::MoeLayerArgs a)
+{
+    if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+    if (out_dtype != EP_BF16 && out_dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (!a.w_gate_up || !a.w_down) return EP_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !scores || !ids || !out)) return EP_ERR_INVALID_ARG;
+    if (!is_aligned(x, 16) || !is_aligned(scores, 4) || !is_aligned(ids, 4) || !is_aligned(out, 16) ||
+        !is_aligned(a.w_gate_up, 16) || !is_aligned(a.w_down, 16))
+        return EP_ERR_ALIGNMENT;
+    if (T == 0) return EP_OK;
+    const int64_t pairs = T * b->cfg.topk, D = b->cfg.hidden;
+    const LayerWorkspace w = layer_workspace(pairs, D, dff);
+    if (!workspace || !is_aligned(workspace, kAlign) || workspace_bytes < w.total)
+        return EP_ERR_WORKSPACE;
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    a.x = x;
+    a.scores = scores;
+    a.ids = ids;
+    a.T = (int)T;
+    a.K = b->cfg.topk;
+    a.E = b->cfg.num_experts;
+    a.D = D;
+    a.dff = dff;
+    a.act = act;
+    a.h = reinterpret_cast<uint16_t*>(at + w.h);
+    a.h_most = reinterpret_cast<uint32_t*>(at + w.h_most);
+    a.y = reinterpret_cast<float*>(at + w.y);
+    a.done = reinterpret_cast<uint32_t*>(at + w.done);
+    a.out = out;
+    a.out_f32 = out_dtype == EP_F32;
+    a.err = b->err;
+    return cuda_status(ep::launch_moe_layer(a, b->num_sms, opts(b, as_stream(stream))));
+}
+
+}  // namespace
+
+size_t ep_moe_layer_workspace_bytes(const ep_buffer* buf, int64_t T, int64_t dff)
+{
+    if (check_layer(buf, T, dff) != EP_OK) return 0;
+    return layer_workspace(T * buf->cfg.topk, buf->cfg.hidden, dff).total;
+}
+
+ep_status ep_moe_layer(ep_buffer* buf, const void* x, const float* scores, const int32_t* ids, int64_t T,
+                       const void* w_gate_up, const void* w_down, int64_t dff, int32_t act, void* out,
+                       int32_t out_dtype, void* workspace, size_t workspace_bytes, ep_stream_t stream)
+{
+    const Range range(buf, "ep_moe_layer");
+    const ep_status st = check_layer(buf, T, dff);
+    if (st != EP_OK) return st;
+    ep::MoeLayerArgs a = {};
+    a.format = -1;
+    a.w_gate_up = w_gate_up;
+    a.w_down = w_down;
+    return enqueue_layer(buf, x, scores, ids, T, dff, act, out, out_dtype, workspace, workspace_bytes,
+                         stream, a);
+}
+
+ep_status ep_moe_layer_fp4(ep_buffer* buf, const void* x, const float* scores, const int32_t* ids,
+                           int64_t T, const ep_fp4* w_gate_up, const ep_fp4* w_down, int64_t dff,
+                           int32_t act, void* out, int32_t out_dtype, void* workspace,
+                           size_t workspace_bytes, ep_stream_t stream)
+{
+    const Range range(buf, "ep_moe_layer_fp4");
+    const ep_status st = check_layer(buf, T, dff);
+    if (st != EP_OK) return st;
+    const int64_t E = buf->cfg.num_experts, D = buf->cfg.hidden;
+    const ep_status s1 = check_fp4(w_gate_up, E * 2 * dff, D, 1), s2 = check_fp4(w_down, E * D, dff, 1);
+    if (s1 != EP_OK || s2 != EP_OK) return s1 != EP_OK ? s1 : s2;
+    if (w_gate_up->format != w_down->format) return EP_ERR_INVALID_ARG;
+    ep::MoeLayerArgs a = {};
+    a.format = w_gate_up->format;
+    a.w_gate_up = w_gate_up->codes;
+    a.w_down = w_down->codes;
+    a.gate_up_scales = w_gate_up->scales;
+    a.down_scales = w_down->scales;
+    a.gate_up_scale = w_gate_up->tensor_scale;
+    a.down_scale = w_down->tensor_scale;
+    return enqueue_layer(buf, x, scores, ids, T, dff, act, out, out_dtype, workspace, workspace_bytes,
+                         stream, a);
+}
+
 ep_status ep_get_device_error(ep_buffer* buf, ep_stream_t stream, uint32_t* flags)
 {
     if (!buf || !flags) return EP_ERR_INVALID_ARG;

@@ -77,4 +77,30 @@ struct ExpertFp4Args {
 };
 cudaError_t launch_expert_fp4(const ExpertFp4Args& a, int num_sms, const LaunchOpts& o);
 
+// A whole layer for a few tokens (moe_layer.cu).
+constexpr int kLayerMaxTokens = 64, kLayerMaxPairs = 512;
+struct MoeLayerArgs {
+    const void* x;                 // [T][D] bf16
+    const float* scores;           // [T][K]
+    const int32_t* ids;            // [T][K]
+    int T, K, E;                   // T <= kLayerMaxTokens, T * K <= kLayerMaxPairs
+    int64_t D, dff;                // multiples of 128
+    int format;                    // kFp4Mx, kFp4Nv, or any other: bf16 weights
+    const void* w_gate_up;         // [E][2 dff][D] bf16, or codes
+    const void* w_down;            // [E][D][dff]
+    const uint8_t* gate_up_scales; // 4 bits
+    const uint8_t* down_scales;
+    const float* gate_up_scale;    // [E] or null
+    const float* down_scale;
+    int act;
+    uint16_t* h;                   // workspace: [T K][dff]
+    uint32_t* h_most;              // [T K][dff / 32]
+    float* y;                      // [T K][D]
+    uint32_t* done;                // [D / 32]
+    void* out;                     // [T][D]
+    bool out_f32;
+    uint32_t* err;
+};
+cudaError_t launch_moe_layer(const MoeLayerArgs& a, int num_sms, const LaunchOpts& o);
+
 }  // namespace ep

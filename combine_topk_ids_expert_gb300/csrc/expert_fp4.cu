@@ -75,42 +75,82 @@ struct Fp4GemmArgs {
     uint32_t* err;
 };
 
-// One stage's scales into shared memory: of the tile's 128 receive rows at row0, and of the
-// tile's BN rows of W. One warp.
+// One warp's share of a stage's scales, of the tile's 128 receive rows at row0 and of its BN
+// rows of W: what has to pass registers is fetched ahead of the stage's turn, the rest copied.
+// 16 bytes of a line of W's scales come from one tile, or (one SM, gated: 64 gate rows and 64
+// up rows) half from the gate rows' tile and half from the up rows'.
 template <class C>
-__device__ __forceinline__ void load_scales(uint32_t s_a, uint32_t s_b, const Fp4GemmArgs& a, int e,
-                                            int nb, int64_t row0, int stage, int lane)
-{
-    const int64_t tiles = a.din / (4 * Fp4<C::FMT>::kBlock);
-    const int64_t kt0 = (int64_t)stage * C::kTiles;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        // Rows behind the last receive row do not exist: the last one's scales instead.
-        const int64_t row = min(row0 + 32 * q + lane, a.rows - 1);
-        const uint8_t* src = a.x_scales + fp4_scale_at(row, kt0, tiles);
-#pragma unroll
-        for (int j = 0; j < C::kTiles; ++j) {
-            const bool in = kt0 + j < tiles;
-            cp_async<4>(s_a + j * kScaleTile + lane * 16 + q * 4, in ? src + j * 512 : src, in);
-        }
-    }
-    // 16 bytes of a line of W's scales come from one tile, or (one SM, gated: 64 gate rows and
-    // 64 up rows) half from the gate rows' tile and half from the up rows'.
-    constexpr bool kHalves = C::GLU && !C::PAIR;
-    constexpr int kBytes = kHalves ? 8 : 16, kParts = kHalves ? 2 : C::BN / 128;
-#pragma unroll
-    for (int b = 0; b < kParts; ++b) {
+struct StageScales {
+    static constexpr bool kHalves = C::GLU && !C::PAIR;
+    uint32_t x[4][C::kTiles];
+    uint2 w[kHalves ? 2 : 1][C::kTiles];
+
+    static __device__ __forceinline__ const uint8_t* w_tile(const Fp4GemmArgs& a, int e, int nb, int b,
+                                                            int64_t kt0, int64_t tiles)
+    {
         const int64_t row = C::GLU ? ((int64_t)e * 2 + b) * a.dout + nb * C::kOutBN
                                    : (int64_t)e * a.dout + nb * C::BN + b * 128;
-        const uint8_t* src = a.w_scales + fp4_scale_at(row, kt0, tiles) + lane * 16;
-        const uint32_t dst = s_b + lane * 16 + (kHalves ? b * 8 : b * kScaleTile);
+        return a.w_scales + fp4_scale_at(row, kt0, tiles);
+    }
+
+    __device__ __forceinline__ void fetch(const Fp4GemmArgs& a, int e, int nb, int64_t row0, int stage,
+                                          int lane)
+    {
+        const int64_t tiles = a.din / (4 * Fp4<C::FMT>::kBlock), kt0 = (int64_t)stage * C::kTiles;
 #pragma unroll
-        for (int j = 0; j < C::kTiles; ++j) {
-            const bool in = kt0 + j < tiles;
-            cp_async<kBytes>(dst + j * (C::BN / 128) * kScaleTile, in ? src + j * 512 : src, in);
+        for (int q = 0; q < 4; ++q) {
+            // Rows behind the last receive row do not exist: the last one's scales instead.
+            const int64_t row = min(row0 + 32 * q + lane, a.rows - 1);
+            const uint8_t* src = a.x_scales + fp4_scale_at(row, kt0, tiles);
+#pragma unroll
+            for (int j = 0; j < C::kTiles; ++j)
+                x[q][j] = kt0 + j < tiles ? __ldcg(reinterpret_cast<const uint32_t*>(src + j * 512)) : 0u;
+        }
+        if (kHalves) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint8_t* src = w_tile(a, e, nb, b, kt0, tiles) + lane * 16;
+#pragma unroll
+                for (int j = 0; j < C::kTiles; ++j)
+                    w[b % (kHalves ? 2 : 1)][j] = kt0 + j < tiles ? __ldcg(reinterpret_cast<const uint2*>(src + j * 512))
+                                                  : make_uint2(0u, 0u);
+            }
         }
     }
-}
+
+    __device__ __forceinline__ void store(uint32_t s_a, uint32_t s_b, const Fp4GemmArgs& a, int e, int nb,
+                                          int stage, int lane) const
+    {
+        const int64_t tiles = a.din / (4 * Fp4<C::FMT>::kBlock), kt0 = (int64_t)stage * C::kTiles;
+        if (!kHalves) {
+#pragma unroll
+            for (int b = 0; b < C::BN / 128; ++b) {
+                const uint8_t* src = w_tile(a, e, nb, b, kt0, tiles) + lane * 16;
+#pragma unroll
+                for (int j = 0; j < C::kTiles; ++j) {
+                    const bool in = kt0 + j < tiles;
+                    cp_async16(s_b + (j * (C::BN / 128) + b) * kScaleTile + lane * 16,
+                               in ? src + j * 512 : src, in);
+                }
+            }
+            cp_async_commit();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < C::kTiles; ++j)
+                sts32(s_a + j * kScaleTile + lane * 16 + q * 4, x[q][j]);
+        if (kHalves) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < C::kTiles; ++j)
+                    sts64(s_b + j * kScaleTile + lane * 16 + b * 8, w[b % (kHalves ? 2 : 1)][j]);
+        } else {
+            cp_async_wait<0>();
+        }
+    }
+};
 
 // 32 fp32 elements of a row as codes and scales in a matrix of `cols` columns.
 template <int FMT>
@@ -386,12 +426,12 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             for (int k = 0; k < k_iters; ++k, ++g) {
                 if (g % kScaleWarps != mine) continue;
                 const int s = g % STAGES;
+                StageScales<C> sc;
+                sc.fetch(a, p.e, p.nb, row0, k, lane);
                 ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
                 if (!ok) break;
                 const uint32_t ss = ring_scales + (uint32_t)s * (C::kScalesA + C::kScalesB);
-                load_scales<C>(ss, ss + C::kScalesA, a, p.e, p.nb, row0, k, lane);
-                cp_async_commit();
-                cp_async_wait<0>();
+                sc.store(ss, ss + C::kScalesA, a, p.e, p.nb, k, lane);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {

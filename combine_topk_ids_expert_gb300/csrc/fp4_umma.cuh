@@ -96,13 +96,23 @@ inline bool make_code_map(CUtensorMap* m, const void* base, uint64_t cols, uint6
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// N bytes (4, 8 or 16) to shared memory, zeros instead where !in.
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in)
+// 16 bytes from L2 to shared memory, zeros instead where !in. Scales may come from the kernel
+// before, so nothing here reads them by way of L1 (see ep_device.cuh).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
-                 "r"(in ? N : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
                  : "memory");
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts64(uint32_t addr, uint2 v)
+{
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit()

@@ -1,0 +1,826 @@
+// moe_layer.cu - a whole mixture-of-experts layer for a few tokens in two kernels:
+//     h[t,k] = act(Wg_e x_t) * (Wu_e x_t),           e = ids[t][k]
+//     out[t] = sum_k scores[t][k] * (Wd_e h[t,k])
+// with bf16 or 4-bit weights (fp4.cuh). No dispatch, no receive rows, no combine: each CTA
+// works the routing out by itself from the ids (at most kMaxPairs of them).
+//
+// With a few rows per expert the layer is the reading of the experts' weights, so the weights
+// are the M side of the tensor cores' tiles (128 rows, streamed by TMA through a ring as deep
+// as shared memory) and an expert's token rows, 16 at a time, the N side. Nothing touches the
+// weights on their way: 4-bit codes go to the block-scaled instructions as they lie, which
+// leaves the CUDA cores with the activations alone.
+//
+// For 4-bit weights an activation keeps its precision: a row enters as four rows of e2m1
+// digits that share a power of two s for each block of the weights' block size,
+//     x = s (d0 + d1 / 8 + d2 / 64 + d3 / 512) + rest,   |d| <= 4, |rest| <= s / 1024,
+// s = 2^(floor(log2 amax) - 1): each digit is what is left rounded to e2m1 (half steps below
+// 2, whole ones up to 4), which leaves at most 1/2, an eighth of the next digit's range. A bf16
+// element down to a sixteenth of its block's largest is exact, smaller ones are within 2^-11
+// of the largest. The digits are four columns of one product and joined in the epilogue.
+// nv scales (ue4m3) reach over 18 binades only: they count from the row's largest block, and
+// blocks 2^17 below it are within 2^-28 of the row's largest.
+//
+// Work: a unit is a chunk of up to 16 rows of an expert x a tile of 128 weight rows (64 gate
+// and 64 up rows of the same columns in the first kernel). A cluster of 1, 2 or 4 CTAs shares
+// a unit along K, so that few units still fill the SMs; their partial sums meet in shared
+// memory, each CTA adding up a share of the rows in the order of the CTAs. In the second kernel
+// every pair's result goes to a workspace in fp32, and the CTA that completes a tile's last unit
+// adds the experts' results in the order of k. All sums have a fixed order.
+//
+// h is rounded to bf16 (as in the block on receive rows); sums, scores and results are fp32 and
+// rounded once.
+#include "ep_fp4.cuh"
+#include "fp4_umma.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kChunkRows = 16;                  // token rows of a unit
+constexpr int kDigits = 4;
+constexpr int kRowWarps = 8, kEpiWarps = 4, kScaleWarps = 4;
+constexpr int kEpiWarp0 = 2, kScaleWarp0 = 6, kRowWarp0 = 10;
+constexpr int kLayerThreads = 32 * (kRowWarp0 + kRowWarps);
+constexpr uint32_t kLayerTmem = 256;
+constexpr int kMaxSplit = 4;
+constexpr int kFmtBf16 = 2;                     // beside kFp4Mx, kFp4Nv
+
+template <int FMT_, bool DOWN_>
+struct LayerCfg {
+    static constexpr int FMT = FMT_;
+    static constexpr bool DOWN = DOWN_, FP4 = FMT_ != kFmtBf16;
+    static constexpr int kStageK = FP4 ? kFp4StageK : 64;       // 128 bytes of a row
+    static constexpr int kCols = FP4 ? kChunkRows * kDigits : kChunkRows;
+    static constexpr int kTiles = FP4 ? Fp4Mma<FP4 ? FMT_ : kFp4Mx>::kTiles : 0;
+    static constexpr uint32_t kBytesA = kBM * 128, kBytesB = kCols * 128;
+    static constexpr uint32_t kScales = kTiles * kScaleTile;    // of A and of B, each
+    static constexpr uint32_t kStageBytes = kBytesA + kBytesB + 2 * kScales;
+    static constexpr uint32_t kExchange = 2 * kChunkRows * 128 * 4;
+    static constexpr uint32_t kTables = 4 * kMaxExperts + 8 * kLayerMaxPairs + 2 * 2 * kLayerMaxPairs;
+    static constexpr uint32_t kFixed = 1024 + kExchange + kTables + 512;
+    static constexpr int kFit = (int)((kSmemLimit - kFixed) / kStageBytes);
+    static constexpr int STAGES = kFit > 12 ? 12 : kFit;
+    static constexpr size_t kSmem = kFixed + (size_t)STAGES * kStageBytes;
+    static constexpr uint32_t kScaleCol0 = 2 * kChunkRows * kDigits;   // after two accumulators
+    // Arrivals that fill a stage: the copy of A, the scales, the warps that bring rows.
+    static constexpr int kRowArrivals = FP4 ? kRowWarps : kRowWarps / 2;
+    static constexpr uint32_t kFullCount = 1u + (FP4 ? 1u : 0u) + kRowArrivals;
+    static_assert(STAGES >= 4, "ring too shallow");
+    static_assert(kLayerMaxPairs <= kLayerThreads, "a thread to a pair");
+    static_assert(kScaleCol0 + 2 * 2 * 16 <= kLayerTmem, "accumulators and scales");
+};
+
+struct LayerKernelArgs {
+    const int32_t* ids;
+    const float* scores;
+    const uint16_t* rows;          // x [T][K dim], or h [pairs][K dim]
+    const uint8_t* w_scales;
+    const float* w_scale;          // [E] or null
+    uint16_t* h;                   // first kernel: [pairs][dff]
+    uint32_t* h_most;              // [pairs][dff / 64]: the largest |h| (bits) of each tile (nv)
+    float* y;                      // second kernel: [pairs][D]
+    uint32_t* done;                // [D / 32] CTAs that have added their part of a unit to these columns
+    int counters;                  // D / 32
+    void* out;                     // [T][D]
+    int T, K, E;
+    int din, wrows;                // contraction; W's rows of an expert
+    int tiles;                     // tiles of an expert
+    int act;
+    bool out_f32;
+    uint32_t* err;
+};
+
+struct Chunk {
+    uint16_t e, start, rows, pad;
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ int cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return (int)r;
+}
+
+__device__ __forceinline__ void store_out(const LayerKernelArgs& a, int64_t at, float v)
+{
+    if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+    else static_cast<uint16_t*>(a.out)[at] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
+}
+
+// out[t][col] of every token: the pairs' results in the order of k, as in combine.
+__device__ __forceinline__ void join_experts(const LayerKernelArgs& a, int col)
+{
+    for (int t = 0; t < a.T; ++t) {
+        float r = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < a.K; ++k) {
+            const int i = t * a.K + k;
+            if (valid_id(__ldcg(a.ids + i), a.E) >= 0)
+                r = fmaf(__ldcg(a.scores + i), __ldcg(a.y + (int64_t)i * a.wrows + col), r);
+        }
+        store_out(a, (int64_t)t * a.wrows + col, r);
+    }
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Exponent of s of a block (or row) whose largest magnitude has these bits.
+__device__ __forceinline__ int digit_exponent(uint32_t most) { return max((int)(most >> 23), 1) - 128; }
+
+// The ue4m3 code of 2^k, -9 <= k <= 8.
+__device__ __forceinline__ uint32_t ue4m3_pow2(int k)
+{
+    return k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
+}
+
+// 256 elements of a row, 8 in each lane, into the digit rows n0 .. n0 + 3 of a stage's B tile
+// and the words of their scales.
+template <int FMT>
+__device__ __forceinline__ void store_digits(uint32_t sb, uint32_t sscale, int n0, int lane,
+                                             const int4& raw, int row_exp)
+{
+    const uint32_t q[4] = {(uint32_t)raw.x, (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w};
+    float v[8];
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(q[i] << 16);
+        v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+        most = max(most, max(__float_as_uint(v[2 * i]) & 0x7FFFFFFFu,
+                             __float_as_uint(v[2 * i + 1]) & 0x7FFFFFFFu));
+    }
+    most = max(most, __shfl_xor_sync(~0u, most, 1));
+    if (FMT == kFp4Mx) most = max(most, __shfl_xor_sync(~0u, most, 2));
+    int e = digit_exponent(most);               // -127 .. 126
+    uint32_t code;
+    if (FMT == kFp4Mx) {
+        code = (uint32_t)(e + 127);
+    } else {
+        const int k = max(e - row_exp + 8, -9);
+        code = ue4m3_pow2(min(k, 8));
+        e = row_exp - 8 + k;
+    }
+    const bool bad = most >= 0x7F800000u;       // an infinity or a NaN: so is the row's result
+    if (bad) code = FMT == kFp4Mx ? kNanMx : kNanNv;
+    // 2^-e in two factors: a block far below its row's largest has e down to -143.
+    const float f0 = bad ? 0.0f : pow2(-(e >> 1)), f1 = pow2(-(e - (e >> 1)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = bad ? 0.0f : v[i] * f0 * f1;
+    const int unit = lane >> 2;
+#pragma unroll
+    for (int d = 0; d < kDigits; ++d) {
+        uint32_t w = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = cvt_e2m1x2(v[2 * i], v[2 * i + 1]);
+            w |= c << (8 * i);
+            if (d + 1 < kDigits) {
+                const uint32_t h2 = e2m1x2_to_f16x2(c);
+                v[2 * i] = (v[2 * i] - f16_lo(h2)) * 8.0f;
+                v[2 * i + 1] = (v[2 * i + 1] - f16_hi(h2)) * 8.0f;
+            }
+        }
+        const int n = n0 + d;
+        sts32(sb + (uint32_t)(n * 128 + ((unit ^ (n & 7)) << 4) + (lane & 3) * 4), w);
+    }
+    const int block = FMT == kFp4Mx ? lane >> 2 : lane >> 1;
+    if ((lane & (FMT == kFp4Mx ? 3 : 1)) == 0) {
+#pragma unroll
+        for (int d = 0; d < kDigits; ++d) {
+            const int n = n0 + d;
+            sts_u8(sscale + (uint32_t)((block >> 2) * kScaleTile + (n & 31) * 16 + (n >> 5) * 4 + (block & 3)),
+                   code);
+        }
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kLayerThreads, 1)
+moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs a)
+{
+    constexpr int STAGES = C::STAGES, FMT = C::FMT;
+    constexpr bool DOWN = C::DOWN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t ring_b = ring + STAGES * C::kBytesA;
+    const uint32_t ring_s = ring_b + STAGES * C::kBytesB;
+    float* s_x = reinterpret_cast<float*>(smem + STAGES * C::kStageBytes);     // [2][16][128]
+    int* s_cnt = reinterpret_cast<int*>(s_x + 2 * kChunkRows * 128);           // [E]: rows, then first row
+    Chunk* s_chunk = reinterpret_cast<Chunk*>(s_cnt + kMaxExperts);            // [pairs]
+    uint16_t* s_list = reinterpret_cast<uint16_t*>(s_chunk + kLayerMaxPairs);  // pairs by expert
+    int16_t* s_exp = reinterpret_cast<int16_t*>(s_list + kLayerMaxPairs);      // nv: exponents of the rows
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_exp + kLayerMaxPairs);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * STAGES;
+    const uint32_t accum_full0 = empty0 + 8u * STAGES, accum_free0 = accum_full0 + 16u;
+    const uint32_t x_full0 = accum_free0 + 16u, x_free0 = x_full0 + 16u;
+    const uint32_t drain = x_free0 + 16u;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 9);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    int* s_chunks = const_cast<int*>(reinterpret_cast<volatile int*>(s_abort + 1));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = cluster_size(), rank = cluster_rank();
+    const int first = cluster_index(), step = cluster_count();
+    const int pairs = a.T * a.K;
+
+    for (int e = threadIdx.x; e < a.E; e += kLayerThreads) s_cnt[e] = 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8u * s, C::kFullCount);
+            mbar_init(empty0 + 8u * s, 1u);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accum_full0 + 8u * b, 1u);
+            mbar_init(accum_free0 + 8u * b, kEpiWarps);
+            mbar_init(x_full0 + 8u * b, kEpiWarps * split);
+            mbar_init(x_free0 + 8u * b, kEpiWarps * split);
+        }
+        mbar_init(drain, 1u);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<false>(smem_u32(s_tmem), kLayerTmem);
+        tmem_relinquish<false>();
+    }
+    // The second kernel may start while the first one ends: by then the kernels before the
+    // first one are complete, and with them the ids, the scores and the weights. What the first
+    // one writes (h, its maxima, the counters) is waited for where it is used.
+    if (!DOWN) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
+    __syncthreads();
+
+    // ---- routing: the pairs by expert, in chunks ------------------------------------
+    // A thread to a pair. The rank of a pair among its expert's follows the order of the pairs,
+    // so that every CTA has the same rows in the same chunks: warp after warp.
+    int mine = -1, my_rank = 0;
+    if ((int)threadIdx.x < pairs) {
+        const int raw = __ldcg(a.ids + threadIdx.x);
+        mine = valid_id(raw, a.E);
+        if (!DOWN && mine != raw && blockIdx.x == 0) atomicOr(a.err, kErrBadId);
+    }
+    for (int w = 0; 32 * w < pairs; ++w) {
+        if (warp == w) {
+            const unsigned same = __match_any_sync(~0u, mine);
+            if (mine >= 0) my_rank = s_cnt[mine] + __popc(same & lanemask_lt(lane));
+            __syncwarp();
+            if (mine >= 0 && lane == __ffs(same) - 1) s_cnt[mine] += __popc(same);
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        int rows0 = 0, chunks0 = 0;
+        for (int base = 0; base < a.E; base += 32) {
+            const int e = base + lane;
+            const int c = e < a.E ? s_cnt[e] : 0;
+            const int packed = c | ((c + kChunkRows - 1) / kChunkRows) << 16;
+            int v = packed;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int n = __shfl_up_sync(~0u, v, d);
+                if (lane >= d) v += n;
+            }
+            const int row = rows0 + ((v - packed) & 0xFFFF);
+            int chunk = chunks0 + ((v - packed) >> 16);
+            if (e < a.E) s_cnt[e] = row;
+            for (int at = 0; at < c; at += kChunkRows, ++chunk)
+                s_chunk[chunk] = {(uint16_t)e, (uint16_t)(row + at), (uint16_t)min(c - at, kChunkRows), 0};
+            const int all = __shfl_sync(~0u, v, 31);
+            rows0 += all & 0xFFFF;
+            chunks0 += all >> 16;
+        }
+        if (lane == 0) *s_chunks = chunks0;
+    }
+    __syncthreads();
+    if (mine >= 0) s_list[s_cnt[mine] + my_rank] = (uint16_t)threadIdx.x;
+    const int chunks = *s_chunks, units = chunks * a.tiles;
+    const int all_stages = (a.din + C::kStageK - 1) / C::kStageK;
+    const int k_first = rank * all_stages / split, k_last = (rank + 1) * all_stages / split;
+
+    const int64_t thread0 = (int64_t)blockIdx.x * kLayerThreads + threadIdx.x;
+    const int64_t threads = (int64_t)gridDim.x * kLayerThreads;
+    if (!DOWN) {
+        for (int64_t i = thread0; i < a.counters; i += threads) a.done[i] = 0u;
+    } else if (chunks == 0) {   // no token has an expert
+        griddep_wait();
+        for (int64_t i = thread0; i < (int64_t)a.T * a.wrows; i += threads) store_out(a, i, 0.0f);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) cluster_sync();   // the peers' barriers exist before anything reaches them
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+
+    if (warp == 0) {
+        // ---- weights ------------------------------------------------------------
+        int g = 0;
+        bool ok = true;
+        for (int u = first; u < units && ok && !*s_abort; u += step) {
+            const int tile = u / chunks;
+            const int w0 = s_chunk[u - tile * chunks].e * a.wrows + tile * (DOWN ? 128 : 64);
+            const int w1 = w0 + (DOWN ? 64 : a.wrows / 2);
+            for (int k = k_first; k < k_last; ++k, ++g) {
+                const int s = g % STAGES;
+                ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t fb = full0 + 8u * s, sa = ring + (uint32_t)s * C::kBytesA;
+                    const int kc = k * (C::FP4 ? kFp4StageK / 2 : C::kStageK);
+                    mbar_expect_tx(fb, C::kBytesA);
+                    tma_load_2d(sa, &tm_w, kc, w0, fb);
+                    tma_load_2d(sa + C::kBytesA / 2, &tm_w, kc, w1, fb);
+                }
+                __syncwarp();
+            }
+        }
+        // The copies this warp issued land before shared memory goes away.
+        const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
+        for (int i = (g > STAGES ? g - STAGES : 0); i < g; ++i)
+            mbar_wait_until(empty0 + 8u * (i % STAGES), (uint32_t)((i / STAGES) & 1), deadline);
+    } else if (warp == 1) {
+        // ---- products -------------------------------------------------------------
+        int g = 0, tl = 0;
+        bool issued = false, ok = true;
+        for (int u = first; u < units && ok && !*s_abort && k_last > k_first; u += step, ++tl) {
+            const int acc = tl & 1;
+            ok = warp_all(wait_or_abort(accum_free0 + 8u * acc, (uint32_t)(((tl >> 1) & 1) ^ 1), s_abort));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem + (uint32_t)(acc * kChunkRows * kDigits);
+            const int rows = s_chunk[u % chunks].rows;
+            const int n = C::FP4 ? (rows * kDigits + 15) / 16 * 16 : kChunkRows;
+            const uint32_t idesc = C::FP4 ? Fp4Mma<C::FP4 ? FMT : kFp4Mx>::idesc(kBM, n)
+                                          : (1u << 4) | (1u << 7) | (1u << 10) |
+                                                ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+            for (int k = k_first; k < k_last; ++k, ++g) {
+                const int s = g % STAGES;
+                ok = warp_all(wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sa = ring + (uint32_t)s * C::kBytesA;
+                const uint32_t sb = ring_b + (uint32_t)s * C::kBytesB;
+                if (elect_one()) {
+                    if constexpr (C::FP4) {
+                        const uint32_t ss = ring_s + (uint32_t)s * (2 * C::kScales);
+                        const uint32_t ta = tmem + C::kScaleCol0 + (uint32_t)((g & 1) * 32), tb = ta + 16u;
+#pragma unroll
+                        for (int j = 0; j < C::kTiles; ++j) {
+                            tmem_copy_scales<false>(ta + 4u * j, scale_desc(ss + j * kScaleTile));
+                            tmem_copy_scales<false>(tb + 4u * j,
+                                                    scale_desc(ss + C::kScales + j * kScaleTile));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kFp4StageK / kFp4K; ++j) {
+                            const int t = Fp4Mma<FMT>::tile_of_step(j);
+                            umma_fp4<FMT, false>(d_tmem, smem_desc_k128(sa + j * (kFp4K / 2)),
+                                                 smem_desc_k128(sb + j * (kFp4K / 2)),
+                                                 Fp4Mma<FMT>::idesc_step(idesc, j), ta + 4u * t,
+                                                 tb + 4u * t, k > k_first || j > 0 ? 1u : 0u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < C::kStageK / kUmmaK; ++j)
+                            umma_bf16<false>(d_tmem, smem_desc_k128(sa + j * kUmmaK * 2),
+                                             smem_desc_k128(sb + j * kUmmaK * 2), idesc,
+                                             k > k_first || j > 0 ? 1u : 0u);
+                    }
+                    umma_commit<false>(empty0 + 8u * s);
+                    if (k == k_last - 1) umma_commit<false>(accum_full0 + 8u * acc);
+                }
+                __syncwarp();
+                issued = true;
+            }
+        }
+        if (issued) {
+            if (elect_one()) umma_commit_local<false>(drain);
+            __syncwarp();
+            mbar_wait(drain, 0u);
+        }
+    } else if (warp < kEpiWarp0 + kEpiWarps) {
+        // ---- epilogue ---------------------------------------------------------------
+        const int quarter = warp & 3;                  // TMEM lanes this warp may read
+        const int thread = quarter * 32 + lane;        // the tile's row of this lane
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t x_u32 = smem_u32(s_x);
+        const int per = kChunkRows / split;            // rows that a CTA adds up, at most
+        if (DOWN) griddep_wait();                      // the counters, and the workspace
+        int tl = 0;
+        for (int u = first; u < units && !*s_abort; u += step, ++tl) {
+            const int acc = tl & 1, tile = u / chunks;
+            const Chunk c = s_chunk[u - tile * chunks];
+            const uint32_t x0 = x_u32 + (uint32_t)(acc * kChunkRows * 128 * 4);
+            float v[kChunkRows];
+            if (k_last > k_first) {
+                if (!warp_all(wait_or_abort(accum_full0 + 8u * acc, (uint32_t)((tl >> 1) & 1), s_abort))) break;
+                tc_fence_after();
+                const uint32_t t_acc = t_lane + (uint32_t)(acc * kChunkRows * kDigits);
+                if constexpr (C::FP4) {
+#pragma unroll
+                    for (int b = 0; b < kChunkRows / 4; ++b) {   // 4 rows: 16 columns
+                        if (4 * b >= c.rows) break;
+                        uint32_t q[16];
+                        tmem_ld16(t_acc + 16u * b, q);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)     // the least digit first
+                            v[4 * b + i] = __uint_as_float(q[4 * i]) +
+                                           0.125f * (__uint_as_float(q[4 * i + 1]) +
+                                                     0.125f * (__uint_as_float(q[4 * i + 2]) +
+                                                               0.125f * __uint_as_float(q[4 * i + 3])));
+                    }
+                } else {
+                    uint32_t q[16];
+                    tmem_ld16(t_acc, q);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kChunkRows; ++i) v[i] = __uint_as_float(q[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(accum_free0 + 8u * acc);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunkRows; ++i) v[i] = 0.0f;
+            }
+            // To the CTA that adds the row up, once its readers are done with the buffer.
+            if (!warp_all(wait_or_abort<true>(x_free0 + 8u * acc, (uint32_t)(((tl >> 1) & 1) ^ 1), s_abort))) break;
+#pragma unroll
+            for (int i = 0; i < kChunkRows; ++i) {
+                if (i >= c.rows) break;
+                float r = v[i];
+                if (FMT == kFp4Nv) {
+                    const int pair = s_list[c.start + i];
+                    const int e = s_exp[DOWN ? pair : pair / a.K] - 8;   // -135 .. 118
+                    r = r * pow2(e >> 1) * pow2(e - (e >> 1));
+                }
+                const uint32_t to = x0 + (uint32_t)((rank * per + i / split) * 128 + thread) * 4u;
+                st_cluster_f32(map_to_rank(to, i % split), r);
+            }
+            __syncwarp();
+            if (lane < split) mbar_arrive_cluster(map_to_rank(x_full0 + 8u * acc, lane));
+            if (!warp_all(wait_or_abort<true>(x_full0 + 8u * acc, (uint32_t)((tl >> 1) & 1), s_abort))) break;
+            const float gw = a.w_scale ? __ldcg(a.w_scale + c.e) : 1.0f;
+            const float* x = s_x + acc * kChunkRows * 128;
+            for (int j = DOWN ? 0 : quarter >> 1; ; j += DOWN ? 1 : 2) {
+                const int i = j * split + rank;
+                if (i >= c.rows) break;
+                const int pair = s_list[c.start + i];
+                if (DOWN) {
+                    float r = 0.0f;
+                    for (int src = 0; src < split; ++src) r += x[(src * per + j) * 128 + thread];
+                    a.y[(int64_t)pair * a.wrows + tile * 128 + thread] = r * gw;
+                } else {
+                    const int col = thread & 63;
+                    float gate = 0.0f, up = 0.0f;
+                    for (int src = 0; src < split; ++src) {
+                        gate += x[(src * per + j) * 128 + col];
+                        up += x[(src * per + j) * 128 + 64 + col];
+                    }
+                    gate *= gw;
+                    up *= gw;
+                    const uint32_t h2 = pack_bf16x2_rn(up * act_value(gate, a.act), 0.0f);
+                    a.h[(int64_t)pair * (a.wrows / 2) + tile * 64 + col] = (uint16_t)h2;
+                    if (FMT == kFp4Nv) {
+                        // Two words of 32 columns each.
+                        const uint32_t m = __reduce_max_sync(~0u, (h2 << 16) & 0x7FFFFFFFu);
+                        if (lane == 0)
+                            a.h_most[(int64_t)pair * (a.wrows / 64) + tile * 2 + (quarter & 1)] = m;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane < split) mbar_arrive_cluster(map_to_rank(x_free0 + 8u * acc, lane));
+            if (DOWN) {
+                // This warp's 32 columns of the unit are in memory; the last of a tile's units
+                // joins the experts' results there.
+                __threadfence();
+                __syncwarp();
+                uint32_t old = 0u;
+                if (lane == 0)
+                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                                 : "=r"(old) : "l"(a.done + tile * 4 + quarter) : "memory");
+                old = __shfl_sync(~0u, old, 0);
+                if (old + 1u == (uint32_t)(chunks * split)) {
+                    __threadfence();
+                    join_experts(a, tile * 128 + thread);
+                }
+            }
+        }
+    } else if (warp < kScaleWarp0 + kScaleWarps) {
+        // ---- scales of the weights: every kScaleWarps-th stage, by way of registers, the
+        // warp's next stage on its way -----------------------------------------------------
+        if constexpr (C::FP4) {
+            const int64_t tiles = a.din / (4 * Fp4<FMT>::kBlock);
+            const int n_k = k_last - k_first;
+            const int stages = first < units ? ((units - 1 - first) / step + 1) * n_k : 0;
+            uint2 next[2][C::kTiles];
+            auto fetch = [&](int g) {
+                const int i = g / n_k, u = first + i * step, tile = u / chunks;
+                const int64_t w0 = (int64_t)s_chunk[u - tile * chunks].e * a.wrows + tile * (DOWN ? 128 : 64);
+                const int64_t kt = (int64_t)(k_first + g - i * n_k) * C::kTiles;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int64_t row = w0 + b * (DOWN ? 64 : a.wrows / 2);
+                    const uint8_t* src = a.w_scales + fp4_scale_at(row, kt, tiles) + lane * 16;
+#pragma unroll
+                    for (int j = 0; j < C::kTiles; ++j)
+                        next[b][j] = kt + j < tiles ? __ldcg(reinterpret_cast<const uint2*>(src + j * 512))
+                                                    : make_uint2(0u, 0u);
+                }
+            };
+            int g = warp - kScaleWarp0;
+            if (g < stages) fetch(g);
+            for (; g < stages && !*s_abort; g += kScaleWarps) {
+                const int s = g % STAGES;
+                uint2 now[2][C::kTiles];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < C::kTiles; ++j) now[b][j] = next[b][j];
+                if (g + kScaleWarps < stages) fetch(g + kScaleWarps);
+                if (!warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort))) break;
+                const uint32_t dst = ring_s + (uint32_t)s * (2 * C::kScales) + (uint32_t)lane * 16u;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < C::kTiles; ++j) sts64(dst + j * kScaleTile + b * 8, now[b][j]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full0 + 8u * s);
+            }
+        }
+    } else {
+        // ---- token rows --------------------------------------------------------------
+        const int w = warp - kRowWarp0;
+        if (DOWN) griddep_wait();                      // h
+        if constexpr (FMT == kFp4Nv) {
+            // The rows' largest magnitudes over this CTA's part of K.
+            if (DOWN) {
+                const int words = a.din / 32;
+                for (int p = w; p < pairs; p += kRowWarps) {
+                    uint32_t m = 0u;
+                    if (valid_id(__ldcg(a.ids + p), a.E) >= 0)
+                        for (int i = lane; i < words; i += 32) m = max(m, __ldcg(a.h_most + (int64_t)p * words + i));
+                    m = __reduce_max_sync(~0u, m);
+                    if (lane == 0) s_exp[p] = (int16_t)digit_exponent(m);
+                }
+            } else {
+                const int c0 = k_first * C::kStageK, c1 = min(k_last * C::kStageK, a.din);
+                for (int t = w; t < a.T; t += kRowWarps) {
+                    uint32_t m = 0u;
+                    for (int i = c0 + lane * 8; i < c1; i += 256) {
+                        const int4 v = ld_cg_v4(a.rows + (int64_t)t * a.din + i);
+                        const uint32_t q[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            m = max(m, max((q[n] << 16) & 0x7FFFFFFFu, q[n] & 0x7FFF0000u));
+                    }
+                    m = __reduce_max_sync(~0u, m);
+                    if (lane == 0) s_exp[t] = (int16_t)digit_exponent(m);
+                }
+            }
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps) : "memory");
+        }
+        int g = 0;
+        bool ok = true;
+        for (int u = first; u < units && ok && !*s_abort; u += step) {
+            const Chunk c = s_chunk[u % chunks];
+            for (int k = k_first; k < k_last; ++k, ++g) {
+                const int s = g % STAGES;
+                const uint32_t sb = ring_b + (uint32_t)s * C::kBytesB;
+                if constexpr (C::FP4) {
+                    // (stage, row) tasks in turn over the warps.
+                    const uint32_t sscale = ring_s + (uint32_t)s * (2 * C::kScales) + C::kScales;
+                    const int r0 = (w - g * c.rows) & (kRowWarps - 1);
+                    const int col = k * C::kStageK + lane * 8;
+                    int4 raw[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = r0 + i * kRowWarps;
+                        raw[i] = make_int4(0, 0, 0, 0);
+                        if (r < c.rows && col < a.din) {
+                            const int pair = s_list[c.start + r];
+                            raw[i] = ld_cg_v4(a.rows + (int64_t)(DOWN ? pair : pair / a.K) * a.din + col);
+                        }
+                    }
+                    ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = r0 + i * kRowWarps;
+                        if (r >= c.rows) break;
+                        int row_exp = 0;
+                        if (FMT == kFp4Nv) {
+                            const int pair = s_list[c.start + r];
+                            row_exp = s_exp[DOWN ? pair : pair / a.K];
+                        }
+                        store_digits<FMT>(sb, sscale, r * kDigits, lane, raw[i], row_exp);
+                    }
+                } else {
+                    if (w >= C::kRowArrivals) continue;
+                    const int r = w * 4 + (lane >> 3), unit = lane & 7;
+                    int4 raw = make_int4(0, 0, 0, 0);
+                    if (r < c.rows) {
+                        const int pair = s_list[c.start + r];
+                        raw = ld_cg_v4(a.rows + (int64_t)(DOWN ? pair : pair / a.K) * a.din +
+                                       k * C::kStageK + unit * 8);
+                    }
+                    ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
+                    if (!ok) break;
+                    sts128(sb + (uint32_t)(r * 128 + ((unit ^ (r & 7)) << 4)), (uint32_t)raw.x,
+                           (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full0 + 8u * s);
+            }
+        }
+    }
+
+    __syncwarp();
+    if (threadIdx.x == 0 && *s_abort) atomicOr(a.err, kErrTimeout);
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) cluster_sync();   // nothing is on its way to a peer that has left
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<false>(tmem, kLayerTmem);
+    }
+    if (DOWN) griddep_launch_dependents();
+}
+
+// CTAs of a grid of clusters of `split` CTAs, one to an SM, within the SM budget; 0 if none
+// fits. Cached per kernel, split and device.
+template <typename Kernel>
+int layer_grid(Kernel kernel, size_t smem, int split, int num_sms)
+{
+    if (split == 1) return num_sms;
+    struct Entry {
+        const void* kernel;
+        int dev, split, fit;
+    };
+    static std::mutex mu;
+    static Entry entries[32];
+    static int used = 0;
+    int dev = 0, fit = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const void* k = reinterpret_cast<const void*>(kernel);
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used && fit < 0; ++i)
+        if (entries[i].kernel == k && entries[i].dev == dev && entries[i].split == split)
+            fit = entries[i].fit;
+    if (fit < 0) {
+        int sms = 0, n = 0;
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3((unsigned)(sms / split * split));
+        cfg.blockDim = dim3(kLayerThreads);
+        cfg.dynamicSmemBytes = smem;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        fit = n * split;
+        if (used < 32) entries[used++] = {k, dev, split, fit};
+    }
+    return fit < num_sms / split * split ? fit : num_sms / split * split;
+}
+
+// How many CTAs share a unit: what takes the fewest steps in the CTA with the most units, each
+// of which costs its share of the stages and about one more. units: as many as are likely.
+template <class C>
+int layer_split(int64_t units, int stages, int num_sms, int* grid)
+{
+    int best = 0;
+    int64_t least = 0;
+    for (int split = 1; split <= kMaxSplit && split <= stages; split *= 2) {
+        const int ctas = layer_grid(moe_layer_kernel<C>, C::kSmem, split, num_sms);
+        if (ctas < split) continue;
+        const int64_t clusters = ctas / split;
+        const int64_t cost = (units + clusters - 1) / clusters * ((stages + split - 1) / split + 1);
+        if (best == 0 || cost < least) {
+            best = split;
+            least = cost;
+            *grid = ctas;
+        }
+    }
+    return best;
+}
+
+template <class C>
+cudaError_t launch_layer_kernel(const LayerKernelArgs& a, const void* w, int64_t wlines, int num_sms,
+                                const LaunchOpts& o)
+{
+    auto kernel = moe_layer_kernel<C>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = (int64_t)a.T * a.K;
+    const int64_t units = (pairs < a.E ? pairs : a.E) * a.tiles;
+    int grid = 0;
+    const int split = layer_split<C>(units, (a.din + C::kStageK - 1) / C::kStageK, num_sms, &grid);
+    if (split == 0) return cudaErrorNotSupported;
+    CUtensorMap tm;
+    const bool ok = C::FP4 ? make_code_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64)
+                           : make_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64, 64);
+    if (!ok) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (split > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)split;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (o.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kLayerThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = o.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    e = cudaLaunchKernelEx(&cfg, kernel, tm, a);
+    if (e == cudaSuccess && o.launches) ++*o.launches;
+    return e;
+}
+
+template <int FMT>
+cudaError_t launch_layer_format(const MoeLayerArgs& f, int num_sms, const LaunchOpts& o)
+{
+    LayerKernelArgs a = {};
+    a.ids = f.ids;
+    a.scores = f.scores;
+    a.T = f.T;
+    a.K = f.K;
+    a.E = f.E;
+    a.act = f.act;
+    a.h = f.h;
+    a.h_most = f.h_most;
+    a.y = f.y;
+    a.done = f.done;
+    a.counters = (int)(f.D / 32);
+    a.out = f.out;
+    a.out_f32 = f.out_f32;
+    a.err = f.err;
+    a.rows = static_cast<const uint16_t*>(f.x);
+    a.w_scales = f.gate_up_scales;
+    a.w_scale = f.gate_up_scale;
+    a.din = (int)f.D;
+    a.wrows = (int)(2 * f.dff);
+    a.tiles = (int)(f.dff / 64);
+    const cudaError_t e = launch_layer_kernel<LayerCfg<FMT, false>>(a, f.w_gate_up, f.E * 2 * f.dff, num_sms, o);
+    if (e != cudaSuccess) return e;
+    a.rows = f.h;
+    a.w_scales = f.down_scales;
+    a.w_scale = f.down_scale;
+    a.din = (int)f.dff;
+    a.wrows = (int)f.D;
+    a.tiles = (int)(f.D / 128);
+    return launch_layer_kernel<LayerCfg<FMT, true>>(a, f.w_down, f.E * f.D, num_sms, o);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_layer(const MoeLayerArgs& f, int num_sms, const LaunchOpts& o)
+{
+    if (f.format == kFp4Mx) return launch_layer_format<kFp4Mx>(f, num_sms, o);
+    if (f.format == kFp4Nv) return launch_layer_format<kFp4Nv>(f, num_sms, o);
+    return launch_layer_format<kFmtBf16>(f, num_sms, o);
+}
+
+}  // namespace ep

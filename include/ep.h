@@ -534,6 +534,39 @@ EP_API ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const e
                                    int64_t din, int64_t dff, int32_t act, void* h,
                                    const ep_fp4* h_fp4, ep_stream_t stream);
 
+/* ---- A whole layer for a few tokens ------------------------------------------------
+ * What dispatch, the experts' gated block and combine compute together,
+ *     out_TD[t] = sum_k topk_scores_TK[t][k] * Wd_e (act(Wg_e x_t) * (Wu_e x_t)),  e = ids[t][k],
+ * in two kernels and without receive rows, for batches of single tokens, where reading the
+ * weights of the experts in use once is all there is to do: num_tokens <= 64 and
+ * num_tokens * topk <= 512 (EP_ERR_CAPACITY beyond; num_tokens also <= N_max). The buffer
+ * gives hidden size, experts and topk; its layout and workspace are left alone. x_TD bf16, bf16
+ * buffers only; ids as for a dispatch (-1: no expert, a bad id sets EP_DEVERR_BAD_ID); a token
+ * without an expert gets a zero row. D % 128 == 0, dff % 128 == 0. w_gate_up [E][2 dff][D], gate
+ * rows first, w_down [E][D][dff].
+ * h is rounded to bf16; sums are fp32 in an order fixed by the sizes; results are joined in
+ * fp32 in the order of k and rounded once to out_dtype.
+ * ep_moe_layer_fp4: weights in 4 bits, of one format; x and h stay bf16 in all but their last
+ * bits: each is taken apart into four e2m1 digits of a power of two for each block of the
+ * format's size. An element down to a sixteenth of its block's largest is exact, a smaller one
+ * within 2^-11 of the largest; EP_FP4_NV also within 2^-28 of the row's largest. An infinity or
+ * a NaN in a row makes that row's results NaN.
+ * workspace: ep_moe_layer_workspace_bytes, 256-byte aligned, for this call alone until its
+ * work is done. */
+EP_API size_t ep_moe_layer_workspace_bytes(const ep_buffer* buf, int64_t num_tokens, int64_t dff);
+
+EP_API ep_status ep_moe_layer(ep_buffer* buf, const void* x_TD, const float* topk_scores_TK,
+                              const int32_t* topk_expert_ids_TK, int64_t num_tokens,
+                              const void* w_gate_up, const void* w_down, int64_t dff, int32_t act,
+                              void* out_TD, int32_t out_dtype, void* workspace,
+                              size_t workspace_bytes, ep_stream_t stream);
+
+EP_API ep_status ep_moe_layer_fp4(ep_buffer* buf, const void* x_TD, const float* topk_scores_TK,
+                                  const int32_t* topk_expert_ids_TK, int64_t num_tokens,
+                                  const ep_fp4* w_gate_up, const ep_fp4* w_down, int64_t dff,
+                                  int32_t act, void* out_TD, int32_t out_dtype, void* workspace,
+                                  size_t workspace_bytes, ep_stream_t stream);
+
 /* Synchronously read and clear the device error word (EP_DEVERR_* bits).
  * Refused with EP_ERR_CAPTURE_HOST_SYNC while the stream is capturing. Status
  * stays on the device and is read only here ([graph] "Internode" item 1: no
