@@ -1217,7 +1217,7 @@ LayerWorkspace layer_workspace(int64_t pairs, int64_t D, int64_t dff)
 {
     Carve cv;
     LayerWorkspace w;
-    w.h = cv.take((size_t)(pairs * dff * 2));
+    w.h = cv.take((size_t)(pairs * dff * 4));
     w.h_most = cv.take((size_t)(pairs * (dff / 32) * 4));
     w.y = cv.take((size_t)(pairs * D * 4));
     w.done = cv.take((size_t)(D / 32 * 4));
@@ -1266,7 +1266,7 @@ ep_status enqueue_layer(ep_buffer* b, const void* x, const float* scores, const 
     a.D = D;
     a.dff = dff;
     a.act = act;
-    a.h = reinterpret_cast<uint16_t*>(at + w.h);
+    a.h = reinterpret_cast<float*>(at + w.h);
     a.h_most = reinterpret_cast<uint32_t*>(at + w.h_most);
     a.y = reinterpret_cast<float*>(at + w.y);
     a.done = reinterpret_cast<uint32_t*>(at + w.done);

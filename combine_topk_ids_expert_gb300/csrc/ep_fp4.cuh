@@ -93,7 +93,7 @@ struct MoeLayerArgs {
     const float* gate_up_scale;    // [E] or null
     const float* down_scale;
     int act;
-    uint16_t* h;                   // workspace: [T K][dff]
+    float* h;                      // workspace: [T K][dff]
     uint32_t* h_most;              // [T K][dff / 32]
     float* y;                      // [T K][D]
     uint32_t* done;                // [D / 32]

@@ -58,6 +58,10 @@ struct Fp4Cfg {
     static constexpr size_t kSmem = 1024 + (size_t)STAGES * kStageBytes + kTail;
     static_assert(kSmem <= (size_t)kSmemLimit, "ring does not fit in shared memory");
     static_assert(kAcc1 + BN <= kScaleCol0, "accumulators and scales overlap");
+    // A warp that serves every n-th stage waits for a slot's last release by parity: it must not
+    // get there while the release before that one is out, which its own last stage rules out as
+    // long as that is at most a ring's length ago.
+    static_assert(kScaleWarps <= STAGES, "a warp's stages within the ring");
 };
 
 struct Fp4GemmArgs {

@@ -10,13 +10,15 @@
 // weights on their way: 4-bit codes go to the block-scaled instructions as they lie, which
 // leaves the CUDA cores with the activations alone.
 //
-// For 4-bit weights an activation keeps its precision: a row enters as four rows of e2m1
-// digits that share a power of two s for each block of the weights' block size,
+// An activation keeps its precision. With bf16 weights x enters as it is, and h, fp32, as the
+// sum of two bf16 rows (what the first leaves is within 2^-8 of it, what both leave within 2^-16).
+// With 4-bit weights a row enters as rows of e2m1 digits,
+// four for x and five for h, that share a power of two s for each block of the weights' size,
 //     x = s (d0 + d1 / 8 + d2 / 64 + d3 / 512) + rest,   |d| <= 4, |rest| <= s / 1024,
 // s = 2^(floor(log2 amax) - 1): each digit is what is left rounded to e2m1 (half steps below
 // 2, whole ones up to 4), which leaves at most 1/2, an eighth of the next digit's range. A bf16
 // element down to a sixteenth of its block's largest is exact, smaller ones are within 2^-11
-// of the largest. The digits are four columns of one product and joined in the epilogue.
+// of the largest; h is within 2^-14. The digits are columns of one product, joined in the epilogue.
 // nv scales (ue4m3) reach over 18 binades only: they count from the row's largest block, and
 // blocks 2^17 below it are within 2^-28 of the row's largest.
 //
@@ -27,8 +29,8 @@
 // every pair's result goes to a workspace in fp32, and the CTA that completes a tile's last unit
 // adds the experts' results in the order of k. All sums have a fixed order.
 //
-// h is rounded to bf16 (as in the block on receive rows); sums, scores and results are fp32 and
-// rounded once.
+// Sums, h, scores and the pairs' results are fp32; the layer's result is rounded once.
+#include <cstdlib>
 #include "ep_fp4.cuh"
 #include "fp4_umma.cuh"
 
@@ -36,8 +38,9 @@ namespace ep {
 namespace {
 
 constexpr int kChunkRows = 16;                  // token rows of a unit
-constexpr int kDigits = 4;
-constexpr int kRowWarps = 8, kEpiWarps = 4, kScaleWarps = 4;
+constexpr int kDigitsX = 4, kDigitsH = 5;
+constexpr int kAccCols = kChunkRows * kDigitsH; // columns set aside for an accumulator
+constexpr int kRowWarps = 6, kEpiWarps = 4, kScaleWarps = 4;
 constexpr int kEpiWarp0 = 2, kScaleWarp0 = 6, kRowWarp0 = 10;
 constexpr int kLayerThreads = 32 * (kRowWarp0 + kRowWarps);
 constexpr uint32_t kLayerTmem = 256;
@@ -49,34 +52,37 @@ struct LayerCfg {
     static constexpr int FMT = FMT_;
     static constexpr bool DOWN = DOWN_, FP4 = FMT_ != kFmtBf16;
     static constexpr int kStageK = FP4 ? kFp4StageK : 64;       // 128 bytes of a row
-    static constexpr int kCols = FP4 ? kChunkRows * kDigits : kChunkRows;
+    // Rows of the N side that a token row becomes: digits, or h's two bf16 terms.
+    static constexpr int kTerms = FP4 ? (DOWN ? kDigitsH : kDigitsX) : DOWN ? 2 : 1;
+    static constexpr int kCols = kChunkRows * kTerms;
     static constexpr int kTiles = FP4 ? Fp4Mma<FP4 ? FMT_ : kFp4Mx>::kTiles : 0;
     static constexpr uint32_t kBytesA = kBM * 128, kBytesB = kCols * 128;
     static constexpr uint32_t kScales = kTiles * kScaleTile;    // of A and of B, each
     static constexpr uint32_t kStageBytes = kBytesA + kBytesB + 2 * kScales;
     static constexpr uint32_t kExchange = 2 * kChunkRows * 128 * 4;
-    static constexpr uint32_t kTables = 4 * kMaxExperts + 8 * kLayerMaxPairs + 2 * 2 * kLayerMaxPairs;
+    static constexpr uint32_t kTables = 4 * kMaxExperts + (8 + 2 + 2 + 4 + 1) * kLayerMaxPairs;
     static constexpr uint32_t kFixed = 1024 + kExchange + kTables + 512;
     static constexpr int kFit = (int)((kSmemLimit - kFixed) / kStageBytes);
     static constexpr int STAGES = kFit > 12 ? 12 : kFit;
     static constexpr size_t kSmem = kFixed + (size_t)STAGES * kStageBytes;
-    static constexpr uint32_t kScaleCol0 = 2 * kChunkRows * kDigits;   // after two accumulators
-    // Arrivals that fill a stage: the copy of A, the scales, the warps that bring rows.
-    static constexpr int kRowArrivals = FP4 ? kRowWarps : kRowWarps / 2;
-    static constexpr uint32_t kFullCount = 1u + (FP4 ? 1u : 0u) + kRowArrivals;
-    static_assert(STAGES >= 4, "ring too shallow");
-    static_assert(kLayerMaxPairs <= kLayerThreads, "a thread to a pair");
-    static_assert(kScaleCol0 + 2 * 2 * 16 <= kLayerTmem, "accumulators and scales");
+    static constexpr uint32_t kScaleCol0 = 2 * kAccCols;               // after two accumulators
+    // Arrivals that fill a stage: the copy of A, the warp that brings its scales, that of the rows.
+    static constexpr uint32_t kFullCount = FP4 ? 3u : 2u;
+    // A warp that serves every n-th stage waits for a slot's last release by parity: it must not
+    // get there while the release before that one is out, which its own last stage rules out as
+    // long as that is at most a ring's length ago.
+    static_assert(kRowWarps <= STAGES && kScaleWarps <= STAGES, "a warp's stages within the ring");
+    static_assert(kScaleCol0 + 2 * 2 * 16 <= kLayerTmem && kCols <= kAccCols && kCols <= 128, "accumulators and scales");
 };
 
 struct LayerKernelArgs {
     const int32_t* ids;
     const float* scores;
-    const uint16_t* rows;          // x [T][K dim], or h [pairs][K dim]
+    const void* rows;              // x [T][din] bf16, or h [pairs][din] fp32
     const uint8_t* w_scales;
     const float* w_scale;          // [E] or null
-    uint16_t* h;                   // first kernel: [pairs][dff]
-    uint32_t* h_most;              // [pairs][dff / 64]: the largest |h| (bits) of each tile (nv)
+    float* h;                      // first kernel: [pairs][dff]
+    uint32_t* h_most;              // [pairs][dff / 32]: the largest |h| (bits) of 32 columns (nv)
     float* y;                      // second kernel: [pairs][D]
     uint32_t* done;                // [D / 32] CTAs that have added their part of a unit to these columns
     int counters;                  // D / 32
@@ -127,18 +133,42 @@ __device__ __forceinline__ void store_out(const LayerKernelArgs& a, int64_t at, 
     else static_cast<uint16_t*>(a.out)[at] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
 }
 
-// out[t][col] of every token: the pairs' results in the order of k, as in combine.
-__device__ __forceinline__ void join_experts(const LayerKernelArgs& a, int col)
+__device__ __forceinline__ float ld_cg_f32(const float* p)
 {
-    for (int t = 0; t < a.T; ++t) {
-        float r = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < a.K; ++k) {
-            const int i = t * a.K + k;
-            if (valid_id(__ldcg(a.ids + i), a.E) >= 0)
-                r = fmaf(__ldcg(a.scores + i), __ldcg(a.y + (int64_t)i * a.wrows + col), r);
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+// out[t][col] of every token: the pairs' results in the order of k, as in combine. A lane has
+// a column; the results of 32 pairs are on their way at a time (loaded whether or not a pair has
+// an expert: a branch at each would have each waited for, 1000 cycles a pair), their scores in
+// the lanes and the tokens' last pairs in a mask. What this takes, the CTA's next unit waits for.
+__device__ __forceinline__ void join_experts(const LayerKernelArgs& a, int lane, int col0,
+                                             const float* s_score, const uint8_t* s_ok)
+{
+    const int pairs = a.T * a.K;
+    const float* y = a.y + col0 + lane;
+    float r = 0.0f;
+    int64_t at = col0 + lane;
+    for (int i0 = 0; i0 < pairs; i0 += 32) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = ld_cg_f32(y + (int64_t)min(i0 + j, pairs - 1) * a.wrows);
+        const int i = i0 + lane;
+        const float score = i < pairs ? s_score[i] : 0.0f;
+        const unsigned ok = __ballot_sync(~0u, i < pairs && s_ok[i]);
+        const unsigned ends = __ballot_sync(~0u, i < pairs && (i + 1) % a.K == 0);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float s = __shfl_sync(~0u, score, j);
+            if (ok >> j & 1u) r = fmaf(s, v[j], r);
+            if (ends >> j & 1u) {
+                store_out(a, at, r);
+                r = 0.0f;
+                at += a.wrows;
+            }
         }
-        store_out(a, (int64_t)t * a.wrows + col, r);
     }
 }
 
@@ -154,22 +184,51 @@ __device__ __forceinline__ uint32_t ue4m3_pow2(int k)
     return k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
 }
 
-// 256 elements of a row, 8 in each lane, into the digit rows n0 .. n0 + 3 of a stage's B tile
-// and the words of their scales.
-template <int FMT>
-__device__ __forceinline__ void store_digits(uint32_t sb, uint32_t sscale, int n0, int lane,
-                                             const int4& raw, int row_exp)
+// 8 elements of a row: 16 bytes of bf16, or 32 of fp32 (h).
+template <bool F32>
+struct Eight {
+    int4 q[F32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void* rows, int64_t at, bool in)
+    {
+        const uint8_t* p = static_cast<const uint8_t*>(rows) + at * (F32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) q[i] = in ? ld_cg_v4(p + 16 * i) : make_int4(0, 0, 0, 0);
+    }
+
+    __device__ __forceinline__ void floats(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+            const uint32_t w[4] = {(uint32_t)q[i].x, (uint32_t)q[i].y, (uint32_t)q[i].z, (uint32_t)q[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (F32) {
+                    v[4 * i + j] = __uint_as_float(w[j]);
+                } else {
+                    v[2 * j] = __uint_as_float(w[j] << 16);
+                    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+};
+
+// 256 elements of a row, 8 in each lane, into the digit rows from n0 on of a stage's B tile and
+// the words of their scales. One copy of the code, called (the operands of h's fp32 in q1 too).
+template <int FMT, bool H>
+__device__ __noinline__ void store_digits(uint32_t sb, uint32_t sscale, int n0, int lane, int row_exp,
+                                          int x0, int y0, int z0, int w0, int x1, int y1, int z1, int w1)
 {
-    const uint32_t q[4] = {(uint32_t)raw.x, (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w};
+    constexpr int DIGITS = H ? kDigitsH : kDigitsX;
+    Eight<H> raw;
+    raw.q[0] = make_int4(x0, y0, z0, w0);
+    if (H) raw.q[H ? 1 : 0] = make_int4(x1, y1, z1, w1);
     float v[8];
+    raw.floats(v);
     uint32_t most = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(q[i] << 16);
-        v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-        most = max(most, max(__float_as_uint(v[2 * i]) & 0x7FFFFFFFu,
-                             __float_as_uint(v[2 * i + 1]) & 0x7FFFFFFFu));
-    }
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     most = max(most, __shfl_xor_sync(~0u, most, 1));
     if (FMT == kFp4Mx) most = max(most, __shfl_xor_sync(~0u, most, 2));
     int e = digit_exponent(most);               // -127 .. 126
@@ -189,13 +248,13 @@ __device__ __forceinline__ void store_digits(uint32_t sb, uint32_t sscale, int n
     for (int i = 0; i < 8; ++i) v[i] = bad ? 0.0f : v[i] * f0 * f1;
     const int unit = lane >> 2;
 #pragma unroll
-    for (int d = 0; d < kDigits; ++d) {
+    for (int d = 0; d < DIGITS; ++d) {
         uint32_t w = 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = cvt_e2m1x2(v[2 * i], v[2 * i + 1]);
             w |= c << (8 * i);
-            if (d + 1 < kDigits) {
+            if (d + 1 < DIGITS) {
                 const uint32_t h2 = e2m1x2_to_f16x2(c);
                 v[2 * i] = (v[2 * i] - f16_lo(h2)) * 8.0f;
                 v[2 * i + 1] = (v[2 * i + 1] - f16_hi(h2)) * 8.0f;
@@ -207,12 +266,18 @@ __device__ __forceinline__ void store_digits(uint32_t sb, uint32_t sscale, int n
     const int block = FMT == kFp4Mx ? lane >> 2 : lane >> 1;
     if ((lane & (FMT == kFp4Mx ? 3 : 1)) == 0) {
 #pragma unroll
-        for (int d = 0; d < kDigits; ++d) {
+        for (int d = 0; d < DIGITS; ++d) {
             const int n = n0 + d;
             sts_u8(sscale + (uint32_t)((block >> 2) * kScaleTile + (n & 31) * 16 + (n >> 5) * 4 + (block & 3)),
                    code);
         }
     }
+}
+
+// What a bf16 (given as fp32 bits) leaves of v; nothing if it is infinite.
+__device__ __forceinline__ float left_of(float v, uint32_t bf16)
+{
+    return (bf16 & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(bf16);
 }
 
 template <class C>
@@ -232,7 +297,9 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
     Chunk* s_chunk = reinterpret_cast<Chunk*>(s_cnt + kMaxExperts);            // [pairs]
     uint16_t* s_list = reinterpret_cast<uint16_t*>(s_chunk + kLayerMaxPairs);  // pairs by expert
     int16_t* s_exp = reinterpret_cast<int16_t*>(s_list + kLayerMaxPairs);      // nv: exponents of the rows
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_exp + kLayerMaxPairs);
+    float* s_score = reinterpret_cast<float*>(s_exp + kLayerMaxPairs);         // the pairs' scores,
+    uint8_t* s_ok = reinterpret_cast<uint8_t*>(s_score + kLayerMaxPairs);      // and whether they have an expert
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_ok + kLayerMaxPairs);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * STAGES;
     const uint32_t accum_full0 = empty0 + 8u * STAGES, accum_free0 = accum_full0 + 16u;
     const uint32_t x_full0 = accum_free0 + 16u, x_free0 = x_full0 + 16u;
@@ -243,10 +310,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = cluster_size(), rank = cluster_rank();
-    const int first = cluster_index(), step = cluster_count();
     const int pairs = a.T * a.K;
 
-    for (int e = threadIdx.x; e < a.E; e += kLayerThreads) s_cnt[e] = 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8u * s, C::kFullCount);
@@ -273,52 +338,98 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         griddep_wait();
         griddep_launch_dependents();
     }
-    __syncthreads();
 
-    // ---- routing: the pairs by expert, in chunks ------------------------------------
-    // A thread to a pair. The rank of a pair among its expert's follows the order of the pairs,
-    // so that every CTA has the same rows in the same chunks: warp after warp.
-    int mine = -1, my_rank = 0;
-    if ((int)threadIdx.x < pairs) {
-        const int raw = __ldcg(a.ids + threadIdx.x);
-        mine = valid_id(raw, a.E);
-        if (!DOWN && mine != raw && blockIdx.x == 0) atomicOr(a.err, kErrBadId);
-    }
-    for (int w = 0; 32 * w < pairs; ++w) {
-        if (warp == w) {
-            const unsigned same = __match_any_sync(~0u, mine);
-            if (mine >= 0) my_rank = s_cnt[mine] + __popc(same & lanemask_lt(lane));
-            __syncwarp();
-            if (mine >= 0 && lane == __ffs(same) - 1) s_cnt[mine] += __popc(same);
+    if (warp >= kRowWarp0) {
+        // The code that takes a row apart, and x, from memory, while the other warps work the
+        // routing out: what follows them there waits for a row first, and a call's weights have
+        // swept both out of L2. (These bytes of the ring's first slots are written again.)
+        const int w = warp - kRowWarp0;
+        if constexpr (C::FP4) {
+            store_digits<FMT, DOWN>(ring_b + (uint32_t)w * C::kBytesB,
+                                    ring_s + (uint32_t)w * (2 * C::kScales) + C::kScales, 0, lane, 0, 0,
+                                    0, 0, 0, 0, 0, 0, 0);
         }
-        __syncthreads();
-    }
-    if (warp == 0) {
-        int rows0 = 0, chunks0 = 0;
-        for (int base = 0; base < a.E; base += 32) {
-            const int e = base + lane;
-            const int c = e < a.E ? s_cnt[e] : 0;
-            const int packed = c | ((c + kChunkRows - 1) / kChunkRows) << 16;
-            int v = packed;
+        if (!DOWN) {
+            const int64_t bytes = (int64_t)a.T * a.din * 2;
+            for (int64_t i = ((int64_t)blockIdx.x * kRowWarps * 32 + w * 32 + lane) * 128; i < bytes;
+                 i += (int64_t)gridDim.x * kRowWarps * 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(a.rows) + i));
+        }
+    } else {
+        // ---- routing: the pairs by expert, in chunks --------------------------------
+        constexpr int kWarps = kRowWarp0;
+        auto barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); };
+        // Pairs [32 i, 32 i + 32) are warp i's, from kWarps on once more the first ones'. The rank
+        // of a pair among its expert's follows the order of the pairs, so that every CTA has the
+        // same rows in the same chunks: warp after warp.
+        constexpr int kRounds = (kLayerMaxPairs + 32 * kWarps - 1) / (32 * kWarps);
+        int mine[kRounds], my_rank[kRounds];
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int n = __shfl_up_sync(~0u, v, d);
-                if (lane >= d) v += n;
+        for (int n = 0; n < kRounds; ++n) {
+            const int i = n * 32 * kWarps + (int)threadIdx.x;
+            mine[n] = -1;
+            if (i < pairs) {
+                const int raw = __ldcg(a.ids + i);
+                mine[n] = valid_id(raw, a.E);
+                if (!DOWN && mine[n] != raw && blockIdx.x == 0) atomicOr(a.err, kErrBadId);
+                s_ok[i] = mine[n] >= 0;
+                if (DOWN) s_score[i] = __ldcg(a.scores + i);
             }
-            const int row = rows0 + ((v - packed) & 0xFFFF);
-            int chunk = chunks0 + ((v - packed) >> 16);
-            if (e < a.E) s_cnt[e] = row;
-            for (int at = 0; at < c; at += kChunkRows, ++chunk)
-                s_chunk[chunk] = {(uint16_t)e, (uint16_t)(row + at), (uint16_t)min(c - at, kChunkRows), 0};
-            const int all = __shfl_sync(~0u, v, 31);
-            rows0 += all & 0xFFFF;
-            chunks0 += all >> 16;
         }
-        if (lane == 0) *s_chunks = chunks0;
+        for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) s_cnt[e] = 0;
+        barrier();
+#pragma unroll
+        for (int n = 0; n < kRounds; ++n) {
+            for (int w = 0; w < kWarps && 32 * (n * kWarps + w) < pairs; ++w) {
+                if (warp == w) {
+                    const unsigned same = __match_any_sync(~0u, mine[n]);
+                    if (mine[n] >= 0) my_rank[n] = s_cnt[mine[n]] + __popc(same & lanemask_lt(lane));
+                    __syncwarp();
+                    if (mine[n] >= 0 && lane == __ffs(same) - 1) s_cnt[mine[n]] += __popc(same);
+                }
+                barrier();
+            }
+        }
+        if (warp == 0) {
+            int rows0 = 0, chunks0 = 0;
+            for (int base = 0; base < a.E; base += 32) {
+                const int e = base + lane;
+                const int c = e < a.E ? s_cnt[e] : 0;
+                const int packed = c | ((c + kChunkRows - 1) / kChunkRows) << 16;
+                int v = packed;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int n = __shfl_up_sync(~0u, v, d);
+                    if (lane >= d) v += n;
+                }
+                const int row = rows0 + ((v - packed) & 0xFFFF);
+                int chunk = chunks0 + ((v - packed) >> 16);
+                if (e < a.E) s_cnt[e] = row;
+                for (int at = 0; at < c; at += kChunkRows, ++chunk)
+                    s_chunk[chunk] = {(uint16_t)e, (uint16_t)(row + at), (uint16_t)min(c - at, kChunkRows), 0};
+                const int all = __shfl_sync(~0u, v, 31);
+                rows0 += all & 0xFFFF;
+                chunks0 += all >> 16;
+            }
+            if (lane == 0) *s_chunks = chunks0;
+        }
+        barrier();
+#pragma unroll
+        for (int n = 0; n < kRounds; ++n)
+            if (mine[n] >= 0)
+                s_list[s_cnt[mine[n]] + my_rank[n]] = (uint16_t)(n * 32 * kWarps + (int)threadIdx.x);
     }
+    tc_fence_before();
     __syncthreads();
-    if (mine >= 0) s_list[s_cnt[mine] + my_rank] = (uint16_t)threadIdx.x;
+    if (split > 1) cluster_sync();   // the peers' barriers exist before anything reaches them
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+
+    // This cluster's units, one after the other in the list of the tiles' chunks: a tile's chunks
+    // are then a few clusters' work, and joining its experts' results no cluster's habit.
     const int chunks = *s_chunks, units = chunks * a.tiles;
+    const int u_first = (int)((int64_t)units * cluster_index() / cluster_count());
+    const int u_last = (int)((int64_t)units * (cluster_index() + 1) / cluster_count());
     const int all_stages = (a.din + C::kStageK - 1) / C::kStageK;
     const int k_first = rank * all_stages / split, k_last = (rank + 1) * all_stages / split;
 
@@ -330,17 +441,14 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         griddep_wait();
         for (int64_t i = thread0; i < (int64_t)a.T * a.wrows; i += threads) store_out(a, i, 0.0f);
     }
-    tc_fence_before();
-    __syncthreads();
-    if (split > 1) cluster_sync();   // the peers' barriers exist before anything reaches them
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
-
     if (warp == 0) {
         // ---- weights ------------------------------------------------------------
+        // The first rows are asked for first: behind a ring's worth of weights on every SM they
+        // would come after it. (In the second kernel the weights are there long before the rows.)
+        if (!DOWN) asm volatile("bar.sync 3, %0;" ::"n"(32 * (1 + kRowWarps)) : "memory");
         int g = 0;
         bool ok = true;
-        for (int u = first; u < units && ok && !*s_abort; u += step) {
+        for (int u = u_first; u < u_last && ok && !*s_abort; ++u) {
             const int tile = u / chunks;
             const int w0 = s_chunk[u - tile * chunks].e * a.wrows + tile * (DOWN ? 128 : 64);
             const int w1 = w0 + (DOWN ? 64 : a.wrows / 2);
@@ -366,14 +474,14 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         // ---- products -------------------------------------------------------------
         int g = 0, tl = 0;
         bool issued = false, ok = true;
-        for (int u = first; u < units && ok && !*s_abort && k_last > k_first; u += step, ++tl) {
+        for (int u = u_first; u < u_last && ok && !*s_abort && k_last > k_first; ++u, ++tl) {
             const int acc = tl & 1;
             ok = warp_all(wait_or_abort(accum_free0 + 8u * acc, (uint32_t)(((tl >> 1) & 1) ^ 1), s_abort));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d_tmem = tmem + (uint32_t)(acc * kChunkRows * kDigits);
+            const uint32_t d_tmem = tmem + (uint32_t)(acc * kAccCols);
             const int rows = s_chunk[u % chunks].rows;
-            const int n = C::FP4 ? (rows * kDigits + 15) / 16 * 16 : kChunkRows;
+            const int n = (rows * C::kTerms + 15) / 16 * 16;
             const uint32_t idesc = C::FP4 ? Fp4Mma<C::FP4 ? FMT : kFp4Mx>::idesc(kBM, n)
                                           : (1u << 4) | (1u << 7) | (1u << 10) |
                                                 ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
@@ -430,7 +538,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         const int per = kChunkRows / split;            // rows that a CTA adds up, at most
         if (DOWN) griddep_wait();                      // the counters, and the workspace
         int tl = 0;
-        for (int u = first; u < units && !*s_abort; u += step, ++tl) {
+        for (int u = u_first; u < u_last && !*s_abort; ++u, ++tl) {
             const int acc = tl & 1, tile = u / chunks;
             const Chunk c = s_chunk[u - tile * chunks];
             const uint32_t x0 = x_u32 + (uint32_t)(acc * kChunkRows * 128 * 4);
@@ -438,27 +546,23 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             if (k_last > k_first) {
                 if (!warp_all(wait_or_abort(accum_full0 + 8u * acc, (uint32_t)((tl >> 1) & 1), s_abort))) break;
                 tc_fence_after();
-                const uint32_t t_acc = t_lane + (uint32_t)(acc * kChunkRows * kDigits);
-                if constexpr (C::FP4) {
+                const uint32_t t_acc = t_lane + (uint32_t)(acc * kAccCols);
+                constexpr int kRowsLoad = 16 / C::kTerms;       // rows within 16 columns
 #pragma unroll
-                    for (int b = 0; b < kChunkRows / 4; ++b) {   // 4 rows: 16 columns
-                        if (4 * b >= c.rows) break;
-                        uint32_t q[16];
-                        tmem_ld16(t_acc + 16u * b, q);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)     // the least digit first
-                            v[4 * b + i] = __uint_as_float(q[4 * i]) +
-                                           0.125f * (__uint_as_float(q[4 * i + 1]) +
-                                                     0.125f * (__uint_as_float(q[4 * i + 2]) +
-                                                               0.125f * __uint_as_float(q[4 * i + 3])));
-                    }
-                } else {
+                for (int b = 0; b * kRowsLoad < kChunkRows; ++b) {
+                    if (b * kRowsLoad >= c.rows) break;
                     uint32_t q[16];
-                    tmem_ld16(t_acc, q);
+                    tmem_ld16(t_acc + (uint32_t)(b * kRowsLoad * C::kTerms), q);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < kChunkRows; ++i) v[i] = __uint_as_float(q[i]);
+                    for (int i = 0; i < kRowsLoad && b * kRowsLoad + i < kChunkRows; ++i) {
+                        // The least term first.
+                        float r = __uint_as_float(q[C::kTerms * i + C::kTerms - 1]);
+#pragma unroll
+                        for (int n = C::kTerms - 2; n >= 0; --n)
+                            r = __uint_as_float(q[C::kTerms * i + n]) + (C::FP4 ? 0.125f * r : r);
+                        v[b * kRowsLoad + i] = r;
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -503,11 +607,10 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                     }
                     gate *= gw;
                     up *= gw;
-                    const uint32_t h2 = pack_bf16x2_rn(up * act_value(gate, a.act), 0.0f);
-                    a.h[(int64_t)pair * (a.wrows / 2) + tile * 64 + col] = (uint16_t)h2;
+                    const float h = up * act_value(gate, a.act);
+                    a.h[(int64_t)pair * (a.wrows / 2) + tile * 64 + col] = h;
                     if (FMT == kFp4Nv) {
-                        // Two words of 32 columns each.
-                        const uint32_t m = __reduce_max_sync(~0u, (h2 << 16) & 0x7FFFFFFFu);
+                        const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(h) & 0x7FFFFFFFu);
                         if (lane == 0)
                             a.h_most[(int64_t)pair * (a.wrows / 64) + tile * 2 + (quarter & 1)] = m;
                     }
@@ -527,7 +630,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                 old = __shfl_sync(~0u, old, 0);
                 if (old + 1u == (uint32_t)(chunks * split)) {
                     __threadfence();
-                    join_experts(a, tile * 128 + thread);
+                    join_experts(a, lane, tile * 128 + quarter * 32, s_score, s_ok);
                 }
             }
         }
@@ -537,10 +640,10 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         if constexpr (C::FP4) {
             const int64_t tiles = a.din / (4 * Fp4<FMT>::kBlock);
             const int n_k = k_last - k_first;
-            const int stages = first < units ? ((units - 1 - first) / step + 1) * n_k : 0;
+            const int stages = (u_last - u_first) * n_k;
             uint2 next[2][C::kTiles];
             auto fetch = [&](int g) {
-                const int i = g / n_k, u = first + i * step, tile = u / chunks;
+                const int i = g / n_k, u = u_first + i, tile = u / chunks;
                 const int64_t w0 = (int64_t)s_chunk[u - tile * chunks].e * a.wrows + tile * (DOWN ? 128 : 64);
                 const int64_t kt = (int64_t)(k_first + g - i * n_k) * C::kTiles;
 #pragma unroll
@@ -593,8 +696,9 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                 const int c0 = k_first * C::kStageK, c1 = min(k_last * C::kStageK, a.din);
                 for (int t = w; t < a.T; t += kRowWarps) {
                     uint32_t m = 0u;
+#pragma unroll 8
                     for (int i = c0 + lane * 8; i < c1; i += 256) {
-                        const int4 v = ld_cg_v4(a.rows + (int64_t)t * a.din + i);
+                        const int4 v = ld_cg_v4(static_cast<const uint16_t*>(a.rows) + (int64_t)t * a.din + i);
                         const uint32_t q[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
 #pragma unroll
                         for (int n = 0; n < 4; ++n)
@@ -606,59 +710,90 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             }
             asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps) : "memory");
         }
-        int g = 0;
-        bool ok = true;
-        for (int u = first; u < units && ok && !*s_abort; u += step) {
-            const Chunk c = s_chunk[u % chunks];
-            for (int k = k_first; k < k_last; ++k, ++g) {
-                const int s = g % STAGES;
-                const uint32_t sb = ring_b + (uint32_t)s * C::kBytesB;
-                if constexpr (C::FP4) {
-                    // (stage, row) tasks in turn over the warps.
-                    const uint32_t sscale = ring_s + (uint32_t)s * (2 * C::kScales) + C::kScales;
-                    const int r0 = (w - g * c.rows) & (kRowWarps - 1);
-                    const int col = k * C::kStageK + lane * 8;
-                    int4 raw[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = r0 + i * kRowWarps;
-                        raw[i] = make_int4(0, 0, 0, 0);
-                        if (r < c.rows && col < a.din) {
-                            const int pair = s_list[c.start + r];
-                            raw[i] = ld_cg_v4(a.rows + (int64_t)(DOWN ? pair : pair / a.K) * a.din + col);
-                        }
-                    }
-                    ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
-                    if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = r0 + i * kRowWarps;
-                        if (r >= c.rows) break;
-                        int row_exp = 0;
-                        if (FMT == kFp4Nv) {
-                            const int pair = s_list[c.start + r];
-                            row_exp = s_exp[DOWN ? pair : pair / a.K];
-                        }
-                        store_digits<FMT>(sb, sscale, r * kDigits, lane, raw[i], row_exp);
-                    }
-                } else {
-                    if (w >= C::kRowArrivals) continue;
-                    const int r = w * 4 + (lane >> 3), unit = lane & 7;
-                    int4 raw = make_int4(0, 0, 0, 0);
-                    if (r < c.rows) {
-                        const int pair = s_list[c.start + r];
-                        raw = ld_cg_v4(a.rows + (int64_t)(DOWN ? pair : pair / a.K) * a.din +
-                                       k * C::kStageK + unit * 8);
-                    }
-                    ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
-                    if (!ok) break;
-                    sts128(sb + (uint32_t)(r * 128 + ((unit ^ (r & 7)) << 4)), (uint32_t)raw.x,
-                           (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full0 + 8u * s);
+        // Every kRowWarps-th stage is this warp's, a row (bf16: four rows) at a time; the next
+        // ones, also of its next stage, are on their way meanwhile. One copy of the code: it is
+        // long, and comes from memory in every call.
+        constexpr int kPerLoad = C::FP4 ? 1 : 4;       // rows that the warp covers at once
+        constexpr int kAhead = 3;
+        const int lane_row = C::FP4 ? 0 : lane >> 3, lane_col = (C::FP4 ? lane : lane & 7) * 8;
+        const int n_k = k_last - k_first;
+        const int stages = (u_last - u_first) * n_k;
+        // The place that is fetched for: stage pg of this CTA, row pr.
+        int pg = w, pr = 0, p_rows = 0, p_start = 0, p_col = 0;
+        auto enter = [&] {
+            if (pg >= stages) return;
+            const int i = pg / n_k;
+            const Chunk c = s_chunk[(u_first + i) % chunks];
+            p_rows = c.rows;
+            p_start = c.start;
+            p_col = (k_first + pg - i * n_k) * C::kStageK + lane_col;
+        };
+        auto fetch = [&](Eight<DOWN>& into) {
+            if (pg >= stages) return;
+            const int r = pr + lane_row;
+            const bool in = r < p_rows && p_col < a.din;
+            const int pair = s_list[p_start + (in ? r : 0)];
+            into.load(a.rows, (int64_t)(DOWN ? pair : pair / a.K) * a.din + p_col, in);
+            pr += kPerLoad;
+            if (pr >= p_rows) {
+                pr = 0;
+                pg += kRowWarps;
+                enter();
             }
+        };
+        Eight<DOWN> next[kAhead];
+        enter();
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(next[i]);
+        if (!DOWN) asm volatile("bar.arrive 3, %0;" ::"n"(32 * (1 + kRowWarps)) : "memory");
+        for (int g = w; g < stages && !*s_abort; g += kRowWarps) {
+            const int s = g % STAGES;
+            const Chunk c = s_chunk[(u_first + g / n_k) % chunks];
+            const uint32_t sb = ring_b + (uint32_t)s * C::kBytesB;
+            if (!warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort))) break;
+#pragma unroll 1
+            for (int r0 = 0; r0 < c.rows; r0 += kPerLoad) {
+                const Eight<DOWN> now = next[0];
+#pragma unroll
+                for (int i = 0; i + 1 < kAhead; ++i) next[i] = next[i + 1];
+                fetch(next[kAhead - 1]);
+                const int r = r0 + lane_row;
+                if constexpr (C::FP4) {
+                    int row_exp = 0;
+                    if (FMT == kFp4Nv) {
+                        const int pair = s_list[c.start + r];
+                        row_exp = s_exp[DOWN ? pair : pair / a.K];
+                    }
+                    const int4 q0 = now.q[0], q1 = now.q[DOWN ? 1 : 0];
+                    store_digits<FMT, DOWN>(sb, ring_s + (uint32_t)s * (2 * C::kScales) + C::kScales,
+                                            r * C::kTerms, lane, row_exp, q0.x, q0.y, q0.z, q0.w, q1.x,
+                                            q1.y, q1.z, q1.w);
+                } else if (r < c.rows) {
+                    const uint32_t unit = (uint32_t)(lane & 7);
+                    auto put = [&](int n, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+                        sts128(sb + (uint32_t)(n * 128) + ((unit ^ (uint32_t)(n & 7)) << 4), w0, w1, w2, w3);
+                    };
+                    if constexpr (DOWN) {
+                        float v[8];
+                        now.floats(v);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            hi[i] = pack_bf16x2_rn(v[2 * i], v[2 * i + 1]);
+                            lo[i] = pack_bf16x2_rn(left_of(v[2 * i], hi[i] << 16),
+                                                   left_of(v[2 * i + 1], hi[i] & 0xFFFF0000u));
+                        }
+                        put(2 * r, hi[0], hi[1], hi[2], hi[3]);
+                        put(2 * r + 1, lo[0], lo[1], lo[2], lo[3]);
+                    } else {
+                        const int4 q = now.q[0];
+                        put(r, (uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w);
+                    }
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full0 + 8u * s);
         }
     }
 
@@ -748,8 +883,10 @@ cudaError_t launch_layer_kernel(const LayerKernelArgs& a, const void* w, int64_t
     const int64_t pairs = (int64_t)a.T * a.K;
     const int64_t units = (pairs < a.E ? pairs : a.E) * a.tiles;
     int grid = 0;
-    const int split = layer_split<C>(units, (a.din + C::kStageK - 1) / C::kStageK, num_sms, &grid);
+    int split = layer_split<C>(units, (a.din + C::kStageK - 1) / C::kStageK, num_sms, &grid);
     if (split == 0) return cudaErrorNotSupported;
+    const char* ev = getenv(C::DOWN ? "XSPLITB" : "XSPLITA");
+    if (ev) { split = atoi(ev); grid = layer_grid(kernel, C::kSmem, split, num_sms); }
     CUtensorMap tm;
     const bool ok = C::FP4 ? make_code_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64)
                            : make_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64, 64);

@@ -544,13 +544,13 @@ EP_API ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const e
  * buffers only; ids as for a dispatch (-1: no expert, a bad id sets EP_DEVERR_BAD_ID); a token
  * without an expert gets a zero row. D % 128 == 0, dff % 128 == 0. w_gate_up [E][2 dff][D], gate
  * rows first, w_down [E][D][dff].
- * h is rounded to bf16; sums are fp32 in an order fixed by the sizes; results are joined in
- * fp32 in the order of k and rounded once to out_dtype.
- * ep_moe_layer_fp4: weights in 4 bits, of one format; x and h stay bf16 in all but their last
- * bits: each is taken apart into four e2m1 digits of a power of two for each block of the
- * format's size. An element down to a sixteenth of its block's largest is exact, a smaller one
- * within 2^-11 of the largest; EP_FP4_NV also within 2^-28 of the row's largest. An infinity or
- * a NaN in a row makes that row's results NaN.
+ * h is fp32 and enters the down projection as two bf16 terms (2^-16); sums are fp32 in an order
+ * fixed by the sizes; results are joined in fp32 in the order of k and rounded once to out_dtype.
+ * ep_moe_layer_fp4: weights in 4 bits, of one format; x and h are taken apart into e2m1 digits
+ * (four and five) of a power of two for each block of the format's size. An element of x down to
+ * a sixteenth of its block's largest is exact, a smaller one within 2^-11 of the largest, one of
+ * h within 2^-14; EP_FP4_NV also within 2^-28 of the row's largest. An infinity or a NaN in a
+ * row makes that row's results NaN.
  * workspace: ep_moe_layer_workspace_bytes, 256-byte aligned, for this call alone until its
  * work is done. */
 EP_API size_t ep_moe_layer_workspace_bytes(const ep_buffer* buf, int64_t num_tokens, int64_t dff);

@@ -38,21 +38,23 @@ class Layer:
     def run(self, x, scores, ids, **kw):
         return self.buf.moe_layer(x, scores, ids, *self.w, **kw)
 
-    def rest(self, x):
-        """What the digits of a 4-bit form may leave of x [n, cols] (bf16 values)."""
+    def rest(self, x, h=False):
+        """What the digits (bf16 weights: h's two terms) may leave of x [n, cols], bf16 values, or
+        of h."""
         if self.fmt == "bf16":
-            return torch.zeros_like(x)
+            return x.abs() * 2.0 ** -16 if h else torch.zeros_like(x)
         n = F4.BLOCK[self.fmt]
         block = x.abs().unflatten(-1, (-1, n)).amax(-1, keepdim=True).expand(-1, -1, n).flatten(-2)
-        rest = torch.where(x.abs() * 16 >= block, 0.0, block * 2.0 ** -11)
+        rest = block * 2.0 ** -14 if h else \
+            torch.where(x.abs() * 16 >= block, 0.0, block * 2.0 ** -11)
         if self.fmt == "nv":
             rest = torch.maximum(rest, x.abs().amax(-1, keepdim=True) * 2.0 ** -28)
         return rest
 
-    def sums(self, x, w):
+    def sums(self, x, w, h=False):
         """n 2^-23 sum |x w| for any order, an eighth more for the lower digits' own sums, and
         the digits' rest."""
-        return (1.2 * x.shape[-1] * 2.0 ** -23) * (x.abs() @ w.abs().T) + self.rest(x) @ w.abs().T
+        return (1.2 * x.shape[-1] * 2.0 ** -23) * (x.abs() @ w.abs().T) + self.rest(x, h) @ w.abs().T
 
     def reference(self, x, scores, ids, act):
         """(result, how far it may be off before its last rounding) in 64 bits."""
@@ -67,11 +69,10 @@ class Layer:
             g, u = xe @ wg.T, xe @ wu.T
             h = act64(g, act) * u
             dg, du = self.sums(xe, wg), self.sums(xe, wu)
-            # |act'| <= 1.13, |act(g)| <= |g|; the activation's own arithmetic 2^-18; h to bf16.
+            # |act'| <= 1.13, |act(g)| <= |g|; the activation's own arithmetic 2^-18.
             dh = 1.13 * dg * u.abs() + g.abs() * du + 1.13 * dg * du + 2.0 ** -18 * h.abs()
-            dh = dh + BF16 * (h.abs() + dh)
             y = h @ wd.T
-            dy = dh @ wd.abs().T + self.sums(h.abs() + dh, wd)
+            dy = dh @ wd.abs().T + self.sums(h.abs() + dh, wd, h=True)
             s = scores[t, k].double()[:, None]
             out.index_add_(0, t, s * y)
             bound.index_add_(0, t, s.abs() * (dy + 2.0 ** -20 * y.abs()))
@@ -87,10 +88,11 @@ class Layer:
         err = (got.double() - want).abs()
         last = BF16 if out_dtype == torch.bfloat16 else 2.0 ** -24
         assert (err <= bound + last * (want.abs() + bound)).all()
-        # Roundings (of h, each at most 2^-8 relative, and of the result) go both ways: their root
-        # mean square is at most sqrt(2 / 3) 2^-8 of the result's, all else far below.
+        # The last rounding is at most 2^-8 relative in each element; what the digits leave, at most
+        # 2^-11 of a block's largest in the elements below a sixteenth of it, goes both ways and is
+        # a small part of 2^-11 in the root mean square.
         if want.norm() > 0:
-            assert err.norm() <= 2.0 ** -8 * want.norm()
+            assert err.norm() <= (last + 2.0 ** -11) * want.norm()
         assert torch.equal(got, self.run(x, scores, ids, act=act, out_dtype=out_dtype))
         assert self.buf.device_error() == 0
         return got
