@@ -35,6 +35,7 @@ template <int FMT_, bool PAIR_, int OUT_, int STAGES_>
 struct Fp4Cfg {
     static constexpr int FMT = FMT_, OUT = OUT_, STAGES = STAGES_;
     static constexpr bool PAIR = PAIR_, GLU = OUT_ != kOutPlain;
+    static constexpr bool kHalves = GLU && !PAIR;     // W's scales in half lines, by a warp
     static constexpr int BN = PAIR ? 256 : 128;
     static constexpr int kOutBN = GLU ? BN / 2 : BN;
     static constexpr int kTileRows = PAIR ? 256 : 128;
@@ -79,23 +80,13 @@ struct Fp4GemmArgs {
     uint32_t* err;
 };
 
-// One warp's share of a stage's scales, of the tile's 128 receive rows at row0 and of its BN
-// rows of W: what has to pass registers is fetched ahead of the stage's turn, the rest copied.
-// 16 bytes of a line of W's scales come from one tile, or (one SM, gated: 64 gate rows and 64
-// up rows) half from the gate rows' tile and half from the up rows'.
+// The scales of a stage that pass a warp's registers, fetched ahead of the stage's turn: those of
+// the tile's 128 receive rows at row0, 4 bytes at a time, and, in the gated tiles of one SM, those
+// of 64 gate rows and 64 up rows, half a line each. (W's others are copied as they lie.)
 template <class C>
 struct StageScales {
-    static constexpr bool kHalves = C::GLU && !C::PAIR;
     uint32_t x[4][C::kTiles];
-    uint2 w[kHalves ? 2 : 1][C::kTiles];
-
-    static __device__ __forceinline__ const uint8_t* w_tile(const Fp4GemmArgs& a, int e, int nb, int b,
-                                                            int64_t kt0, int64_t tiles)
-    {
-        const int64_t row = C::GLU ? ((int64_t)e * 2 + b) * a.dout + nb * C::kOutBN
-                                   : (int64_t)e * a.dout + nb * C::BN + b * 128;
-        return a.w_scales + fp4_scale_at(row, kt0, tiles);
-    }
+    uint2 w[C::kHalves ? 2 : 1][C::kTiles];
 
     __device__ __forceinline__ void fetch(const Fp4GemmArgs& a, int e, int nb, int64_t row0, int stage,
                                           int lane)
@@ -110,48 +101,31 @@ struct StageScales {
             for (int j = 0; j < C::kTiles; ++j)
                 x[q][j] = kt0 + j < tiles ? __ldcg(reinterpret_cast<const uint32_t*>(src + j * 512)) : 0u;
         }
-        if (kHalves) {
+        if (C::kHalves) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const uint8_t* src = w_tile(a, e, nb, b, kt0, tiles) + lane * 16;
+            for (int b = 0; b < (C::kHalves ? 2 : 1); ++b) {
+                const int64_t row = ((int64_t)e * 2 + b) * a.dout + nb * C::kOutBN;
+                const uint8_t* src = a.w_scales + fp4_scale_at(row, kt0, tiles) + lane * 16;
 #pragma unroll
                 for (int j = 0; j < C::kTiles; ++j)
-                    w[b % (kHalves ? 2 : 1)][j] = kt0 + j < tiles ? __ldcg(reinterpret_cast<const uint2*>(src + j * 512))
-                                                  : make_uint2(0u, 0u);
+                    w[b][j] = kt0 + j < tiles ? __ldcg(reinterpret_cast<const uint2*>(src + j * 512))
+                                              : make_uint2(0u, 0u);
             }
         }
     }
 
-    __device__ __forceinline__ void store(uint32_t s_a, uint32_t s_b, const Fp4GemmArgs& a, int e, int nb,
-                                          int stage, int lane) const
+    __device__ __forceinline__ void store(uint32_t s_a, uint32_t s_b, int lane) const
     {
-        const int64_t tiles = a.din / (4 * Fp4<C::FMT>::kBlock), kt0 = (int64_t)stage * C::kTiles;
-        if (!kHalves) {
-#pragma unroll
-            for (int b = 0; b < C::BN / 128; ++b) {
-                const uint8_t* src = w_tile(a, e, nb, b, kt0, tiles) + lane * 16;
-#pragma unroll
-                for (int j = 0; j < C::kTiles; ++j) {
-                    const bool in = kt0 + j < tiles;
-                    cp_async16(s_b + (j * (C::BN / 128) + b) * kScaleTile + lane * 16,
-                               in ? src + j * 512 : src, in);
-                }
-            }
-            cp_async_commit();
-        }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int j = 0; j < C::kTiles; ++j)
-                sts32(s_a + j * kScaleTile + lane * 16 + q * 4, x[q][j]);
-        if (kHalves) {
+            for (int j = 0; j < C::kTiles; ++j) sts32(s_a + j * kScaleTile + lane * 16 + q * 4, x[q][j]);
+        if (C::kHalves) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < (C::kHalves ? 2 : 1); ++b)
 #pragma unroll
                 for (int j = 0; j < C::kTiles; ++j)
-                    sts64(s_b + j * kScaleTile + lane * 16 + b * 8, w[b % (kHalves ? 2 : 1)][j]);
-        } else {
-            cp_async_wait<0>();
+                    sts64(s_b + j * kScaleTile + lane * 16 + b * 8, w[b][j]);
         }
     }
 };
@@ -191,7 +165,7 @@ __device__ __forceinline__ void store_fp4x32(const float (&v)[32], float g, uint
 template <class C>
 __global__ void __launch_bounds__(kFp4Threads, 1)
 expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                  const Fp4GemmArgs a)
+                  const __grid_constant__ CUtensorMap tm_s, const Fp4GemmArgs a)
 {
     constexpr int STAGES = C::STAGES, BN = C::BN;
     constexpr bool PAIR = C::PAIR;
@@ -259,7 +233,8 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     const int total = q.total;
 
     if (warp == 0) {
-        // ---- codes ----------------------------------------------------------
+        // ---- codes, and W's scales --------------------------------------------
+        const int tiles = (int)(a.din / (4 * Fp4<C::FMT>::kBlock));
         int g = 0;
         bool ok = true;
         for (int u = first; u < total && ok && !*s_abort; u += step) {
@@ -269,25 +244,39 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             // rows and 64 up rows (a pair: gate rows in the leader, up rows in the other).
             const int w0 = C::GLU ? p.e * 2 * (int)a.dout + p.nb * C::kOutBN + r * (int)a.dout
                                   : p.e * (int)a.dout + p.nb * BN + r * 128;
+            // The first of the 128-row groups of W whose scales the tile takes, and the next one's
+            // distance.
+            const int g0 = (C::GLU ? p.e * 2 * (int)a.dout + p.nb * C::kOutBN
+                                   : p.e * (int)a.dout + p.nb * BN) >> 7;
+            const int g_step = C::GLU ? (int)a.dout >> 7 : 1;
             for (int k = 0; k < k_iters; ++k, ++g) {
                 const int s = g % STAGES;
                 ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
                 if (!ok) break;
                 const uint32_t sa = ring + (uint32_t)s * (C::kBytesA + C::kBytesB);
                 const uint32_t sb = sa + C::kBytesA;
+                const uint32_t ss = ring_scales + (uint32_t)s * (C::kScalesA + C::kScalesB) + C::kScalesA;
                 const int kc = k * (kFp4StageK / 2);
+                // The last stage may be half a stage: what is copied behind the last column is not
+                // multiplied.
+                constexpr uint32_t kBytes = C::kBytesA + C::kBytesB + (C::kHalves ? 0u : C::kScalesB);
                 if (elect_one()) {
-                    if (!PAIR) {
-                        const uint32_t fb = full0 + 8u * s;
-                        mbar_expect_tx(fb, C::kBytesA + C::kBytesB);
-                        tma_load_2d(sa, &tm_a, kc, row0, fb);
-                        tma_load_2d(sb, &tm_b, kc, w0, fb);
-                        if (C::GLU) tma_load_2d(sb + C::kBytesB / 2, &tm_b, kc, w0 + (int)a.dout, fb);
+                    const uint32_t fb = PAIR ? lead_full0 + 8u * s : full0 + 8u * s;
+                    // Both CTAs of a pair copy onto the leader's barrier, which expects both.
+                    if (leader) mbar_expect_tx(full0 + 8u * s, (PAIR ? 2u : 1u) * kBytes);
+                    auto load = [&](uint32_t dst, const CUtensorMap* tm, int c0, int c1) {
+                        if (PAIR) tma_load_2d_pair(dst, tm, c0, c1, fb);
+                        else tma_load_2d(dst, tm, c0, c1, fb);
+                    };
+                    load(sa, &tm_a, kc, row0);
+                    load(sb, &tm_b, kc, w0);
+                    if (C::kHalves) {
+                        load(sb + C::kBytesB / 2, &tm_b, kc, w0 + (int)a.dout);
                     } else {
-                        if (leader) mbar_expect_tx(full0 + 8u * s, 2u * (C::kBytesA + C::kBytesB));
-                        const uint32_t fb = lead_full0 + 8u * s;
-                        tma_load_2d_pair(sa, &tm_a, kc, row0, fb);
-                        tma_load_2d_pair(sb, &tm_b, kc, w0, fb);
+#pragma unroll
+                        for (int b = 0; b < BN / 128; ++b)
+                            load(ss + b * C::kTiles * kScaleTile, &tm_s, 0,
+                                 (g0 + b * g_step) * tiles + k * C::kTiles);
                     }
                 }
                 __syncwarp();
@@ -299,7 +288,12 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             mbar_wait_until(empty0 + 8u * (i % STAGES), (uint32_t)((i / STAGES) & 1), deadline);
     } else if (warp == 1 && leader) {
         // ---- scales to tensor memory, products --------------------------------
-        int g = 0, tl = 0;
+        constexpr uint32_t kCodeStep = (C::kBytesA + C::kBytesB) >> 4;     // a stage's, in descriptors
+        constexpr uint32_t kScaleStep = (C::kScalesA + C::kScalesB) >> 4;
+        const uint32_t code0 = desc_lo(ring), scale0 = desc_lo(ring_scales);
+        uint32_t code = code0, scale = scale0;         // the slot's
+        uint32_t ts = 0u, phase = 0u;                  // scale columns, the slot's parity
+        int s = 0, tl = 0;
         bool issued = false, ok = true;
         for (int u = first; u < total && ok && !*s_abort; u += step, ++tl) {
             const int acc = tl & 1;
@@ -311,37 +305,47 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem + (acc ? C::kAcc1 : 0u);
-            for (int k = 0; k < k_iters; ++k, ++g) {
-                const int s = g % STAGES;
-                ok = warp_all(wait_or_abort<PAIR>(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort));
+            int left = (int)a.din / kFp4K;             // steps of the contraction
+            for (uint32_t some = 0u; left > 0; left -= kFp4StageK / kFp4K, some = 1u) {
+                ok = warp_all(wait_or_abort<PAIR>(full0 + 8u * s, phase, s_abort));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sa = ring + (uint32_t)s * (C::kBytesA + C::kBytesB);
-                const uint32_t ss = ring_scales + (uint32_t)s * (C::kScalesA + C::kScalesB);
-                const uint32_t ta = tmem + C::kScaleCol0 +
-                                    (uint32_t)(g % C::kScaleBufs) * (C::kColsA + C::kColsB);
-                const uint32_t tb = ta + C::kColsA;
                 if (elect_one()) {
+                    const uint32_t ta = tmem + C::kScaleCol0 + ts, tb = ta + C::kColsA;
 #pragma unroll
                     for (int j = 0; j < C::kTiles; ++j)
-                        tmem_copy_scales<PAIR>(ta + 4u * j, scale_desc(ss + j * kScaleTile));
+                        tmem_copy_scales<PAIR>(ta + 4u * j,
+                                               desc_of(scale + j * (kScaleTile >> 4), kScaleDescHi));
 #pragma unroll
                     for (int j = 0; j < C::kTiles * (BN / 128); ++j)
-                        tmem_copy_scales<PAIR>(tb + 4u * j,
-                                               scale_desc(ss + C::kScalesA + j * kScaleTile));
+                        tmem_copy_scales<PAIR>(
+                            tb + 4u * j,
+                            desc_of(scale + (C::kScalesA >> 4) +
+                                        (j % (BN / 128) * C::kTiles + j / (BN / 128)) * (kScaleTile >> 4),
+                                    kScaleDescHi));
 #pragma unroll
                     for (int j = 0; j < kFp4StageK / kFp4K; ++j) {
+                        if (j >= left) break;
                         const int t = Fp4Mma<C::FMT>::tile_of_step(j);
-                        umma_fp4<C::FMT, PAIR>(d_tmem, smem_desc_k128(sa + j * (kFp4K / 2)),
-                                               smem_desc_k128(sa + C::kBytesA + j * (kFp4K / 2)),
+                        umma_fp4<C::FMT, PAIR>(d_tmem, desc_of(code + j * (kFp4K / 2 >> 4), kCodeDescHi),
+                                               desc_of(code + ((C::kBytesA + j * (kFp4K / 2)) >> 4), kCodeDescHi),
                                                Fp4Mma<C::FMT>::idesc_step(C::kIdesc, j), ta + 4u * t,
-                                               tb + 4u * t * (BN / 128), (k | j) != 0 ? 1u : 0u);
+                                               tb + 4u * t * (BN / 128), j == 0 ? some : 1u);
                     }
                     umma_commit<PAIR>(empty0 + 8u * s);
-                    if (k == k_iters - 1) umma_commit<PAIR>(accum_full0 + 8u * acc);
+                    if (left <= kFp4StageK / kFp4K) umma_commit<PAIR>(accum_full0 + 8u * acc);
                 }
                 __syncwarp();
                 issued = true;
+                if (C::kScaleBufs == 2) ts ^= C::kColsA + C::kColsB;
+                code += kCodeStep;
+                scale += kScaleStep;
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                    code = code0;
+                    scale = scale0;
+                }
             }
         }
         if (issued) {
@@ -384,7 +388,7 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     tmem_ld32(t_acc + (uint32_t)(c + C::kOutBN), qu);
                     tmem_wait_ld();
                     // Both accumulators have no column of what is left to drain (see below).
-                    if (PAIR && i == kRounds / 2 - 1) {
+                    if (PAIR && i == 0) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(lead_free0);
@@ -395,7 +399,7 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                                act_value(__uint_as_float(q32[n]) * gw, a.act);
                 } else {
                     tmem_wait_ld();
-                    if (PAIR && i == kRounds / 2 - 1) {
+                    if (PAIR && i == 0) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(lead_free0);
@@ -420,29 +424,38 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             }
         }
     } else if (warp >= 2 + kDrainWarps) {
-        // ---- scales to shared memory: every kScaleWarps-th stage ----------------
-        const int mine = warp - 2 - kDrainWarps;
-        int g = 0;
-        bool ok = true;
-        for (int u = first; u < total && ok && !*s_abort; u += step) {
-            const TileRef p = tile_of(q, E, nbk, u);
-            const int64_t row0 = (int64_t)__ldcg(a.expert_offset + p.e) + p.mt * C::kTileRows + r * kBM;
-            for (int k = 0; k < k_iters; ++k, ++g) {
-                if (g % kScaleWarps != mine) continue;
-                const int s = g % STAGES;
-                StageScales<C> sc;
-                sc.fetch(a, p.e, p.nb, row0, k, lane);
-                ok = warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort));
-                if (!ok) break;
-                const uint32_t ss = ring_scales + (uint32_t)s * (C::kScalesA + C::kScalesB);
-                sc.store(ss, ss + C::kScalesA, a, p.e, p.nb, k, lane);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(lead_full0 + 8u * s);
-                    else mbar_arrive(full0 + 8u * s);
-                }
+        // ---- scales to shared memory: every kScaleWarps-th stage, the warp's next one on its way
+        StageScales<C> next;
+        int pu = first, pk = warp - 2 - kDrainWarps;   // unit and stage that are fetched for
+        TileRef pp = {};
+        int64_t prow0 = 0;
+        auto enter = [&] {
+            while (pu < total && pk >= k_iters) {
+                pk -= k_iters;
+                pu += step;
             }
+            if (pu >= total) return;
+            pp = tile_of(q, E, nbk, pu);
+            prow0 = (int64_t)__ldcg(a.expert_offset + pp.e) + pp.mt * C::kTileRows + r * kBM;
+        };
+        enter();
+        if (pu < total) next.fetch(a, pp.e, pp.nb, prow0, pk, lane);
+        const int stages = first < total ? ((total - 1 - first) / step + 1) * k_iters : 0;
+        for (int g = warp - 2 - kDrainWarps; g < stages && !*s_abort; g += kScaleWarps) {
+            const int s = g % STAGES;
+            if (!warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort))) break;
+            const uint32_t ss = ring_scales + (uint32_t)s * (C::kScalesA + C::kScalesB);
+            next.store(ss, ss + C::kScalesA, lane);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(lead_full0 + 8u * s);
+                else mbar_arrive(full0 + 8u * s);
+            }
+            // Not before: the fence and the arrival would wait for these loads.
+            pk += kScaleWarps;
+            if (pk >= k_iters) enter();
+            if (pu < total) next.fetch(a, pp.e, pp.nb, prow0, pk, lane);
         }
     }
 
@@ -470,10 +483,12 @@ cudaError_t launch_form(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o
         grid = cluster_grid(kernel, kFp4Threads, C::kSmem, num_sms);
         if (grid < 2) return cudaErrorNotSupported;
     }
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, ts;
     const uint64_t wrows = (uint64_t)f.E * (uint64_t)(C::GLU ? 2 * f.dout : f.dout);
     if (!make_code_map(&ta, f.x_codes, (uint64_t)f.din, (uint64_t)f.rows, kBM) ||
-        !make_code_map(&tb, f.w_codes, (uint64_t)f.din, wrows, C::GLU && !PAIR ? 64 : 128))
+        !make_code_map(&tb, f.w_codes, (uint64_t)f.din, wrows, C::kHalves ? 64 : 128) ||
+        !make_scale_map(&ts, f.w_scales, wrows / 128 * (uint64_t)(f.din / (4 * Fp4<FMT>::kBlock)),
+                        C::kTiles))
         return cudaErrorInvalidValue;
     Fp4GemmArgs a = {};
     a.cnt = f.cnt;
@@ -499,7 +514,7 @@ cudaError_t launch_form(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = o.stream;
     set_attrs(&cfg, attr, PAIR, o.pdl);
-    e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, ts, a);
     if (e == cudaSuccess && o.launches) ++*o.launches;
     return e;
 }

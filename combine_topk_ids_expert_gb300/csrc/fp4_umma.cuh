@@ -37,12 +37,17 @@ struct Fp4Mma {
     static __host__ __device__ constexpr int tile_of_step(int j) { return FMT == kFp4Mx ? j >> 1 : j; }
 };
 
-// Descriptor of one tile of scales: 32 lines of 16 bytes, no swizzle, 128 bytes from one
-// group of 8 lines to the next.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
+// Descriptors in two halves, of which only the lower one moves (by bytes / 16; shared memory
+// ends below the 14 bits of its address): what the issuing thread computes for an instruction is
+// one addition. Computed whole each time they took longer than the products.
+//   codes: lines of 128 bytes, 128-byte swizzle, 1024 bytes from one group of 8 to the next;
+//   scales: a tile's 32 lines of 16 bytes, no swizzle, 128 bytes from one group of 8 to the next.
+constexpr uint32_t kCodeDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kScaleDescHi = (128 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi)
 {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
-           ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    return (uint64_t)lo | ((uint64_t)hi << 32);
 }
 
 // A tile of scales to 4 columns of tensor memory, in all four groups of lanes. In order with
@@ -96,13 +101,18 @@ inline bool make_code_map(CUtensorMap* m, const void* base, uint64_t cols, uint6
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 16 bytes from L2 to shared memory, zeros instead where !in. Scales may come from the kernel
-// before, so nothing here reads them by way of L1 (see ep_device.cuh).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
+// Tensor map over tiles of scales, one after the other, in boxes of box_tiles.
+inline bool make_scale_map(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {kScaleTile / 4, tiles};
+    const cuuint64_t strides[1] = {kScaleTile};
+    const cuuint32_t box[2] = {kScaleTile / 4, box_tiles};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
@@ -113,17 +123,6 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
 __device__ __forceinline__ void sts64(uint32_t addr, uint2 v)
 {
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit()
-{
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-template <int LEFT>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 }  // namespace

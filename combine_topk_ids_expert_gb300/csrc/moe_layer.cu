@@ -472,7 +472,9 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             mbar_wait_until(empty0 + 8u * (i % STAGES), (uint32_t)((i / STAGES) & 1), deadline);
     } else if (warp == 1) {
         // ---- products -------------------------------------------------------------
-        int g = 0, tl = 0;
+        const uint32_t a0 = desc_lo(ring), b0 = desc_lo(ring_b), scale0 = desc_lo(ring_s);
+        uint32_t da = a0, db = b0, ds = scale0, ts = 0u, phase = 0u;   // the slot's
+        int s = 0, tl = 0;
         bool issued = false, ok = true;
         for (int u = u_first; u < u_last && ok && !*s_abort && k_last > k_first; ++u, ++tl) {
             const int acc = tl & 1;
@@ -485,36 +487,33 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             const uint32_t idesc = C::FP4 ? Fp4Mma<C::FP4 ? FMT : kFp4Mx>::idesc(kBM, n)
                                           : (1u << 4) | (1u << 7) | (1u << 10) |
                                                 ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            for (int k = k_first; k < k_last; ++k, ++g) {
-                const int s = g % STAGES;
-                ok = warp_all(wait_or_abort(full0 + 8u * s, (uint32_t)((g / STAGES) & 1), s_abort));
+            for (int k = k_first; k < k_last; ++k) {
+                ok = warp_all(wait_or_abort(full0 + 8u * s, phase, s_abort));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sa = ring + (uint32_t)s * C::kBytesA;
-                const uint32_t sb = ring_b + (uint32_t)s * C::kBytesB;
                 if (elect_one()) {
                     if constexpr (C::FP4) {
-                        const uint32_t ss = ring_s + (uint32_t)s * (2 * C::kScales);
-                        const uint32_t ta = tmem + C::kScaleCol0 + (uint32_t)((g & 1) * 32), tb = ta + 16u;
+                        const uint32_t ta = tmem + C::kScaleCol0 + ts, tb = ta + 16u;
 #pragma unroll
                         for (int j = 0; j < C::kTiles; ++j) {
-                            tmem_copy_scales<false>(ta + 4u * j, scale_desc(ss + j * kScaleTile));
-                            tmem_copy_scales<false>(tb + 4u * j,
-                                                    scale_desc(ss + C::kScales + j * kScaleTile));
+                            tmem_copy_scales<false>(ta + 4u * j,
+                                                    desc_of(ds + j * (kScaleTile >> 4), kScaleDescHi));
+                            tmem_copy_scales<false>(
+                                tb + 4u * j, desc_of(ds + ((C::kScales + j * kScaleTile) >> 4), kScaleDescHi));
                         }
 #pragma unroll
                         for (int j = 0; j < kFp4StageK / kFp4K; ++j) {
                             const int t = Fp4Mma<FMT>::tile_of_step(j);
-                            umma_fp4<FMT, false>(d_tmem, smem_desc_k128(sa + j * (kFp4K / 2)),
-                                                 smem_desc_k128(sb + j * (kFp4K / 2)),
+                            umma_fp4<FMT, false>(d_tmem, desc_of(da + j * (kFp4K / 2 >> 4), kCodeDescHi),
+                                                 desc_of(db + j * (kFp4K / 2 >> 4), kCodeDescHi),
                                                  Fp4Mma<FMT>::idesc_step(idesc, j), ta + 4u * t,
                                                  tb + 4u * t, k > k_first || j > 0 ? 1u : 0u);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < C::kStageK / kUmmaK; ++j)
-                            umma_bf16<false>(d_tmem, smem_desc_k128(sa + j * kUmmaK * 2),
-                                             smem_desc_k128(sb + j * kUmmaK * 2), idesc,
+                            umma_bf16<false>(d_tmem, desc_of(da + j * (kUmmaK * 2 >> 4), kCodeDescHi),
+                                             desc_of(db + j * (kUmmaK * 2 >> 4), kCodeDescHi), idesc,
                                              k > k_first || j > 0 ? 1u : 0u);
                     }
                     umma_commit<false>(empty0 + 8u * s);
@@ -522,6 +521,17 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                 }
                 __syncwarp();
                 issued = true;
+                ts ^= 32u;
+                da += C::kBytesA >> 4;
+                db += C::kBytesB >> 4;
+                ds += (2 * C::kScales) >> 4;
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                    da = a0;
+                    db = b0;
+                    ds = scale0;
+                }
             }
         }
         if (issued) {
@@ -660,21 +670,17 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             if (g < stages) fetch(g);
             for (; g < stages && !*s_abort; g += kScaleWarps) {
                 const int s = g % STAGES;
-                uint2 now[2][C::kTiles];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < C::kTiles; ++j) now[b][j] = next[b][j];
-                if (g + kScaleWarps < stages) fetch(g + kScaleWarps);
                 if (!warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort))) break;
                 const uint32_t dst = ring_s + (uint32_t)s * (2 * C::kScales) + (uint32_t)lane * 16u;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int j = 0; j < C::kTiles; ++j) sts64(dst + j * kScaleTile + b * 8, now[b][j]);
+                    for (int j = 0; j < C::kTiles; ++j) sts64(dst + j * kScaleTile + b * 8, next[b][j]);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full0 + 8u * s);
+                // Not before: the fence would wait for these loads.
+                if (g + kScaleWarps < stages) fetch(g + kScaleWarps);
             }
         }
     } else {
