@@ -1121,10 +1121,6 @@ ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x, const float* scores, co
     if (T > 0 && (!x || !scores)) return EP_ERR_INVALID_ARG;
     if (!is_aligned(x, 16) || !is_aligned(scores, 4)) return EP_ERR_ALIGNMENT;
     cudaStream_t s = as_stream(stream);
-    const ep_status sl = enqueue_layout(buf, ids, T, N, s);
-    if (sl != EP_OK) return sl;
-    fill_dispatch(buf, out);
-    if (T == 0) return EP_OK;
     ep::PermuteFp4Args a = {};
     a.x = x;
     a.scores = scores;
@@ -1138,7 +1134,22 @@ ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x, const float* scores, co
     a.scales = rows->scales;
     a.recv_scores = buf->recv_scores;
     a.recv_src = buf->recv_src;
-    return cuda_status(ep::launch_permute_fp4(a, buf->num_sms, opts(buf, s)));
+    cudaError_t e = cudaErrorNotSupported;
+    if (buf->onepass && T > 0) {
+        ep::LayoutArgs la = layout_args(buf, ids, T, N);
+        la.tpt = ep::tokens_per_tile(T, la.K, buf->num_sms * ep::dispatch_fp4_tiles_per_sm());
+        la.ntiles = (int)ep::tile_count(T, la.tpt);
+        e = ep::launch_dispatch_fp4(la, a, opts(buf, s), buf->coop_pdl, buf->dispatch_small_pairs);
+        if (e == cudaSuccess) remember_layout(buf, T, N);
+        else if (e != cudaErrorNotSupported) return EP_ERR_CUDA;
+    }
+    if (e != cudaSuccess) {
+        const ep_status sl = enqueue_layout(buf, ids, T, N, s);
+        if (sl != EP_OK) return sl;
+        if (T > 0 && ep::launch_permute_fp4(a, buf->num_sms, opts(buf, s)) != cudaSuccess) return EP_ERR_CUDA;
+    }
+    fill_dispatch(buf, out);
+    return EP_OK;
 }
 
 static ep_status enqueue_fp4(ep_buffer* b, const ep_fp4* x, const ep_fp4* w, int64_t din,

@@ -53,6 +53,12 @@ struct PermuteFp4Args {
     int32_t* recv_src;
 };
 cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const LaunchOpts& o);
+// Layout and rows in one cooperative kernel; cudaErrorNotSupported where a tile's tables do not fit
+// or the tiles cannot all be resident. l has at most dispatch_fp4_tiles_per_sm() tiles per SM.
+// pdl_ok and small_pairs as for launch_dispatch_onepass.
+int dispatch_fp4_tiles_per_sm();
+cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& a, const LaunchOpts& o,
+                                bool pdl_ok, int64_t small_pairs);
 
 // The experts' products in 4 bits (expert_fp4.cu).
 struct ExpertFp4Args {

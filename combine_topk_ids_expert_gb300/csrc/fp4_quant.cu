@@ -11,6 +11,7 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kDispatchFp4PerSm = 2;   // tiles of the one-pass dispatch on an SM
 
 // What 16 elements become: 8 bytes of codes, and on every fourth block's first thread the
 // word of four scales.
@@ -105,55 +106,161 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(Fp4Args a)
     griddep_launch_dependents();
 }
 
-// One CTA per token at a time: read and quantised once, written to each of its rows.
-constexpr int kPermuteThreads = 128;
+// A part of a token's row, 64 units of 16 elements, is a warp's: read and quantised once, written
+// to each of the token's rows. raw: the part's elements, two units a lane.
+constexpr int kPermuteThreads = 256;
+constexpr int kPartUnits = 64;
 
+__device__ __forceinline__ void fetch_part(const PermuteFp4Args& a, int64_t t, int part, int per_row,
+                                           int lane, int4 (&raw)[2][2])
+{
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.D * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int unit = part * kPartUnits + 32 * i + lane;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            raw[i][h] = unit < per_row ? ld_cg_v4(x + unit * 32 + 16 * h) : make_int4(0, 0, 0, 0);
+    }
+}
+
+// row_of(k): the receive row of the token's slot k, or -1.
+template <int FMT, bool TENSOR_SCALE, class RowOf>
+__device__ __forceinline__ void put_part(const PermuteFp4Args& a, int part, int per_row, int lane, float g,
+                                         const int4 (&raw)[2][2], RowOf row_of)
+{
+    const int64_t tiles = a.D / (4 * Fp4<FMT>::kBlock);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int unit = part * kPartUnits + 32 * i + lane;
+        float v[16];
+        bf16x16(raw[i][0], raw[i][1], v);
+        uint32_t word;
+        bool writes;
+        const uint2 q = quantize16<FMT, TENSOR_SCALE>(v, g, unit, &word, &writes);
+        const int kt = unit / (FMT == kFp4Mx ? 8 : 4);
+        for (int k = 0; k < a.K; ++k) {
+            const int64_t p = row_of(k);
+            if (p < 0 || unit >= per_row) continue;
+            *reinterpret_cast<uint2*>(a.codes + p * (a.D / 2) + unit * 8) = q;
+            if (writes) *reinterpret_cast<uint32_t*>(a.scales + fp4_scale_at(p, kt, tiles)) = word;
+        }
+    }
+}
+
+// After a layout of its own kernels: parts in turn over the warps.
 template <int FMT, bool TENSOR_SCALE>
 __global__ void __launch_bounds__(kPermuteThreads) permute_fp4_kernel(PermuteFp4Args a)
 {
-    __shared__ int s_pos[kMaxTopk];
-    __shared__ int s_n;
     griddep_wait();
-    const int per_row = (int)(a.D / 16);
-    const int64_t tiles = a.D / (4 * Fp4<FMT>::kBlock);
+    const int lane = threadIdx.x & 31;
+    const int per_row = (int)(a.D / 16), parts = (per_row + kPartUnits - 1) / kPartUnits;
     const float g = TENSOR_SCALE ? __ldcg(a.tensor_scale) : 1.0f;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            int n = 0;
-            for (int k0 = 0; k0 < a.K; k0 += 32) {
-                const int k = k0 + (int)threadIdx.x;
-                const int p = k < a.K ? __ldcg(a.pos + t * a.K + k) : -1;
-                if (p >= 0) {
-                    a.recv_scores[p] = __ldcg(a.scores + t * a.K + k);
-                    a.recv_src[p] = (int32_t)(t * a.K + k);
-                }
-                const unsigned some = __ballot_sync(~0u, p >= 0);
-                if (p >= 0) s_pos[n + __popc(some & lanemask_lt(threadIdx.x))] = p;
-                n += __popc(some);
-            }
-            if (threadIdx.x == 0) s_n = n;
-        }
-        __syncthreads();
-        const int n = s_n;
-        if (n == 0) continue;
-        const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.D * 2;
-        for (int u0 = (int)threadIdx.x & ~31; u0 < per_row; u0 += kPermuteThreads) {
-            const int unit = u0 + ((int)threadIdx.x & 31);
-            const bool in = unit < per_row;
-            float v[16] = {};
-            if (in) bf16x16(ld_cg_v4(x + unit * 32), ld_cg_v4(x + unit * 32 + 16), v);
-            uint32_t word;
-            bool writes;
-            const uint2 q = quantize16<FMT, TENSOR_SCALE>(v, g, unit, &word, &writes);
-            if (!in) continue;
-            const int kt = unit / (FMT == kFp4Mx ? 8 : 4);
-            for (int j = 0; j < n; ++j) {
-                const int64_t p = s_pos[j];
-                *reinterpret_cast<uint2*>(a.codes + p * (a.D / 2) + unit * 8) = q;
-                if (writes) *reinterpret_cast<uint32_t*>(a.scales + fp4_scale_at(p, kt, tiles)) = word;
+    const int64_t items = a.T * parts;
+    for (int64_t item = ((int64_t)blockIdx.x * kPermuteThreads + threadIdx.x) >> 5; item < items;
+         item += (int64_t)gridDim.x * (kPermuteThreads / 32)) {
+        const int64_t t = item / parts;
+        const int part = (int)(item - t * parts);
+        int4 raw[2][2];
+        fetch_part(a, t, part, per_row, lane, raw);
+        // Lane k has the row of slot k, and of slot k + 32.
+        int pos[2] = {-1, -1};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int k = 32 * n + lane;
+            if (k < a.K) pos[n] = __ldcg(a.pos + t * a.K + k);
+            if (part == 0 && pos[n] >= 0) {
+                a.recv_scores[pos[n]] = __ldcg(a.scores + t * a.K + k);
+                a.recv_src[pos[n]] = (int32_t)(t * a.K + k);
             }
         }
+        put_part<FMT, TENSOR_SCALE>(a, part, per_row, lane, g, raw, [&](int k) {
+            return __shfl_sync(~0u, k < 32 ? pos[0] : pos[1], k & 31);
+        });
+    }
+    griddep_launch_dependents();
+}
+
+// Layout, positions and rows in one kernel, a CTA to a tile of tokens, as the one-pass dispatch
+// of whole rows (its layout, with a grid barrier or, for small calls, every id counted by every
+// CTA). The tile's x comes to L2 meanwhile. Shared memory: [kLayoutWarps * Ep][tile pairs][3 * Ep]
+// ints.
+template <int FMT, bool TENSOR_SCALE, bool SMALL>
+__global__ void __launch_bounds__(kLayoutThreads, kDispatchFp4PerSm)
+dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
+{
+    extern __shared__ __align__(16) int s_dyn[];
+    __shared__ int s_rank[3][kMaxRanks];
+    __shared__ int s_tok[kMaxRanks];
+    __shared__ int s_wsum[kLayoutWarps];
+    __shared__ int s_flag;
+    __shared__ uint32_t s_epoch;
+    int* s_base = s_dyn;
+    int* s_pos = s_base + kLayoutWarps * L.Ep;
+    int* s_seed = s_pos + L.tpt * L.K;
+    int* s_tot = s_seed + L.Ep;
+    int* s_off = s_tot + L.Ep;
+    const int tile = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = (int64_t)tile * L.tpt, t1 = min(L.T, t0 + L.tpt);
+    const int n_my = (int)(t1 - t0), K = L.K;
+    griddep_wait();
+    const uint8_t* x0 = static_cast<const uint8_t*>(a.x) + t0 * a.D * 2;
+    for (int64_t i = (int64_t)threadIdx.x * 128; i < n_my * a.D * 2; i += (int64_t)kLayoutThreads * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(x0 + i));
+    if constexpr (SMALL) {
+        redundant_counts(L, tile, s_seed, s_tot, s_rank);
+        layout_offsets(L, s_base, s_seed, s_tot, s_off, s_rank, s_wsum);
+    } else {
+        if (!onepass_layout(L, tile, s_base, s_seed, s_tot, s_off, s_rank, s_tok, s_wsum, &s_flag,
+                            &s_epoch, s_pos, nullptr, [] {})) {
+            if (threadIdx.x == 0) atomicOr(L.err, kErrTimeout);
+            griddep_launch_dependents();
+            return;
+        }
+    }
+    if (tile == 0) {
+        for (int e = threadIdx.x; e < L.E; e += blockDim.x) {
+            L.cnt[e] = s_tot[e];
+            L.expert_offset[e] = s_off[e];
+        }
+        if (threadIdx.x < L.R) {
+            L.rows_per_rank[threadIdx.x] = s_rank[0][threadIdx.x];
+            L.rank_prefix[threadIdx.x] = s_rank[1][threadIdx.x];
+            L.tokens_in_rank[threadIdx.x] = s_rank[2][threadIdx.x];
+        }
+    }
+    tile_positions(L, tile, s_base, L.pos, s_pos, s_seed, SMALL ? nullptr : s_pos);
+    // Rows the layout can have; others only after its barrier words were corrupted.
+    const int64_t rows = (int64_t)L.R * L.S;
+    for (int j = threadIdx.x; j < n_my * K; j += kLayoutThreads) {
+        const int p = s_pos[j];
+        if (p < 0) continue;
+        if (p >= rows) {
+            atomicOr(L.err, kErrRowOob);
+            s_pos[j] = -1;
+            continue;
+        }
+        a.recv_scores[p] = __ldcg(a.scores + t0 * K + j);
+        a.recv_src[p] = (int32_t)(t0 * K + j);
+    }
+    __syncthreads();
+    const int per_row = (int)(a.D / 16), parts = (per_row + kPartUnits - 1) / kPartUnits;
+    const float g = TENSOR_SCALE ? __ldcg(a.tensor_scale) : 1.0f;
+    // The next part's elements are on their way while this one is written.
+    int4 next[2][2];
+    const int items = n_my * parts;
+    if (warp < items) fetch_part(a, t0 + warp / parts, warp % parts, per_row, lane, next);
+    for (int item = warp; item < items; item += kLayoutWarps) {
+        const int tt = item / parts, part = item - tt * parts;
+        int4 raw[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            raw[i][0] = next[i][0];
+            raw[i][1] = next[i][1];
+        }
+        const int after = item + kLayoutWarps;
+        if (after < items) fetch_part(a, t0 + after / parts, after % parts, per_row, lane, next);
+        put_part<FMT, TENSOR_SCALE>(a, part, per_row, lane, g, raw, [&](int k) { return s_pos[tt * K + k]; });
     }
     griddep_launch_dependents();
 }
@@ -188,12 +295,61 @@ cudaError_t launch_dequantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const LaunchOpts& o)
 {
     const int64_t most = (int64_t)num_sms * (2048 / kPermuteThreads);
-    const int grid = (int)(a.T < most ? a.T : most);
+    const int64_t items = a.T * ((a.D / 16 + kPartUnits - 1) / kPartUnits);
+    const int64_t need = (items + kPermuteThreads / 32 - 1) / (kPermuteThreads / 32);
+    const int grid = (int)(need < most ? need : most);
     if (a.format == kFp4Mx)
         return launch_kernel(permute_fp4_kernel<kFp4Mx, false>, grid, kPermuteThreads, 0, o, a);
     return a.tensor_scale
                ? launch_kernel(permute_fp4_kernel<kFp4Nv, true>, grid, kPermuteThreads, 0, o, a)
                : launch_kernel(permute_fp4_kernel<kFp4Nv, false>, grid, kPermuteThreads, 0, o, a);
+}
+
+
+int dispatch_fp4_tiles_per_sm() { return kDispatchFp4PerSm; }
+
+cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& a, const LaunchOpts& o,
+                                bool pdl_ok, int64_t small_pairs)
+{
+    if (!l.gbar || l.ntiles <= 0) return cudaErrorNotSupported;
+    const int64_t tile_pairs = l.tpt * l.K;
+    if (tile_pairs > kMaxTilePairs) return cudaErrorNotSupported;
+    const size_t smem = (size_t)((kLayoutWarps + 3) * (int64_t)l.Ep + tile_pairs) * 4;
+    const bool small = l.T * l.K <= small_pairs;
+    void (*kernel)(LayoutArgs, PermuteFp4Args) =
+        a.format == kFp4Mx ? (small ? dispatch_fp4_kernel<kFp4Mx, false, true>
+                                    : dispatch_fp4_kernel<kFp4Mx, false, false>)
+        : a.tensor_scale   ? (small ? dispatch_fp4_kernel<kFp4Nv, true, true>
+                                    : dispatch_fp4_kernel<kFp4Nv, true, false>)
+                           : (small ? dispatch_fp4_kernel<kFp4Nv, false, true>
+                                    : dispatch_fp4_kernel<kFp4Nv, false, false>);
+    int dev = 0, sms = 0, per_sm = 0;
+    // Every CTA has to be resident for the grid barrier.
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess ||
+        smem > 100 * 1024 || cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kLayoutThreads, smem) != cudaSuccess)
+        return cudaErrorNotSupported;
+    if ((int64_t)per_sm * sms < l.ntiles) return cudaErrorNotSupported;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(l.ntiles);
+    cfg.blockDim = dim3(kLayoutThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = o.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (o.pdl && pdl_ok) ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, l, a);
+    if (e == cudaErrorCooperativeLaunchTooLarge) {   // fewer SMs than the device reports (MPS)
+        cudaGetLastError();
+        return cudaErrorNotSupported;
+    }
+    if (e == cudaSuccess && o.launches) ++*o.launches;
+    return e;
 }
 
 }  // namespace ep

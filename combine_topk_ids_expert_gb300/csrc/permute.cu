@@ -199,90 +199,6 @@ permute_bulk_kernel(PermuteArgs a, int stages, int slot_bytes)
     griddep_launch_dependents();
 }
 
-// Layout of a small call without a grid barrier: every CTA counts all of the
-// call's pairs itself (its ids stay in L2 after the first CTA reads them), so
-// the CTAs never wait for one another. s_tot[e] = pairs of expert e in the
-// call; s_seed[e] = those before this tile's first pair; tile 0 also counts
-// each rank's distinct tokens into s_rank[2] and reports invalid ids.
-// Ends with __syncthreads.
-__device__ void redundant_counts(const LayoutArgs& L, int tile, int* s_seed, int* s_tot,
-                                 int (*s_rank)[kMaxRanks])
-{
-    const int64_t np = L.T * L.K;
-    const int64_t p0 = (int64_t)tile * L.tpt * L.K;   // this tile's first pair
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < L.Ep; e += blockDim.x) {
-        s_seed[e] = 0;
-        s_tot[e] = 0;
-    }
-    if (threadIdx.x < L.R) s_rank[2][threadIdx.x] = 0;
-    __syncthreads();
-    const int64_t np32 = (np + 31) & ~(int64_t)31;
-    bool bad = false;
-    // Warp w takes the 32-pair chunks w, w + 8, ...; each lane loads the ids of
-    // kRedBatch chunks before matching them, so the loads are in flight together.
-    constexpr int kRedBatch = 16;
-    for (int64_t cb = (int64_t)warp * 32; cb < np32; cb += (int64_t)kRedBatch * kLayoutThreads) {
-        int raw[kRedBatch];
-#pragma unroll
-        for (int u = 0; u < kRedBatch; ++u) {
-            const int64_t i = cb + (int64_t)u * kLayoutThreads + lane;
-            raw[u] = (i < np) ? __ldcg(L.ids + i) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kRedBatch; ++u) {
-            const int64_t c = cb + (int64_t)u * kLayoutThreads;
-            if (c >= np32) break;   // the same for every lane of the warp
-            const int e = valid_id(raw[u], L.E);
-            bad |= (e != raw[u]);
-            const unsigned peers = __match_any_sync(0xffffffffu, e);
-            if (e >= 0 && lane == __ffs(peers) - 1) {
-                atomicAdd(&s_tot[e], __popc(peers));
-                // lanes of this chunk whose pair comes before the tile
-                const unsigned before = (c + 32 <= p0) ? 0xffffffffu
-                                        : (c >= p0)    ? 0u
-                                                       : (1u << (unsigned)(p0 - c)) - 1u;
-                const int nb = __popc(peers & before);
-                if (nb) atomicAdd(&s_seed[e], nb);
-            }
-        }
-    }
-    if (tile == 0) {
-        if (bad) atomicOr(L.err, kErrBadId);
-        // Distinct tokens per rank over the call: the rank set of every token,
-        // kTokBatch tokens per thread with their first 8 ids loaded together.
-        constexpr int kTokBatch = 4;
-        const int eloc = L.E / L.R;
-        for (int64_t tb = threadIdx.x; tb < L.T; tb += (int64_t)kTokBatch * kLayoutThreads) {
-            unsigned long long mask[kTokBatch];
-#pragma unroll
-            for (int u = 0; u < kTokBatch; ++u) {
-                mask[u] = 0ull;
-                const int64_t t = tb + (int64_t)u * kLayoutThreads;
-                if (t >= L.T) continue;
-                int e8[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    e8[k] = (k < L.K) ? valid_id(__ldcg(L.ids + t * L.K + k), L.E) : -1;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (e8[k] >= 0) mask[u] |= 1ull << (e8[k] / eloc);
-                for (int k = 8; k < L.K; ++k) {
-                    const int e = valid_id(__ldcg(L.ids + t * L.K + k), L.E);
-                    if (e >= 0) mask[u] |= 1ull << (e / eloc);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kTokBatch; ++u)
-                while (mask[u]) {
-                    atomicAdd(&s_rank[2][__ffsll((long long)mask[u]) - 1], 1);
-                    mask[u] &= mask[u] - 1ull;
-                }
-        }
-    }
-    __syncthreads();
-}
-
 // Receive rows of pool token t for lane k < K: read from the positions its
 // owner tile published (L.pos), once that tile's ready word holds this call's
 // generation. -1 if the word does not come within the wait limit (then

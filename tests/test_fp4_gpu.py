@@ -114,9 +114,12 @@ def make_ids(T, E, K, seed, drop=0.1):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("layout,R", [("strided", 2), ("packed", 2), ("strided", 1)])
-@pytest.mark.parametrize("T,N", [(1, 1), (13, 16), (301, 301)])
-def test_dispatch_fp4(fmt, layout, R, T, N):
-    D, E, K = 384, 8, 3
+@pytest.mark.parametrize("T,N", [(1, 1), (13, 16), (301, 301), (1000, 1003)])
+@pytest.mark.parametrize("onepass", ["1", "0"])
+def test_dispatch_fp4(fmt, layout, R, T, N, onepass, monkeypatch):
+    """One kernel, with and without its grid barrier (T * K above 2048), or kernel after kernel."""
+    monkeypatch.setenv("EP_DISPATCH_ONEPASS", onepass)
+    D, E, K = 1152 if T == 301 else 384, 8, 3
     buf = ep.Buffer(N, D, E, R, K, layout=layout)
     ids = make_ids(T, E, K, T)
     x = torch.randn((T, D), device="cuda", generator=gen(2)).bfloat16()
