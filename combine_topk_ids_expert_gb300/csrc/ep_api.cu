@@ -1062,7 +1062,8 @@ static ep_status check_fp4(const ep_fp4* q, int64_t rows, int64_t cols, int64_t 
     if (rows > 0 && (!q->codes || !q->scales)) return EP_ERR_INVALID_ARG;
     if (!is_aligned(q->codes, 16) || !is_aligned(q->scales, 16) || !is_aligned(q->tensor_scale, 4))
         return EP_ERR_ALIGNMENT;
-    if (cols > INT32_MAX || rows > INT64_MAX / 4 / cols) return EP_ERR_CAPACITY;
+    // Rows and columns are counted in int32, bytes in int64.
+    if (cols > INT32_MAX || rows > INT32_MAX) return EP_ERR_CAPACITY;
     return EP_OK;
 }
 
@@ -1071,7 +1072,7 @@ static ep::Fp4Args fp4_args(const ep_fp4* q, int64_t rows, int64_t cols, int64_t
     ep::Fp4Args a = {};
     a.rows = rows;
     a.cols = cols;
-    a.rows_per_scale = rows_per_scale;
+    a.rows_per_scale = std::min<int64_t>(rows_per_scale, INT32_MAX);
     a.format = q->format;
     a.codes = q->codes;
     a.scales = q->scales;

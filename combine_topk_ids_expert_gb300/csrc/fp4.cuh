@@ -42,6 +42,29 @@ __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi)
     return r;
 }
 
+// Eight fp32 to the word of their e2m1.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// 1 / v within an ulp or two (rcp.approx), which is all that quotients for rounding need.
+__device__ __forceinline__ float rcp_near(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // The two values of the byte's two e2m1, as two fp16 (the low nibble's in the low half).
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte)
 {
@@ -100,7 +123,8 @@ constexpr uint32_t kNanMx = 0xFFu, kNanNv = 0x7Fu;
 // reciprocal gives, except next to a number of at most BITS fraction bits (the borders
 // between the format's numbers are such), where the remainder x - q d g decides, whose sign
 // one fma gives exactly: the quotient then lies on the border or on the right side of it.
-// d: few bits (a scale, or 6), so that q d is exact. rinv: 1 / (d g).
+// d: few bits (a scale, or 6), so that q d is exact. rinv: 1 / (d g), off by 2^-22 at most, so that
+// x rinv is within 2^-21 and a number within 2^-20 of a border is looked at.
 template <int BITS>
 __device__ __forceinline__ float quotient_for_rounding(float x, float d, float g, float rinv)
 {
@@ -123,34 +147,40 @@ __device__ __forceinline__ uint32_t fp4_scale_code(float amax, float g)
         return e == 255u ? kNanMx : e < 2u ? 0u : e - 2u;
     }
     if (!(amax < __uint_as_float(0x7F800000u))) return kNanNv;
-    return cvt_ue4m3(quotient_for_rounding<4>(amax, 6.0f, g, 1.0f / (6.0f * g)));
+    return cvt_ue4m3(quotient_for_rounding<4>(amax, 6.0f, g, rcp_near(6.0f * g)));
 }
 
 // Codes of 16 elements in a block with scale code c.
 template <int FMT, bool TENSOR_SCALE>
 __device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], uint32_t c, float g)
 {
-    uint32_t w[2] = {0u, 0u};
+    float q[16];
     if (FMT == kFp4Mx) {
         if (c == kNanMx) return make_uint2(0u, 0u);
         const float inv = __uint_as_float((254u - c) << 23);   // 2^(127 - c), c <= 252
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i >> 2] |= cvt_e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * (i & 3));
-        return make_uint2(w[0], w[1]);
+        for (int i = 0; i < 16; ++i) q[i] = v[i] * inv;
+        return make_uint2(cvt_e2m1x8(q), cvt_e2m1x8(q + 8));
     }
     if (c == kNanNv || c == 0u) return make_uint2(0u, 0u);
     const float s = ue4m3_value(c);
-    const float rinv = 1.0f / (s * g);
-    auto q = [&](float x) {
-        if (TENSOR_SCALE) return quotient_for_rounding<2>(x, s, g, rinv);
-        // x has 8 bits and s 4, so the quotient is on a border or 2^-12 away from it.
-        return __uint_as_float((__float_as_uint(x * rinv) + 8u) & ~15u);
-    };
+    const float rinv = rcp_near(s * g);
+    uint32_t least = ~0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i >> 2] |= cvt_e2m1x2(q(v[2 * i]), q(v[2 * i + 1])) << (8 * (i & 3));
-    return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 16; ++i) {
+        q[i] = v[i] * rinv;
+        // Nearly zero fraction bits behind the first two: next to a border, or to a code.
+        const uint32_t b = __float_as_uint(q[i]) + 8u;
+        least = min(least, b & 0x1FFFF0u);
+        // Without a matrix's scale, or where it is a power of two, x has 8 bits and s 4: the
+        // quotient is on a border or 2^-12 away from it, and its last bits are the reciprocal's.
+        if (!TENSOR_SCALE) q[i] = __uint_as_float(b & ~15u);
+    }
+    if (TENSOR_SCALE && least == 0u) {   // seldom: x / g has to fall there
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = quotient_for_rounding<2>(v[i], s, g, rinv);
+    }
+    return make_uint2(cvt_e2m1x8(q), cvt_e2m1x8(q + 8));
 }
 
 // 16 bf16 (32 bytes) as fp32.
@@ -165,7 +195,18 @@ __device__ __forceinline__ void bf16x16(const int4& a, const int4& b, float (&v)
     }
 }
 
-// Largest magnitude of 16 bf16: as integers, in which NaN is above infinity.
+// Largest magnitude of 16 bf16, as they lie: as integers, in which NaN is above infinity.
+__device__ __forceinline__ float amax16(const int4& a, const int4& b)
+{
+    const uint32_t q[8] = {(uint32_t)a.x, (uint32_t)a.y, (uint32_t)a.z, (uint32_t)a.w,
+                           (uint32_t)b.x, (uint32_t)b.y, (uint32_t)b.z, (uint32_t)b.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, q[i] & 0x7FFF7FFFu);
+    return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
+}
+
+// The same of 16 fp32.
 __device__ __forceinline__ float amax16(const float (&v)[16])
 {
     uint32_t m = 0u;

@@ -16,10 +16,10 @@ constexpr int kDispatchFp4PerSm = 2;   // tiles of the one-pass dispatch on an S
 // What 16 elements become: 8 bytes of codes, and on every fourth block's first thread the
 // word of four scales.
 template <int FMT, bool TENSOR_SCALE>
-__device__ __forceinline__ uint2 quantize16(const float (&v)[16], float g, int unit, uint32_t* word,
+__device__ __forceinline__ uint2 quantize16(const int4 (&raw)[2], float g, int unit, uint32_t* word,
                                             bool* writes)
 {
-    float m = amax16(v);
+    float m = amax16(raw[0], raw[1]);
     if (FMT == kFp4Mx) m = __uint_as_float(max(__float_as_uint(m), __shfl_xor_sync(~0u, __float_as_uint(m), 1)));
     const uint32_t c = fp4_scale_code<FMT>(m, g);
     // The word of 4 blocks from its 4 (nv) or 8 (mx) threads.
@@ -29,32 +29,60 @@ __device__ __forceinline__ uint2 quantize16(const float (&v)[16], float g, int u
     w |= __shfl_xor_sync(~0u, w, FMT == kFp4Mx ? 4 : 2);
     *word = w;
     *writes = (unit & (FMT == kFp4Mx ? 7 : 3)) == 0;
+    float v[16];
+    bf16x16(raw[0], raw[1], v);
     return fp4_codes16<FMT, TENSOR_SCALE>(v, c, g);
 }
 
+// 32 bytes of a lane: in one access where the matrix is aligned to it (two of 16 bytes touch every
+// sector of a warp's kilobyte twice), with `wide` the same for the whole grid.
+__device__ __forceinline__ void load32(const uint8_t* p, bool wide, int4& a, int4& b)
+{
+    if (wide) {
+        asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                       "=r"(b.w)
+                     : "l"(p));
+    } else {
+        a = ld_cg_v4(p);
+        b = ld_cg_v4(p + 16);
+    }
+}
+
+__device__ __forceinline__ void store32(uint8_t* p, bool wide, const uint32_t (&w)[8])
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// A warp takes 32 units of a row after the other (grid: columns x, rows y; no index of an
+// element is divided: that cost a quarter of the time).
 template <int FMT, bool TENSOR_SCALE>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(Fp4Args a)
+__global__ void __launch_bounds__(kThreads, 5) quantize_kernel(Fp4Args a)
 {
     griddep_wait();
-    const int64_t per_row = a.cols / 16, total = a.rows * per_row;
+    const int lane = threadIdx.x & 31, per_row = (int)(a.cols / 16);
     const int64_t tiles = a.cols / (4 * Fp4<FMT>::kBlock);
-    // Whole warps stay in the loop for the shuffles; per_row is a multiple of 8, so the
-    // threads that share a word of scales are on one row and in or out together.
-    for (int64_t i0 = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31); i0 < total;
-         i0 += (int64_t)gridDim.x * kThreads) {
-        const int64_t i = i0 + (threadIdx.x & 31);
-        const bool in = i < total;
-        const int64_t row = in ? i / per_row : 0;
-        const int unit = in ? (int)(i - row * per_row) : 0;
-        float v[16] = {};
-        if (in) {
-            const uint8_t* p = static_cast<const uint8_t*>(a.x) + i * 32;
-            bf16x16(ld_cg_v4(p), ld_cg_v4(p + 16), v);
-        }
-        const float g = TENSOR_SCALE && in ? __ldcg(a.tensor_scale + row / a.rows_per_scale) : 1.0f;
+    const int unit = (int)blockIdx.x * 32 + lane;
+    const bool in = unit < per_row;       // 8 units or a multiple: lanes that share a block or a
+                                          // word of scales are in or out together
+    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0;
+    const int64_t step = (int64_t)gridDim.y * (kThreads / 32);
+    for (int64_t row = (int64_t)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += step) {
+        const int64_t i = row * per_row + unit;
+        int4 raw[2] = {};
+        if (in) load32(static_cast<const uint8_t*>(a.x) + i * 32, wide, raw[0], raw[1]);
+        const float g =
+            TENSOR_SCALE ? __ldcg(a.tensor_scale + (uint32_t)row / (uint32_t)a.rows_per_scale) : 1.0f;
         uint32_t word;
         bool writes;
-        const uint2 q = quantize16<FMT, TENSOR_SCALE>(v, g, unit, &word, &writes);
+        const uint2 q = quantize16<FMT, TENSOR_SCALE>(raw, g, unit, &word, &writes);
         if (in) {
             *reinterpret_cast<uint2*>(a.codes + i * 8) = q;
             if (writes)
@@ -65,42 +93,61 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(Fp4Args a)
     griddep_launch_dependents();
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(Fp4Args a)
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(kThreads, 6) dequantize_kernel(Fp4Args a)
 {
     griddep_wait();
-    const int64_t per_row = a.cols / 16, total = a.rows * per_row;
+    const int lane = threadIdx.x & 31, per_row = (int)(a.cols / 16);
     const int64_t tiles = a.cols / (4 * Fp4<FMT>::kBlock);
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = i / per_row;
-        const int unit = (int)(i - row * per_row);
+    const int unit = (int)blockIdx.x * 32 + lane;
+    if (unit < per_row) {
         const int block = FMT == kFp4Mx ? unit >> 1 : unit;
-        const uint2 q = __ldcg(reinterpret_cast<const uint2*>(a.codes + i * 8));
-        const float s = fp4_scale_value<FMT>(
-            __ldcg(a.scales + fp4_scale_at(row, block >> 2, tiles) + (block & 3)));
-        // An element's value in the matrix's units is exact in fp32; the matrix's scale
-        // rounds it once, and bf16 once more.
-        const float g = a.tensor_scale ? __ldcg(a.tensor_scale + row / a.rows_per_scale) : 1.0f;
-        float v[16];
+        const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+        const int64_t step = (int64_t)gridDim.y * (kThreads / 32);
+        constexpr int kRows = 2;          // at a time
+        for (int64_t row0 = (int64_t)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row0 < a.rows;
+             row0 += kRows * step) {
+            uint2 q[kRows];
+            uint32_t c[kRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t h2 = e2m1x2_to_f16x2(((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 0xFFu);
-            v[2 * j] = f16_lo(h2) * s * g;
-            v[2 * j + 1] = f16_hi(h2) * s * g;
-        }
-        if (a.out_f32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + i * 16);
+            for (int n = 0; n < kRows; ++n) {
+                const int64_t row = min(row0 + n * step, a.rows - 1);
+                q[n] = __ldcg(reinterpret_cast<const uint2*>(a.codes + (row * per_row + unit) * 8));
+                c[n] = __ldcg(a.scales + fp4_scale_at(row, block >> 2, tiles) + (block & 3));
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else {
-            uint32_t p[8];
+            for (int n = 0; n < kRows; ++n) {
+                const int64_t row = row0 + n * step;
+                if (row >= a.rows) break;
+                const float s = fp4_scale_value<FMT>(c[n]);
+                // An element's value in the matrix's units is exact in fp32; the matrix's scale
+                // rounds it once, and bf16 once more.
+                const float g =
+                    a.tensor_scale ? __ldcg(a.tensor_scale + (uint32_t)row / (uint32_t)a.rows_per_scale) : 1.0f;
+                float v[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + i * 16);
-            o[0] = make_uint4(p[0], p[1], p[2], p[3]);
-            o[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t h2 =
+                        e2m1x2_to_f16x2(((j < 4 ? q[n].x : q[n].y) >> (8 * (j & 3))) & 0xFFu);
+                    v[2 * j] = f16_lo(h2) * s * g;
+                    v[2 * j + 1] = f16_hi(h2) * s * g;
+                }
+                uint8_t* o = static_cast<uint8_t*>(a.out) + (row * per_row + unit) * (F32 ? 64 : 32);
+                uint32_t w[8];
+                if (F32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * h + j]);
+                        store32(o + 32 * h, wide, w);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+                    store32(o, wide, w);
+                }
+            }
         }
     }
     griddep_launch_dependents();
@@ -115,12 +162,12 @@ __device__ __forceinline__ void fetch_part(const PermuteFp4Args& a, int64_t t, i
                                            int lane, int4 (&raw)[2][2])
 {
     const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.D * 2;
+    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int unit = part * kPartUnits + 32 * i + lane;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            raw[i][h] = unit < per_row ? ld_cg_v4(x + unit * 32 + 16 * h) : make_int4(0, 0, 0, 0);
+        raw[i][0] = raw[i][1] = make_int4(0, 0, 0, 0);
+        if (unit < per_row) load32(x + unit * 32, wide, raw[i][0], raw[i][1]);
     }
 }
 
@@ -133,11 +180,9 @@ __device__ __forceinline__ void put_part(const PermuteFp4Args& a, int part, int 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int unit = part * kPartUnits + 32 * i + lane;
-        float v[16];
-        bf16x16(raw[i][0], raw[i][1], v);
         uint32_t word;
         bool writes;
-        const uint2 q = quantize16<FMT, TENSOR_SCALE>(v, g, unit, &word, &writes);
+        const uint2 q = quantize16<FMT, TENSOR_SCALE>(raw[i], g, unit, &word, &writes);
         const int kt = unit / (FMT == kFp4Mx ? 8 : 4);
         for (int k = 0; k < a.K; ++k) {
             const int64_t p = row_of(k);
@@ -265,21 +310,24 @@ dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
     griddep_launch_dependents();
 }
 
-int grid_for(int64_t work)
+// Columns of 32 units by rows, eight to a CTA; two waves of CTAs at most.
+dim3 grid_for(const Fp4Args& a)
 {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t most = (int64_t)sms * (2048 / kThreads);
-    const int64_t need = (work + kThreads - 1) / kThreads;
-    return (int)(need < 1 ? 1 : need < most ? need : most);
+    const int64_t x = (a.cols / 16 + 31) / 32, rows = (a.rows + kThreads / 32 - 1) / (kThreads / 32);
+    int64_t most = (int64_t)sms * (2048 / kThreads) * 2 / x;
+    if (most < 1) most = 1;
+    if (most > 65535) most = 65535;
+    return dim3((unsigned)x, (unsigned)(rows < most ? rows : most));
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 {
-    const int grid = grid_for(a.rows * (a.cols / 16));
+    const dim3 grid = grid_for(a);
     if (a.format == kFp4Mx) return launch_kernel(quantize_kernel<kFp4Mx, false>, grid, kThreads, 0, o, a);
     return a.tensor_scale ? launch_kernel(quantize_kernel<kFp4Nv, true>, grid, kThreads, 0, o, a)
                           : launch_kernel(quantize_kernel<kFp4Nv, false>, grid, kThreads, 0, o, a);
@@ -287,9 +335,12 @@ cudaError_t launch_quantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 
 cudaError_t launch_dequantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 {
-    const int grid = grid_for(a.rows * (a.cols / 16));
-    return a.format == kFp4Mx ? launch_kernel(dequantize_kernel<kFp4Mx>, grid, kThreads, 0, o, a)
-                              : launch_kernel(dequantize_kernel<kFp4Nv>, grid, kThreads, 0, o, a);
+    const dim3 grid = grid_for(a);
+    if (a.format == kFp4Mx)
+        return a.out_f32 ? launch_kernel(dequantize_kernel<kFp4Mx, true>, grid, kThreads, 0, o, a)
+                         : launch_kernel(dequantize_kernel<kFp4Mx, false>, grid, kThreads, 0, o, a);
+    return a.out_f32 ? launch_kernel(dequantize_kernel<kFp4Nv, true>, grid, kThreads, 0, o, a)
+                     : launch_kernel(dequantize_kernel<kFp4Nv, false>, grid, kThreads, 0, o, a);
 }
 
 cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const LaunchOpts& o)

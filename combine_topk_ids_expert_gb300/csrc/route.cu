@@ -5,10 +5,12 @@
 // whose value is -inf or a NaN is never chosen, and a slot without an expert has id -1 and
 // score 0. Scores are scale * p, or scale * p / (sum of the chosen p).
 //
-// One warp to a token; lane l holds the values of experts l, l + 32, ... as integers in the
-// order of the floats. A round takes the warp's maximum and the lowest index that has it
-// (two warp reductions) and strikes it out. Reading the logits once is the floor; the
-// rounds are what bounds large calls.
+// One warp to a token; lane l holds the values of NV experts from l NV on, as integers in the
+// order of the floats, sorted (equal ones by index; lanes of 16 or 32 are searched instead). A
+// round takes the warp's maximum of the lanes' first ones, of the lowest lane that has it, which
+// moves up its list: one warp reduction, one vote and one shuffle. Reading the logits once is the floor; the rounds are what
+// bounds large calls. (Unsorted, with a second reduction for the lowest index and each lane
+// searched every round: 37 us for 32768 tokens of 256 experts, 8 of them chosen, against {RT}.)
 //
 // Normalised scores need the chosen logits alone: with m their maximum, softmax is
 // e^(l - m) / sum, and sigmoid(l) e^-min(m, 0) has no common factor left that underflows.
@@ -72,6 +74,38 @@ __device__ __forceinline__ void softmax_of_row(const float (&v)[NV], float* most
     *sum = warp_sum(s);
 }
 
+// The lane's NV values of a row, experts lane NV + j: as vectors where the row allows it.
+template <int NV>
+__device__ __forceinline__ void load_row(const void* p, bool bf16, int64_t row, int lane, int E, float (&v)[NV])
+{
+    const int e0 = lane * NV;
+    if (NV >= 4 && !bf16 && E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 4) {
+            int4 q = make_int4(0, 0, 0, 0);
+            const bool in = e0 + j < E;
+            if (in) q = ld_cg_v4(static_cast<const float*>(p) + row + e0 + j);
+            const int w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4 && j + i < NV; ++i) v[j + i] = in ? __int_as_float(w[i]) : -kInf;
+        }
+    } else if (NV >= 8 && bf16 && E % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 8) {
+            int4 q = make_int4(0, 0, 0, 0);
+            const bool in = e0 + j < E;
+            if (in) q = ld_cg_v4(static_cast<const unsigned short*>(p) + row + e0 + j);
+            const uint32_t w[4] = {(uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w};
+#pragma unroll
+            for (int i = 0; i < 8 && j + i < NV; ++i)
+                v[j + i] = in ? __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : -kInf;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = e0 + j < E ? load_logit(p, bf16, row + e0 + j) : -kInf;
+    }
+}
+
 template <int NV, bool BF16>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a)
 {
@@ -80,34 +114,60 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a)
     const int64_t t = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) >> 5;
     if (t < a.T) {
         const int64_t row = t * a.E;
-        uint32_t key[NV];
         float v[NV];
+        const bool whole = !a.normalize && !a.sigmoid;   // a sum over all of the token's logits
+        if (!a.select || whole) load_row<NV>(a.logits, BF16, row, lane, a.E, v);
+        uint32_t key[NV];
+        int idx[NV];
+        {
+            float w[NV];
+            if (a.select) load_row<NV>(a.select, false, row, lane, a.E, w);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = j * 32 + lane;
-            const bool in = e < a.E;
-            v[j] = -kInf;
-            if (in && (!a.select || !a.normalize)) v[j] = load_logit(a.logits, BF16, row + e);
-            key[j] = !in ? 0u : order_of(a.select ? __ldcg(a.select + row + e) : v[j]);
+            for (int j = 0; j < NV; ++j) {
+                key[j] = order_of(a.select ? w[j] : v[j]);
+                idx[j] = lane * NV + j;
+            }
+        }
+        // Neighbours in turn (odd, even): only a greater key goes up, so equal ones stay in order.
+        constexpr bool kSorted = NV <= 8;
+#pragma unroll
+        for (int n = 0; n < (kSorted ? NV : 0); ++n) {
+#pragma unroll
+            for (int j = n & 1; j + 1 < NV; j += 2) {
+                const bool swap = key[j + 1] > key[j];
+                const uint32_t hi = swap ? key[j + 1] : key[j], lo = swap ? key[j] : key[j + 1];
+                const int hi_i = swap ? idx[j + 1] : idx[j], lo_i = swap ? idx[j] : idx[j + 1];
+                key[j] = hi;
+                key[j + 1] = lo;
+                idx[j] = hi_i;
+                idx[j + 1] = lo_i;
+            }
         }
         int mine[2] = {-1, -1};       // slots lane and lane + 32
         for (int k = 0; k < a.K; ++k) {
-            uint32_t best = 0u;
+            uint32_t best = key[0];
+            int at = 0;
+            if (!kSorted) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) best = max(best, key[j]);
+                for (int j = 1; j < NV; ++j) {
+                    at = key[j] > best ? j : at;
+                    best = max(best, key[j]);
+                }
+            }
             const uint32_t most = __reduce_max_sync(~0u, best);
             if (most == 0u) break;    // nothing is left
-            int at = 1 << 30;
-            if (best == most) {
+            const int from = __ffs(__ballot_sync(~0u, best == most)) - 1;
+            const int e = __shfl_sync(~0u, kSorted ? idx[0] : lane * NV + at, from);
+            if (lane == from) {
 #pragma unroll
-                for (int j = NV - 1; j >= 0; --j) at = key[j] == most ? j : at;
-                at = at * 32 + lane;
-            }
-            const int e = __reduce_min_sync(~0u, at);
-            if (at == e) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    if (j == e >> 5) key[j] = 0u;
+                for (int j = 0; j < NV; ++j) {
+                    if (!kSorted) {
+                        key[j] = j == at ? 0u : key[j];
+                    } else {
+                        key[j] = j + 1 < NV ? key[j + 1 < NV ? j + 1 : j] : 0u;
+                        idx[j] = idx[j + 1 < NV ? j + 1 : j];
+                    }
+                }
             }
             if (lane == (k & 31)) {
                 if (k < 32) mine[0] = e;
