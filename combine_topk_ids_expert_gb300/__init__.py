@@ -76,16 +76,19 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+_lib = _abi.lib
+
 # The current stream's handle without a Stream object around it: 0.2 against 3 us, of
 # calls that take about 10.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         if _raw_stream is None:
             return torch.cuda.current_stream().cuda_stream
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -111,16 +114,18 @@ def _empty_on(device: torch.device, shape: tuple, dtype: torch.dtype, stream,
     return t
 
 
-def _on_device_of(first: torch.Tensor, **others: torch.Tensor | None):
+_HERE = contextlib.nullcontext()
+
+
+def _on_device_of(first: torch.Tensor, *others: torch.Tensor | None):
     """A context in which `first`'s device is the current one, checked to be the others' too."""
-    if not first.is_cuda:
+    dev = first.get_device()      # -1 on the host
+    if dev < 0:
         raise ValueError("expected a CUDA tensor")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    if first.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(first.device)
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected all tensors on {first.device}, got one on {t.device}")
+    return _HERE if dev == _current_device() else torch.cuda.device(first.device)
 
 
 def _check_dtype(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
@@ -400,7 +405,7 @@ def route(logits_TE: torch.Tensor, topk: int, score: str = "softmax", normalize:
         _check_dtype(select, torch.float32, "select")
         if select.shape != logits_TE.shape:
             raise ValueError(f"select must be shaped as logits, got {tuple(select.shape)}")
-    with _on_device_of(logits_TE, select=select):
+    with _on_device_of(logits_TE, select):
         ids = _empty_on(logits_TE.device, (T, topk), torch.int32, stream)
         scores = _empty_on(logits_TE.device, (T, topk), torch.float32, stream)
         ep_route(logits_TE, select, topk, kind, normalize, scale, ids, scores, stream)
@@ -419,7 +424,7 @@ def route_backward(grad_scores_TK: torch.Tensor, logits_TE: torch.Tensor,
     if ids.dim() != 2 or ids.shape[0] != logits_TE.shape[0] or grad_scores_TK.shape != ids.shape:
         raise ValueError(f"ids and grad_scores must be [{logits_TE.shape[0]}, topk], got "
                          f"{tuple(ids.shape)} and {tuple(grad_scores_TK.shape)}")
-    with _on_device_of(logits_TE, topk_expert_ids_TK=ids, grad_scores_TK=grad_scores_TK):
+    with _on_device_of(logits_TE, ids, grad_scores_TK):
         grad = _empty_on(logits_TE.device, tuple(logits_TE.shape), logits_TE.dtype, stream)
         ep_route_backward(grad_scores_TK, logits_TE, ids, kind, normalize, scale, grad, stream)
     return grad
@@ -485,6 +490,15 @@ class FP4:
                                  f"{tuple(g.shape)}")
         object.__setattr__(self, "_checked", self._form())
 
+    @classmethod
+    def _of(cls, codes: torch.Tensor, scales: torch.Tensor, format: str, rows: int, cols: int) -> FP4:
+        """Of tensors that the package has just made: nothing to check."""
+        q = object.__new__(cls)
+        q.__dict__.update(codes=codes, scales=scales, format=format, tensor_scale=None, rows=rows,
+                          cols=cols)
+        q.__dict__["_checked"] = q._form()
+        return q
+
     def _form(self) -> tuple:
         c, s, g = self.codes, self.scales, self.tensor_scale
         return c.shape, c.dtype, s.shape, s.dtype, None if g is None else (g.shape, g.dtype)
@@ -511,8 +525,8 @@ class FP4:
             raise ValueError("the tensors of this FP4 changed their shapes or types since it was "
                              "made: make another one of them")
         g = self.tensor_scale
-        if self.scales.device != self.codes.device or \
-                (g is not None and g.device != self.codes.device):
+        dev = self.codes.get_device()
+        if self.scales.get_device() != dev or (g is not None and g.get_device() != dev):
             raise ValueError("the tensors of this FP4 are on several devices")
         return EpFp4(_ptr(self.codes), _ptr(self.scales), _ptr(g), _FP4_FORMATS[self.format])
 
@@ -521,8 +535,11 @@ class FP4:
         if dtype not in _TORCH_TO_EP:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
         with _on_device_of(self.codes):
-            out = _empty_on(self.codes.device, (*self.codes.shape[:-1], self.cols), dtype, stream)
-            ep_dequantize_fp4(self, out, stream)
+            lead = self.codes.shape[:-1]
+            out = _empty_on(self.codes.device, (*lead, self.cols), dtype, stream)
+            check(_lib().ep_dequantize_fp4(C.byref(self._struct()), self.rows, self.cols,
+                                           max(1, lead[-1]), _ptr(out), _TORCH_TO_EP[dtype],
+                                           _stream(stream)), "ep_dequantize_fp4")
         return out
 
 
@@ -556,13 +573,18 @@ def quantize_fp4(x: torch.Tensor, format: str = "nv", tensor_scale: torch.Tensor
     if x.dim() < 2 or not x.shape[-1] or x.shape[-1] % 128:
         raise ValueError(f"x must be [..., rows, cols] with cols a multiple of 128, got "
                          f"{tuple(x.shape)}")
-    with _on_device_of(x, tensor_scale=tensor_scale):
+    with _on_device_of(x, tensor_scale):
         cols = x.shape[-1]
-        codes = _empty_on(x.device, (*x.shape[:-1], cols // 2), torch.uint8, stream)
-        scales = _empty_on(x.device, _fp4_tiles(x.numel() // cols, cols, format), torch.uint8,
-                           stream)
-        q = FP4(codes, scales, format, tensor_scale)
-        ep_quantize_fp4(x, q, stream)
+        lead = x.shape[:-1]
+        rows = x.numel() // cols
+        codes = _empty_on(x.device, (*lead, cols // 2), torch.uint8, stream)
+        scales = _empty_on(x.device, _fp4_tiles(rows, cols, format), torch.uint8, stream)
+        if tensor_scale is None:
+            q = FP4._of(codes, scales, format, rows, cols)
+        else:
+            q = FP4(codes, scales, format, tensor_scale)
+        check(_lib().ep_quantize_fp4(_ptr(x), rows, cols, max(1, lead[-1]), C.byref(q._struct()),
+                                     _stream(stream)), "ep_quantize_fp4")
     return q
 
 
@@ -825,15 +847,21 @@ class Buffer:
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             self.handle = ep_buffer_init(self.cfg, self.workspace)
         self._base = self.workspace.data_ptr()
+        self._typed: dict = {}
+        self._layer_bytes: dict = {}
 
     # -- views -------------------------------------------------------------
     def _view(self, ptr: int, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
-        n = 1
-        for s in shape:
+        # One operation on the workspace as elements of this type: a result is nine of these.
+        base = self._typed.get(dtype)
+        if base is None:
+            base = self._typed[dtype] = self.workspace.view(dtype)
+        strides, n = [], 1
+        for s in reversed(shape):
+            strides.append(n)
             n *= s
-        esize = torch.empty((), dtype=dtype).element_size()
-        off = ptr - self._base
-        return self.workspace[off:off + n * esize].view(dtype).view(*shape)
+        return base.as_strided(shape, strides[::-1],
+                               base.storage_offset() + (ptr - self._base) // base.element_size())
 
     def _layout(self, L: EpLayout) -> Layout:
         T, E, R, K = L.num_tokens, self.E, self.R, self.K
@@ -1168,6 +1196,10 @@ class Buffer:
 
     def _fp4_rows(self, rows: int, cols: int, format: str, tensor_scale, stream,
                   kept: bool = True) -> FP4:
+        if tensor_scale is None:
+            return FP4._of(self._empty((rows, cols // 2), torch.uint8, stream, kept),
+                           self._empty(_fp4_tiles(rows, cols, format), torch.uint8, stream, kept),
+                           format, rows, cols)
         return FP4(self._empty((rows, cols // 2), torch.uint8, stream, kept),
                    self._empty(_fp4_tiles(rows, cols, format), torch.uint8, stream, kept), format,
                    tensor_scale)
@@ -1272,7 +1304,9 @@ class Buffer:
             out = self._empty((T, self.D), torch.bfloat16 if out_dtype is None else out_dtype, stream)
         elif out.shape != (T, self.D):
             raise ValueError(f"out must be {[T, self.D]}, got {list(out.shape)}")
-        nbytes = ep_moe_layer_workspace_bytes(self.handle, T, dff)
+        nbytes = self._layer_bytes.get((T, dff))
+        if nbytes is None:
+            nbytes = self._layer_bytes[T, dff] = ep_moe_layer_workspace_bytes(self.handle, T, dff)
         if nbytes == 0:
             raise EpError(_abi.EP_ERR_CAPACITY if T > 64 or T * self.K > 512
                           else _abi.EP_ERR_INVALID_ARG, "ep_moe_layer")
