@@ -311,6 +311,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = cluster_size(), rank = cluster_rank();
     const int pairs = a.T * a.K;
+    const int all_stages = (a.din + C::kStageK - 1) / C::kStageK;
+    const int k_first = rank * all_stages / split, k_last = (rank + 1) * all_stages / split;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -349,11 +351,57 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                                     ring_s + (uint32_t)w * (2 * C::kScales) + C::kScales, 0, lane, 0, 0,
                                     0, 0, 0, 0, 0, 0, 0);
         }
-        if (!DOWN) {
+        if constexpr (FMT == kFp4Nv && !DOWN) {
+            // The rows' largest magnitudes over this CTA's part of K.
+            const int c0 = k_first * C::kStageK, c1 = min(k_last * C::kStageK, a.din);
+            for (int t = w; t < a.T; t += kRowWarps) {
+                uint32_t m = 0u;
+#pragma unroll 8
+                for (int i = c0 + lane * 8; i < c1; i += 256) {
+                    const int4 v = ld_cg_v4(static_cast<const uint16_t*>(a.rows) + (int64_t)t * a.din + i);
+                    const uint32_t q[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        m = max(m, max((q[n] << 16) & 0x7FFFFFFFu, q[n] & 0x7FFF0000u));
+                }
+                m = __reduce_max_sync(~0u, m);
+                if (lane == 0) s_exp[t] = (int16_t)digit_exponent(m);
+            }
+        } else if (!DOWN) {
             const int64_t bytes = (int64_t)a.T * a.din * 2;
             for (int64_t i = ((int64_t)blockIdx.x * kRowWarps * 32 + w * 32 + lane) * 128; i < bytes;
                  i += (int64_t)gridDim.x * kRowWarps * 32 * 128)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(a.rows) + i));
+        }
+    } else if (pairs <= 32) {
+        // ---- routing: the pairs by expert, in chunks; few of them in one warp ---------
+        if (warp == 0) {
+            const int raw = lane < pairs ? __ldcg(a.ids + lane) : -1;
+            const int e = valid_id(raw, a.E);
+            const float score = DOWN && lane < pairs ? __ldcg(a.scores + lane) : 0.0f;
+            if (!DOWN && e != raw && blockIdx.x == 0) atomicOr(a.err, kErrBadId);
+            const unsigned same = __match_any_sync(~0u, e);
+            // An expert's first pair counts its rows and chunks.
+            const bool leads = e >= 0 && lane == __ffs(same) - 1;
+            const int count = leads ? __popc(same) : 0;
+            const int packed = count | ((count + kChunkRows - 1) / kChunkRows) << 16;
+            int v = packed;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int n = __shfl_up_sync(~0u, v, d);
+                if (lane >= d) v += n;
+            }
+            const int row = (v - packed) & 0xFFFF, chunk = (v - packed) >> 16;
+            for (int n = 0; n * kChunkRows < count; ++n)
+                s_chunk[chunk + n] = {(uint16_t)e, (uint16_t)(row + n * kChunkRows),
+                                      (uint16_t)min(count - n * kChunkRows, kChunkRows), 0};
+            const int first_row = __shfl_sync(~0u, row, __ffs(same) - 1);
+            if (e >= 0) s_list[first_row + __popc(same & lanemask_lt(lane))] = (uint16_t)lane;
+            if (lane < pairs) {
+                s_ok[lane] = e >= 0;
+                if (DOWN) s_score[lane] = score;
+            }
+            if (lane == 31) *s_chunks = v >> 16;
         }
     } else {
         // ---- routing: the pairs by expert, in chunks --------------------------------
@@ -430,9 +478,6 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
     const int chunks = *s_chunks, units = chunks * a.tiles;
     const int u_first = (int)((int64_t)units * cluster_index() / cluster_count());
     const int u_last = (int)((int64_t)units * (cluster_index() + 1) / cluster_count());
-    const int all_stages = (a.din + C::kStageK - 1) / C::kStageK;
-    const int k_first = rank * all_stages / split, k_last = (rank + 1) * all_stages / split;
-
     const int64_t thread0 = (int64_t)blockIdx.x * kLayerThreads + threadIdx.x;
     const int64_t threads = (int64_t)gridDim.x * kLayerThreads;
     if (!DOWN) {
@@ -687,35 +732,6 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         // ---- token rows --------------------------------------------------------------
         const int w = warp - kRowWarp0;
         if (DOWN) griddep_wait();                      // h
-        if constexpr (FMT == kFp4Nv) {
-            // The rows' largest magnitudes over this CTA's part of K.
-            if (DOWN) {
-                const int words = a.din / 32;
-                for (int p = w; p < pairs; p += kRowWarps) {
-                    uint32_t m = 0u;
-                    if (valid_id(__ldcg(a.ids + p), a.E) >= 0)
-                        for (int i = lane; i < words; i += 32) m = max(m, __ldcg(a.h_most + (int64_t)p * words + i));
-                    m = __reduce_max_sync(~0u, m);
-                    if (lane == 0) s_exp[p] = (int16_t)digit_exponent(m);
-                }
-            } else {
-                const int c0 = k_first * C::kStageK, c1 = min(k_last * C::kStageK, a.din);
-                for (int t = w; t < a.T; t += kRowWarps) {
-                    uint32_t m = 0u;
-#pragma unroll 8
-                    for (int i = c0 + lane * 8; i < c1; i += 256) {
-                        const int4 v = ld_cg_v4(static_cast<const uint16_t*>(a.rows) + (int64_t)t * a.din + i);
-                        const uint32_t q[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            m = max(m, max((q[n] << 16) & 0x7FFFFFFFu, q[n] & 0x7FFF0000u));
-                    }
-                    m = __reduce_max_sync(~0u, m);
-                    if (lane == 0) s_exp[t] = (int16_t)digit_exponent(m);
-                }
-            }
-            asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps) : "memory");
-        }
         // Every kRowWarps-th stage is this warp's, a row (bf16: four rows) at a time; the next
         // ones, also of its next stage, are on their way meanwhile. One copy of the code: it is
         // long, and comes from memory in every call.
@@ -752,6 +768,20 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) fetch(next[i]);
         if (!DOWN) asm volatile("bar.arrive 3, %0;" ::"n"(32 * (1 + kRowWarps)) : "memory");
+        if constexpr (FMT == kFp4Nv && DOWN) {
+            // The rows' largest magnitudes, from those that the first kernel left of 32 columns.
+            const int words = a.din / 32;
+            for (int p = w; p < pairs; p += kRowWarps) {
+                uint32_t m = 0u;
+                if (s_ok[p]) {
+#pragma unroll 4
+                    for (int i = lane; i < words; i += 32) m = max(m, __ldcg(a.h_most + (int64_t)p * words + i));
+                }
+                m = __reduce_max_sync(~0u, m);
+                if (lane == 0) s_exp[p] = (int16_t)digit_exponent(m);
+            }
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps) : "memory");
+        }
         for (int g = w; g < stages && !*s_abort; g += kRowWarps) {
             const int s = g % STAGES;
             const Chunk c = s_chunk[(u_first + g / n_k) % chunks];
