@@ -195,15 +195,18 @@ __device__ __forceinline__ void bf16x16(const int4& a, const int4& b, float (&v)
     }
 }
 
-// Largest magnitude of 16 bf16, as they lie: as integers, in which NaN is above infinity.
+// Largest magnitude of 8 or 16 bf16, as they lie: as integers, in which NaN is above infinity.
+__device__ __forceinline__ float amax8(const int4& a)
+{
+    const uint32_t m =
+        __vmaxu2(__vmaxu2((uint32_t)a.x & 0x7FFF7FFFu, (uint32_t)a.y & 0x7FFF7FFFu),
+                 __vmaxu2((uint32_t)a.z & 0x7FFF7FFFu, (uint32_t)a.w & 0x7FFF7FFFu));
+    return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ float amax16(const int4& a, const int4& b)
 {
-    const uint32_t q[8] = {(uint32_t)a.x, (uint32_t)a.y, (uint32_t)a.z, (uint32_t)a.w,
-                           (uint32_t)b.x, (uint32_t)b.y, (uint32_t)b.z, (uint32_t)b.w};
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, q[i] & 0x7FFF7FFFu);
-    return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
+    return __uint_as_float(max(__float_as_uint(amax8(a)), __float_as_uint(amax8(b))));
 }
 
 // The same of 16 fp32.

@@ -356,13 +356,18 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             const int c0 = k_first * C::kStageK, c1 = min(k_last * C::kStageK, a.din);
             for (int t = w; t < a.T; t += kRowWarps) {
                 uint32_t m = 0u;
-#pragma unroll 8
-                for (int i = c0 + lane * 8; i < c1; i += 256) {
-                    const int4 v = ld_cg_v4(static_cast<const uint16_t*>(a.rows) + (int64_t)t * a.din + i);
-                    const uint32_t q[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+                for (int i0 = c0; i0 < c1; i0 += 8 * 256) {   // eight loads on their way
+                    int4 v[8];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        m = max(m, max((q[n] << 16) & 0x7FFFFFFFu, q[n] & 0x7FFF0000u));
+                    for (int n = 0; n < 8; ++n) {
+                        const int i = i0 + n * 256 + lane * 8;
+                        v[n] = make_int4(0, 0, 0, 0);
+                        if (i < c1)
+                            v[n] = ld_cg_v4(static_cast<const uint16_t*>(a.rows) + (int64_t)t * a.din + i);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+                        m = max(m, __float_as_uint(amax8(v[n])));
                 }
                 m = __reduce_max_sync(~0u, m);
                 if (lane == 0) s_exp[t] = (int16_t)digit_exponent(m);
@@ -732,53 +737,57 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         // ---- token rows --------------------------------------------------------------
         const int w = warp - kRowWarp0;
         if (DOWN) griddep_wait();                      // h
-        // Every kRowWarps-th stage is this warp's, a row (bf16: four rows) at a time; the next
-        // ones, also of its next stage, are on their way meanwhile. One copy of the code: it is
-        // long, and comes from memory in every call.
+        // Every kRowWarps-th stage is this warp's, four rows (bf16: four times four) at a time. A
+        // stage's later rows are fetched before its earlier ones are taken apart; its first ones
+        // only after the arrival for the stage before: the fence and the arrival wait for the loads
+        // that are out, and behind a ring's worth of weights a load takes microseconds.
         constexpr int kPerLoad = C::FP4 ? 1 : 4;       // rows that the warp covers at once
-        constexpr int kAhead = 3;
+        constexpr int kAhead = 4;
         const int lane_row = C::FP4 ? 0 : lane >> 3, lane_col = (C::FP4 ? lane : lane & 7) * 8;
         const int n_k = k_last - k_first;
         const int stages = (u_last - u_first) * n_k;
-        // The place that is fetched for: stage pg of this CTA, row pr.
-        int pg = w, pr = 0, p_rows = 0, p_start = 0, p_col = 0;
-        auto enter = [&] {
-            if (pg >= stages) return;
-            const int i = pg / n_k;
+        auto fetch = [&](Eight<DOWN> (&into)[kAhead], int g, int r0) {
+            const int i = g / n_k;
             const Chunk c = s_chunk[(u_first + i) % chunks];
-            p_rows = c.rows;
-            p_start = c.start;
-            p_col = (k_first + pg - i * n_k) * C::kStageK + lane_col;
-        };
-        auto fetch = [&](Eight<DOWN>& into) {
-            if (pg >= stages) return;
-            const int r = pr + lane_row;
-            const bool in = r < p_rows && p_col < a.din;
-            const int pair = s_list[p_start + (in ? r : 0)];
-            into.load(a.rows, (int64_t)(DOWN ? pair : pair / a.K) * a.din + p_col, in);
-            pr += kPerLoad;
-            if (pr >= p_rows) {
-                pr = 0;
-                pg += kRowWarps;
-                enter();
+            const int col = (k_first + g - i * n_k) * C::kStageK + lane_col;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int r = r0 + j * kPerLoad + lane_row;
+                if (r0 + j * kPerLoad >= c.rows) break;
+                const bool in = r < c.rows && col < a.din;
+                const int pair = s_list[c.start + (in ? r : 0)];
+                into[j].load(a.rows, (int64_t)(DOWN ? pair : pair / a.K) * a.din + col, in);
             }
         };
-        Eight<DOWN> next[kAhead];
-        enter();
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(next[i]);
+        Eight<DOWN> cur[kAhead], later[kAhead];
+        if (w < stages) fetch(cur, w, 0);
         if (!DOWN) asm volatile("bar.arrive 3, %0;" ::"n"(32 * (1 + kRowWarps)) : "memory");
         if constexpr (FMT == kFp4Nv && DOWN) {
             // The rows' largest magnitudes, from those that the first kernel left of 32 columns.
             const int words = a.din / 32;
-            for (int p = w; p < pairs; p += kRowWarps) {
-                uint32_t m = 0u;
-                if (s_ok[p]) {
-#pragma unroll 4
-                    for (int i = lane; i < words; i += 32) m = max(m, __ldcg(a.h_most + (int64_t)p * words + i));
+            for (int p0 = w * 8; p0 < pairs; p0 += kRowWarps * 8) {
+                uint32_t m[8] = {};
+                for (int i0 = lane; i0 < words; i0 += 64) {   // sixteen loads on their way
+                    uint32_t v[8][2];
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int i = i0 + 32 * h;
+                            v[n][h] = 0u;
+                            if (p0 + n < pairs && i < words)
+                                v[n][h] = __float_as_uint(ld_cg_f32(reinterpret_cast<const float*>(a.h_most) +
+                                                                    (int64_t)(p0 + n) * words + i));
+                        }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) m[n] = max(m[n], max(v[n][0], v[n][1]));
                 }
-                m = __reduce_max_sync(~0u, m);
-                if (lane == 0) s_exp[p] = (int16_t)digit_exponent(m);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const uint32_t most = __reduce_max_sync(~0u, m[n]);
+                    // A pair without an expert has none, and what is there is not used.
+                    if (lane == 0 && p0 + n < pairs) s_exp[p0 + n] = (int16_t)digit_exponent(most & 0x7FFFFFFFu);
+                }
             }
             asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps) : "memory");
         }
@@ -788,48 +797,55 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             const uint32_t sb = ring_b + (uint32_t)s * C::kBytesB;
             if (!warp_all(wait_or_abort(empty0 + 8u * s, (uint32_t)(((g / STAGES) & 1) ^ 1), s_abort))) break;
 #pragma unroll 1
-            for (int r0 = 0; r0 < c.rows; r0 += kPerLoad) {
-                const Eight<DOWN> now = next[0];
+            for (int r0 = 0; r0 < c.rows; r0 += kAhead * kPerLoad) {
+                const bool more = r0 + kAhead * kPerLoad < c.rows;
+                if (more) fetch(later, g, r0 + kAhead * kPerLoad);
 #pragma unroll
-                for (int i = 0; i + 1 < kAhead; ++i) next[i] = next[i + 1];
-                fetch(next[kAhead - 1]);
-                const int r = r0 + lane_row;
-                if constexpr (C::FP4) {
-                    int row_exp = 0;
-                    if (FMT == kFp4Nv) {
-                        const int pair = s_list[c.start + r];
-                        row_exp = s_exp[DOWN ? pair : pair / a.K];
-                    }
-                    const int4 q0 = now.q[0], q1 = now.q[DOWN ? 1 : 0];
-                    store_digits<FMT, DOWN>(sb, ring_s + (uint32_t)s * (2 * C::kScales) + C::kScales,
-                                            r * C::kTerms, lane, row_exp, q0.x, q0.y, q0.z, q0.w, q1.x,
-                                            q1.y, q1.z, q1.w);
-                } else if (r < c.rows) {
-                    const uint32_t unit = (uint32_t)(lane & 7);
-                    auto put = [&](int n, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-                        sts128(sb + (uint32_t)(n * 128) + ((unit ^ (uint32_t)(n & 7)) << 4), w0, w1, w2, w3);
-                    };
-                    if constexpr (DOWN) {
-                        float v[8];
-                        now.floats(v);
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            hi[i] = pack_bf16x2_rn(v[2 * i], v[2 * i + 1]);
-                            lo[i] = pack_bf16x2_rn(left_of(v[2 * i], hi[i] << 16),
-                                                   left_of(v[2 * i + 1], hi[i] & 0xFFFF0000u));
+                for (int j = 0; j < kAhead; ++j) {
+                    const int r = r0 + j * kPerLoad + lane_row;
+                    if (r0 + j * kPerLoad >= c.rows) break;
+                    if constexpr (C::FP4) {
+                        int row_exp = 0;
+                        if (FMT == kFp4Nv) {
+                            const int pair = s_list[c.start + r];
+                            row_exp = s_exp[DOWN ? pair : pair / a.K];
                         }
-                        put(2 * r, hi[0], hi[1], hi[2], hi[3]);
-                        put(2 * r + 1, lo[0], lo[1], lo[2], lo[3]);
-                    } else {
-                        const int4 q = now.q[0];
-                        put(r, (uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w);
+                        const int4 q0 = cur[j].q[0], q1 = cur[j].q[DOWN ? 1 : 0];
+                        store_digits<FMT, DOWN>(sb, ring_s + (uint32_t)s * (2 * C::kScales) + C::kScales,
+                                                r * C::kTerms, lane, row_exp, q0.x, q0.y, q0.z, q0.w, q1.x,
+                                                q1.y, q1.z, q1.w);
+                    } else if (r < c.rows) {
+                        const uint32_t unit = (uint32_t)(lane & 7);
+                        auto put = [&](int n, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+                            sts128(sb + (uint32_t)(n * 128) + ((unit ^ (uint32_t)(n & 7)) << 4), w0, w1, w2, w3);
+                        };
+                        if constexpr (DOWN) {
+                            float v[8];
+                            cur[j].floats(v);
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                hi[i] = pack_bf16x2_rn(v[2 * i], v[2 * i + 1]);
+                                lo[i] = pack_bf16x2_rn(left_of(v[2 * i], hi[i] << 16),
+                                                       left_of(v[2 * i + 1], hi[i] & 0xFFFF0000u));
+                            }
+                            put(2 * r, hi[0], hi[1], hi[2], hi[3]);
+                            put(2 * r + 1, lo[0], lo[1], lo[2], lo[3]);
+                        } else {
+                            const int4 q = cur[j].q[0];
+                            put(r, (uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w);
+                        }
                     }
+                }
+                if (more) {
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) cur[j] = later[j];
                 }
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(full0 + 8u * s);
+            if (g + kRowWarps < stages) fetch(cur, g + kRowWarps, 0);
         }
     }
 
