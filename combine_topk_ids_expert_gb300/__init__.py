@@ -1167,6 +1167,10 @@ class Buffer:
                                self._new_rows(w_down.din, stream, kept=False), stream)
         return self.expert_gemv_w4(h, w_down, y_recv, stream)
 
+    def _here(self, *tensors: torch.Tensor | None):
+        """A context in which the buffer's device is the current one, with `tensors` on it."""
+        return _on_device_of(self.workspace, *tensors)
+
     # -- the same block in 4-bit floating point ----------------------------------
     def dispatch_fp4(self, x_TD: torch.Tensor, topk_scores_TK: torch.Tensor,
                      topk_expert_ids_TK: torch.Tensor, num_tokens_per_rank: int | None = None,
@@ -1185,9 +1189,14 @@ class Buffer:
         if self.D % 128:
             raise ValueError(f"4-bit rows need a hidden size that is a multiple of 128, got {self.D}")
         N = T if num_tokens_per_rank is None else num_tokens_per_rank
-        rows = self.R * ep_pad_tokens(N) * self.K
-        q = self._fp4_rows(rows, self.D, format, tensor_scale, stream)
-        d = ep_dispatch_fp4(self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, N, q, stream)
+        if not T <= N <= self.cfg.num_max_tokens_per_rank:
+            raise EpError(_abi.EP_ERR_CAPACITY if N >= T else _abi.EP_ERR_INVALID_ARG,
+                          "ep_dispatch_fp4")
+        with self._here(x_TD, topk_scores_TK, topk_expert_ids_TK, tensor_scale):
+            q = self._fp4_rows(self.R * ep_pad_tokens(N) * self.K, self.D, format, tensor_scale,
+                               stream)
+            d = ep_dispatch_fp4(self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, N, q,
+                                stream)
         S = d.layout.rank_stride
         lead = (self.R * S,) if self.packed else (self.R, S)
         return DispatchResult(recv_x=q, recv_scores=self._view(d.recv_scores, torch.float32, lead),
@@ -1207,21 +1216,20 @@ class Buffer:
     def _rows_fp4(self, x: FP4, name: str, width: int) -> FP4:
         """x, checked to be rows of the last call's receive layout, `width` columns wide."""
         n = self.R * self._last_stride()
-        if not isinstance(x, FP4):
-            raise TypeError(f"{name} must be an FP4, got {type(x).__name__}")
         if x.cols != width or x.rows != n or (x.tensor_scale is not None
                                               and x.tensor_scale.numel() != 1):
             raise ValueError(f"{name} must hold the receive layout's {n} rows of {width} columns "
                              f"(with one tensor_scale), got {x.rows} of {x.cols}")
         return x
 
-    def _weights_fp4(self, w: FP4, name: str, rows: int | None, format: str) -> int:
-        """Rows of each expert's w, checked to be [E, rows, any] in `format`."""
-        if not isinstance(w, FP4):
-            raise TypeError(f"{name} must be an FP4, got {type(w).__name__}")
-        n, _ = self._weights(w.codes, name + ".codes", rows, None)
-        if w.format != format:
-            raise ValueError(f"{name} is {w.format}, the rows are {format}")
+    def _weights_fp4(self, w: FP4, name: str, x_recv: FP4) -> int:
+        """Rows of each expert's w, checked to be [E, rows, any] in the rows' format."""
+        for n, q in ((name, w), ("x_recv", x_recv)):
+            if not isinstance(q, FP4):
+                raise TypeError(f"{n} must be an FP4, got {type(q).__name__}")
+        n, _ = self._weights(w.codes, name + ".codes", None, None)
+        if w.format != x_recv.format:
+            raise ValueError(f"{name} is {w.format}, the rows are {x_recv.format}")
         if n % 128:
             raise ValueError(f"{name} must hold a multiple of 128 rows for each expert, got {n}")
         return n
@@ -1230,10 +1238,11 @@ class Buffer:
                         stream=None) -> torch.Tensor:
         """y = x W_e^T over each expert's receive rows (dispatch_fp4's recv_x) with weights
         [E, dout, din], both in 4 bits; y in bf16."""
-        dout = self._weights_fp4(weights, "weights", None, x_recv.format)
+        dout = self._weights_fp4(weights, "weights", x_recv)
         self._rows_fp4(x_recv, "x_recv", weights.cols)
-        y_recv = self._out_rows(y_recv, "y_recv", dout, stream)
-        ep_expert_gemm_fp4(self.handle, x_recv, weights, weights.cols, dout, y_recv, stream)
+        with self._here(x_recv.codes, weights.codes, y_recv):
+            y_recv = self._out_rows(y_recv, "y_recv", dout, stream)
+            ep_expert_gemm_fp4(self.handle, x_recv, weights, weights.cols, dout, y_recv, stream)
         return y_recv
 
     def expert_glu_fp4(self, x_recv: FP4, w_gate_up: FP4, act: str = "silu",
@@ -1241,7 +1250,7 @@ class Buffer:
                        h_scale: torch.Tensor | None = None, stream=None):
         """h = act(x Wg^T) * (x Wu^T) over each expert's receive rows, both in 4 bits: in bf16,
         or, with quantize, as an FP4 of the same format (h_scale: its tensor_scale)."""
-        rows = self._weights_fp4(w_gate_up, "w_gate_up", None, x_recv.format)
+        rows = self._weights_fp4(w_gate_up, "w_gate_up", x_recv)
         if rows % 256:
             raise ValueError(f"w_gate_up must hold gate and up rows, 128 of each or a multiple, "
                              f"got {rows} rows")
@@ -1255,8 +1264,9 @@ class Buffer:
                 raise ValueError(f"h is {h.format}, the rows are {x_recv.format}")
         else:
             h = self._out_rows(h, "h", dff, stream)
-        ep_expert_glu_fp4(self.handle, x_recv, w_gate_up, w_gate_up.cols, dff,
-                          self._activation(act), h, stream)
+        with self._here(x_recv.codes, w_gate_up.codes, h.codes if isinstance(h, FP4) else h):
+            ep_expert_glu_fp4(self.handle, x_recv, w_gate_up, w_gate_up.cols, dff,
+                              self._activation(act), h, stream)
         return h
 
     def expert_ffn_fp4(self, x_recv: FP4, w_gate_up: FP4, w_down: FP4, act: str = "silu",
@@ -1264,7 +1274,7 @@ class Buffer:
                        stream=None) -> torch.Tensor:
         """expert_ffn with rows, weights and what is between them in 4 bits: two kernels, y in
         bf16, ready for combine."""
-        dff = self._weights_fp4(w_gate_up, "w_gate_up", None, x_recv.format) // 2
+        dff = self._weights_fp4(w_gate_up, "w_gate_up", x_recv) // 2
         if w_down.cols != dff:
             raise ValueError(f"w_down takes {w_down.cols} columns, w_gate_up gives {dff}")
         h = self._fp4_rows(self.R * self._last_stride(), dff, x_recv.format, h_scale, stream,
@@ -1300,9 +1310,8 @@ class Buffer:
             raise ValueError(f"x, scores and ids must be [T, {self.D}], [T, {self.K}] and "
                              f"[T, {self.K}], got {tuple(x_TD.shape)}, "
                              f"{tuple(topk_scores_TK.shape)}, {tuple(topk_expert_ids_TK.shape)}")
-        if out is None:
-            out = self._empty((T, self.D), torch.bfloat16 if out_dtype is None else out_dtype, stream)
-        elif out.shape != (T, self.D):
+        kind = self._activation(act)
+        if out is not None and out.shape != (T, self.D):
             raise ValueError(f"out must be {[T, self.D]}, got {list(out.shape)}")
         nbytes = self._layer_bytes.get((T, dff))
         if nbytes is None:
@@ -1310,10 +1319,15 @@ class Buffer:
         if nbytes == 0:
             raise EpError(_abi.EP_ERR_CAPACITY if T > 64 or T * self.K > 512
                           else _abi.EP_ERR_INVALID_ARG, "ep_moe_layer")
-        work = self._empty((nbytes,), torch.uint8, stream, kept=False)
-        (ep_moe_layer_fp4 if fp4 else ep_moe_layer)(
-            self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, w_gate_up, w_down, dff,
-            self._activation(act), out, work, stream)
+        with self._here(x_TD, topk_scores_TK, topk_expert_ids_TK, out,
+                        *((w_gate_up.codes, w_down.codes) if fp4 else (w_gate_up, w_down))):
+            if out is None:
+                out = self._empty((T, self.D), torch.bfloat16 if out_dtype is None else out_dtype,
+                                  stream)
+            work = self._empty((nbytes,), torch.uint8, stream, kept=False)
+            (ep_moe_layer_fp4 if fp4 else ep_moe_layer)(
+                self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, w_gate_up, w_down, dff,
+                kind, out, work, stream)
         return out
 
     def _last_stride(self) -> int:

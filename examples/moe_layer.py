@@ -5,7 +5,8 @@
 ``train_step`` is a layer's forward and backward pass on one GPU: dispatch, the experts'
 gated feed-forward block, combine, and the gradients back through all three. The example
 fits the layer to a random target layer for a few steps, quantises the experts to 4 bits
-with group scales, and answers a batch of single tokens through ``decode_step``.
+with group scales, and answers a batch of single tokens through ``decode_step``; then to
+4-bit floating point, and answers it through the layer for a few tokens, ``moe_layer``.
 """
 from __future__ import annotations
 
@@ -84,10 +85,9 @@ def decode_step(buf: ep.Buffer, w_gate_up: ep.W4, w_down: ep.W4, x, ids, scores)
     return buf.combine(buf.expert_ffn_w4(d.recv_x, w_gate_up, w_down), scores)
 
 
-def route(logits: torch.Tensor, topk: int):
-    """(ids int32, normalised scores fp32) of the topk experts of each token."""
-    top = logits.softmax(dim=-1).topk(topk, dim=-1)
-    return top.indices.to(torch.int32), top.values / top.values.sum(-1, keepdim=True)
+def quantise_fp4(w: torch.Tensor) -> ep.FP4:
+    """w [E, rows, cols] as e2m1 with a scale for 16 elements and one for each expert."""
+    return ep.quantize_fp4(w, "nv", w.abs().amax((1, 2)).float() / (6 * 448))
 
 
 def main(tokens: int = 2048, hidden: int = 512, inter: int = 256, experts: int = 16, topk: int = 4,
@@ -97,7 +97,7 @@ def main(tokens: int = 2048, hidden: int = 512, inter: int = 256, experts: int =
     target, layer = (Experts.random(experts, hidden, inter, gen) for _ in range(2))
     buf = ep.Buffer(tokens, hidden, experts, 1, topk)
     x = torch.randn((tokens, hidden), generator=gen, device="cuda").bfloat16()
-    ids, scores = route(torch.randn((tokens, experts), generator=gen, device="cuda"), topk)
+    ids, scores = ep.route(torch.randn((tokens, experts), generator=gen, device="cuda"), topk)
     want = forward(buf, target, x, ids, scores)
     losses = []
     for i in range(steps):
@@ -111,9 +111,13 @@ def main(tokens: int = 2048, hidden: int = 512, inter: int = 256, experts: int =
     got = decode_step(buf, *w4, x[:batch], ids[:batch].contiguous(), scores[:batch].contiguous())
     off = float((got.float() - out).norm() / out.norm())
     say(f"decoded {batch} tokens on 4-bit experts: {100 * off:.1f}% from the bf16 layer's output")
+    got = buf.moe_layer(x[:batch], scores[:batch].contiguous(), ids[:batch].contiguous(),
+                        quantise_fp4(layer.w_gate_up), quantise_fp4(layer.w_down))
+    off_fp4 = float((got.float() - out).norm() / out.norm())
+    say(f"and on experts in 4-bit floating point: {100 * off_fp4:.1f}%")
     assert buf.device_error() == 0
     buf.close()
-    return {"losses": losses, "decode_off": off}
+    return {"losses": losses, "decode_off": off, "decode_fp4_off": off_fp4}
 
 
 if __name__ == "__main__":

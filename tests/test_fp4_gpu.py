@@ -370,3 +370,112 @@ def test_empty_step():
     q = ep.quantize_fp4(x, "mx")
     assert q.dequantize().shape == (0, 256)
     buf.close()
+
+
+def test_refusals():
+    T, D, E, K = 8, 256, 4, 2
+    buf = ep.Buffer(T, D, E, 1, K, layout="packed")
+    x = torch.zeros((T, D), dtype=torch.bfloat16, device="cuda")
+    scores, ids = torch.ones((T, K), device="cuda"), make_ids(T, E, K, 1)
+    c, sc = F4.random_fp4(gen(1), (E, 128), D, "nv")
+    w = ep.FP4(c, ep.tile_fp4_scales(sc), "nv")
+    q = ep.quantize_fp4(torch.zeros((T * K, D), dtype=torch.bfloat16, device="cuda"), "nv")
+    with pytest.raises(ep.EpError) as e:                      # no layout yet
+        ep.ep_expert_gemm_fp4(buf.handle, q, w, D, 128,
+                              torch.empty((T * K, 128), dtype=torch.bfloat16, device="cuda"))
+    assert e.value.status == ep._abi.EP_ERR_NO_LAYOUT
+    with pytest.raises(ep.EpError) as e:
+        buf.dispatch_fp4(x, scores, ids, T + 1)
+    assert e.value.status == ep._abi.EP_ERR_CAPACITY
+    with pytest.raises(ep.EpError):
+        buf.dispatch_fp4(x, scores, ids, T - 1)
+    with pytest.raises(ValueError, match="format"):
+        buf.dispatch_fp4(x, scores, ids, format="int4")
+    with pytest.raises(ValueError, match="x, scores and ids"):
+        buf.dispatch_fp4(x, scores[:4], ids)
+    with pytest.raises(ValueError, match="tensor_scale"):
+        buf.dispatch_fp4(x, scores, ids, format="mx", tensor_scale=torch.ones(1, device="cuda"))
+    rows = buf.dispatch_fp4(x, scores, ids, format="mx").recv_x
+    with pytest.raises(ValueError, match="mx"):
+        buf.expert_gemm_fp4(rows, w)                          # one format only
+    rows = buf.dispatch_fp4(x, scores, ids).recv_x
+    with pytest.raises(TypeError):
+        buf.expert_gemm_fp4(rows, c)
+    with pytest.raises(TypeError):
+        buf.expert_gemm_fp4(x, w)
+    with pytest.raises(ValueError, match="gate and up"):
+        buf.expert_glu_fp4(rows, w)                           # 128 rows: no gate and up of 128 each
+    c2, sc2 = F4.random_fp4(gen(2), (E, 256), D, "nv")
+    wg = ep.FP4(c2, ep.tile_fp4_scales(sc2), "nv")
+    with pytest.raises(ValueError, match="w_down"):
+        buf.expert_ffn_fp4(rows, wg, w)                       # w_down takes 256 columns, h has 128
+    with pytest.raises(ValueError, match="act"):
+        buf.expert_glu_fp4(rows, wg, act="relu")
+    small = ep.quantize_fp4(torch.zeros((4, D), dtype=torch.bfloat16, device="cuda"), "nv")
+    with pytest.raises(ValueError, match="receive layout"):
+        buf.expert_gemm_fp4(small, w)
+    with pytest.raises(ValueError, match="contiguous"):
+        ep.quantize_fp4(torch.zeros((4, 2 * D), dtype=torch.bfloat16, device="cuda")[:, :D])
+    f32 = ep.Buffer(T, D, E, 1, K, dtype=torch.float32)
+    with pytest.raises(ep.EpError) as e:
+        f32.dispatch_fp4(x, scores, ids)
+    assert e.value.status == ep._abi.EP_ERR_INVALID_ARG
+    odd = ep.Buffer(T, 192, E, 1, K)
+    with pytest.raises(ValueError, match="128"):
+        odd.dispatch_fp4(x[:, :192].contiguous(), scores, ids)
+    with pytest.raises(ValueError, match="changed"):
+        q.codes.resize_(1, 1)
+        q.dequantize()
+    for b in (buf, f32, odd):
+        b.close()
+
+
+def test_routed_step_together():
+    """As they are used: the router, the quantising dispatch, the experts in 4 bits, combine, and the
+    router's gradient; and the layer for a few tokens on the same weights, which keeps x and h in
+    bf16's precision, within what quantising them costs."""
+    T, D, F, E, K = 48, 512, 256, 8, 2
+    g = gen(21)
+    buf = ep.Buffer(T, D, E, 1, K, layout="packed")
+    ws = [ep.quantize_fp4((torch.randn((E, r, c), device="cuda", generator=g) * c ** -0.5).bfloat16(),
+                          "nv", torch.full((E,), 2.0 ** -8, device="cuda"))
+          for r, c in ((2 * F, D), (D, F))]
+    x = torch.randn((T, D), device="cuda", generator=g).bfloat16()
+    logits = torch.randn((T, E), device="cuda", generator=g)
+    select = logits.clone()
+    select[40:] = -torch.inf                       # padding
+    ids, scores = ep.route(logits, K, "sigmoid", select=select)
+    d = buf.dispatch_fp4(x, scores, ids)
+    y = buf.expert_ffn_fp4(d.recv_x, *ws)
+    out = buf.combine(y, scores)
+    _, grad_scores = buf.combine_backward(torch.randn_like(out), y, scores)
+    grad = ep.route_backward(grad_scores, logits, ids, "sigmoid")
+    assert (out[40:] == 0).all() and (grad[40:] == 0).all() and torch.isfinite(grad).all()
+    few = buf.moe_layer(x, scores, ids, *ws)
+    assert (few[40:] == 0).all()
+    # An element of e2m1 with a scale that fits its block is off by at most 1/12 of the block's
+    # largest, 0.04 in the root mean square of normal ones; two such roundings and the gate's slope
+    # keep the result within a quarter.
+    off = (few.float() - out.float()).norm() / few.float().norm()
+    assert 0.01 < off < 0.25
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ids2, scores2 = ep.route(logits, K, "sigmoid", select=select, stream=s)
+    d2 = buf.dispatch_fp4(x, scores2, ids2, stream=s)
+    out2 = buf.combine(buf.expert_ffn_fp4(d2.recv_x, *ws, stream=s), scores2, stream=s)
+    s.synchronize()
+    assert torch.equal(out, out2)
+    assert buf.device_error() == 0
+    buf.close()
+
+
+@pytest.mark.parametrize("offset", [8, 16])
+def test_quantize_unaligned_to_32_bytes(offset):
+    """A matrix at 16 bytes from a 32-byte boundary (offset 8 elements): both ways of reading."""
+    flat = torch.randn(40 * 256 + 16, device="cuda", generator=gen(3)).bfloat16()
+    x = flat[offset:offset + 40 * 256].view(40, 256)
+    assert_quantized(ep.quantize_fp4(x, "nv"), x)
+    q = ep.quantize_fp4(x, "mx")
+    out = flat.clone()[offset:offset + 40 * 256].view(40, 256)
+    ep.ep_dequantize_fp4(q, out)
+    assert torch.equal(out, q.dequantize())
