@@ -522,10 +522,7 @@ cudaError_t launch_form(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o
 template <int FMT, int OUT>
 cudaError_t launch_out(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o)
 {
-    // Pairs where they leave no more than three quarters of the SMs without a tile (as the
-    // bf16 products choose), single SMs else.
-    const int64_t cols = f.glu ? 2 * f.dout : f.dout;
-    if (f.kind != 1 && cols % 256 == 0 && (f.kind == 2 || 4 * f.row_tiles * (cols / 256) >= num_sms)) {
+    if (f.kind == 2 && (f.glu ? 2 * f.dout : f.dout) % 256 == 0) {
         const cudaError_t e = launch_form<FMT, true, OUT>(f, num_sms, o);
         if (e != cudaErrorNotSupported) return e;
     }

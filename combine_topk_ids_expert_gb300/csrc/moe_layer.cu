@@ -110,6 +110,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
         : "r"(taddr));
 }
 
+// Weights are read once in a call: first to leave L2, so that x, h, the pairs' results and the
+// kernels' own code stay (each of which some warp waits for at the start of a kernel).
+__device__ __forceinline__ uint64_t evict_first()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void tma_load_2d_once(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
+                                                 uint32_t bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -356,18 +375,17 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
             const int c0 = k_first * C::kStageK, c1 = min(k_last * C::kStageK, a.din);
             for (int t = w; t < a.T; t += kRowWarps) {
                 uint32_t m = 0u;
-                for (int i0 = c0; i0 < c1; i0 += 8 * 256) {   // eight loads on their way
-                    int4 v[8];
+                for (int i0 = c0; i0 < c1; i0 += 16 * 256) {   // sixteen loads on their way
+                    int4 v[16];
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) {
+                    for (int n = 0; n < 16; ++n) {
                         const int i = i0 + n * 256 + lane * 8;
                         v[n] = make_int4(0, 0, 0, 0);
                         if (i < c1)
                             v[n] = ld_cg_v4(static_cast<const uint16_t*>(a.rows) + (int64_t)t * a.din + i);
                     }
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
-                        m = max(m, __float_as_uint(amax8(v[n])));
+                    for (int n = 0; n < 16; ++n) m = max(m, __float_as_uint(amax8(v[n])));
                 }
                 m = __reduce_max_sync(~0u, m);
                 if (lane == 0) s_exp[t] = (int16_t)digit_exponent(m);
@@ -496,6 +514,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
         // The first rows are asked for first: behind a ring's worth of weights on every SM they
         // would come after it. (In the second kernel the weights are there long before the rows.)
         if (!DOWN) asm volatile("bar.sync 3, %0;" ::"n"(32 * (1 + kRowWarps)) : "memory");
+        const uint64_t policy = evict_first();
         int g = 0;
         bool ok = true;
         for (int u = u_first; u < u_last && ok && !*s_abort; ++u) {
@@ -510,8 +529,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                     const uint32_t fb = full0 + 8u * s, sa = ring + (uint32_t)s * C::kBytesA;
                     const int kc = k * (C::FP4 ? kFp4StageK / 2 : C::kStageK);
                     mbar_expect_tx(fb, C::kBytesA);
-                    tma_load_2d(sa, &tm_w, kc, w0, fb);
-                    tma_load_2d(sa + C::kBytesA / 2, &tm_w, kc, w1, fb);
+                    tma_load_2d_once(sa, &tm_w, kc, w0, fb, policy);
+                    tma_load_2d_once(sa + C::kBytesA / 2, &tm_w, kc, w1, fb, policy);
                 }
                 __syncwarp();
             }
