@@ -1194,12 +1194,9 @@ static ep_status enqueue_fp4(ep_buffer* b, const ep_fp4* x, const ep_fp4* w, int
     a.E = b->cfg.num_experts;
     a.act = act;
     a.glu = glu;
-    // Pairs (256 x 256 tiles) from 512 rows per expert on average, as ep_expert_gemm. The whole
-    // block, nv / mx, pairs against single SMs (128 x 128): 1024 rows of 8 experts, 4096 wide,
-    // 145 / 139 against 161 / 148 us; 256 rows of 256 experts (Zipf), 7168 wide, 2250 / 2110
-    // against 2170 / 2030 us (fewer rows of padding, and two whole accumulators); 83 rows of 16
-    // experts, 1024 wide, 28 / 26 against 21 / 20 us (more tiles than SM pairs).
-    a.kind = b->gemm_kind > 0 ? b->gemm_kind : b->last_T * b->cfg.topk >= 512 * E ? 2 : 1;
+    a.kind = b->gemm_kind;
+    a.row_tiles = std::max<int64_t>(std::min<int64_t>(E, b->last_T * b->cfg.topk),
+                                    b->last_T * b->cfg.topk / 256);
     a.light_rows = b->gemm_light_rows;
     a.err = b->err;
     return cuda_status(ep::launch_expert_fp4(a, b->num_sms, opts(b, as_stream(stream))));

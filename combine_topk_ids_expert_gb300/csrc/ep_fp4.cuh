@@ -76,8 +76,10 @@ struct ExpertFp4Args {
     int64_t rows, din, dout;       // din % 128 == 0, dout % 128 == 0
     int format, E, act;
     bool glu;                      // W has dout gate rows, then dout up rows; y = act(g) * u
-    int kind;                      // 1 single SMs, 2 pairs (where W's rows are a multiple of 256)
+    int kind;                      // 1 single SMs, 2 pairs (where W's rows are a multiple of 256),
+                                   // 0: by the number of tiles
     int light_rows;                // as GemmArgs
+    int64_t row_tiles;             // row tiles of 256 that the call is likely to have
     uint32_t* err;
 };
 cudaError_t launch_expert_fp4(const ExpertFp4Args& a, int num_sms, const LaunchOpts& o);

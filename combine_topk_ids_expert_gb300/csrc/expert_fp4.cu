@@ -18,6 +18,15 @@
 // with two whole accumulators.
 //
 // Products are exact and summed in fp32; tensor scales enter in the epilogue.
+//
+// Measured (nv, the block with its dispatch; 8192 rows over 8 experts, 4096 -> 2 x 2048 -> 4096):
+// 186 us as it was first; 160 with W's scales by TMA onto the pair's own barrier (copied row by
+// row, or completed on a barrier of their own, they came late); 156 with descriptors moved by
+// additions; 145 with the dispatch in one kernel; 118 with arrivals that order shared memory
+// only (a release at cluster scope, 0.5 to 1 us each, was in the chain of every stage and of
+// every change of tiles). A stage's MMAs take 512 cycles; the first stages of a tile, which are
+// there already, take about 610. Tried without gain: the next tile found a tile ahead, codes
+// prefetched to L2, scales moved to tensor memory in one stage of a tile only (to time it).
 #include "ep_fp4.cuh"
 #include "expert_tile.cuh"
 #include "fp4_umma.cuh"
@@ -391,7 +400,7 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     if (PAIR && i == 0) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(lead_free0);
+                        if (lane == 0) mbar_arrive_cluster_own(lead_free0);
                     }
 #pragma unroll
                     for (int n = 0; n < 32; ++n)
@@ -402,7 +411,7 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     if (PAIR && i == 0) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(lead_free0);
+                        if (lane == 0) mbar_arrive_cluster_own(lead_free0);
                     }
 #pragma unroll
                     for (int n = 0; n < 32; ++n) v[n] = __uint_as_float(q32[n]) * gw;
@@ -449,7 +458,7 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(lead_full0 + 8u * s);
+                if (PAIR) mbar_arrive_cluster_own(lead_full0 + 8u * s);
                 else mbar_arrive(full0 + 8u * s);
             }
             // Not before: the fence and the arrival would wait for these loads.
@@ -522,7 +531,12 @@ cudaError_t launch_form(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o
 template <int FMT, int OUT>
 cudaError_t launch_out(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o)
 {
-    if (f.kind == 2 && (f.glu ? 2 * f.dout : f.dout) % 256 == 0) {
+    // Pairs (256 x 256) where every pair of SMs has a tile, else single SMs (128 x 128). The whole
+    // block, nv / mx, pairs against singles: 1024 rows of 8 experts, 4096 wide, 118 / 109 against
+    // 161 / 148 us; 256 rows of 256 experts (Zipf), 7168 wide, 1878 / 1663 against 2180 / 2009 us;
+    // 83 rows of 16 experts, 1024 wide (64 tiles of pairs), 26 / 24 against 21 / 20 us.
+    const int64_t cols = f.glu ? 2 * f.dout : f.dout;
+    if (f.kind != 1 && cols % 256 == 0 && (f.kind == 2 || 2 * f.row_tiles * (cols / 256) >= num_sms)) {
         const cudaError_t e = launch_form<FMT, true, OUT>(f, num_sms, o);
         if (e != cudaErrorNotSupported) return e;
     }

@@ -101,6 +101,16 @@ inline bool make_code_map(CUtensorMap* m, const void* base, uint64_t cols, uint6
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Arrive on an mbarrier of any CTA of the cluster, after this thread's accesses to its own CTA's
+// shared memory (and what is ordered before them: tcgen05 loads behind their fence). A release at
+// cluster scope would also wait for every global access of the thread: half a microsecond to
+// one, at each arrival.
+__device__ __forceinline__ void mbar_arrive_cluster_own(uint32_t bar)
+{
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Tensor map over tiles of scales, one after the other, in boxes of box_tiles.
 inline bool make_scale_map(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles)
 {
