@@ -12,8 +12,7 @@
 //
 // An activation keeps its precision. With bf16 weights x enters as it is, and h, fp32, as the
 // sum of two bf16 rows (what the first leaves is within 2^-8 of it, what both leave within 2^-16).
-// With 4-bit weights a row enters as rows of e2m1 digits,
-// four for x and five for h, that share a power of two s for each block of the weights' size,
+// With 4-bit weights a row enters as rows of e2m1 digits, four for x and five for h, that share a power of two s for each block of the weights' size,
 //     x = s (d0 + d1 / 8 + d2 / 64 + d3 / 512) + rest,   |d| <= 4, |rest| <= s / 1024,
 // s = 2^(floor(log2 amax) - 1): each digit is what is left rounded to e2m1 (half steps below
 // 2, whole ones up to 4), which leaves at most 1/2, an eighth of the next digit's range. A bf16
@@ -31,8 +30,8 @@
 //
 // Sums, h, scores and the pairs' results are fp32; the layer's result is rounded once.
 //
-// Measured (D 7168, dff 2048, 8 of 256 experts; GB/s of weights): 1 token 116 us in bf16 (6.1
-// TB/s), 44 us mx, 50 us nv (4.0); 16 tokens 1284 us (7.0) and 437 us mx (5.5). Bound by HBM
+// Measured (D 7168, dff 2048, 8 of 256 experts; GB/s of weights): 1 token 112 us in bf16 (6.3
+// TB/s), 42 us mx, 48 us nv (4.1); 16 tokens 1258 us (7.1) and 409 us mx (5.8). Bound by HBM
 // from a few tokens on. One token: about 5 us to the first product of each kernel (launch,
 // routing, the first rows behind their latency), 2 us from one kernel to the other, and a
 // quarter of a wave. Steps, for 16 tokens mx: 1275 us as it was first (joins by one CTA, each
