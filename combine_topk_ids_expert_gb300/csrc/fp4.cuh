@@ -77,6 +77,19 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte)
     return r;
 }
 
+// The eight of a word.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t word, uint32_t (&h2)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h2[0]), "=r"(h2[1]), "=r"(h2[2]), "=r"(h2[3])
+        : "r"(word));
+}
+
 __device__ __forceinline__ float f16_lo(uint32_t h2)
 {
     float f;
@@ -137,6 +150,10 @@ __device__ __forceinline__ float quotient_for_rounding(float x, float d, float g
     return border ? __fmaf_rn(rest, rinv * 1024.0f, qr) : q0;
 }
 
+// Numbers below and above a quotient that an fp32 product with a reciprocal off by 2^-22 gives: if
+// both round to the same code, so does the quotient itself, and only else has it to be looked at.
+constexpr float kBelow = 1.0f - 0x1p-20f, kAbove = 1.0f + 0x1p-20f;
+
 // The block's scale code from the largest magnitude in it (not NaN: then, and for an
 // infinity, the code is the NaN). g: the matrix's scale, 1 without one.
 template <int FMT>
@@ -147,7 +164,23 @@ __device__ __forceinline__ uint32_t fp4_scale_code(float amax, float g)
         return e == 255u ? kNanMx : e < 2u ? 0u : e - 2u;
     }
     if (!(amax < __uint_as_float(0x7F800000u))) return kNanNv;
-    return cvt_ue4m3(quotient_for_rounding<4>(amax, 6.0f, g, rcp_near(6.0f * g)));
+    const float rinv = rcp_near(6.0f * g);
+    uint16_t both;   // what lies a little below the quotient and a little above it round to
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(both)
+        : "f"(amax * (rinv * kAbove)), "f"(amax * (rinv * kBelow)));
+    if ((both >> 8) == (both & 0xFF)) return both & 0xFFu;
+    return cvt_ue4m3(quotient_for_rounding<4>(amax, 6.0f, g, rinv));
+}
+
+// (a, b) * (m, m) in one instruction.
+__device__ __forceinline__ void mul2(float a, float b, float m, float& x, float& y)
+{
+    asm("{\n\t.reg .b64 p, q;\n\t"
+        "mov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(m));
 }
 
 // Codes of 16 elements in a block with scale code c.
@@ -159,26 +192,36 @@ __device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], uint32_t c, f
         if (c == kNanMx) return make_uint2(0u, 0u);
         const float inv = __uint_as_float((254u - c) << 23);   // 2^(127 - c), c <= 252
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = v[i] * inv;
+        for (int i = 0; i < 16; i += 2) mul2(v[i], v[i + 1], inv, q[i], q[i + 1]);
         return make_uint2(cvt_e2m1x8(q), cvt_e2m1x8(q + 8));
     }
     if (c == kNanNv || c == 0u) return make_uint2(0u, 0u);
     const float s = ue4m3_value(c);
     const float rinv = rcp_near(s * g);
-    uint32_t least = ~0u;
+    if (TENSOR_SCALE) {
+        const float lo = rinv * kBelow, hi = rinv * kAbove;
+        uint32_t w[2], differ = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        q[i] = v[i] * rinv;
-        // Nearly zero fraction bits behind the first two: next to a border, or to a code.
-        const uint32_t b = __float_as_uint(q[i]) + 8u;
-        least = min(least, b & 0x1FFFF0u);
-        // Without a matrix's scale, or where it is a power of two, x has 8 bits and s 4: the
-        // quotient is on a border or 2^-12 away from it, and its last bits are the reciprocal's.
-        if (!TENSOR_SCALE) q[i] = __uint_as_float(b & ~15u);
-    }
-    if (TENSOR_SCALE && least == 0u) {   // seldom: x / g has to fall there
+        for (int h = 0; h < 2; ++h) {
+            float below[8], above[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = quotient_for_rounding<2>(v[i], s, g, rinv);
+            for (int i = 0; i < 8; i += 2) {
+                mul2(v[8 * h + i], v[8 * h + i + 1], lo, below[i], below[i + 1]);
+                mul2(v[8 * h + i], v[8 * h + i + 1], hi, above[i], above[i + 1]);
+            }
+            w[h] = cvt_e2m1x8(below);
+            differ |= w[h] ^ cvt_e2m1x8(above);
+        }
+        if (differ == 0u) return make_uint2(w[0], w[1]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = quotient_for_rounding<2>(v[i], s, g, rinv);   // seldom
+    } else {
+        // x has 8 bits and s 4: the quotient is on a border or 2^-12 away from it, and its last
+        // bits are the reciprocal's.
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) mul2(v[i], v[i + 1], rinv, q[i], q[i + 1]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = __uint_as_float((__float_as_uint(q[i]) + 8u) & ~15u);
     }
     return make_uint2(cvt_e2m1x8(q), cvt_e2m1x8(q + 8));
 }

@@ -2,10 +2,13 @@
 // rows to microscaled 4-bit floating point (fp4.cuh has the format), and back.
 //
 // One thread takes 16 consecutive elements: a block of nv, half a block of mx (whose halves
-// meet in one shuffle). The floor is the bytes; what bounds it is the work per element: 20
-// instructions for the largest magnitude, a product with the scale's reciprocal, the look for a
-// border and half a conversion. 134 M elements with a matrix's scale, 344 MB: 106 us (3.2 TB/s,
-// issue slots 72% busy); back to bf16 88 us (3.9 TB/s, writes mostly).
+// meet in one shuffle). The floor is the bytes, and without a matrix's scale that is what it
+// takes: 134 M elements, 344 MB, 54 us in nv and 52 in mx (6.4 and 6.6 TB/s), 54 and 62 us back to
+// bf16. With a matrix's scale 68 us: issue slots (every element is multiplied and converted
+// twice to see whether it lies next to a border). Steps for that case, there and back: 106 + 88
+// us; 138 together with products of two elements in one instruction, borders found from two
+// conversions (before: from each quotient's last bits), the next row on its way during this
+// one's work, and one resident wave of CTAs.
 #include "ep_fp4.cuh"
 #include "fp4.cuh"
 
@@ -63,10 +66,32 @@ __device__ __forceinline__ void store32(uint8_t* p, bool wide, const uint32_t (&
     }
 }
 
-// A warp takes 32 units of a row after the other (grid: columns x, rows y; no index of an
-// element is divided: that cost a quarter of the time).
+// The scale of the matrix that a warp's row is in; its rows go up, so that a division is needed
+// only where they enter another matrix.
+struct RowScale {
+    int64_t end = 0;
+    float g = 1.0f;
+    __device__ __forceinline__ void enter(const Fp4Args& a, int64_t row)
+    {
+        if (row < end) return;
+        const uint32_t m = (uint32_t)row / (uint32_t)a.rows_per_scale;
+        end = (int64_t)(m + 1) * a.rows_per_scale;
+        g = __ldcg(a.tensor_scale + m);
+    }
+};
+
+// A warp takes 32 units of a row after the other, the next row's on their way (grid: columns x,
+// rows y, all resident at once; no index of an element is divided: that cost a quarter of the
+// time).
+// CTAs on an SM. Quantising with a matrix's scale spills at 5 (70.6 against 67.8 us); the others take
+// 54 and 52 us with 5, 57 with 4, 60 and 52 with 6. Back: 54 us (nv) and 62 (mx) with 4, 57 and
+// 64 with 5, 59 and 54 with 3.
+template <bool TENSOR_SCALE>
+constexpr int kQuantPerSm = TENSOR_SCALE ? 4 : 5;
+constexpr int kBackPerSm = 4;
+
 template <int FMT, bool TENSOR_SCALE>
-__global__ void __launch_bounds__(kThreads, 5) quantize_kernel(Fp4Args a)
+__global__ void __launch_bounds__(kThreads, kQuantPerSm<TENSOR_SCALE>) quantize_kernel(Fp4Args a)
 {
     griddep_wait();
     const int lane = threadIdx.x & 31, per_row = (int)(a.cols / 16);
@@ -76,27 +101,54 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_kernel(Fp4Args a)
                                           // word of scales are in or out together
     const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0;
     const int64_t step = (int64_t)gridDim.y * (kThreads / 32);
-    for (int64_t row = (int64_t)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += step) {
-        const int64_t i = row * per_row + unit;
-        int4 raw[2] = {};
-        if (in) load32(static_cast<const uint8_t*>(a.x) + i * 32, wide, raw[0], raw[1]);
-        const float g =
-            TENSOR_SCALE ? __ldcg(a.tensor_scale + (uint32_t)row / (uint32_t)a.rows_per_scale) : 1.0f;
+    int64_t row = (int64_t)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + (row * per_row + unit) * 32;
+    uint8_t* codes = a.codes + (row * per_row + unit) * 8;
+    int4 next[2] = {};
+    if (in && row < a.rows) load32(x, wide, next[0], next[1]);
+    RowScale rs;
+    for (; row < a.rows; row += step) {
+        const int4 raw[2] = {next[0], next[1]};
+        x += step * per_row * 32;
+        if (in && row + step < a.rows) load32(x, wide, next[0], next[1]);
+        if (TENSOR_SCALE) rs.enter(a, row);
         uint32_t word;
         bool writes;
-        const uint2 q = quantize16<FMT, TENSOR_SCALE>(raw, g, unit, &word, &writes);
+        const uint2 q = quantize16<FMT, TENSOR_SCALE>(raw, rs.g, unit, &word, &writes);
         if (in) {
-            *reinterpret_cast<uint2*>(a.codes + i * 8) = q;
+            *reinterpret_cast<uint2*>(codes) = q;
             if (writes)
                 *reinterpret_cast<uint32_t*>(
                     a.scales + fp4_scale_at(row, unit / (FMT == kFp4Mx ? 8 : 4), tiles)) = word;
         }
+        codes += step * per_row * 8;
     }
     griddep_launch_dependents();
 }
 
+// 16 elements back. An element in the matrix's units is exact: nv's in fp16 (six bits, 2^-10 to
+// 2688), mx's in fp32. The matrix's scale rounds it once, and bf16 once more.
+template <int FMT>
+__device__ __forceinline__ void dequantize16(uint2 q, uint32_t c, float g, float (&v)[16])
+{
+    uint32_t h2[8];
+    e2m1x8_to_f16x2(q.x, reinterpret_cast<uint32_t(&)[4]>(h2[0]));
+    e2m1x8_to_f16x2(q.y, reinterpret_cast<uint32_t(&)[4]>(h2[4]));
+    float m = g;
+    if (FMT == kFp4Mx) {
+        m = ue8m0_value(c);
+    } else {
+        uint32_t s2;      // the scale, twice
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)(c * 0x101u)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h2[j]) : "r"(s2));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mul2(f16_lo(h2[j]), f16_hi(h2[j]), m, v[2 * j], v[2 * j + 1]);
+}
+
 template <int FMT, bool F32>
-__global__ void __launch_bounds__(kThreads, 6) dequantize_kernel(Fp4Args a)
+__global__ void __launch_bounds__(kThreads, kBackPerSm) dequantize_kernel(Fp4Args a)
 {
     griddep_wait();
     const int lane = threadIdx.x & 31, per_row = (int)(a.cols / 16);
@@ -106,34 +158,34 @@ __global__ void __launch_bounds__(kThreads, 6) dequantize_kernel(Fp4Args a)
         const int block = FMT == kFp4Mx ? unit >> 1 : unit;
         const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
         const int64_t step = (int64_t)gridDim.y * (kThreads / 32);
-        constexpr int kRows = 2;          // at a time
-        for (int64_t row0 = (int64_t)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row0 < a.rows;
-             row0 += kRows * step) {
-            uint2 q[kRows];
-            uint32_t c[kRows];
+        constexpr int kRows = 2;          // at a time, the next ones on their way
+        uint2 q[kRows], qn[kRows];
+        uint32_t c[kRows], cn[kRows];
+        auto fetch = [&](int64_t row0) {
 #pragma unroll
             for (int n = 0; n < kRows; ++n) {
                 const int64_t row = min(row0 + n * step, a.rows - 1);
-                q[n] = __ldcg(reinterpret_cast<const uint2*>(a.codes + (row * per_row + unit) * 8));
-                c[n] = __ldcg(a.scales + fp4_scale_at(row, block >> 2, tiles) + (block & 3));
+                qn[n] = __ldcg(reinterpret_cast<const uint2*>(a.codes + (row * per_row + unit) * 8));
+                cn[n] = __ldcg(a.scales + fp4_scale_at(row, block >> 2, tiles) + (block & 3));
             }
+        };
+        int64_t row0 = (int64_t)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
+        if (row0 < a.rows) fetch(row0);
+        RowScale rs;
+        for (; row0 < a.rows; row0 += kRows * step) {
+#pragma unroll
+            for (int n = 0; n < kRows; ++n) {
+                q[n] = qn[n];
+                c[n] = cn[n];
+            }
+            if (row0 + kRows * step < a.rows) fetch(row0 + kRows * step);
 #pragma unroll
             for (int n = 0; n < kRows; ++n) {
                 const int64_t row = row0 + n * step;
                 if (row >= a.rows) break;
-                const float s = fp4_scale_value<FMT>(c[n]);
-                // An element's value in the matrix's units is exact in fp32; the matrix's scale
-                // rounds it once, and bf16 once more.
-                const float g =
-                    a.tensor_scale ? __ldcg(a.tensor_scale + (uint32_t)row / (uint32_t)a.rows_per_scale) : 1.0f;
+                if (FMT == kFp4Nv && a.tensor_scale) rs.enter(a, row);
                 float v[16];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t h2 =
-                        e2m1x2_to_f16x2(((j < 4 ? q[n].x : q[n].y) >> (8 * (j & 3))) & 0xFFu);
-                    v[2 * j] = f16_lo(h2) * s * g;
-                    v[2 * j + 1] = f16_hi(h2) * s * g;
-                }
+                dequantize16<FMT>(q[n], c[n], rs.g, v);
                 uint8_t* o = static_cast<uint8_t*>(a.out) + (row * per_row + unit) * (F32 ? 64 : 32);
                 uint32_t w[8];
                 if (F32) {
@@ -312,14 +364,14 @@ dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
     griddep_launch_dependents();
 }
 
-// Columns of 32 units by rows, eight to a CTA; two waves of CTAs at most.
-dim3 grid_for(const Fp4Args& a)
+// Columns of 32 units by rows, eight to a CTA; as many CTAs as are resident at once, if need be.
+dim3 grid_for(const Fp4Args& a, int per_sm)
 {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t x = (a.cols / 16 + 31) / 32, rows = (a.rows + kThreads / 32 - 1) / (kThreads / 32);
-    int64_t most = (int64_t)sms * (2048 / kThreads) * 2 / x;
+    int64_t most = (int64_t)sms * per_sm / x;
     if (most < 1) most = 1;
     if (most > 65535) most = 65535;
     return dim3((unsigned)x, (unsigned)(rows < most ? rows : most));
@@ -329,7 +381,7 @@ dim3 grid_for(const Fp4Args& a)
 
 cudaError_t launch_quantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 {
-    const dim3 grid = grid_for(a);
+    const dim3 grid = grid_for(a, a.tensor_scale ? kQuantPerSm<true> : kQuantPerSm<false>);
     if (a.format == kFp4Mx) return launch_kernel(quantize_kernel<kFp4Mx, false>, grid, kThreads, 0, o, a);
     return a.tensor_scale ? launch_kernel(quantize_kernel<kFp4Nv, true>, grid, kThreads, 0, o, a)
                           : launch_kernel(quantize_kernel<kFp4Nv, false>, grid, kThreads, 0, o, a);
@@ -337,7 +389,7 @@ cudaError_t launch_quantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 
 cudaError_t launch_dequantize_fp4(const Fp4Args& a, const LaunchOpts& o)
 {
-    const dim3 grid = grid_for(a);
+    const dim3 grid = grid_for(a, kBackPerSm);
     if (a.format == kFp4Mx)
         return a.out_f32 ? launch_kernel(dequantize_kernel<kFp4Mx, true>, grid, kThreads, 0, o, a)
                          : launch_kernel(dequantize_kernel<kFp4Mx, false>, grid, kThreads, 0, o, a);
