@@ -51,6 +51,7 @@ struct PermuteFp4Args {
     uint8_t* scales;           // tiles of 128 rows
     float* recv_scores;
     int32_t* recv_src;
+    int kept;                  // one kernel: tokens of a tile whose codes wait in shared memory
 };
 cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const LaunchOpts& o);
 // Layout and rows in one cooperative kernel; cudaErrorNotSupported where a tile's tables do not fit

@@ -9,14 +9,22 @@
 // us; 138 together with products of two elements in one instruction, borders found from two
 // conversions (before: from each quotient's last bits), the next row on its way during this
 // one's work, and one resident wave of CTAs.
+#include <algorithm>
 #include "ep_fp4.cuh"
 #include "fp4.cuh"
+#include "umma.cuh"
 
 namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kDispatchFp4PerSm = 2;   // tiles of the one-pass dispatch on an SM
+constexpr size_t kDispatchFp4Smem = 100 * 1024;   // of such a tile
+// Receive rows whose codes wait in shared memory for the layout. The wait is long enough for a few
+// tokens: 4096 tokens (D 4096, top 2) take 20.9 us with none kept, 20.1 with 16 rows, 19.5 with 32;
+// 8192 tokens (D 7168, top 8) 105, 104 and 110, with as many as fit 128: reading and writing then
+// no longer overlap.
+constexpr int kKeptRows = 16;
 
 // What 16 elements become: 8 bytes of codes, and on every fourth block's first thread the
 // word of four scales.
@@ -282,8 +290,10 @@ __global__ void __launch_bounds__(kPermuteThreads) permute_fp4_kernel(PermuteFp4
 
 // Layout, positions and rows in one kernel, a CTA to a tile of tokens, as the one-pass dispatch
 // of whole rows (its layout, with a grid barrier or, for small calls, every id counted by every
-// CTA). The tile's x comes to L2 meanwhile. Shared memory: [kLayoutWarps * Ep][tile pairs][3 * Ep]
-// ints.
+// CTA). While the CTAs wait for one another at the barrier, the first a.kept tokens of the tile
+// are quantised into shared memory, from where bulk copies bring their codes to the rows once
+// these are known; the tile's other x comes to L2. Shared memory: [kLayoutWarps * Ep][3 * Ep][tile
+// pairs] ints, the kept tokens' codes and words of scales.
 template <int FMT, bool TENSOR_SCALE, bool SMALL>
 __global__ void __launch_bounds__(kLayoutThreads, kDispatchFp4PerSm)
 dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
@@ -294,24 +304,67 @@ dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
     __shared__ int s_wsum[kLayoutWarps];
     __shared__ int s_flag;
     __shared__ uint32_t s_epoch;
+    __shared__ int s_next;
     int* s_base = s_dyn;
-    int* s_pos = s_base + kLayoutWarps * L.Ep;
-    int* s_seed = s_pos + L.tpt * L.K;
+    int* s_seed = s_base + kLayoutWarps * L.Ep;
     int* s_tot = s_seed + L.Ep;
     int* s_off = s_tot + L.Ep;
+    int* s_pos = s_off + L.Ep;
+    uint8_t* s_codes = reinterpret_cast<uint8_t*>(s_pos + (L.tpt * L.K + 3) / 4 * 4);
+    uint32_t* s_words = reinterpret_cast<uint32_t*>(s_codes + a.kept * (a.D / 2));
     const int tile = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t0 = (int64_t)tile * L.tpt, t1 = min(L.T, t0 + L.tpt);
     const int n_my = (int)(t1 - t0), K = L.K;
     griddep_wait();
+    const int per_row = (int)(a.D / 16), parts = (per_row + kPartUnits - 1) / kPartUnits;
+    const int tiles = (int)(a.D / (4 * Fp4<FMT>::kBlock));
+    const float g = TENSOR_SCALE ? __ldcg(a.tensor_scale) : 1.0f;
+    const int kept = SMALL ? 0 : min(n_my, a.kept);
+    if (threadIdx.x == 0) s_next = 0;
     const uint8_t* x0 = static_cast<const uint8_t*>(a.x) + t0 * a.D * 2;
-    for (int64_t i = (int64_t)threadIdx.x * 128; i < n_my * a.D * 2; i += (int64_t)kLayoutThreads * 128)
+    for (int64_t i = (int64_t)threadIdx.x * 128 + kept * a.D * 2; i < n_my * a.D * 2; i += (int64_t)kLayoutThreads * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(x0 + i));
+    // Parts of the kept tokens, taken in turn by whichever warp has time.
+    auto keep = [&] {
+        __syncwarp();
+        auto take = [&] {
+            int i = 0;
+            if (lane == 0) i = atomicAdd(&s_next, 1);
+            return __shfl_sync(~0u, i, 0);
+        };
+        int4 next[2][2];
+        int item = take();
+        const int items = kept * parts;
+        if (item < items) fetch_part(a, t0 + item / parts, item % parts, per_row, lane, next);
+        while (item < items) {
+            const int tt = item / parts, part = item - tt * parts;
+            int4 raw[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                raw[i][0] = next[i][0];
+                raw[i][1] = next[i][1];
+            }
+            item = take();
+            if (item < items) fetch_part(a, t0 + item / parts, item % parts, per_row, lane, next);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int unit = part * kPartUnits + 32 * i + lane;
+                uint32_t word;
+                bool writes;
+                const uint2 q = quantize16<FMT, TENSOR_SCALE>(raw[i], g, unit, &word, &writes);
+                if (unit >= per_row) continue;
+                *reinterpret_cast<uint2*>(s_codes + tt * (a.D / 2) + unit * 8) = q;
+                if (writes) s_words[tt * tiles + unit / (FMT == kFp4Mx ? 8 : 4)] = word;
+            }
+        }
+        fence_proxy_async();   // the bulk copies read the codes
+    };
     if constexpr (SMALL) {
         redundant_counts(L, tile, s_seed, s_tot, s_rank);
         layout_offsets(L, s_base, s_seed, s_tot, s_off, s_rank, s_wsum);
     } else {
         if (!onepass_layout(L, tile, s_base, s_seed, s_tot, s_off, s_rank, s_tok, s_wsum, &s_flag,
-                            &s_epoch, s_pos, nullptr, [] {})) {
+                            &s_epoch, s_pos, nullptr, [] {}, keep)) {
             if (threadIdx.x == 0) atomicOr(L.err, kErrTimeout);
             griddep_launch_dependents();
             return;
@@ -343,13 +396,23 @@ dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
         a.recv_src[p] = (int32_t)(t0 * K + j);
     }
     __syncthreads();
-    const int per_row = (int)(a.D / 16), parts = (per_row + kPartUnits - 1) / kPartUnits;
-    const float g = TENSOR_SCALE ? __ldcg(a.tensor_scale) : 1.0f;
+    for (int j = threadIdx.x; j < kept * K; j += kLayoutThreads) {
+        const int p = s_pos[j];
+        if (p >= 0)
+            bulk_s2g(a.codes + p * (a.D / 2), smem_u32(s_codes + j / K * (a.D / 2)), (uint32_t)(a.D / 2));
+    }
+    bulk_commit();
+    for (int j = warp; j < kept * K; j += kLayoutWarps) {
+        const int p = s_pos[j];
+        if (p < 0) continue;
+        for (int kt = lane; kt < tiles; kt += 32)
+            *reinterpret_cast<uint32_t*>(a.scales + fp4_scale_at(p, kt, tiles)) = s_words[j / K * tiles + kt];
+    }
     // The next part's elements are on their way while this one is written.
     int4 next[2][2];
-    const int items = n_my * parts;
-    if (warp < items) fetch_part(a, t0 + warp / parts, warp % parts, per_row, lane, next);
-    for (int item = warp; item < items; item += kLayoutWarps) {
+    const int items = n_my * parts, first = kept * parts + warp;
+    if (first < items) fetch_part(a, t0 + first / parts, first % parts, per_row, lane, next);
+    for (int item = first; item < items; item += kLayoutWarps) {
         const int tt = item / parts, part = item - tt * parts;
         int4 raw[2][2];
 #pragma unroll
@@ -361,6 +424,7 @@ dispatch_fp4_kernel(LayoutArgs L, PermuteFp4Args a)
         if (after < items) fetch_part(a, t0 + after / parts, after % parts, per_row, lane, next);
         put_part<FMT, TENSOR_SCALE>(a, part, per_row, lane, g, raw, [&](int k) { return s_pos[tt * K + k]; });
     }
+    bulk_wait_all();
     griddep_launch_dependents();
 }
 
@@ -413,14 +477,20 @@ cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const Launc
 
 int dispatch_fp4_tiles_per_sm() { return kDispatchFp4PerSm; }
 
-cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& a, const LaunchOpts& o,
+cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& args, const LaunchOpts& o,
                                 bool pdl_ok, int64_t small_pairs)
 {
+    PermuteFp4Args a = args;
     if (!l.gbar || l.ntiles <= 0) return cudaErrorNotSupported;
     const int64_t tile_pairs = l.tpt * l.K;
     if (tile_pairs > kMaxTilePairs) return cudaErrorNotSupported;
-    const size_t smem = (size_t)((kLayoutWarps + 3) * (int64_t)l.Ep + tile_pairs) * 4;
+    const size_t tables = (size_t)((kLayoutWarps + 3) * (int64_t)l.Ep + (tile_pairs + 3) / 4 * 4) * 4;
     const bool small = l.T * l.K <= small_pairs;
+    const size_t token = (size_t)(a.D / 2 + a.D / (a.format == kFp4Mx ? 32 : 16));
+    a.kept = 0;
+    if (!small && tables < kDispatchFp4Smem)
+        a.kept = (int)std::min<int64_t>(std::min<int64_t>(l.tpt, kKeptRows / l.K), (int64_t)((kDispatchFp4Smem - tables) / token));
+    const size_t smem = tables + a.kept * token;
     void (*kernel)(LayoutArgs, PermuteFp4Args) =
         a.format == kFp4Mx ? (small ? dispatch_fp4_kernel<kFp4Mx, false, true>
                                     : dispatch_fp4_kernel<kFp4Mx, false, false>)
@@ -430,8 +500,9 @@ cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& a, co
                                     : dispatch_fp4_kernel<kFp4Nv, false, false>);
     int dev = 0, sms = 0, per_sm = 0;
     // Every CTA has to be resident for the grid barrier.
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess ||
-        smem > 100 * 1024 || cudaGetDevice(&dev) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kDispatchFp4Smem) != cudaSuccess ||
+        smem > kDispatchFp4Smem || cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kLayoutThreads, smem) != cudaSuccess)
         return cudaErrorNotSupported;
