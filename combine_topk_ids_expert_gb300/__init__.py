@@ -1317,8 +1317,8 @@ class Buffer:
         if nbytes is None:
             nbytes = self._layer_bytes[T, dff] = ep_moe_layer_workspace_bytes(self.handle, T, dff)
         if nbytes == 0:
-            raise EpError(_abi.EP_ERR_CAPACITY if T > 64 or T * self.K > 512
-                          else _abi.EP_ERR_INVALID_ARG, "ep_moe_layer")
+            raise EpError(_abi.EP_ERR_CAPACITY if T > min(64, self.cfg.num_max_tokens_per_rank)
+                          or T * self.K > 512 else _abi.EP_ERR_INVALID_ARG, "ep_moe_layer")
         with self._here(x_TD, topk_scores_TK, topk_expert_ids_TK, out,
                         *((w_gate_up.codes, w_down.codes) if fp4 else (w_gate_up, w_down))):
             if out is None:

@@ -41,7 +41,6 @@
 // Tried: warps that share a stage's rows (each waits for every slot), the row loop unrolled
 // over four rows (its code, 19 KB, comes from memory in every call), the scales of the weights
 // fetched before the arrival of the stage at hand.
-#include <cstdlib>
 #include "ep_fp4.cuh"
 #include "fp4_umma.cuh"
 
@@ -973,10 +972,8 @@ cudaError_t launch_layer_kernel(const LayerKernelArgs& a, const void* w, int64_t
     const int64_t pairs = (int64_t)a.T * a.K;
     const int64_t units = (pairs < a.E ? pairs : a.E) * a.tiles;
     int grid = 0;
-    int split = layer_split<C>(units, (a.din + C::kStageK - 1) / C::kStageK, num_sms, &grid);
+    const int split = layer_split<C>(units, (a.din + C::kStageK - 1) / C::kStageK, num_sms, &grid);
     if (split == 0) return cudaErrorNotSupported;
-    const char* ev = getenv(C::DOWN ? "XSPLITB" : "XSPLITA");
-    if (ev) { split = atoi(ev); grid = layer_grid(kernel, C::kSmem, split, num_sms); }
     CUtensorMap tm;
     const bool ok = C::FP4 ? make_code_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64)
                            : make_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64, 64);
