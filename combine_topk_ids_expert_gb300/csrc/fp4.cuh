@@ -164,6 +164,7 @@ __device__ __forceinline__ uint32_t fp4_scale_code(float amax, float g)
         return e == 255u ? kNanMx : e < 2u ? 0u : e - 2u;
     }
     if (!(amax < __uint_as_float(0x7F800000u))) return kNanNv;
+    if (amax == 0.0f) return 0u;   // g may be 0 for a matrix of zeros
     const float rinv = rcp_near(6.0f * g);
     uint16_t both;   // what lies a little below the quotient and a little above it round to
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"

@@ -473,7 +473,8 @@ EP_API ep_status ep_route_backward(const float* grad_scores_TK, const void* logi
  * block of consecutive elements of a row:
  *   EP_FP4_MX  blocks of 32, scale 2^(c - 127), c = floor(log2 amax) - 2 + 127, at least 0
  *   EP_FP4_NV  blocks of 16, scale s of ue4m3, amax / (6 g) rounded to the nearest and at
- *              most 448; g: one fp32 number for the matrix (tensor_scale, 2^-60 to 2^60), or 1
+ *              most 448; g: one fp32 number for the matrix (tensor_scale, 2^-60 to 2^60; 0 if it
+ *              is all zeros), or 1
  * An element stands for e2m1 * scale * g; quantised it is x / (scale * g) rounded to the
  * nearest (ties to the even code) and at most 6 in magnitude, decided on the exact quotient.
  * A block whose scale is 0 gets zeros. A block with an infinity or a NaN gets the scale

@@ -479,3 +479,76 @@ def test_quantize_unaligned_to_32_bytes(offset):
     out = flat.clone()[offset:offset + 40 * 256].view(40, 256)
     ep.ep_dequantize_fp4(q, out)
     assert torch.equal(out, q.dequantize())
+
+
+@pytest.mark.parametrize("E,rows", [(5, 1999), (2500, 7)])
+def test_quantize_many_rows(E, rows):
+    """More rows than warps at once, so that a warp goes from matrix to matrix, or over many."""
+    g = gen(4)
+    x = torch.randn((E, rows, 512), device="cuda", generator=g).bfloat16()
+    ts = 0.001 * (1 + torch.rand(E, device="cuda", generator=g))
+    q = ep.quantize_fp4(x, "nv", ts)
+    scales = ep.untile_fp4_scales(q.scales, E * rows).view(E, rows, -1)
+    for e in (0, 1, E // 2, E - 1):
+        codes, scale = F4.quantize(x[e], "nv", float(ts[e].double()))
+        assert torch.equal(scales[e].cpu(), scale)
+        assert torch.equal(F4.unpack(q.codes[e]), codes)
+        want = F4.values(codes, scale, "nv", 1.0).float() * ts[e].cpu()
+        assert torch.equal(q.dequantize(torch.float32)[e].cpu(), want)
+    # A matrix by itself is quantised as in the batch, its rows' other warps and lanes apart.
+    for e in range(0, E, 97):
+        alone = ep.quantize_fp4(x[e], "nv", ts[e:e + 1])
+        assert torch.equal(alone.codes, q.codes[e])
+        assert torch.equal(alone.dequantize(), q.dequantize()[e])
+
+
+def test_quantize_a_matrix_of_zeros():
+    """Scaled by its own largest magnitude, 0: scales and products of zeros, not NaN."""
+    x = torch.randn((3, 128, 256), device="cuda", generator=gen(5)).bfloat16()
+    x[1] = 0
+    ts = x.abs().amax((1, 2)).float() / (6 * 448)
+    q = ep.quantize_fp4(x, "nv", ts)
+    assert (ep.untile_fp4_scales(q.scales, 384)[128:256] == 0).all()
+    assert (q.dequantize() == 0)[1].all()
+    assert torch.isfinite(q.dequantize()).all()
+
+
+@pytest.mark.parametrize("T,D,E,K", [(2500, 1024, 8, 1), (1500, 640, 4, 2), (900, 512, 24, 5),
+                                     (400, 256, 1024, 8), (300, 384, 64, 20)])
+def test_dispatch_fp4_with_a_barrier(T, D, E, K):
+    """Calls above 2048 pairs: tokens that wait in shared memory and others, few and many experts,
+    also captured and replayed on other ids."""
+    buf = ep.Buffer(T, D, E, 1, K)
+    x = torch.randn((T, D), device="cuda", generator=gen(6)).bfloat16()
+    scores = torch.rand((T, K), device="cuda", generator=gen(7))
+    ts = torch.tensor([0.0021], device="cuda")
+    whole = ep.quantize_fp4(x, "nv", ts)
+    token_scales = ep.untile_fp4_scales(whole.scales, T)
+    ids = make_ids(T, E, K, 8)
+
+    def check(d):
+        pos = d.layout.pos.flatten().long()
+        src = torch.arange(T * K, device="cuda")[pos >= 0]
+        pos = pos[pos >= 0]
+        assert torch.equal(pos.sort().values, torch.arange(len(pos), device="cuda"))
+        by_expert = ids.flatten().long()[src]
+        order = by_expert.sort(stable=True).indices
+        assert torch.equal(pos[order], torch.arange(len(pos), device="cuda"))
+        assert torch.equal(d.recv_x.codes[pos], whole.codes[src // K])
+        assert torch.equal(ep.untile_fp4_scales(d.recv_x.scales, d.recv_x.rows)[pos],
+                           token_scales[src // K])
+        assert torch.equal(d.recv_scores.flatten()[pos], scores.flatten()[src])
+        assert torch.equal(d.recv_src.flatten()[pos].long(), src)
+
+    check(buf.dispatch_fp4(x, scores, ids, tensor_scale=ts))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d = buf.dispatch_fp4(x, scores, ids, tensor_scale=ts)
+    for seed in (9, 10):
+        ids.copy_(make_ids(T, E, K, seed, drop=0.3))
+        graph.replay()
+        check(d)
+    del graph
+    assert buf.device_error() == 0
+    buf.close()
