@@ -55,6 +55,10 @@ constexpr int kEpiWarp0 = 2, kScaleWarp0 = 6, kRowWarp0 = 10;
 constexpr int kLayerThreads = 32 * (kRowWarp0 + kRowWarps);
 constexpr uint32_t kLayerTmem = 256;
 constexpr int kMaxSplit = 4;
+// Of a CTA's weights in the second kernel, fetched to L2 by the first: 1 token of bf16 (2 x 4096 x
+// 2048 x 2 experts) 30.0 us without, 28.8 with 96 KB, 28.4 with 192, 28.1 with 512; 1 token nv
+// (8 x 7168) 46.3, 46.3, 47.6 and 50.2, where more of them is in memory's way.
+constexpr int kNextBytes = 96 * 1024;
 constexpr int kFmtBf16 = 2;                     // beside kFp4Mx, kFp4Nv
 
 template <int FMT_, bool DOWN_>
@@ -103,6 +107,10 @@ struct LayerKernelArgs {
     int act;
     bool out_f32;
     uint32_t* err;
+    // First kernel: the second one's tiles, stages and clusters, and the stages of each of its CTAs
+    // that are fetched to L2 (0: none).
+    int next_tiles, next_stages, next_split, next_clusters, next_fetched;
+    const uint8_t* next_scales;
 };
 
 struct Chunk {
@@ -137,6 +145,14 @@ __device__ __forceinline__ void tma_load_2d_once(uint32_t dst, const CUtensorMap
         "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
         : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* tm, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
@@ -309,9 +325,44 @@ __device__ __forceinline__ float left_of(float v, uint32_t bf16)
     return (bf16 & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(bf16);
 }
 
+// The weights that this CTA's successor in the second kernel reads first, to L2, while this kernel
+// ends and that one works its routing out: HBM would have nothing to do.
+template <class C>
+__device__ __forceinline__ void fetch_next(const CUtensorMap& tm, const LayerKernelArgs& a,
+                                           const Chunk* s_chunk, int chunks, int lane)
+{
+    const int cluster = (int)blockIdx.x / a.next_split, rank = (int)blockIdx.x % a.next_split;
+    if (cluster >= a.next_clusters) return;
+    const int64_t units = (int64_t)chunks * a.next_tiles;
+    const int u_first = (int)(units * cluster / a.next_clusters);
+    const int u_last = (int)(units * (cluster + 1) / a.next_clusters);
+    const int k_first = rank * a.next_stages / a.next_split, k_last = (rank + 1) * a.next_stages / a.next_split;
+    int left = a.next_fetched;
+    for (int u = u_first; u < u_last; ++u) {
+        const int tile = u / chunks;
+        const int w0 = (s_chunk[u - tile * chunks].e * a.next_tiles + tile) * 128;
+        for (int k = k_first; k < k_last; ++k) {
+            if (--left < 0) return;
+            if (elect_one()) {
+                const int kc = k * (C::FP4 ? kFp4StageK / 2 : C::kStageK);
+                tma_prefetch_2d(&tm, kc, w0);
+                tma_prefetch_2d(&tm, kc, w0 + 64);
+            }
+            __syncwarp();
+            if constexpr (C::FP4) {
+                const int64_t tiles = a.wrows / 2 / (4 * Fp4<C::FMT>::kBlock), kt = (int64_t)k * C::kTiles;
+                if (lane < 4 * C::kTiles && kt + lane / 4 < tiles)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.next_scales + fp4_scale_at(w0, kt, tiles) +
+                                                                  lane * 128));
+            }
+        }
+    }
+}
+
 template <class C>
 __global__ void __launch_bounds__(kLayerThreads, 1)
-moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs a)
+moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_next,
+                 const LayerKernelArgs a)
 {
     constexpr int STAGES = C::STAGES, FMT = C::FMT;
     constexpr bool DOWN = C::DOWN;
@@ -545,6 +596,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const LayerKernelArgs
                 __syncwarp();
             }
         }
+        if constexpr (!DOWN)
+            if (ok) fetch_next<C>(tm_next, a, s_chunk, chunks, lane);
         // The copies this warp issued land before shared memory goes away.
         const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
         for (int i = (g > STAGES ? g - STAGES : 0); i < g; ++i)
@@ -962,46 +1015,52 @@ int layer_split(int64_t units, int stages, int num_sms, int* grid)
     return best;
 }
 
+// A kernel's clusters, and the map of its weights.
 template <class C>
-cudaError_t launch_layer_kernel(const LayerKernelArgs& a, const void* w, int64_t wlines, int num_sms,
-                                const LaunchOpts& o)
-{
-    auto kernel = moe_layer_kernel<C>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-    if (e != cudaSuccess) return e;
-    const int64_t pairs = (int64_t)a.T * a.K;
-    const int64_t units = (pairs < a.E ? pairs : a.E) * a.tiles;
-    int grid = 0;
-    const int split = layer_split<C>(units, (a.din + C::kStageK - 1) / C::kStageK, num_sms, &grid);
-    if (split == 0) return cudaErrorNotSupported;
+struct LayerPlan {
+    int split = 0, grid = 0, stages = 0;
     CUtensorMap tm;
-    const bool ok = C::FP4 ? make_code_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64)
-                           : make_map(&tm, w, (uint64_t)a.din, (uint64_t)wlines, 64, 64);
-    if (!ok) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (split > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)split;
-        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-        ++n;
+
+    cudaError_t make(const void* w, int64_t wlines, int64_t din, int64_t units, int num_sms)
+    {
+        const cudaError_t e = cudaFuncSetAttribute(moe_layer_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        stages = (int)((din + C::kStageK - 1) / C::kStageK);
+        split = layer_split<C>(units, stages, num_sms, &grid);
+        if (split == 0) return cudaErrorNotSupported;
+        const bool ok = C::FP4 ? make_code_map(&tm, w, (uint64_t)din, (uint64_t)wlines, 64)
+                               : make_map(&tm, w, (uint64_t)din, (uint64_t)wlines, 64, 64);
+        return ok ? cudaSuccess : cudaErrorInvalidValue;
     }
-    if (o.pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
+
+    cudaError_t launch(const LayerKernelArgs& a, const CUtensorMap& next, const LaunchOpts& o) const
+    {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        int n = 0;
+        if (split > 1) {
+            attr[n].id = cudaLaunchAttributeClusterDimension;
+            attr[n].val.clusterDim.x = (unsigned)split;
+            attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+            ++n;
+        }
+        if (o.pdl) {
+            attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[n].val.programmaticStreamSerializationAllowed = 1;
+            ++n;
+        }
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3(kLayerThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cfg.stream = o.stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = n;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_layer_kernel<C>, tm, next, a);
+        if (e == cudaSuccess && o.launches) ++*o.launches;
+        return e;
     }
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kLayerThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = o.stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, kernel, tm, a);
-    if (e == cudaSuccess && o.launches) ++*o.launches;
-    return e;
-}
+};
 
 template <int FMT>
 cudaError_t launch_layer_format(const MoeLayerArgs& f, int num_sms, const LaunchOpts& o)
@@ -1021,13 +1080,28 @@ cudaError_t launch_layer_format(const MoeLayerArgs& f, int num_sms, const Launch
     a.out = f.out;
     a.out_f32 = f.out_f32;
     a.err = f.err;
+    // Units as many as are likely: every pair another expert's.
+    const int64_t pairs = (int64_t)f.T * f.K, experts = pairs < f.E ? pairs : f.E;
+    LayerPlan<LayerCfg<FMT, false>> up;
+    LayerPlan<LayerCfg<FMT, true>> down;
+    cudaError_t e = up.make(f.w_gate_up, f.E * 2 * f.dff, f.D, experts * (f.dff / 64), num_sms);
+    if (e != cudaSuccess) return e;
+    e = down.make(f.w_down, f.E * f.D, f.dff, experts * (f.D / 128), num_sms);
+    if (e != cudaSuccess) return e;
+
     a.rows = static_cast<const uint16_t*>(f.x);
     a.w_scales = f.gate_up_scales;
     a.w_scale = f.gate_up_scale;
     a.din = (int)f.D;
     a.wrows = (int)(2 * f.dff);
     a.tiles = (int)(f.dff / 64);
-    const cudaError_t e = launch_layer_kernel<LayerCfg<FMT, false>>(a, f.w_gate_up, f.E * 2 * f.dff, num_sms, o);
+    a.next_tiles = (int)(f.D / 128);
+    a.next_stages = down.stages;
+    a.next_split = down.split;
+    a.next_clusters = down.grid / down.split;
+    a.next_fetched = kNextBytes / (int)LayerCfg<FMT, true>::kBytesA;
+    a.next_scales = f.down_scales;
+    e = up.launch(a, down.tm, o);
     if (e != cudaSuccess) return e;
     a.rows = f.h;
     a.w_scales = f.down_scales;
@@ -1035,7 +1109,7 @@ cudaError_t launch_layer_format(const MoeLayerArgs& f, int num_sms, const Launch
     a.din = (int)f.dff;
     a.wrows = (int)f.D;
     a.tiles = (int)(f.D / 128);
-    return launch_layer_kernel<LayerCfg<FMT, true>>(a, f.w_down, f.E * f.D, num_sms, o);
+    return down.launch(a, down.tm, o);
 }
 
 }  // namespace
