@@ -5,14 +5,17 @@
 // whose value is -inf or a NaN is never chosen, and a slot without an expert has id -1 and
 // score 0. Scores are scale * p, or scale * p / (sum of the chosen p).
 //
-// One warp to a token; lane l holds the values of NV experts from l NV on, as integers in the
-// order of the floats, sorted (equal ones by index; lanes of 16 or 32 are searched instead). A
-// round takes the warp's maximum of the lanes' first ones, of the lowest lane that has it, which
-// moves up its list: one warp reduction, one vote and one shuffle. Reading the logits once is the
-// floor (7.9 us for 32768 tokens of 256 experts with a mask); sorting and the rounds are what
-// bounds large calls: 23.5 us with 8 experts chosen, the integer pipe busy 80% of the time.
-// (Unsorted, with a second reduction for the lowest index and each lane searched every round:
-// 37 us.) The gradient of the same tokens takes 17.3 us at a floor of 10.4: 60% of HBM's rate.
+// One warp to a token; lane l holds the values of NV experts from l NV on, sorted (lanes of 32 are
+// searched instead). A round takes the warp's maximum of the lanes' first ones, of the lowest lane
+// that has it, which moves up its list: one warp reduction, one vote. Which of its lane's experts
+// a slot's value was is looked up at the end, as sorting values alone takes two instructions a
+// comparison, with their places five. Reading the logits once is the floor (7.9 us for 32768 tokens
+// of 256 experts with a mask); what bounds large calls is issuing instructions (82% of the slots):
+// 17.0 us with 8 chosen, of these 11 for one round and 0.8 for each further one. Steps: 37 us
+// unsorted, 23.5 with the places sorted along, 17.0. 512 experts (NV 16), sorted against searched:
+// 25 and 16 us for one chosen, 27 and 27 for four, 31 and 45 for eight. Warps that go from token to
+// token, the next one's values on their way, are slower (24.5: fewer of them fit). The gradient of
+// the same tokens takes 17 us at a floor of 10.4: 60% of HBM's rate.
 //
 // Normalised scores need the chosen logits alone: with m their maximum, softmax is
 // e^(l - m) / sum, and sigmoid(l) e^-min(m, 0) has no common factor left that underflows.
@@ -33,14 +36,6 @@ __device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i)
     return __ldcg(static_cast<const float*>(p) + i);
 }
 
-// Integers in the order of the floats, both zeros alike; 0 for what must not be chosen.
-__device__ __forceinline__ uint32_t order_of(float v)
-{
-    if (!(v > -kInf)) return 0u;
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -48,11 +43,12 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// The largest of the warp's, NaN left out.
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, d));
-    return v;
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
 // sigmoid(l) e^-m for m <= 0, where m = 0 if any of the logits it is used for is above 0.
@@ -108,99 +104,159 @@ __device__ __forceinline__ void load_row(const void* p, bool bf16, int64_t row, 
     }
 }
 
-template <int NV, bool BF16>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a)
+// Sorted, the largest first: odd-even merges of neighbours, pairs of pairs, and so on.
+template <int NV>
+__device__ __forceinline__ void sort_down(float (&v)[NV])
+{
+#pragma unroll
+    for (int p = 1; p < NV; p *= 2) {
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+            for (int j = k % p; j + k < NV; j += 2 * k) {
+#pragma unroll
+                for (int i = 0; i < k; ++i) {
+                    if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const float x = v[i + j], y = v[i + j + k];
+                        v[i + j] = fmaxf(x, y);
+                        v[i + j + k] = fminf(x, y);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// CTAs on an SM.
+constexpr int route_per_sm(int nv) { return nv <= 8 ? 12 : nv == 16 ? 8 : 6; }
+
+// WIDE: more than 32 slots, a lane then has two.
+template <int NV, bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kRouteThreads, route_per_sm(NV)) route_kernel(RouteArgs a)
 {
     griddep_wait();
+    constexpr int SLOTS = WIDE ? 2 : 1;
     const int lane = threadIdx.x & 31;
     const int64_t t = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) >> 5;
     if (t < a.T) {
         const int64_t row = t * a.E;
-        float v[NV];
         const bool whole = !a.normalize && !a.sigmoid;   // a sum over all of the token's logits
-        if (!a.select || whole) load_row<NV>(a.logits, BF16, row, lane, a.E, v);
-        uint32_t key[NV];
-        int idx[NV];
-        {
-            float w[NV];
-            if (a.select) load_row<NV>(a.select, false, row, lane, a.E, w);
+        constexpr bool kSorted = NV <= 16;
+        float v[NV], key[NV], sorted[kSorted ? NV : 1];
+        if (a.select) {
+            load_row<NV>(a.select, false, row, lane, a.E, key);
+            if (whole) load_row<NV>(a.logits, BF16, row, lane, a.E, v);
+        } else {
+            load_row<NV>(a.logits, BF16, row, lane, a.E, key);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                key[j] = order_of(a.select ? w[j] : v[j]);
-                idx[j] = lane * NV + j;
-            }
+            for (int j = 0; j < NV; ++j) v[j] = key[j];
         }
-        // Neighbours in turn (odd, even): only a greater key goes up, so equal ones stay in order.
-        constexpr bool kSorted = NV <= 8;
 #pragma unroll
-        for (int n = 0; n < (kSorted ? NV : 0); ++n) {
+        for (int j = 0; j < NV; ++j) key[j] = fmaxf(key[j], -kInf);   // no NaN
+        if constexpr (kSorted) {
 #pragma unroll
-            for (int j = n & 1; j + 1 < NV; j += 2) {
-                const bool swap = key[j + 1] > key[j];
-                const uint32_t hi = swap ? key[j + 1] : key[j], lo = swap ? key[j] : key[j + 1];
-                const int hi_i = swap ? idx[j + 1] : idx[j], lo_i = swap ? idx[j] : idx[j + 1];
-                key[j] = hi;
-                key[j + 1] = lo;
-                idx[j] = hi_i;
-                idx[j + 1] = lo_i;
-            }
+            for (int j = 0; j < NV; ++j) sorted[j] = key[j];
+            sort_down(sorted);
         }
-        int mine[2] = {-1, -1};       // slots lane and lane + 32
+        int mine[SLOTS];              // slots lane and lane + 32: experts
+        float key_of[SLOTS];          // the slots' keys,
+        int from_of[SLOTS];           // and the lanes they came from
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            mine[i] = -1;
+            key_of[i] = -kInf;
+            from_of[i] = 0;
+        }
         for (int k = 0; k < a.K; ++k) {
-            uint32_t best = key[0];
+            float best = kSorted ? sorted[0] : key[0];
             int at = 0;
             if (!kSorted) {
 #pragma unroll
                 for (int j = 1; j < NV; ++j) {
                     at = key[j] > best ? j : at;
-                    best = max(best, key[j]);
+                    best = fmaxf(best, key[j]);
                 }
             }
-            const uint32_t most = __reduce_max_sync(~0u, best);
-            if (most == 0u) break;    // nothing is left
+            const float most = warp_max(best);
+            if (most == -kInf) break;    // nothing is left
             const int from = __ffs(__ballot_sync(~0u, best == most)) - 1;
-            const int e = __shfl_sync(~0u, kSorted ? idx[0] : lane * NV + at, from);
+            const int e = kSorted ? 0 : __shfl_sync(~0u, lane * NV + at, from);
             if (lane == from) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    if (!kSorted) {
-                        key[j] = j == at ? 0u : key[j];
-                    } else {
-                        key[j] = j + 1 < NV ? key[j + 1 < NV ? j + 1 : j] : 0u;
-                        idx[j] = idx[j + 1 < NV ? j + 1 : j];
-                    }
+                    if constexpr (kSorted) sorted[j] = j + 1 < NV ? sorted[j + 1 < NV ? j + 1 : j] : -kInf;
+                    else key[j] = j == at ? -kInf : key[j];
                 }
             }
-            if (lane == (k & 31)) {
-                if (k < 32) mine[0] = e;
-                else mine[1] = e;
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                if (lane == k - 32 * i) {
+                    key_of[i] = most;
+                    from_of[i] = from;
+                    if (!kSorted) mine[i] = e;
+                }
             }
         }
-        float l[2], p[2];
+        if constexpr (kSorted) {
+            // Where in its lane a slot's key was (sorting keys with their places takes five
+            // instructions a comparison, keys alone two): of several equal ones, which come out
+            // one after the other, as many are skipped as slots before this one had.
+            uint64_t again = 0u;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            l[i] = mine[i] >= 0 ? load_logit(a.logits, BF16, row + mine[i]) : -kInf;
+            for (int i = 0; i < SLOTS; ++i) {
+                float before = __shfl_up_sync(~0u, key_of[i], 1);
+                int lane_before = __shfl_up_sync(~0u, from_of[i], 1);
+                if (i > 0) {
+                    const float end = __shfl_sync(~0u, key_of[0], 31);
+                    const int lane_end = __shfl_sync(~0u, from_of[0], 31);
+                    if (lane == 0) {
+                        before = end;
+                        lane_before = lane_end;
+                    }
+                }
+                again |= (uint64_t)__ballot_sync(~0u, (i > 0 || lane > 0) && key_of[i] != -kInf &&
+                                                          before == key_of[i] && lane_before == from_of[i])
+                         << (32 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                uint32_t equal = 0u;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (__shfl_sync(~0u, key[j], from_of[i]) == key_of[i]) equal |= 1u << j;
+                if (again != 0u)
+                    for (int n = __clzll(~(again << (63 - 32 * i - lane))); n > 0; --n) equal &= equal - 1u;
+                if (key_of[i] != -kInf) mine[i] = from_of[i] * NV + __ffs(equal) - 1;
+            }
+        }
+        float l[SLOTS], p[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            l[i] = mine[i] < 0 ? -kInf : a.select ? load_logit(a.logits, BF16, row + mine[i]) : key_of[i];
         float total = 1.0f;
         if (a.normalize) {
-            float m = warp_max(fmaxf(l[0], l[1]));
+            float m = warp_max(fmaxf(l[0], l[SLOTS - 1]));
             if (a.sigmoid) m = fminf(m, 0.0f);
+            float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < SLOTS; ++i) {
                 p[i] = mine[i] < 0 || m == -kInf ? 0.0f
                        : a.sigmoid ? sigmoid_over(l[i], m) : expf(l[i] - m);
-            total = warp_sum(p[0] + p[1]);
+                sum += p[i];
+            }
+            total = warp_sum(sum);
         } else if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) p[i] = mine[i] < 0 ? 0.0f : sigmoid_over(l[i], 0.0f);
+            for (int i = 0; i < SLOTS; ++i) p[i] = mine[i] < 0 ? 0.0f : sigmoid_over(l[i], 0.0f);
         } else {
             float m;
             softmax_of_row(v, &m, &total);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < SLOTS; ++i)
                 p[i] = mine[i] < 0 || m == -kInf ? 0.0f : expf(l[i] - m);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SLOTS; ++i) {
             const int k = i * 32 + lane;
             if (k < a.K) {
                 a.ids[t * a.K + k] = mine[i];
@@ -304,8 +360,11 @@ cudaError_t launch_nv(const RouteArgs& a, bool backward, const LaunchOpts& o)
     if (backward)
         return a.bf16 ? launch_kernel(route_backward_kernel<NV, true>, grid, kRouteThreads, 0, o, a)
                       : launch_kernel(route_backward_kernel<NV, false>, grid, kRouteThreads, 0, o, a);
-    return a.bf16 ? launch_kernel(route_kernel<NV, true>, grid, kRouteThreads, 0, o, a)
-                  : launch_kernel(route_kernel<NV, false>, grid, kRouteThreads, 0, o, a);
+    if (a.K > 32)
+        return a.bf16 ? launch_kernel(route_kernel<NV, true, true>, grid, kRouteThreads, 0, o, a)
+                      : launch_kernel(route_kernel<NV, false, true>, grid, kRouteThreads, 0, o, a);
+    return a.bf16 ? launch_kernel(route_kernel<NV, true, false>, grid, kRouteThreads, 0, o, a)
+                  : launch_kernel(route_kernel<NV, false, false>, grid, kRouteThreads, 0, o, a);
 }
 
 cudaError_t launch_any(const RouteArgs& a, bool backward, const LaunchOpts& o)

@@ -197,3 +197,23 @@ def test_routed_layer_dispatches():
     assert (gl[15:] == 0).all() and gl[:15].abs().sum() > 0
     assert buf.device_error() == 0
     buf.close()
+
+
+@pytest.mark.parametrize("T,E,K", [(40, 8, 4), (40, 30, 30), (60, 100, 12), (60, 256, 8),
+                                   (60, 256, 64), (30, 400, 40), (30, 512, 10), (20, 900, 33)])
+@pytest.mark.parametrize("levels", [1, 2, 5])
+def test_many_equal_values(T, E, K, levels):
+    """Runs of equal values in a lane, over lanes and over the 32nd slot; both zeros, infinities."""
+    g = gen(E + K + levels)
+    select = torch.randint(0, levels, (T, E), device="cuda", generator=g).float()
+    select[::3] *= -0.0
+    select[1, E // 3:E // 3 + 4] = math.inf
+    select[2, E // 2:] = -math.inf
+    select[4, ::2] = math.nan
+    logits = torch.randn((T, E), device="cuda", generator=g)
+    ids, scores = ep.route(logits, K, "sigmoid", select=select)
+    want = choose(select, K)
+    assert torch.equal(ids.long(), want)
+    by_logits, _ = ep.route(select.bfloat16(), K, "sigmoid")
+    assert torch.equal(by_logits.long(), choose(select.bfloat16(), K))
+    assert torch.isfinite(scores).all()
