@@ -15,7 +15,8 @@
 // unsorted, 23.5 with the places sorted along, 17.0. 512 experts (NV 16), sorted against searched:
 // 25 and 16 us for one chosen, 27 and 27 for four, 31 and 45 for eight. Warps that go from token to
 // token, the next one's values on their way, are slower (24.5: fewer of them fit). The gradient of
-// the same tokens takes 17 us at a floor of 10.4: 60% of HBM's rate.
+// the same tokens takes 11.9 us at a floor of 10.4 (17 with two slots to every lane, stored by single
+// elements).
 //
 // Normalised scores need the chosen logits alone: with m their maximum, softmax is
 // e^(l - m) / sum, and sigmoid(l) e^-min(m, 0) has no common factor left that underflows.
@@ -55,7 +56,7 @@ __device__ __forceinline__ float warp_max(float v)
 __device__ __forceinline__ float sigmoid_over(float l, float m)
 {
     const float e = expf(-fabsf(l));
-    return l >= 0.0f ? 1.0f / (1.0f + e) : expf(l - m) / (1.0f + e);
+    return (l >= 0.0f ? 1.0f : expf(l - m)) / (1.0f + e);
 }
 
 // A token's softmax statistics over all experts: the maximum and the sum of e^(l - max).
@@ -275,23 +276,25 @@ __global__ void __launch_bounds__(kRouteThreads, route_per_sm(NV)) route_kernel(
 //   normalised sigmoid   the same with a further factor 1 - p_e
 // The row is put together in shared memory; an id that occurs more than once adds up in the
 // order of its slots.
-template <int NV, bool BF16>
+template <int NV, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs a)
 {
-    __shared__ float s_row[kRouteThreads / 32][NV * 32];
+    constexpr int SLOTS = WIDE ? 2 : 1;
+    __shared__ __align__(16) float s_row[kRouteThreads / 32][NV * 32];
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) >> 5;
     if (t < a.T) {
         const int64_t row = t * a.E;
-        int id[2];
-        float l[2], c[2], w[2];
+        int id[SLOTS];
+        float l[SLOTS], c[SLOTS], w[SLOTS];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SLOTS; ++i) {
             const int k = i * 32 + lane;
-            id[i] = k < a.K ? __ldcg(a.ids + t * a.K + k) : -1;
-            if (id[i] < 0 || id[i] >= a.E) id[i] = -1;
-            c[i] = id[i] >= 0 ? a.scale * __ldcg(a.grad_scores + t * a.K + k) : 0.0f;
+            const int raw = k < a.K ? __ldcg(a.ids + t * a.K + k) : -1;
+            const float grad = k < a.K ? __ldcg(a.grad_scores + t * a.K + k) : 0.0f;
+            id[i] = raw >= 0 && raw < a.E ? raw : -1;
+            c[i] = id[i] >= 0 ? a.scale * grad : 0.0f;
             l[i] = id[i] >= 0 ? load_logit(a.logits, BF16, row + id[i]) : -kInf;
         }
         float v[NV];
@@ -303,27 +306,34 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
                 v[j] = j * 32 + lane < a.E ? load_logit(a.logits, BF16, row + j * 32 + lane) : -kInf;
             softmax_of_row(v, &most, &sum);
         } else if (a.normalize) {
-            most = warp_max(fmaxf(l[0], l[1]));
+            most = warp_max(fmaxf(l[0], l[SLOTS - 1]));
             if (a.sigmoid) most = fminf(most, 0.0f);
         }
         // w: p, or s where scores are normalised.
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < SLOTS; ++i)
             w[i] = id[i] < 0 || most == -kInf ? 0.0f
                    : a.sigmoid ? sigmoid_over(l[i], most) : expf(l[i] - most);
-        if (a.normalize) sum = warp_sum(w[0] + w[1]);
+        if (a.normalize) sum = warp_sum(WIDE ? w[0] + w[SLOTS - 1] : w[0]);
         if (sum == 0.0f) sum = 1.0f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) w[i] /= sum;
-        if (a.normalize || whole) inner = warp_sum(c[0] * w[0] + c[1] * w[1]);
+        for (int i = 0; i < SLOTS; ++i) w[i] /= sum;
+        if (a.normalize || whole) inner = warp_sum(WIDE ? c[0] * w[0] + c[SLOTS - 1] * w[SLOTS - 1] : c[0] * w[0]);
         float* r = s_row[warp];
+        if (whole) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            r[j * 32 + lane] =
-                whole && j * 32 + lane < a.E && most > -kInf ? -inner * (expf(v[j] - most) / sum) : 0.0f;
+            for (int j = 0; j < NV; ++j)
+                r[j * 32 + lane] =
+                    j * 32 + lane < a.E && most > -kInf ? -inner * (expf(v[j] - most) / sum) : 0.0f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < (NV + 3) / 4; ++j)
+                if (NV >= 4 || lane < NV * 8)
+                    *reinterpret_cast<float4*>(r + (j * 32 + lane) * 4) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SLOTS; ++i) {
             if (i * 32 >= a.K) break;
             // 1 - p = sigmoid(-l).
             const float d = w[i] * (whole ? c[i] : a.normalize ? c[i] - inner : c[i]) *
@@ -336,16 +346,34 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
                 __syncwarp();
             }
         }
+        // Four elements to a lane where the rows allow it.
+        if (a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.grad_logits) % 16 == 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = j * 32 + lane;
-            if (e >= a.E) continue;
-            if (BF16) {
-                uint32_t b;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(0.0f), "f"(r[e]));
-                static_cast<uint16_t*>(a.grad_logits)[row + e] = (uint16_t)b;
-            } else {
-                static_cast<float*>(a.grad_logits)[row + e] = r[e];
+            for (int j = 0; j < (NV + 3) / 4; ++j) {
+                const int e = (j * 32 + lane) * 4;
+                if (e >= a.E) break;
+                const float4 q = *reinterpret_cast<const float4*>(r + e);
+                if (BF16) {
+                    uint2 h;
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(q.y), "f"(q.x));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(q.w), "f"(q.z));
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.grad_logits) + row + e) = h;
+                } else {
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.grad_logits) + row + e) = q;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int e = j * 32 + lane;
+                if (e >= a.E) break;
+                if (BF16) {
+                    uint32_t h;
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(0.0f), "f"(r[e]));
+                    static_cast<uint16_t*>(a.grad_logits)[row + e] = (uint16_t)h;
+                } else {
+                    static_cast<float*>(a.grad_logits)[row + e] = r[e];
+                }
             }
         }
     }
@@ -357,14 +385,15 @@ cudaError_t launch_nv(const RouteArgs& a, bool backward, const LaunchOpts& o)
 {
     const int64_t ctas = (a.T + kRouteThreads / 32 - 1) / (kRouteThreads / 32);
     const dim3 grid((unsigned)ctas);
+    const bool wide = a.K > 32;
+    void (*kernel)(RouteArgs);
     if (backward)
-        return a.bf16 ? launch_kernel(route_backward_kernel<NV, true>, grid, kRouteThreads, 0, o, a)
-                      : launch_kernel(route_backward_kernel<NV, false>, grid, kRouteThreads, 0, o, a);
-    if (a.K > 32)
-        return a.bf16 ? launch_kernel(route_kernel<NV, true, true>, grid, kRouteThreads, 0, o, a)
-                      : launch_kernel(route_kernel<NV, false, true>, grid, kRouteThreads, 0, o, a);
-    return a.bf16 ? launch_kernel(route_kernel<NV, true, false>, grid, kRouteThreads, 0, o, a)
-                  : launch_kernel(route_kernel<NV, false, false>, grid, kRouteThreads, 0, o, a);
+        kernel = a.bf16 ? (wide ? route_backward_kernel<NV, true, true> : route_backward_kernel<NV, true, false>)
+                        : (wide ? route_backward_kernel<NV, false, true> : route_backward_kernel<NV, false, false>);
+    else
+        kernel = a.bf16 ? (wide ? route_kernel<NV, true, true> : route_kernel<NV, true, false>)
+                        : (wide ? route_kernel<NV, false, true> : route_kernel<NV, false, false>);
+    return launch_kernel(kernel, grid, kRouteThreads, 0, o, a);
 }
 
 cudaError_t launch_any(const RouteArgs& a, bool backward, const LaunchOpts& o)
