@@ -807,6 +807,42 @@ class DispatchResult:
     layout: Layout
 
 
+class _OfWorkspace:
+    """Fields that are views of a buffer's workspace, each made when it is first asked for: nine
+    of them cost more than a small call's kernels take."""
+
+    @classmethod
+    def _with(cls, views: dict, **fields):
+        """views: name: (the workspace as elements of the field's type, offset in these, shape)."""
+        o = object.__new__(cls)
+        o.__dict__.update(fields)
+        o.__dict__["_views"] = views
+        return o
+
+    def __getattr__(self, name: str):
+        view = self.__dict__.get("_views", {}).get(name)
+        if view is None:
+            raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
+        t = self.__dict__[name] = _strided(*view)
+        return t
+
+
+def _strided(base: torch.Tensor, offset: int, shape: tuple) -> torch.Tensor:
+    strides, n = [], 1
+    for s in reversed(shape):
+        strides.append(n)
+        n *= s
+    return base.as_strided(shape, strides[::-1], offset)
+
+
+class _WorkspaceLayout(_OfWorkspace, Layout):
+    pass
+
+
+class _WorkspaceResult(_OfWorkspace, DispatchResult):
+    pass
+
+
 @dataclass
 class DedupResult:
     recv_x: torch.Tensor              # [R, P, D]: one row per distinct (token, rank)
@@ -851,41 +887,42 @@ class Buffer:
         self._layer_bytes: dict = {}
 
     # -- views -------------------------------------------------------------
-    def _view(self, ptr: int, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
-        # One operation on the workspace as elements of this type: a result is nine of these.
+    def _place(self, ptr: int, dtype: torch.dtype, shape: tuple) -> tuple:
+        """What _strided takes for the workspace's elements of this type from ptr on."""
         base = self._typed.get(dtype)
         if base is None:
-            base = self._typed[dtype] = self.workspace.view(dtype)
-        strides, n = [], 1
-        for s in reversed(shape):
-            strides.append(n)
-            n *= s
-        return base.as_strided(shape, strides[::-1],
-                               base.storage_offset() + (ptr - self._base) // base.element_size())
+            typed = self.workspace.view(dtype)
+            base = self._typed[dtype] = typed, typed.storage_offset(), typed.element_size()
+        typed, first, size = base
+        return typed, first + (ptr - self._base) // size, shape
+
+    def _view(self, ptr: int, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
+        return _strided(*self._place(ptr, dtype, shape))
 
     def _layout(self, L: EpLayout) -> Layout:
         T, E, R, K = L.num_tokens, self.E, self.R, self.K
         self._stride = L.rank_stride
-        i32 = torch.int32
-        return Layout(
-            tokens_per_expert=self._view(L.tokens_per_expert, i32, (E,)),
-            expert_offset=self._view(L.expert_offset, i32, (E,)),
-            rows_per_rank=self._view(L.rows_per_rank, i32, (R,)),
-            rank_prefix=self._view(L.rank_prefix, i32, (R,)),
-            tokens_in_rank=self._view(L.tokens_in_rank, i32, (R,)),
-            pos=self._view(L.pos, i32, (T, K)),
+        i32, at = torch.int32, self._place
+        return _WorkspaceLayout._with(
+            {"tokens_per_expert": at(L.tokens_per_expert, i32, (E,)),
+             "expert_offset": at(L.expert_offset, i32, (E,)),
+             "rows_per_rank": at(L.rows_per_rank, i32, (R,)),
+             "rank_prefix": at(L.rank_prefix, i32, (R,)),
+             "tokens_in_rank": at(L.tokens_in_rank, i32, (R,)),
+             "pos": at(L.pos, i32, (T, K))},
             num_tokens=T, padded_tokens=L.padded_tokens, rank_stride=L.rank_stride,
             packed=bool(L.packed))
 
-    def _dispatch_result(self, d: EpDispatchOut) -> DispatchResult:
+    def _dispatch_result(self, d: EpDispatchOut, recv_x: FP4 | None = None) -> DispatchResult:
         S = d.layout.rank_stride
         self._stride = S
         lead = (self.R * S,) if self.packed else (self.R, S)
-        return DispatchResult(
-            recv_x=self._view(d.recv_x, self.dtype, lead + (self.D,)),
-            recv_scores=self._view(d.recv_scores, torch.float32, lead),
-            recv_src=self._view(d.recv_src, torch.int32, lead),
-            layout=self._layout(d.layout))
+        views = {"recv_scores": self._place(d.recv_scores, torch.float32, lead),
+                 "recv_src": self._place(d.recv_src, torch.int32, lead)}
+        if recv_x is None:
+            views["recv_x"] = self._place(d.recv_x, self.dtype, lead + (self.D,))
+            return _WorkspaceResult._with(views, layout=self._layout(d.layout))
+        return _WorkspaceResult._with(views, recv_x=recv_x, layout=self._layout(d.layout))
 
     # -- memory of results -----------------------------------------------------
     def _empty(self, shape: tuple, dtype: torch.dtype, stream, kept: bool = True) -> torch.Tensor:
@@ -1197,11 +1234,7 @@ class Buffer:
                                stream)
             d = ep_dispatch_fp4(self.handle, x_TD, topk_scores_TK, topk_expert_ids_TK, T, N, q,
                                 stream)
-        S = d.layout.rank_stride
-        lead = (self.R * S,) if self.packed else (self.R, S)
-        return DispatchResult(recv_x=q, recv_scores=self._view(d.recv_scores, torch.float32, lead),
-                              recv_src=self._view(d.recv_src, torch.int32, lead),
-                              layout=self._layout(d.layout))
+        return self._dispatch_result(d, q)
 
     def _fp4_rows(self, rows: int, cols: int, format: str, tensor_scale, stream,
                   kept: bool = True) -> FP4:
