@@ -812,10 +812,11 @@ class _OfWorkspace:
     of them cost more than a small call's kernels take."""
 
     @classmethod
-    def _with(cls, views: dict, **fields):
-        """views: name: (the workspace as elements of the field's type, offset in these, shape)."""
+    def _with(cls, space: _Space, views: dict, **fields):
+        """views: name: (address, type, shape)."""
         o = object.__new__(cls)
         o.__dict__.update(fields)
+        o.__dict__["_space"] = space
         o.__dict__["_views"] = views
         return o
 
@@ -823,16 +824,26 @@ class _OfWorkspace:
         view = self.__dict__.get("_views", {}).get(name)
         if view is None:
             raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
-        t = self.__dict__[name] = _strided(*view)
+        t = self.__dict__[name] = self._space.view(*view)
         return t
 
 
-def _strided(base: torch.Tensor, offset: int, shape: tuple) -> torch.Tensor:
-    strides, n = [], 1
-    for s in reversed(shape):
-        strides.append(n)
-        n *= s
-    return base.as_strided(shape, strides[::-1], offset)
+class _Space:
+    """A workspace, and what it is as elements of the types that were asked for."""
+
+    def __init__(self, workspace: torch.Tensor):
+        self.workspace, self.base, self.typed = workspace, workspace.data_ptr(), {}
+
+    def view(self, ptr: int, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
+        base = self.typed.get(dtype)
+        if base is None:
+            base = self.typed[dtype] = self.workspace.view(dtype)
+        strides, n = [], 1
+        for s in reversed(shape):
+            strides.append(n)
+            n *= s
+        return base.as_strided(shape, strides[::-1],
+                               base.storage_offset() + (ptr - self.base) // base.element_size())
 
 
 class _WorkspaceLayout(_OfWorkspace, Layout):
@@ -882,34 +893,25 @@ class Buffer:
         with torch.cuda.device(dev):
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             self.handle = ep_buffer_init(self.cfg, self.workspace)
-        self._base = self.workspace.data_ptr()
-        self._typed: dict = {}
+        self._space = _Space(self.workspace)
         self._layer_bytes: dict = {}
 
     # -- views -------------------------------------------------------------
-    def _place(self, ptr: int, dtype: torch.dtype, shape: tuple) -> tuple:
-        """What _strided takes for the workspace's elements of this type from ptr on."""
-        base = self._typed.get(dtype)
-        if base is None:
-            typed = self.workspace.view(dtype)
-            base = self._typed[dtype] = typed, typed.storage_offset(), typed.element_size()
-        typed, first, size = base
-        return typed, first + (ptr - self._base) // size, shape
-
     def _view(self, ptr: int, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
-        return _strided(*self._place(ptr, dtype, shape))
+        return self._space.view(ptr, dtype, shape)
 
     def _layout(self, L: EpLayout) -> Layout:
         T, E, R, K = L.num_tokens, self.E, self.R, self.K
         self._stride = L.rank_stride
-        i32, at = torch.int32, self._place
+        i32 = torch.int32
         return _WorkspaceLayout._with(
-            {"tokens_per_expert": at(L.tokens_per_expert, i32, (E,)),
-             "expert_offset": at(L.expert_offset, i32, (E,)),
-             "rows_per_rank": at(L.rows_per_rank, i32, (R,)),
-             "rank_prefix": at(L.rank_prefix, i32, (R,)),
-             "tokens_in_rank": at(L.tokens_in_rank, i32, (R,)),
-             "pos": at(L.pos, i32, (T, K))},
+            self._space,
+            {"tokens_per_expert": (L.tokens_per_expert, i32, (E,)),
+             "expert_offset": (L.expert_offset, i32, (E,)),
+             "rows_per_rank": (L.rows_per_rank, i32, (R,)),
+             "rank_prefix": (L.rank_prefix, i32, (R,)),
+             "tokens_in_rank": (L.tokens_in_rank, i32, (R,)),
+             "pos": (L.pos, i32, (T, K))},
             num_tokens=T, padded_tokens=L.padded_tokens, rank_stride=L.rank_stride,
             packed=bool(L.packed))
 
@@ -917,12 +919,13 @@ class Buffer:
         S = d.layout.rank_stride
         self._stride = S
         lead = (self.R * S,) if self.packed else (self.R, S)
-        views = {"recv_scores": self._place(d.recv_scores, torch.float32, lead),
-                 "recv_src": self._place(d.recv_src, torch.int32, lead)}
+        views = {"recv_scores": (d.recv_scores, torch.float32, lead),
+                 "recv_src": (d.recv_src, torch.int32, lead)}
+        layout = self._layout(d.layout)
         if recv_x is None:
-            views["recv_x"] = self._place(d.recv_x, self.dtype, lead + (self.D,))
-            return _WorkspaceResult._with(views, layout=self._layout(d.layout))
-        return _WorkspaceResult._with(views, recv_x=recv_x, layout=self._layout(d.layout))
+            views["recv_x"] = d.recv_x, self.dtype, lead + (self.D,)
+            return _WorkspaceResult._with(self._space, views, layout=layout)
+        return _WorkspaceResult._with(self._space, views, recv_x=recv_x, layout=layout)
 
     # -- memory of results -----------------------------------------------------
     def _empty(self, shape: tuple, dtype: torch.dtype, stream, kept: bool = True) -> torch.Tensor:

@@ -10,6 +10,7 @@
 // conversions (before: from each quotient's last bits), the next row on its way during this
 // one's work, and one resident wave of CTAs.
 #include <algorithm>
+#include <mutex>
 #include "ep_fp4.cuh"
 #include "fp4.cuh"
 #include "umma.cuh"
@@ -477,6 +478,37 @@ cudaError_t launch_permute_fp4(const PermuteFp4Args& a, int num_sms, const Launc
 
 int dispatch_fp4_tiles_per_sm() { return kDispatchFp4PerSm; }
 
+namespace {
+
+// CTAs of the one-pass dispatch that the device holds at once, 0 if it cannot be asked; the latest
+// answers are kept (asking takes as long as the launch).
+int64_t resident_ctas(const void* kernel, size_t smem)
+{
+    struct Entry {
+        const void* kernel;
+        int dev;
+        size_t smem;
+        int64_t ctas;
+    };
+    static std::mutex mu;
+    static Entry entries[16];
+    static unsigned next = 0;
+    int dev = 0, sms = 0, per_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const Entry& e : entries)
+        if (e.kernel == kernel && e.dev == dev && e.smem == smem) return e.ctas;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kDispatchFp4Smem) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kLayoutThreads, smem) != cudaSuccess)
+        return 0;
+    entries[next++ % 16] = {kernel, dev, smem, (int64_t)per_sm * sms};
+    return (int64_t)per_sm * sms;
+}
+
+}  // namespace
+
 cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& args, const LaunchOpts& o,
                                 bool pdl_ok, int64_t small_pairs)
 {
@@ -498,15 +530,9 @@ cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& args,
                                     : dispatch_fp4_kernel<kFp4Nv, true, false>)
                            : (small ? dispatch_fp4_kernel<kFp4Nv, false, true>
                                     : dispatch_fp4_kernel<kFp4Nv, false, false>);
-    int dev = 0, sms = 0, per_sm = 0;
     // Every CTA has to be resident for the grid barrier.
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kDispatchFp4Smem) != cudaSuccess ||
-        smem > kDispatchFp4Smem || cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kLayoutThreads, smem) != cudaSuccess)
+    if (smem > kDispatchFp4Smem || resident_ctas(reinterpret_cast<const void*>(kernel), smem) < l.ntiles)
         return cudaErrorNotSupported;
-    if ((int64_t)per_sm * sms < l.ntiles) return cudaErrorNotSupported;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(l.ntiles);
     cfg.blockDim = dim3(kLayoutThreads);
