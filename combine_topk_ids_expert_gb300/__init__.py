@@ -1325,8 +1325,8 @@ class Buffer:
                   stream=None) -> torch.Tensor:
         """dispatch, the experts' gated block and combine in two kernels, for at most 64 tokens
         and 512 (token, k) pairs: weights w_gate_up [E, 2 dff, D] and w_down [E, D, dff], bf16
-        tensors or FP4 (activations keep bf16's precision). Leaves the last dispatch's layout and
-        receive rows alone."""
+        tensors or FP4 (activations within 2^-22 of their block's largest: include/ep.h). Leaves
+        the last dispatch's layout and receive rows alone."""
         fp4 = isinstance(w_gate_up, FP4)
         if fp4 != isinstance(w_down, FP4):
             raise TypeError("w_gate_up and w_down must both be tensors or both FP4")

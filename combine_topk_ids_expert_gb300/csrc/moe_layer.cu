@@ -10,16 +10,23 @@
 // weights on their way: 4-bit codes go to the block-scaled instructions as they lie, which
 // leaves the CUDA cores with the activations alone.
 //
-// An activation keeps its precision. With bf16 weights x enters as it is, and h, fp32, as the
-// sum of two bf16 rows (what the first leaves is within 2^-8 of it, what both leave within 2^-16).
-// With 4-bit weights a row enters as rows of e2m1 digits, four for x and five for h, that share a power of two s for each block of the weights' size,
-//     x = s (d0 + d1 / 8 + d2 / 64 + d3 / 512) + rest,   |d| <= 4, |rest| <= s / 1024,
-// s = 2^(floor(log2 amax) - 1): each digit is what is left rounded to e2m1 (half steps below
-// 2, whole ones up to 4), which leaves at most 1/2, an eighth of the next digit's range. A bf16
-// element down to a sixteenth of its block's largest is exact, smaller ones are within 2^-11
-// of the largest; h is within 2^-14. The digits are columns of one product, joined in the epilogue.
+// With bf16 weights x enters as it is, and h, fp32, as the sum of two bf16 rows (what the first
+// leaves is within 2^-8 of it, what both leave within 2^-16).
+// With 4-bit weights a row enters as eight rows of e2m1 digits that share a power of two s for each
+// block of the weights' size:
+//     x = s (d0 + d1 / 8 + d2 / 64 + ... + d7 / 8^7) + rest,   -4 <= d <= 3,   |rest| <= s / 2^22,
+// s = 2^floor(log2 amax): x / s is rounded to an integer of 2^-21, whose octal digits, each 4 less,
+// are all values of e2m1. A bf16 element down to 2^-14 of its block's largest is exact, every other
+// one and h within 2^-22 of the largest, about what fp32 sums with the largest would leave, so
+// that elements beside a dominant one keep their bits. (Four digits of x and five of h left 2^-11
+// and 2^-14: beside an element 3 x 2^12 times their size the others were lost.) The digits are
+// columns of one product, joined in the epilogue. Taken from an integer all at once they cost what
+// four cost rounded one after the other; their rows in the ring leave it 5 stages of 7. Against the
+// shorter digits: 1 token 47.4 for 46.3 us (nv, 8 of 256, 7168 wide), 16 tokens 417 for 410 (mx),
+// 64 tokens over 8 experts 141 for 123 (4096 wide).
 // nv scales (ue4m3) reach over 18 binades only: they count from the row's largest block, and
-// blocks 2^17 below it are within 2^-28 of the row's largest.
+// blocks 2^17 below it are within 2^-39 of the row's largest. mx's scales are s / 8, and the
+// sums 8 times that, so that s times a digit of 2 stays finite.
 //
 // Work: a unit is a chunk of up to 16 rows of an expert x a tile of 128 weight rows (64 gate
 // and 64 up rows of the same columns in the first kernel). A cluster of 1, 2 or 4 CTAs shares
@@ -48,12 +55,11 @@ namespace ep {
 namespace {
 
 constexpr int kChunkRows = 16;                  // token rows of a unit
-constexpr int kDigitsX = 4, kDigitsH = 5;
-constexpr int kAccCols = kChunkRows * kDigitsH; // columns set aside for an accumulator
-constexpr int kRowWarps = 6, kEpiWarps = 4, kScaleWarps = 4;
+constexpr int kDigits = 8;                      // of x and of h (4-bit weights)
+constexpr int kAccCols = kChunkRows * kDigits;  // columns set aside for an accumulator
+constexpr int kEpiWarps = 4, kScaleWarps = 4;
 constexpr int kEpiWarp0 = 2, kScaleWarp0 = 6, kRowWarp0 = 10;
-constexpr int kLayerThreads = 32 * (kRowWarp0 + kRowWarps);
-constexpr uint32_t kLayerTmem = 256;
+constexpr uint32_t kLayerTmem = 512;            // a CTA has its SM for itself (shared memory)
 constexpr int kMaxSplit = 4;
 // Of a CTA's weights in the second kernel, fetched to L2 by the first: 1 token of bf16 (2 x 4096 x
 // 2048 x 2 experts) 30.0 us without, 28.8 with 96 KB, 28.4 with 192, 28.1 with 512; 1 token nv
@@ -67,7 +73,7 @@ struct LayerCfg {
     static constexpr bool DOWN = DOWN_, FP4 = FMT_ != kFmtBf16;
     static constexpr int kStageK = FP4 ? kFp4StageK : 64;       // 128 bytes of a row
     // Rows of the N side that a token row becomes: digits, or h's two bf16 terms.
-    static constexpr int kTerms = FP4 ? (DOWN ? kDigitsH : kDigitsX) : DOWN ? 2 : 1;
+    static constexpr int kTerms = FP4 ? kDigits : DOWN ? 2 : 1;
     static constexpr int kCols = kChunkRows * kTerms;
     static constexpr int kTiles = FP4 ? Fp4Mma<FP4 ? FMT_ : kFp4Mx>::kTiles : 0;
     static constexpr uint32_t kBytesA = kBM * 128, kBytesB = kCols * 128;
@@ -80,6 +86,8 @@ struct LayerCfg {
     static constexpr int STAGES = kFit > 12 ? 12 : kFit;
     static constexpr size_t kSmem = kFixed + (size_t)STAGES * kStageBytes;
     static constexpr uint32_t kScaleCol0 = 2 * kAccCols;               // after two accumulators
+    static constexpr int kRowWarps = FP4 ? 5 : 6;                      // at most STAGES (below)
+    static constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
     // Arrivals that fill a stage: the copy of A, the warp that brings its scales, that of the rows.
     static constexpr uint32_t kFullCount = FP4 ? 3u : 2u;
     // A warp that serves every n-th stage waits for a slot's last release by parity: it must not
@@ -160,11 +168,6 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 __device__ __forceinline__ int cluster_size()
 {
     uint32_t r;
@@ -220,8 +223,9 @@ __device__ __forceinline__ void join_experts(const LayerKernelArgs& a, int lane,
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Exponent of s of a block (or row) whose largest magnitude has these bits.
-__device__ __forceinline__ int digit_exponent(uint32_t most) { return max((int)(most >> 23), 1) - 128; }
+// Exponent of s of a block (or row) whose largest magnitude has these bits: -126 .. 127, 128 if
+// it is infinite or NaN.
+__device__ __forceinline__ int digit_exponent(uint32_t most) { return max((int)(most >> 23), 1) - 127; }
 
 // The ue4m3 code of 2^k, -9 <= k <= 8.
 __device__ __forceinline__ uint32_t ue4m3_pow2(int k)
@@ -259,13 +263,38 @@ struct Eight {
     }
 };
 
-// 256 elements of a row, 8 in each lane, into the digit rows from n0 on of a stage's B tile and
-// the words of their scales. One copy of the code, called (the operands of h's fp32 in q1 too).
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t select)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(select));
+    return r;
+}
+
+// An element's digits as e2m1, one to a byte: those of 8^0 .. 8^3 in lo, of 8^4 .. 8^7 in hi, of
+// the integer n nearest to v f0 f1, |n| <= 2^22.
+__device__ __forceinline__ void digits_of(float v, float f0, float f1, uint32_t& lo, uint32_t& hi)
+{
+    // 1.5 * 2^23 and n add up to the float whose bits are those of 1.5 * 2^23 and n. With 4 in
+    // each of eight octal places added, n's balanced digits -4 .. 3 stand there as 0 .. 7.
+    constexpr uint32_t kFours = 044444444u;
+    uint32_t u = __float_as_uint(__fmaf_rn(v * f0, f1, 12582912.0f)) - __float_as_uint(12582912.0f) + kFours;
+    // Octal digits to nibbles, then each to its code: bytes 0 .. 7 of a table.
+    u = (u & 0x00000FFFu) | ((u << 4) & 0x0FFF0000u);
+    u = (u & 0x003F003Fu) | ((u << 2) & 0x3F003F00u);
+    u = (u & 0x07070707u) | ((u << 1) & 0x70707070u);
+    constexpr uint32_t kBelowZero = 0x0A0C0D0Eu, kFromZero = 0x05040200u;   // -4 -3 -2 -1, 0 1 2 3
+    lo = prmt(kBelowZero, kFromZero, u);
+    hi = prmt(kBelowZero, kFromZero, u >> 16);
+}
+
+// 256 elements of a row, 8 in each lane, into the kDigits digit rows from n0 (a multiple of 8) on
+// of a stage's B tile and the words of their scales. One copy of the code, called (the operands of
+// h's fp32 in q1 too).
 template <int FMT, bool H>
 __device__ __noinline__ void store_digits(uint32_t sb, uint32_t sscale, int n0, int lane, int row_exp,
                                           int x0, int y0, int z0, int w0, int x1, int y1, int z1, int w1)
 {
-    constexpr int DIGITS = H ? kDigitsH : kDigitsX;
+    static_assert(kDigits == 8, "a B tile's rows of 128 bytes repeat their swizzle every eight");
     Eight<H> raw;
     raw.q[0] = make_int4(x0, y0, z0, w0);
     if (H) raw.q[H ? 1 : 0] = make_int4(x1, y1, z1, w1);
@@ -276,47 +305,53 @@ __device__ __noinline__ void store_digits(uint32_t sb, uint32_t sscale, int n0, 
     for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     most = max(most, __shfl_xor_sync(~0u, most, 1));
     if (FMT == kFp4Mx) most = max(most, __shfl_xor_sync(~0u, most, 2));
-    int e = digit_exponent(most);               // -127 .. 126
+    int e = digit_exponent(most);
     uint32_t code;
     if (FMT == kFp4Mx) {
-        code = (uint32_t)(e + 127);
+        e = max(e, -124);
+        code = (uint32_t)(e - 3 + 127);
     } else {
         const int k = max(e - row_exp + 8, -9);
         code = ue4m3_pow2(min(k, 8));
         e = row_exp - 8 + k;
     }
-    const bool bad = most >= 0x7F800000u;       // an infinity or a NaN: so is the row's result
-    if (bad) code = FMT == kFp4Mx ? kNanMx : kNanNv;
-    // 2^-e in two factors: a block far below its row's largest has e down to -143.
-    const float f0 = bad ? 0.0f : pow2(-(e >> 1)), f1 = pow2(-(e - (e >> 1)));
+    // An infinity or a NaN: so is the row's result, whatever the digits.
+    if (most >= 0x7F800000u) code = FMT == kFp4Mx ? kNanMx : kNanNv;
+    // 2^(21 - e) in two factors: -107 .. 164.
+    const int to = 21 - e;
+    const float f0 = pow2(to >> 1), f1 = pow2(to - (to >> 1));
+    // Bytes of two elements' digits, turned into words of eight elements' digits of one place.
+    uint32_t p[2][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = bad ? 0.0f : v[i] * f0 * f1;
+    for (int i = 0; i < 4; ++i) {
+        uint32_t lo0, hi0, lo1, hi1;
+        digits_of(v[2 * i], f0, f1, lo0, hi0);
+        digits_of(v[2 * i + 1], f0, f1, lo1, hi1);
+        p[0][i] = lo0 | lo1 << 4;
+        p[1][i] = hi0 | hi1 << 4;
+    }
+    const uint32_t to_row = sb + (uint32_t)(n0 * 128 + (lane & 3) * 4);
     const int unit = lane >> 2;
 #pragma unroll
-    for (int d = 0; d < DIGITS; ++d) {
-        uint32_t w = 0u;
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t a = prmt(p[h][0], p[h][1], 0x5140u), b = prmt(p[h][2], p[h][3], 0x5140u);
+        const uint32_t c = prmt(p[h][0], p[h][1], 0x7362u), d = prmt(p[h][2], p[h][3], 0x7362u);
+        const uint32_t place[4] = {prmt(a, b, 0x5410u), prmt(a, b, 0x7632u), prmt(c, d, 0x5410u),
+                                   prmt(c, d, 0x7632u)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t c = cvt_e2m1x2(v[2 * i], v[2 * i + 1]);
-            w |= c << (8 * i);
-            if (d + 1 < DIGITS) {
-                const uint32_t h2 = e2m1x2_to_f16x2(c);
-                v[2 * i] = (v[2 * i] - f16_lo(h2)) * 8.0f;
-                v[2 * i + 1] = (v[2 * i + 1] - f16_hi(h2)) * 8.0f;
-            }
-        }
-        const int n = n0 + d;
-        sts32(sb + (uint32_t)(n * 128 + ((unit ^ (n & 7)) << 4) + (lane & 3) * 4), w);
-    }
-    const int block = FMT == kFp4Mx ? lane >> 2 : lane >> 1;
-    if ((lane & (FMT == kFp4Mx ? 3 : 1)) == 0) {
-#pragma unroll
-        for (int d = 0; d < DIGITS; ++d) {
-            const int n = n0 + d;
-            sts_u8(sscale + (uint32_t)((block >> 2) * kScaleTile + (n & 31) * 16 + (n >> 5) * 4 + (block & 3)),
-                   code);
+        for (int j = 0; j < 4; ++j) {
+            const int n = 7 - (4 * h + j);      // the highest place in the first row
+            sts32(to_row + (uint32_t)(n * 128 + ((unit ^ n) << 4)), place[j]);
         }
     }
+    // The word of four blocks' scales, the same for each of the digits: a lane to a digit.
+    constexpr int kLanes = FMT == kFp4Mx ? 4 : 2;      // of a block
+    uint32_t word = code << (8 * (lane / kLanes & 3));
+    word |= __shfl_xor_sync(~0u, word, kLanes);
+    word |= __shfl_xor_sync(~0u, word, 2 * kLanes);
+    const int n = n0 + lane % (4 * kLanes);
+    if (lane % (4 * kLanes) < kDigits)
+        sts32(sscale + (uint32_t)(lane / (4 * kLanes) * kScaleTile + (n & 31) * 16 + (n >> 5) * 4), word);
 }
 
 // What a bf16 (given as fp32 bits) leaves of v; nothing if it is infinite.
@@ -360,11 +395,11 @@ __device__ __forceinline__ void fetch_next(const CUtensorMap& tm, const LayerKer
 }
 
 template <class C>
-__global__ void __launch_bounds__(kLayerThreads, 1)
+__global__ void __launch_bounds__(C::kThreads, 1)
 moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_next,
                  const LayerKernelArgs a)
 {
-    constexpr int STAGES = C::STAGES, FMT = C::FMT;
+    constexpr int STAGES = C::STAGES, FMT = C::FMT, kRowWarps = C::kRowWarps;
     constexpr bool DOWN = C::DOWN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -562,8 +597,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     const int chunks = *s_chunks, units = chunks * a.tiles;
     const int u_first = (int)((int64_t)units * cluster_index() / cluster_count());
     const int u_last = (int)((int64_t)units * (cluster_index() + 1) / cluster_count());
-    const int64_t thread0 = (int64_t)blockIdx.x * kLayerThreads + threadIdx.x;
-    const int64_t threads = (int64_t)gridDim.x * kLayerThreads;
+    const int64_t thread0 = (int64_t)blockIdx.x * C::kThreads + threadIdx.x;
+    const int64_t threads = (int64_t)gridDim.x * C::kThreads;
     if (!DOWN) {
         for (int64_t i = thread0; i < a.counters; i += threads) a.done[i] = 0u;
     } else if (chunks == 0) {   // no token has an expert
@@ -703,7 +738,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
 #pragma unroll
                         for (int n = C::kTerms - 2; n >= 0; --n)
                             r = __uint_as_float(q[C::kTerms * i + n]) + (C::FP4 ? 0.125f * r : r);
-                        v[b * kRowsLoad + i] = r;
+                        v[b * kRowsLoad + i] = FMT == kFp4Mx ? 8.0f * r : r;
                     }
                 }
                 tc_fence_before();
@@ -721,7 +756,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
                 float r = v[i];
                 if (FMT == kFp4Nv) {
                     const int pair = s_list[c.start + i];
-                    const int e = s_exp[DOWN ? pair : pair / a.K] - 8;   // -135 .. 118
+                    const int e = s_exp[DOWN ? pair : pair / a.K] - 8;   // -134 .. 120
                     r = r * pow2(e >> 1) * pow2(e - (e >> 1));
                 }
                 const uint32_t to = x0 + (uint32_t)((rank * per + i / split) * 128 + thread) * 4u;
@@ -954,7 +989,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
 // CTAs of a grid of clusters of `split` CTAs, one to an SM, within the SM budget; 0 if none
 // fits. Cached per kernel, split and device.
 template <typename Kernel>
-int layer_grid(Kernel kernel, size_t smem, int split, int num_sms)
+int layer_grid(Kernel kernel, int threads, size_t smem, int split, int num_sms)
 {
     if (split == 1) return num_sms;
     struct Entry {
@@ -977,7 +1012,7 @@ int layer_grid(Kernel kernel, size_t smem, int split, int num_sms)
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         cfg.gridDim = dim3((unsigned)(sms / split * split));
-        cfg.blockDim = dim3(kLayerThreads);
+        cfg.blockDim = dim3((unsigned)threads);
         cfg.dynamicSmemBytes = smem;
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)split;
@@ -1002,7 +1037,7 @@ int layer_split(int64_t units, int stages, int num_sms, int* grid)
     int best = 0;
     int64_t least = 0;
     for (int split = 1; split <= kMaxSplit && split <= stages; split *= 2) {
-        const int ctas = layer_grid(moe_layer_kernel<C>, C::kSmem, split, num_sms);
+        const int ctas = layer_grid(moe_layer_kernel<C>, C::kThreads, C::kSmem, split, num_sms);
         if (ctas < split) continue;
         const int64_t clusters = ctas / split;
         const int64_t cost = (units + clusters - 1) / clusters * ((stages + split - 1) / split + 1);
@@ -1051,7 +1086,7 @@ struct LayerPlan {
             ++n;
         }
         cfg.gridDim = dim3((unsigned)grid);
-        cfg.blockDim = dim3(kLayerThreads);
+        cfg.blockDim = dim3(C::kThreads);
         cfg.dynamicSmemBytes = C::kSmem;
         cfg.stream = o.stream;
         cfg.attrs = attr;

@@ -547,11 +547,11 @@ EP_API ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const e
  * rows first, w_down [E][D][dff].
  * h is fp32 and enters the down projection as two bf16 terms (2^-16); sums are fp32 in an order
  * fixed by the sizes; results are joined in fp32 in the order of k and rounded once to out_dtype.
- * ep_moe_layer_fp4: weights in 4 bits, of one format; x and h are taken apart into e2m1 digits
- * (four and five) of a power of two for each block of the format's size. An element of x down to
- * a sixteenth of its block's largest is exact, a smaller one within 2^-11 of the largest, one of
- * h within 2^-14; EP_FP4_NV also within 2^-28 of the row's largest. An infinity or a NaN in a
- * row makes that row's results NaN.
+ * ep_moe_layer_fp4: weights in 4 bits, of one format; x and h are taken apart into eight e2m1
+ * digits of a power of two for each block of the format's size. An element of x down to 2^-14
+ * of its block's largest is exact; every other one, and h, is within 2^-22 of its block's largest,
+ * EP_FP4_NV also within 2^-39 of the row's largest. An infinity or a NaN in a row makes that
+ * row's results NaN.
  * workspace: ep_moe_layer_workspace_bytes, 256-byte aligned, for this call alone until its
  * work is done. */
 EP_API size_t ep_moe_layer_workspace_bytes(const ep_buffer* buf, int64_t num_tokens, int64_t dff);

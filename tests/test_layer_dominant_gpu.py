@@ -1,0 +1,108 @@
+"""The layer for a few tokens where an activation is far above the others of its block: what the
+4-bit form holds of the others, shown by weights that are zero at the large ones."""
+import pytest
+import torch
+
+import combine_topk_ids_expert_gb300 as ep
+import fp4_util as F4
+from test_fp4_gpu import gen
+from test_moe_layer_gpu import Layer
+
+pytestmark = pytest.mark.gpu
+
+
+class Fine(Layer):
+    """Layer with the bounds of eight digits."""
+
+    def rest(self, x, h=False):
+        """x: bf16 down to 2^-14 of its block's largest exact, every other element within 2^-22 of
+        the largest; nv: 2^-39 of the row's largest."""
+        n = F4.BLOCK[self.fmt]
+        block = x.abs().unflatten(-1, (-1, n)).amax(-1, keepdim=True).expand(-1, -1, n).flatten(-2)
+        rest = block * 2.0 ** -22
+        if not h:
+            rest = torch.where(x.abs() * 2.0 ** 14 >= block, 0.0, rest)
+        if self.fmt == "nv":
+            rest = torch.maximum(rest, x.abs().amax(-1, keepdim=True) * 2.0 ** -39)
+        return rest
+
+    def sums(self, x, w, h=False):
+        """n 2^-23 sum |digit w| for any order. Octal digits from -4 to 3 add up to at most 3.7
+        times the number in magnitude (8 - 4 - 4/8 - ..), 4 with the joining of the digits' sums."""
+        return (4 * x.shape[-1] * 2.0 ** -23) * (x.abs() @ w.abs().T) + self.rest(x, h) @ w.abs().T
+
+    def change(self, i, codes=None, scales=None):
+        """Weights i with codes(nibbles [E, rows, cols]) and scales(codes [E, rows, blocks]) changed."""
+        w = self.w[i]
+        E, rows, cols = w.codes.shape[0], w.codes.shape[1], w.cols
+        c = torch.stack((w.codes & 15, w.codes >> 4), dim=-1).flatten(-2)
+        s = ep.untile_fp4_scales(w.scales, E * rows).view(E, rows, -1).clone()
+        if codes:
+            codes(c)
+        if scales:
+            scales(s)
+        packed = (c[..., 0::2] | c[..., 1::2] << 4).contiguous()
+        self.w[i] = ep.FP4(packed, ep.tile_fp4_scales(s), w.format, w.tensor_scale)
+        v = F4.values(c.view(-1, cols), s.view(-1, s.shape[-1]), w.format).cuda().view(E, rows, cols)
+        if w.tensor_scale is not None:
+            v = v * w.tensor_scale.double()[:, None, None]
+        self.v[i] = v
+
+
+def check(layer, x, ids, off):
+    """Each element within the bound; off: in the root mean square, relative."""
+    scores = torch.rand(ids.shape, device="cuda", generator=gen(3)) + 0.5
+    got = layer.run(x, scores, ids, out_dtype=torch.float32)
+    want, bound = layer.reference(x, scores, ids, "silu")
+    err = (got.double() - want).abs()
+    assert err.norm() <= off * want.norm(), float(err.norm() / want.norm())
+    assert (err <= bound + 2.0 ** -24 * want.abs()).all()
+    assert layer.buf.device_error() == 0
+    layer.buf.close()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("blocks", ["all", "one"])
+@pytest.mark.parametrize("power", [6, 10, 12])
+def test_beside_a_dominant_element_of_x(fmt, blocks, power):
+    """One element of 3 x 2^power in every block, or in one of the row, beside unit normals."""
+    D, F, E, K, T = 768, 128, 3, 2, 5
+    layer = Fine(D, F, E, K, fmt, seed=power)
+    n, g = F4.BLOCK[fmt], gen(power)
+    at = torch.randint(0, n, (D // n,), device="cuda", generator=g) + torch.arange(0, D, n, device="cuda")
+    if blocks == "one":
+        at = at[D // n // 2:][:1]
+
+    def zero(c):
+        c[..., at] = 0
+
+    layer.change(0, codes=zero)
+    x = torch.randn((T, D), device="cuda", generator=g).bfloat16()
+    x[:, at] = 3 * 2.0 ** power * (1 - 2 * torch.randint(0, 2, (T, len(at)), device="cuda", generator=g)).bfloat16()
+    ids = torch.rand((T, E), device="cuda", generator=g).topk(K, dim=1).indices.to(torch.int32)
+    # 3 x 2^12: an element below 1/2 is off by up to 2^-9, 2^-9 / 3^0.5 and of two elements in five in the
+    # root mean square: 0.0007 of the projections, at most three times that of the result.
+    check(layer, x, ids, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_beside_a_dominant_element_of_h(fmt):
+    """One column of each block of h 2^11 times the others, by its up projection's scales."""
+    D, F, E, K, T = 256, 384, 3, 2, 5
+    layer = Fine(D, F, E, K, fmt, seed=1)
+    n, g = F4.BLOCK[fmt], gen(11)
+    at = torch.randint(0, n, (F // n,), device="cuda", generator=g) + torch.arange(0, F, n, device="cuda")
+
+    def large(s):
+        s[:, F + at] += 11 if fmt == "mx" else 88
+
+    def zero(c):
+        c[..., at] = 0
+
+    layer.change(0, scales=large)
+    layer.change(1, codes=zero)
+    x = torch.randn((T, D), device="cuda", generator=g).bfloat16()
+    ids = torch.rand((T, E), device="cuda", generator=g).topk(K, dim=1).indices.to(torch.int32)
+    # h is within 2^-22 of its block's largest, which is at most 2^14 times the others' root mean
+    # square (its own magnitude included): 2^-8 / 3^0.5.
+    check(layer, x, ids, 2.0 ** -8)
