@@ -10,8 +10,8 @@
 // weights on their way: 4-bit codes go to the block-scaled instructions as they lie, which
 // leaves the CUDA cores with the activations alone.
 //
-// With bf16 weights x enters as it is, and h, fp32, as the sum of two bf16 rows (what the first
-// leaves is within 2^-8 of it, what both leave within 2^-16).
+// With bf16 weights x enters as it is, and h, fp32, as the sum of three bf16 rows: its first 8 bits,
+// the next 8 and the last, cut and not rounded, so that the three are h and none of them overflows.
 // With 4-bit weights a row enters as eight rows of e2m1 digits that share a power of two s for each
 // block of the weights' size:
 //     x = s (d0 + d1 / 8 + d2 / 64 + ... + d7 / 8^7) + rest,   -4 <= d <= 3,   |rest| <= s / 2^22,
@@ -72,8 +72,8 @@ struct LayerCfg {
     static constexpr int FMT = FMT_;
     static constexpr bool DOWN = DOWN_, FP4 = FMT_ != kFmtBf16;
     static constexpr int kStageK = FP4 ? kFp4StageK : 64;       // 128 bytes of a row
-    // Rows of the N side that a token row becomes: digits, or h's two bf16 terms.
-    static constexpr int kTerms = FP4 ? kDigits : DOWN ? 2 : 1;
+    // Rows of the N side that a token row becomes: digits, or h's three bf16 terms.
+    static constexpr int kTerms = FP4 ? kDigits : DOWN ? 3 : 1;
     static constexpr int kCols = kChunkRows * kTerms;
     static constexpr int kTiles = FP4 ? Fp4Mma<FP4 ? FMT_ : kFp4Mx>::kTiles : 0;
     static constexpr uint32_t kBytesA = kBM * 128, kBytesB = kCols * 128;
@@ -354,10 +354,17 @@ __device__ __noinline__ void store_digits(uint32_t sb, uint32_t sscale, int n0, 
         sts32(sscale + (uint32_t)(lane / (4 * kLanes) * kScaleTile + (n & 31) * 16 + (n >> 5) * 4), word);
 }
 
-// What a bf16 (given as fp32 bits) leaves of v; nothing if it is infinite.
-__device__ __forceinline__ float left_of(float v, uint32_t bf16)
+// The first 8 bits of two numbers, as bf16, and what is left of them (nothing of an infinity or a
+// NaN, which these bits hold).
+__device__ __forceinline__ uint32_t cut_bf16x2(float& a, float& b)
 {
-    return (bf16 & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(bf16);
+    const uint32_t h = prmt(__float_as_uint(a), __float_as_uint(b), 0x7632u);
+    auto left = [](float v, uint32_t cut) {
+        return (cut & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(cut);
+    };
+    a = left(a, h << 16);
+    b = left(b, h & 0xFFFF0000u);
+    return h;
 }
 
 // The weights that this CTA's successor in the second kernel reads first, to L2, while this kernel
@@ -947,15 +954,13 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
                         if constexpr (DOWN) {
                             float v[8];
                             cur[j].floats(v);
-                            uint32_t hi[4], lo[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                hi[i] = pack_bf16x2_rn(v[2 * i], v[2 * i + 1]);
-                                lo[i] = pack_bf16x2_rn(left_of(v[2 * i], hi[i] << 16),
-                                                       left_of(v[2 * i + 1], hi[i] & 0xFFFF0000u));
+                            for (int n = 0; n < C::kTerms; ++n) {
+                                uint32_t q[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) q[i] = cut_bf16x2(v[2 * i], v[2 * i + 1]);
+                                put(C::kTerms * r + n, q[0], q[1], q[2], q[3]);
                             }
-                            put(2 * r, hi[0], hi[1], hi[2], hi[3]);
-                            put(2 * r + 1, lo[0], lo[1], lo[2], lo[3]);
                         } else {
                             const int4 q = cur[j].q[0];
                             put(r, (uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w);

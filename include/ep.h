@@ -545,7 +545,7 @@ EP_API ep_status ep_expert_glu_fp4(ep_buffer* buf, const ep_fp4* x_recv, const e
  * buffers only; ids as for a dispatch (-1: no expert, a bad id sets EP_DEVERR_BAD_ID); a token
  * without an expert gets a zero row. D % 128 == 0, dff % 128 == 0. w_gate_up [E][2 dff][D], gate
  * rows first, w_down [E][D][dff].
- * h is fp32 and enters the down projection as two bf16 terms (2^-16); sums are fp32 in an order
+ * h is fp32 and enters the down projection whole, as three bf16 terms; sums are fp32 in an order
  * fixed by the sizes; results are joined in fp32 in the order of k and rounded once to out_dtype.
  * ep_moe_layer_fp4: weights in 4 bits, of one format; x and h are taken apart into eight e2m1
  * digits of a power of two for each block of the format's size. An element of x down to 2^-14

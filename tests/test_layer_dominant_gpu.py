@@ -1,5 +1,6 @@
-"""The layer for a few tokens where an activation is far above the others of its block: what the
-4-bit form holds of the others, shown by weights that are zero at the large ones."""
+"""What the layer for a few tokens holds of its activations. The 4-bit form: of those far below the
+largest of their block, shown by weights that are zero at the large ones. On bf16 weights: all of
+h."""
 import pytest
 import torch
 
@@ -106,3 +107,41 @@ def test_beside_a_dominant_element_of_h(fmt):
     # h is within 2^-22 of its block's largest, which is at most 2^14 times the others' root mean
     # square (its own magnitude included): 2^-8 / 3^0.5.
     check(layer, x, ids, 2.0 ** -8)
+
+
+def bf16_layer(gate, up, down):
+    """One expert, one column of h for each row of gate and up [128, 2]: x has two elements."""
+    buf = ep.Buffer(4, 128, 1, 1, 1)
+    w1 = torch.zeros((1, 256, 128), dtype=torch.bfloat16, device="cuda")
+    w1[0, :128, :2], w1[0, 128:, :2] = gate, up
+    w2 = (torch.eye(128, device="cuda") * down).bfloat16()[None].contiguous()
+
+    def run(x0, x1):
+        x = torch.zeros((1, 128), dtype=torch.bfloat16, device="cuda")
+        x[0, 0], x[0, 1] = x0, x1
+        return buf.moe_layer(x, torch.ones((1, 1), device="cuda"),
+                             torch.zeros((1, 1), dtype=torch.int32, device="cuda"), w1, w2,
+                             out_dtype=torch.float32)[0]
+    return buf, run
+
+
+def test_h_enters_whole_on_bf16_weights():
+    """Gates of 128 or more are silu's own results, so that h is a product of 16 and 8 bits, and a down
+    projection of ones gives it back."""
+    g = gen(5)
+    a, b, c = (torch.randint(lo, 256, (128,), device="cuda", generator=g) for lo in (128, 0, 128))
+    gate = torch.stack((a, b), 1).bfloat16()
+    up = torch.stack((c, torch.zeros_like(c)), 1).bfloat16()
+    buf, run = bf16_layer(gate, up, 1.0)
+    want = (a * 256 + b) * c
+    assert torch.equal(run(1.0, 2.0 ** -8).double(), want.double() / 256)
+    buf.close()
+
+
+def test_h_above_the_largest_bf16():
+    """4095^2 2^104: fp32 holds it, bf16 does not."""
+    both = torch.tensor([[255.0, 0.9375]], device="cuda").expand(128, 2).bfloat16()
+    buf, run = bf16_layer(both, both, 2.0 ** -10)
+    out = run(2.0 ** 56, 2.0 ** 56).double()
+    assert torch.equal(out, torch.full_like(out, 4095.0 ** 2 * 2.0 ** 94))
+    buf.close()
