@@ -130,7 +130,7 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t c)
     return FMT == kFp4Mx ? ue8m0_value(c) : ue4m3_value(c);
 }
 
-constexpr uint32_t kNanMx = 0xFFu, kNanNv = 0x7Fu;
+constexpr uint32_t kNanMx = 0xFFu, kNanNv = 0x7Fu, kLargestNv = 0x7Eu;
 
 // x / (d g) near enough to round it to a format of few bits: what an fp32 product with the
 // reciprocal gives, except next to a number of at most BITS fraction bits (the borders
@@ -214,8 +214,18 @@ __device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], uint32_t c, f
             differ |= w[h] ^ cvt_e2m1x8(above);
         }
         if (differ == 0u) return make_uint2(w[0], w[1]);
+        // Some element lies next to a border. In a block whose scale is the largest there is, elements
+        // may be anything above the grid, up to quotients that overflow and leave no sign.
+        float near[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = quotient_for_rounding<2>(v[i], s, g, rinv);   // seldom
+        for (int i = 0; i < 16; ++i) near[i] = v[i];
+        if (c == kLargestNv) {
+            const float far = 1024.0f * s * g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) near[i] = fminf(fmaxf(v[i], -far), far);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = quotient_for_rounding<2>(near[i], s, g, rinv);
     } else {
         // x has 8 bits and s 4: the quotient is on a border or 2^-12 away from it, and its last
         // bits are the reciprocal's.
