@@ -308,8 +308,8 @@ expert_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             const int acc = tl & 1;
             // A pair: the tile before has drained the columns that both accumulators have.
             // One SM: the last tile of this accumulator has been drained.
-            if (PAIR) ok = tl == 0 || wait_or_abort(accum_free0, (uint32_t)((tl - 1) & 1), s_abort);
-            else ok = wait_or_abort(accum_free0 + 8u * acc, (uint32_t)(((tl >> 1) & 1) ^ 1), s_abort);
+            if (PAIR) ok = tl == 0 || wait_or_abort<PAIR>(accum_free0, (uint32_t)((tl - 1) & 1), s_abort);
+            else ok = wait_or_abort<PAIR>(accum_free0 + 8u * acc, (uint32_t)(((tl >> 1) & 1) ^ 1), s_abort);
             ok = warp_all(ok);
             if (!ok) break;
             tc_fence_after();

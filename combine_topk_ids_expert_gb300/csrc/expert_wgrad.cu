@@ -213,7 +213,7 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
             if (w.k_iters == 0) continue;
             const int acc = tl & 1, use = tl >> 1;
             ++tl;
-            ok = warp_all(wait_or_abort(accum_empty0 + 8u * acc, (uint32_t)((use & 1) ^ 1), s_abort));
+            ok = warp_all(wait_or_abort<PAIR>(accum_empty0 + 8u * acc, (uint32_t)((use & 1) ^ 1), s_abort));
             if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
