@@ -1285,7 +1285,13 @@ class Buffer:
                        h: torch.Tensor | FP4 | None = None, quantize: bool = False,
                        h_scale: torch.Tensor | None = None, stream=None):
         """h = act(x Wg^T) * (x Wu^T) over each expert's receive rows, both in 4 bits: in bf16,
-        or, with quantize, as an FP4 of the same format (h_scale: its tensor_scale)."""
+        or, with quantize, as an FP4 of the same format (h_scale: its tensor_scale). A given h
+        says by itself which."""
+        if h is not None and (h_scale is not None or (quantize and not isinstance(h, FP4))):
+            raise ValueError("a given h is a bfloat16 tensor, or an FP4 with its own tensor_scale: "
+                             "quantize and h_scale are for one that is made")
+        if h_scale is not None and not quantize:
+            raise ValueError("h_scale needs quantize=True")
         rows = self._weights_fp4(w_gate_up, "w_gate_up", x_recv)
         if rows % 256:
             raise ValueError(f"w_gate_up must hold gate and up rows, 128 of each or a multiple, "
