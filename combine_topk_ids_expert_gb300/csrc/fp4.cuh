@@ -124,12 +124,6 @@ __device__ __forceinline__ float ue8m0_value(uint32_t c)
     return __uint_as_float(c == 0u ? 0x00400000u : c == 255u ? 0x7FC00000u : c << 23);
 }
 
-template <int FMT>
-__device__ __forceinline__ float fp4_scale_value(uint32_t c)
-{
-    return FMT == kFp4Mx ? ue8m0_value(c) : ue4m3_value(c);
-}
-
 constexpr uint32_t kNanMx = 0xFFu, kNanNv = 0x7Fu, kLargestNv = 0x7Eu;
 
 // x / (d g) near enough to round it to a format of few bits: what an fp32 product with the

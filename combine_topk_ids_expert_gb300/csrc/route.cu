@@ -380,19 +380,22 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
     griddep_launch_dependents();
 }
 
+template <int NV, bool WIDE>
+auto kernel_of(const RouteArgs& a, bool backward) -> void (*)(RouteArgs)
+{
+    if (backward)
+        return a.bf16 ? route_backward_kernel<NV, true, WIDE> : route_backward_kernel<NV, false, WIDE>;
+    return a.bf16 ? route_kernel<NV, true, WIDE> : route_kernel<NV, false, WIDE>;
+}
+
 template <int NV>
 cudaError_t launch_nv(const RouteArgs& a, bool backward, const LaunchOpts& o)
 {
     const int64_t ctas = (a.T + kRouteThreads / 32 - 1) / (kRouteThreads / 32);
     const dim3 grid((unsigned)ctas);
-    const bool wide = a.K > 32;
-    void (*kernel)(RouteArgs);
-    if (backward)
-        kernel = a.bf16 ? (wide ? route_backward_kernel<NV, true, true> : route_backward_kernel<NV, true, false>)
-                        : (wide ? route_backward_kernel<NV, false, true> : route_backward_kernel<NV, false, false>);
-    else
-        kernel = a.bf16 ? (wide ? route_kernel<NV, true, true> : route_kernel<NV, true, false>)
-                        : (wide ? route_kernel<NV, false, true> : route_kernel<NV, false, false>);
+    auto kernel = kernel_of<NV, false>(a, backward);
+    if constexpr (NV > 1)     // 32 experts never have more than 32 slots
+        if (a.K > 32) kernel = kernel_of<NV, true>(a, backward);
     return launch_kernel(kernel, grid, kRouteThreads, 0, o, a);
 }
 
