@@ -1197,6 +1197,7 @@ static ep_status enqueue_fp4(ep_buffer* b, const ep_fp4* x, const ep_fp4* w, int
     a.kind = b->gemm_kind;
     a.row_tiles = std::max<int64_t>(std::min<int64_t>(E, b->last_T * b->cfg.topk),
                                     b->last_T * b->cfg.topk / 256);
+    a.mean_rows = b->last_T * b->cfg.topk / E;
     a.light_rows = b->gemm_light_rows;
     a.err = b->err;
     return cuda_status(ep::launch_expert_fp4(a, b->num_sms, opts(b, as_stream(stream))));

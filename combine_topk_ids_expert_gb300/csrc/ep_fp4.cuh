@@ -81,6 +81,7 @@ struct ExpertFp4Args {
                                    // 0: by the number of tiles
     int light_rows;                // as GemmArgs
     int64_t row_tiles;             // row tiles of 256 that the call is likely to have
+    int64_t mean_rows;             // rows of an expert, on average over all
     uint32_t* err;
 };
 cudaError_t launch_expert_fp4(const ExpertFp4Args& a, int num_sms, const LaunchOpts& o);

@@ -531,12 +531,22 @@ cudaError_t launch_form(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o
 template <int FMT, int OUT>
 cudaError_t launch_out(const ExpertFp4Args& f, int num_sms, const LaunchOpts& o)
 {
-    // Pairs (256 x 256) where every pair of SMs has a tile, else single SMs (128 x 128). The whole
-    // block, nv / mx, pairs against singles: 1024 rows of 8 experts, 4096 wide, 118 / 109 against
-    // 161 / 148 us; 256 rows of 256 experts (Zipf), 7168 wide, 1878 / 1663 against 2180 / 2009 us;
-    // 83 rows of 16 experts, 1024 wide (64 tiles of pairs), 26 / 24 against 21 / 20 us.
+    // Pairs (256 x 256) where every pair of SMs has a tile and an expert's rows fill more than a
+    // tile of single SMs (128 x 128) on average. The whole block in nv, single SMs against pairs, us
+    // by rows of an expert:
+    //                                          8           32           64           128          256
+    //     256 experts, 7168 wide, dff 2048   976 / 1049  1006 / 1080  1042 / 1114  1347 / 1171
+    //     256 experts, 2048 wide, dff 512    125 / 145    134 / 152    141 / 158    189 / 177
+    //     64 experts, 4096 wide, dff 2048                 173 / 182    175 / 186    226 / 199    333 / 259
+    //     8 experts, 4096 wide, dff 2048      45 / 47      43 / 47      44 / 49      53 / 52      67 / 63
+    //     16 experts, 1024 wide, dff 512      19 / 23      20 / 24      20 / 25      26 / 27      30 / 33
+    // (the last one has a tile for every pair from 512 rows on). Skewed (Zipf), the first one takes
+    // 1184 / 1173 with 64 rows on average and 1396 / 1300 with 112, uniform with 112 1103 / 1133.
+    // Calls with less than a row of an expert are 7% slower to 9% faster on single SMs, by the width.
+    constexpr int64_t kPairRows = 96;
     const int64_t cols = f.glu ? 2 * f.dout : f.dout;
-    if (f.kind != 1 && cols % 256 == 0 && (f.kind == 2 || 2 * f.row_tiles * (cols / 256) >= num_sms)) {
+    if (f.kind != 1 && cols % 256 == 0 &&
+        (f.kind == 2 || (f.mean_rows >= kPairRows && 2 * f.row_tiles * (cols / 256) >= num_sms))) {
         const cudaError_t e = launch_form<FMT, true, OUT>(f, num_sms, o);
         if (e != cudaErrorNotSupported) return e;
     }

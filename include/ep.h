@@ -526,8 +526,9 @@ EP_API ep_status ep_dispatch_fp4(ep_buffer* buf, const void* x_TD, const float* 
  * goes to `h` as bf16, or, where `h_fp4` is given instead, quantised from fp32 into it (the
  * same format, its tensor_scale one number or NULL), ready for the down projection.
  * din % 128 == 0, dout % 128 == 0, dff % 128 == 0. Tiles of 256 rows x 256 columns on an SM
- * pair where there are enough of them for all SMs, else 128 x 128 on one (EP_GEMM_KERNEL as for
- * ep_expert_gemm); both add a row's products in the same order. */
+ * pair where there are enough of them for all SMs and 96 rows or more of an expert on average, else
+ * 128 x 128 on one (EP_GEMM_KERNEL as for ep_expert_gemm); both add a row's products in the
+ * same order. */
 EP_API ep_status ep_expert_gemm_fp4(ep_buffer* buf, const ep_fp4* x_recv, const ep_fp4* weights,
                                     int64_t din, int64_t dout, void* y_recv, ep_stream_t stream);
 
