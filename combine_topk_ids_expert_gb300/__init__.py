@@ -895,6 +895,7 @@ class Buffer:
             self.handle = ep_buffer_init(self.cfg, self.workspace)
         self._space = _Space(self.workspace)
         self._layer_bytes: dict = {}
+        self._stride: int | None = None        # of the last call's receive layout
 
     # -- views -------------------------------------------------------------
     def _view(self, ptr: int, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
@@ -1373,6 +1374,8 @@ class Buffer:
         return out
 
     def _last_stride(self) -> int:
+        if self._stride is None:
+            raise EpError(_abi.EP_ERR_NO_LAYOUT, "receive rows of a buffer without a dispatch")
         return self._stride
 
     def device_error(self, stream=None) -> int:

@@ -23,3 +23,15 @@ def test_a_given_h_says_by_itself_how_it_is_held():
 def test_a_scale_of_h_needs_quantisation():
     with pytest.raises(ValueError, match="h_scale needs"):
         glu(h_scale=torch.ones(1))
+
+
+def test_receive_rows_before_a_dispatch():
+    buf = object.__new__(ep.Buffer)          # no GPU needed for what comes first
+    buf.R, buf.E, buf.packed, buf._stride = 1, 4, True, None
+    rows = ep.FP4(torch.zeros((4, 64), dtype=torch.uint8), torch.zeros((1, 2, 32, 4, 4), dtype=torch.uint8),
+                  "nv")
+    w = ep.FP4(torch.zeros((4, 128, 64), dtype=torch.uint8),
+               torch.zeros((4, 2, 32, 4, 4), dtype=torch.uint8), "nv")
+    with pytest.raises(ep.EpError) as e:
+        buf.expert_gemm_fp4(rows, w)
+    assert e.value.status == ep._abi.EP_ERR_NO_LAYOUT
