@@ -145,3 +145,29 @@ def test_h_above_the_largest_bf16():
     out = run(2.0 ** 56, 2.0 ** 56).double()
     assert torch.equal(out, torch.full_like(out, 4095.0 ** 2 * 2.0 ** 94))
     buf.close()
+
+
+def test_the_largest_bf16_on_4_bit_weights():
+    """x and h of 1.9921875 x 2^127 through weights of 1: every digit's product stays finite."""
+    def fp4(rows, at, scale):
+        """mx, row r: 1.0 at column at[r], all blocks of the row with this scale code."""
+        codes = torch.zeros((rows, 128), dtype=torch.uint8)
+        codes[torch.arange(rows), at] = 2
+        scales = scale[:, None].expand(rows, 4).to(torch.uint8).contiguous()
+        packed = (codes[:, 0::2] | codes[:, 1::2] << 4).contiguous()
+        return ep.FP4(packed[None].contiguous().cuda(), ep.tile_fp4_scales(scales.cuda()), "mx")
+
+    # gate: x[0] by 1; up: x[40] = 2^100 by 2^-100, in another block; down: h by 2^-10.
+    at = torch.cat((torch.zeros(128, dtype=torch.long), torch.full((128,), 40)))
+    w1 = fp4(256, at, torch.cat((torch.full((128,), 127), torch.full((128,), 27))))
+    w2 = fp4(128, torch.arange(128), torch.full((128,), 117))
+    buf = ep.Buffer(4, 128, 1, 1, 1)
+    x = torch.zeros((1, 128), dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[0, 40] = 1.9921875 * 2.0 ** 127, 2.0 ** 100
+    out = buf.moe_layer(x, torch.ones((1, 1), device="cuda"),
+                        torch.zeros((1, 1), dtype=torch.int32, device="cuda"), w1, w2,
+                        out_dtype=torch.float32)[0].double()
+    # Columns of h other than a block's own are zeros to w2's rows; each has one.
+    assert torch.equal(out, torch.full_like(out, 1.9921875 * 2.0 ** 117))
+    assert buf.device_error() == 0
+    buf.close()
