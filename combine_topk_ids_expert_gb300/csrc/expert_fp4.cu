@@ -9,8 +9,8 @@
 // scales of its rows; four more warps bring the scales, each every fourth stage. A tile of
 // receive rows starts anywhere in the 128-row tiles that scales lie in, so its scales are
 // copied row by row, 4 bytes for 4 blocks, to where the tile's own rows want them; W's come
-// as whole tiles by TMA (gated tiles of one SM: half lines, by the warps). The issuing thread moves a stage's scales to tensor memory and multiplies;
-// both run in order.
+// as whole tiles by TMA (gated tiles of one SM: half lines, by the warps). The issuing thread moves a
+// stage's scales to tensor memory and multiplies; both run in order.
 //
 // Tensor memory: the accumulator of 256 columns (an SM pair, tiles of 256 rows x 256 columns)
 // does not fit twice beside the scales, so the two accumulators overlap: each tile's epilogue

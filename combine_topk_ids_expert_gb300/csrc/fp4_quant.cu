@@ -4,11 +4,12 @@
 // One thread takes 16 consecutive elements: a block of nv, half a block of mx (whose halves
 // meet in one shuffle). The floor is the bytes, and without a matrix's scale that is what it
 // takes: 134 M elements, 344 MB, 54 us in nv and 52 in mx (6.4 and 6.6 TB/s), 54 and 62 us back to
-// bf16. With a matrix's scale 68 us: issue slots (every element is multiplied and converted
-// twice to see whether it lies next to a border). Steps for that case, there and back: 106 + 88
-// us; 138 together with products of two elements in one instruction, borders found from two
-// conversions (before: from each quotient's last bits), the next row on its way during this
-// one's work, and one resident wave of CTAs.
+// bf16. With a matrix's scale 78 us: issue slots, 70% of them used (every element is multiplied and
+// converted twice to see whether it lies next to a border, and where the scale comes from the
+// matrix's own largest element some of most warps' elements do). Steps for that case, there and
+// back: 106 + 88 us; 138 together with products of two elements in one instruction, borders found
+// from two conversions (before: from each quotient's last bits), the next row on its way during
+// this one's work, and one resident wave of CTAs; 133.
 #include <algorithm>
 #include <mutex>
 #include "ep_fp4.cuh"
@@ -24,7 +25,7 @@ constexpr size_t kDispatchFp4Smem = 100 * 1024;   // of such a tile
 // Receive rows whose codes wait in shared memory for the layout. The wait is long enough for a few
 // tokens: 4096 tokens (D 4096, top 2) take 20.9 us with none kept, 20.1 with 16 rows, 19.5 with 32;
 // 8192 tokens (D 7168, top 8) 105, 104 and 110, with as many as fit 128: reading and writing then
-// no longer overlap.
+// no longer overlap. (Between the two: 32 is the first size's best, 16 the second's.)
 constexpr int kKeptRows = 16;
 
 // What 16 elements become: 8 bytes of codes, and on every fourth block's first thread the
@@ -92,7 +93,7 @@ struct RowScale {
 // A warp takes 32 units of a row after the other, the next row's on their way (grid: columns x,
 // rows y, all resident at once; no index of an element is divided: that cost a quarter of the
 // time).
-// CTAs on an SM. Quantising with a matrix's scale spills at 5 (70.6 against 67.8 us); the others take
+// CTAs on an SM. Quantising with a matrix's scale takes 84 us with 5 and 78 with 4; the others take
 // 54 and 52 us with 5, 57 with 4, 60 and 52 with 6. Back: 54 us (nv) and 62 (mx) with 4, 57 and
 // 64 with 5, 59 and 54 with 3.
 template <bool TENSOR_SCALE>
@@ -521,7 +522,8 @@ cudaError_t launch_dispatch_fp4(const LayoutArgs& l, const PermuteFp4Args& args,
     const size_t token = (size_t)(a.D / 2 + a.D / (a.format == kFp4Mx ? 32 : 16));
     a.kept = 0;
     if (!small && tables < kDispatchFp4Smem)
-        a.kept = (int)std::min<int64_t>(std::min<int64_t>(l.tpt, kKeptRows / l.K), (int64_t)((kDispatchFp4Smem - tables) / token));
+        a.kept = (int)std::min<int64_t>(std::min<int64_t>(l.tpt, kKeptRows / l.K),
+                                        (int64_t)((kDispatchFp4Smem - tables) / token));
     const size_t smem = tables + a.kept * token;
     void (*kernel)(LayoutArgs, PermuteFp4Args) =
         a.format == kFp4Mx ? (small ? dispatch_fp4_kernel<kFp4Mx, false, true>

@@ -37,17 +37,20 @@
 //
 // Sums, h, scores and the pairs' results are fp32; the layer's result is rounded once.
 //
-// Measured (D 7168, dff 2048, 8 of 256 experts; GB/s of weights): 1 token 112 us in bf16 (6.3
-// TB/s), 42 us mx, 48 us nv (4.1); 16 tokens 1258 us (7.1) and 409 us mx (5.8). Bound by HBM
-// from a few tokens on. One token: about 5 us to the first product of each kernel (launch,
-// routing, the first rows behind their latency), 2 us from one kernel to the other, and a
-// quarter of a wave. Steps, for 16 tokens mx: 1275 us as it was first (joins by one CTA, each
-// load waited for), 725 with joins in batches, 516 with a cluster's units next to one another,
-// 447 with one copy of the digits' code, 430 with descriptors moved by additions. For one token
-// nv: 74, 69, 66, 64; 62 with loads after the arrivals, 50 with the weights first to leave L2.
+// Measured (D 7168, dff 2048, 8 of 256 experts; rate of the weights): 1 token 115 us in bf16 (6.1
+// TB/s), 44 us mx (4.3), 48 us nv (4.1); 16 tokens 1277 us (7.0), 427 us mx (5.5) and 486 us nv (5.2);
+// 64 tokens 2786 us (7.1), 986 us (5.3) and 1140 us (4.9). Bound by HBM from a few tokens on;
+// 64 tokens over 8 experts, 4096 wide, by the work on the rows (141 us mx, 113 us in bf16). One
+// token: about 5 us to the first product of each kernel (launch, routing, the first rows behind
+// their latency), 2 us from one kernel to the other, and a quarter of a wave. Steps, with the
+// shorter digits of before, for 16 tokens mx: 1275 us as it was first (joins by one CTA, each load
+// waited for), 725 with joins in batches, 516 with a cluster's units next to one another, 447 with
+// one copy of the digits' code, 430 with descriptors moved by additions, 410 with the weights first
+// to leave L2. For one token nv: 74, 69, 66, 64; 62 with loads after the arrivals, 50 with the
+// weights first to leave L2.
 // Tried: warps that share a stage's rows (each waits for every slot), the row loop unrolled
-// over four rows (its code, 19 KB, comes from memory in every call), the scales of the weights
-// fetched before the arrival of the stage at hand.
+// over four rows (its code comes from memory in every call), the scales of the weights fetched
+// before the arrival of the stage at hand.
 #include "ep_fp4.cuh"
 #include "fp4_umma.cuh"
 
@@ -63,7 +66,8 @@ constexpr uint32_t kLayerTmem = 512;            // a CTA has its SM for itself (
 constexpr int kMaxSplit = 4;
 // Of a CTA's weights in the second kernel, fetched to L2 by the first: 1 token of bf16 (2 x 4096 x
 // 2048 x 2 experts) 30.0 us without, 28.8 with 96 KB, 28.4 with 192, 28.1 with 512; 1 token nv
-// (8 x 7168) 46.3, 46.3, 47.6 and 50.2, where more of them is in memory's way.
+// (8 x 7168) 46.3, 46.3, 47.6 and 50.2, where more of them is in memory's way. Those two sizes are
+// all that was measured: the least amount that helped one and did not hurt the other.
 constexpr int kNextBytes = 96 * 1024;
 constexpr int kFmtBf16 = 2;                     // beside kFp4Mx, kFp4Nv
 
@@ -94,7 +98,8 @@ struct LayerCfg {
     // get there while the release before that one is out, which its own last stage rules out as
     // long as that is at most a ring's length ago.
     static_assert(kRowWarps <= STAGES && kScaleWarps <= STAGES, "a warp's stages within the ring");
-    static_assert(kScaleCol0 + 2 * 2 * 16 <= kLayerTmem && kCols <= kAccCols && kCols <= 128, "accumulators and scales");
+    static_assert(kScaleCol0 + 2 * 2 * 16 <= kLayerTmem && kCols <= kAccCols && kCols <= 128,
+                  "accumulators and scales");
 };
 
 struct LayerKernelArgs {
